@@ -392,6 +392,154 @@ int pw_plan_kernel_times(pw_plan_t plan, pw_kernel_time* out, int max, int* n);
 int pw_plan_reset_times(pw_plan_t plan);
 
 /* ======================================================================== *
+ * Operators around an MOE step, for a model's block and for training
+ * (PATHWAYS page, section 6.3: the routing of a mixture of experts is a
+ * learned function; section 2: the programs are training steps). The MOE step
+ * computes A (router, gates), the exchange, B (expert FFN) and the combine;
+ * these calls add what stands before and after it in a block (the norms with
+ * the block's gate and residual scale), the loss that balances its router,
+ * and the gradients of everything but the experts' own products.
+ *
+ * They need no plan: each call takes a descriptor, its buffers and, where it
+ * has one, a workspace of the size its *_workspace call reports (device,
+ * 256-byte aligned; contents need not be cleared and nothing is kept in it
+ * between calls, so calls that are ordered may share one; calls that overlap
+ * must not). They enqueue kernel launches only, so they can be captured into
+ * HIP graphs and replayed. All buffers and the stream must belong to the
+ * current device. Buffers are contiguous; outputs must not overlap inputs or
+ * each other except where said. Sums are fp32 or wider and in a fixed order:
+ * equal inputs give equal bits.
+ * ======================================================================== */
+
+/* ---- router balance: loss, per-expert counts, gradient of the logits ------
+ * p = softmax(logits[t]), over the tokens with valid[t] != 0, n of them:
+ *   counts[e]    = tuples routed to e; counts[E] = n
+ *   prob_mean[e] = 1/n sum_t p[t][e]
+ *   loss[0]      = balance_coef E sum_e counts[e] / (k n) prob_mean[e]
+ *   loss[1]      = z_coef / n sum_t (log sum_e exp logits[t][e])^2
+ * and zeros if n == 0. Tokens with valid[t] == 0 are not looked at. An expert
+ * id outside [0, E) is no tuple. A token whose logits are all -infinity has
+ * zero probabilities and a zero logarithm. */
+typedef struct {
+  uint64_t tokens;       /* at most 2^28; tokens x top_k below 2^31             */
+  uint32_t num_experts;  /* 2..256                                              */
+  uint32_t top_k;        /* tuples per token, 1..8, at most num_experts         */
+  float balance_coef;
+  float z_coef;
+} pw_balance_desc;
+
+typedef struct {
+  const float* logits;     /* [tokens][E]                                       */
+  const int32_t* experts;  /* [tokens][k]                                       */
+  const uint8_t* valid;    /* [tokens], nullable (every token is valid)         */
+  int32_t* counts;         /* [E + 1]: written by pw_router_balance, read by
+                              pw_router_grad (the counts are constants there)   */
+  float* prob_mean;        /* [E]; nullable                                     */
+  float* loss;             /* [2]                                               */
+  /* pw_router_grad only */
+  const float* gates;      /* [tokens][k] softmax over the kept logits; NULL: no
+                              gradient comes from the gates                     */
+  const float* dgates;     /* [tokens][k] gradient of the gates (with gates)    */
+  const float* grad_loss;  /* [2] upstream gradients of loss[0..1]; NULL: ones  */
+  float* dlogits;          /* [tokens][E], written whole: zero where valid == 0 */
+} pw_balance_io;
+
+int pw_router_balance_workspace(const pw_balance_desc* d, size_t* bytes);
+/* Loss and counts. */
+int pw_router_balance(const pw_balance_desc* d, const pw_balance_io* io, void* ws, size_t ws_bytes, void* stream);
+/* The whole gradient of the router logits: of both losses, and of the gates
+ * (softmax over the k kept logits). */
+int pw_router_grad(const pw_balance_desc* d, const pw_balance_io* io, void* stream);
+
+/* ---- gradients of an MOE step's combine, dispatch and router ---------------
+ * The step's own buffers (pw_exchange on an MOE plan) are the inputs: y is
+ * b_out, gates, src_index and dst.shard_offsets as the step wrote them. The
+ * caller runs the gradient of the experts' products between the two calls
+ * (from dy to dxd, both in dispatched order). */
+typedef struct {
+  uint64_t tokens;       /* 1..2^28 (0: nothing is done)                        */
+  uint64_t rows;         /* rows y, dy, dxd and src_index hold, at most 2 tokens */
+  uint32_t d;            /* a multiple of 256, at most 1280                     */
+  uint32_t num_experts;  /* 2..64                                               */
+  uint32_t top_k;        /* 2                                                   */
+  uint32_t dtype;        /* PW_BF16                                             */
+} pw_moe_grad_desc;
+
+typedef struct {
+  const void* dout;         /* [tokens][d] gradient of the combined output      */
+  const void* y;            /* [rows][d] expert outputs                         */
+  const float* gates;       /* [tokens][2]                                      */
+  const int32_t* src_index; /* [rows] tuple held by each dispatched row         */
+  const int64_t* offsets;   /* [E + 1] segment offsets; rows from offsets[E] on
+                               hold nothing and are left as they are            */
+  const uint8_t* valid;     /* [tokens], nullable: where 0 (padding), dy and
+                               dgates are zero whatever dout, y and gates hold  */
+  void* dy;                 /* [rows][d]: dy[slot] = gate dout[token]           */
+  float* dgates;            /* [tokens][2]: dout[token] . y[slot], 0 if dropped */
+  int32_t* slot_of;         /* [tokens][2]: the row of each tuple, -1 if dropped */
+} pw_combine_grad_io;
+
+typedef struct {
+  const void* dxd;          /* [rows][d] gradient of the dispatched rows        */
+  const float* dlogits;     /* [tokens][E] (pw_router_grad)                     */
+  const void* w_router;     /* [d][E] bf16, as the plan was given it            */
+  const void* x;            /* [tokens][d] the step's tokens (with dw_router)   */
+  const int32_t* slot_of;   /* [tokens][2] (pw_moe_combine_grad)                */
+  const uint8_t* valid;     /* [tokens], nullable: where 0 (padding), dx is zero
+                               and x adds nothing to dw_router                  */
+  void* dx;                 /* [tokens][d]: both tuples' dxd rows + dlogits . w_router^T */
+  float* dw_router;         /* [d][E] fp32: x^T . dlogits; nullable             */
+} pw_dispatch_grad_io;
+
+int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_grad_io* io, void* stream);
+int pw_moe_dispatch_grad_workspace(const pw_moe_grad_desc* d, size_t* bytes);
+int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch_grad_io* io, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* ---- norms around a block, with its gate and residual scale ----------------
+ * One call stands between two blocks: it closes the block whose input was x
+ * and whose output is y, and opens the next one:
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) * w        (over a row's d elements)
+ *   r = x_scale x + y_scale gate * N(y; w_y)       (the residual stream)
+ *   h = N(r; w_r)                                  (the next block's input)
+ * with gate [gates][d], each row shared by rows / gates consecutive rows.
+ * Parts that are NULL drop out: y (r = x_scale x), w_y (y as it is), gate
+ * (ones), w_r with h (no next norm). Intermediate values stay fp32; r and h
+ * are each rounded once (h is the norm of r before its rounding). */
+typedef struct {
+  uint64_t rows;     /* at most 2^31 - 1; a multiple of gates                   */
+  uint32_t d;        /* 1..8192                                                 */
+  uint32_t dtype;    /* pw_dtype of rows, weights and gates                     */
+  uint32_t gates;    /* rows of gate; 0: none                                   */
+  float x_scale, y_scale, eps;  /* finite; eps > 0                              */
+} pw_norm_desc;
+
+typedef struct {
+  const void* x;     /* [rows][d]                        (pw_block_norm)        */
+  const void* y;     /* [rows][d]; nullable                                     */
+  const void* w_y;   /* [d]; nullable (needs y)                                 */
+  const void* gate;  /* [gates][d]; NULL if and only if gates == 0 (needs y)    */
+  const void* w_r;   /* [d]; nullable                                           */
+  void* r;           /* [rows][d] (may be x). pw_block_norm writes it if not NULL;
+                        pw_block_norm_grad reads it where w_r is given           */
+  void* h;           /* [rows][d] (with w_r)             (pw_block_norm)        */
+  /* pw_block_norm_grad only */
+  const void* dr;    /* [rows][d] gradient of r from its other uses; nullable (0) */
+  const void* dh;    /* [rows][d] gradient of h (with w_r)                      */
+  const uint8_t* valid; /* [rows], nullable: where 0 (padding), dx and dy are zero and
+                        the row adds nothing to dw_y, dgate and dw_r, whatever it holds */
+  void* dx;          /* [rows][d] (may be dr)                                   */
+  void* dy;          /* [rows][d] (with y)                                      */
+  float* dw_y;       /* [d] (with w_y)                                          */
+  float* dgate;      /* [gates][d] (with gate)                                  */
+  float* dw_r;       /* [d] (with w_r)                                          */
+} pw_norm_io;
+
+int pw_block_norm(const pw_norm_desc* d, const pw_norm_io* io, void* stream);
+int pw_block_norm_grad_workspace(const pw_norm_desc* d, size_t* bytes);
+int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, void* ws, size_t ws_bytes, void* stream);
+
+/* ======================================================================== *
  * Multi-tenant scheduler (PATHWAYS page, section 5.2 "Multi-tenancy",
  * Figures 8 and 9; Appendix D, Figure 11): programs of several clients are
  * gang-scheduled onto the whole GPU one after another, interleaved at the

@@ -75,6 +75,39 @@ class pw_kernel_time(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_uint64), ("total_ms", C.c_double)]
 
 
+class pw_balance_desc(C.Structure):
+    _fields_ = [("tokens", C.c_uint64), ("num_experts", C.c_uint32), ("top_k", C.c_uint32),
+                ("balance_coef", C.c_float), ("z_coef", C.c_float)]
+
+
+class pw_balance_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("logits", "experts", "valid", "counts", "prob_mean", "loss", "gates", "dgates",
+                                          "grad_loss", "dlogits")]
+
+
+class pw_moe_grad_desc(C.Structure):
+    _fields_ = [("tokens", C.c_uint64), ("rows", C.c_uint64), ("d", C.c_uint32), ("num_experts", C.c_uint32),
+                ("top_k", C.c_uint32), ("dtype", C.c_uint32)]
+
+
+class pw_combine_grad_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("dout", "y", "gates", "src_index", "offsets", "valid", "dy", "dgates", "slot_of")]
+
+
+class pw_dispatch_grad_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("dxd", "dlogits", "w_router", "x", "slot_of", "valid", "dx", "dw_router")]
+
+
+class pw_norm_desc(C.Structure):
+    _fields_ = [("rows", C.c_uint64), ("d", C.c_uint32), ("dtype", C.c_uint32), ("gates", C.c_uint32),
+                ("x_scale", C.c_float), ("y_scale", C.c_float), ("eps", C.c_float)]
+
+
+class pw_norm_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x", "y", "w_y", "gate", "w_r", "r", "h", "dr", "dh", "valid", "dx", "dy", "dw_y",
+                                          "dgate", "dw_r")]
+
+
 PW_PROG_CHAIN, PW_PROG_EXCHANGE = 0, 1
 
 
@@ -120,6 +153,18 @@ _SIGNATURES = {
     "pw_plan_chain_placement": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t]),
     "pw_plan_kernel_times": (C.c_int, [C.c_void_p, C.POINTER(pw_kernel_time), C.c_int, C.POINTER(C.c_int)]),
     "pw_plan_reset_times": (C.c_int, [C.c_void_p]),
+    "pw_router_balance_workspace": (C.c_int, [C.POINTER(pw_balance_desc), C.POINTER(C.c_size_t)]),
+    "pw_router_balance": (C.c_int, [C.POINTER(pw_balance_desc), C.POINTER(pw_balance_io), C.c_void_p, C.c_size_t,
+                                    C.c_void_p]),
+    "pw_router_grad": (C.c_int, [C.POINTER(pw_balance_desc), C.POINTER(pw_balance_io), C.c_void_p]),
+    "pw_moe_combine_grad": (C.c_int, [C.POINTER(pw_moe_grad_desc), C.POINTER(pw_combine_grad_io), C.c_void_p]),
+    "pw_moe_dispatch_grad_workspace": (C.c_int, [C.POINTER(pw_moe_grad_desc), C.POINTER(C.c_size_t)]),
+    "pw_moe_dispatch_grad": (C.c_int, [C.POINTER(pw_moe_grad_desc), C.POINTER(pw_dispatch_grad_io), C.c_void_p,
+                                       C.c_size_t, C.c_void_p]),
+    "pw_block_norm": (C.c_int, [C.POINTER(pw_norm_desc), C.POINTER(pw_norm_io), C.c_void_p]),
+    "pw_block_norm_grad_workspace": (C.c_int, [C.POINTER(pw_norm_desc), C.POINTER(C.c_size_t)]),
+    "pw_block_norm_grad": (C.c_int, [C.POINTER(pw_norm_desc), C.POINTER(pw_norm_io), C.c_void_p, C.c_size_t,
+                                     C.c_void_p]),
     "pw_sched_create": (C.c_int, [C.c_uint32, C.POINTER(C.c_void_p)]),
     "pw_sched_add_client": (C.c_int, [C.c_void_p, C.c_uint32, C.POINTER(C.c_uint32)]),
     "pw_sched_submit": (C.c_int, [C.c_void_p, C.c_uint32, C.POINTER(pw_program), C.POINTER(C.c_uint64)]),
@@ -480,6 +525,299 @@ class MoE:
         io.dst.num_tuples = rows
         io.b_out = _ptr(self.y)
         return self.plan.exchange_end(io, stream)
+
+
+def _address(t):
+    """A tensor's address; an empty tensor has none, and any that is not NULL
+    stands for it (nothing is read or written there)."""
+    return None if t is None else t.data_ptr() or 256
+
+
+class _Operator:
+    """What the plan-less operators share: the device, the workspace, checked
+    arguments, and output buffers, made by the first call that needs them and
+    kept (so every call returns the same tensors; make one call before
+    capturing a HIP graph). Calls of one object share its buffers: order them."""
+
+    def __init__(self, device):
+        import torch
+        dev = torch.device(device)
+        self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
+        self._index = self.device.index
+        self._buffers = {}
+        self._ws = None
+
+    def _buf(self, name, shape, dtype):
+        import torch
+        b = self._buffers.get(name)
+        if b is None:
+            b = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.device)
+        return b
+
+    def _workspace(self, sizer, d):
+        import torch
+        need = C.c_size_t(0)
+        check(sizer(C.byref(d), C.byref(need)))
+        if need.value and (self._ws is None or self._ws.numel() < need.value):
+            self._ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+
+    def _arg(self, name, t, shape, *dtypes):
+        """The address of a tensor that must be contiguous, on this device, of
+        this shape and of one of these types; None stays None."""
+        if t is None:
+            return None
+        if (t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != self._index):
+            raise PwError(PW_ERR_INVALID, f"{name} must be a contiguous {' or '.join(str(x) for x in dtypes)} tensor of shape "
+                                          f"{shape} on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return _address(t)
+
+    def _run(self, fn, d, io, stream, ws=False):
+        import torch
+        args = (C.c_void_p(self._ws.data_ptr()) if self._ws is not None else None,
+                self._ws.numel() if self._ws is not None else 0) if ws else ()
+        s = C.c_void_p((stream if stream is not None else torch.cuda.current_stream(self._index)).cuda_stream)
+        if torch.cuda.current_device() == self._index:
+            check(fn(C.byref(d), C.byref(io), *args, s))
+        else:
+            with torch.cuda.device(self._index):
+                check(fn(C.byref(d), C.byref(io), *args, s))
+
+
+class RouterBalance(_Operator):
+    """Balance loss of a router with per-expert counts, and the gradient of
+    its logits (pw_router_balance, pw_router_grad). logits [tokens][E] fp32 and
+    experts [tokens][k] int32 as MoE writes them; valid [tokens] bool or uint8
+    leaves padding out (None: every token counts)."""
+
+    def __init__(self, tokens, num_experts, top_k=2, balance_coef=1e-2, z_coef=0.0, device="cuda"):
+        super().__init__(device)
+        self.T, self.E, self.k = tokens, num_experts, top_k
+        self._counts = None  # of the last loss() call
+        self.desc = pw_balance_desc(tokens, num_experts, top_k, balance_coef, z_coef)
+        self._workspace(lib.pw_router_balance_workspace, self.desc)
+
+    def _io(self, logits, experts, valid):
+        import torch
+        io = pw_balance_io()
+        io.logits = self._arg("logits", logits, (self.T, self.E), torch.float32)
+        io.experts = self._arg("experts", experts, (self.T, self.k), torch.int32)
+        io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
+        return io
+
+    def loss(self, logits, experts, valid=None, stream=None):
+        """(counts [E + 1] int32: tuples per expert, then tokens counted;
+        prob_mean [E]; loss [2]: balance, z)."""
+        import torch
+        io = self._io(logits, experts, valid)
+        counts = self._buf("counts", (self.E + 1,), torch.int32)
+        mean = self._buf("prob_mean", (self.E,), torch.float32)
+        loss = self._buf("loss", (2,), torch.float32)
+        io.counts, io.prob_mean, io.loss = _address(counts), _address(mean), _address(loss)
+        self._run(lib.pw_router_balance, self.desc, io, stream, ws=True)
+        self._counts = counts
+        return counts, mean, loss
+
+    def grad(self, logits, experts=None, counts=None, gates=None, dgates=None, valid=None, grad_loss=None, stream=None):
+        """dlogits [tokens][E]: of both losses (grad_loss [2], None: ones; counts
+        None: those of the last loss() call) and of the gates, if given."""
+        import torch
+        io = self._io(logits, experts, valid)
+        if counts is None:
+            counts = self._counts
+        io.counts = self._arg("counts", counts, (self.E + 1,), torch.int32)
+        io.gates = self._arg("gates", gates, (self.T, self.k), torch.float32)
+        io.dgates = self._arg("dgates", dgates, (self.T, self.k), torch.float32)
+        io.grad_loss = self._arg("grad_loss", grad_loss, (2,), torch.float32)
+        out = self._buf("dlogits", (self.T, self.E), torch.float32)
+        io.dlogits = _address(out)
+        self._run(lib.pw_router_grad, self.desc, io, stream)
+        return out
+
+
+class MoEGrad(_Operator):
+    """Gradients of an MoE step's combine (pw_moe_combine_grad), and of its
+    dispatch and router (pw_moe_dispatch_grad). rows: dispatched rows at most
+    (MoE.static_rows). The gradient of the experts' products, from dy to dxd
+    in dispatched order, stands between the two calls and is the caller's."""
+
+    def __init__(self, tokens, d, num_experts, rows=None, device="cuda"):
+        super().__init__(device)
+        self.T, self.d, self.E = tokens, d, num_experts
+        self._slot_of = None  # of the last combine() call
+        self.rows = 2 * tokens if rows is None else rows
+        self.desc = pw_moe_grad_desc(tokens, self.rows, d, num_experts, 2, PW_BF16)
+        self._workspace(lib.pw_moe_dispatch_grad_workspace, self.desc)
+
+    def _rows(self, t):
+        """The descriptor of a call whose dispatched buffers are like t."""
+        n = t.shape[0]
+        if n > self.rows:
+            raise PwError(PW_ERR_INVALID, f"{n} dispatched rows, at most {self.rows}")
+        self.desc.rows = n
+        return n
+
+    def combine(self, dout, y, gates, src_index, offsets, valid=None, dy=None, stream=None):
+        """(dy like y, dgates [tokens][2] fp32, slot_of [tokens][2] int32) from
+        the step's y, gates, src_index and offsets. Rows of dy behind
+        offsets[E] are left as they are; dy=None: a kept buffer."""
+        import torch
+        n = self._rows(y)
+        bf = torch.bfloat16
+        if dy is None:
+            dy = self._buf("dy", (self.rows, self.d), bf)[:n]
+        dgates = self._buf("dgates", (self.T, 2), torch.float32)
+        slot_of = self._buf("slot_of", (self.T, 2), torch.int32)
+        if src_index.dim() == 1 and src_index.shape[0] > n:
+            src_index = src_index[:n]
+        io = pw_combine_grad_io()
+        io.dout = self._arg("dout", dout, (self.T, self.d), bf)
+        io.y = self._arg("y", y, (n, self.d), bf)
+        io.gates = self._arg("gates", gates, (self.T, 2), torch.float32)
+        io.src_index = self._arg("src_index", src_index, (n,), torch.int32)
+        io.offsets = self._arg("offsets", offsets, (self.E + 1,), torch.int64)
+        io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
+        io.dy = self._arg("dy", dy, (n, self.d), bf)
+        io.dgates, io.slot_of = _address(dgates), _address(slot_of)
+        self._run(lib.pw_moe_combine_grad, self.desc, io, stream)
+        self._slot_of = slot_of
+        return dy, dgates, slot_of
+
+    def dispatch(self, dxd, dlogits, w_router, x=None, slot_of=None, valid=None, stream=None):
+        """(dx [tokens][d] bf16, dw_router [d][E] fp32); slot_of None: that of
+        the last combine() call; x None: dx alone (dw_router None)."""
+        import torch
+        n = self._rows(dxd)
+        bf = torch.bfloat16
+        if slot_of is None:
+            slot_of = self._slot_of
+        dx = self._buf("dx", (self.T, self.d), bf)
+        dw = self._buf("dw_router", (self.d, self.E), torch.float32) if x is not None else None
+        io = pw_dispatch_grad_io()
+        io.dxd = self._arg("dxd", dxd, (n, self.d), bf)
+        io.dlogits = self._arg("dlogits", dlogits, (self.T, self.E), torch.float32)
+        io.w_router = self._arg("w_router", w_router, (self.d, self.E), bf)
+        io.x = self._arg("x", x, (self.T, self.d), bf)
+        io.slot_of = self._arg("slot_of", slot_of, (self.T, 2), torch.int32)
+        io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
+        io.dx = _address(dx)
+        io.dw_router = _address(dw)
+        self._run(lib.pw_moe_dispatch_grad, self.desc, io, stream, ws=True)
+        return dx, dw
+
+
+class BlockNorm(_Operator):
+    """Norms around a block with its gate and residual scale (pw_block_norm,
+    pw_block_norm_grad): r = x_scale x + y_scale gate * norm(y; w_y) closes a
+    block, h = norm(r; w_r) opens the next. Tensors given as None drop their
+    part out. Rows, weights and gates are of one dtype; gates is the number of
+    gate rows, each for rows / gates consecutive rows (0: no gate)."""
+
+    def __init__(self, rows, d, dtype=PW_BF16, gates=0, x_scale=1.0, y_scale=1.0, eps=1e-6, device="cuda"):
+        import torch
+        super().__init__(device)
+        self.T, self.d, self.G = rows, d, gates
+        self.dtype = torch.float32 if dtype == PW_F32 else torch.bfloat16
+        self.desc = pw_norm_desc(rows, d, dtype, gates, x_scale, y_scale, eps)
+        self._workspace(lib.pw_block_norm_grad_workspace, self.desc)
+
+    def _io(self, y, w_y, gate, w_r):
+        io = pw_norm_io()
+        io.y = self._arg("y", y, (self.T, self.d), self.dtype)
+        io.w_y = self._arg("w_y", w_y, (self.d,), self.dtype)
+        io.gate = self._arg("gate", gate, (self.G, self.d), self.dtype)
+        io.w_r = self._arg("w_r", w_r, (self.d,), self.dtype)
+        return io
+
+    def forward(self, x, y=None, w_y=None, gate=None, w_r=None, r=None, stream=None):
+        """(r, h): r is None where y is (the stream is x itself), h where w_r
+        is. r may be given (x itself, to update it in place)."""
+        io = self._io(y, w_y, gate, w_r)
+        io.x = self._arg("x", x, (self.T, self.d), self.dtype)
+        if y is None and r is not None:
+            raise PwError(PW_ERR_INVALID, "r is written with y only")
+        if y is not None and r is None:
+            r = self._buf("r", (self.T, self.d), self.dtype)
+        h = self._buf("h", (self.T, self.d), self.dtype) if w_r is not None else None
+        io.r = self._arg("r", r, (self.T, self.d), self.dtype)
+        io.h = _address(h)
+        self._run(lib.pw_block_norm, self.desc, io, stream)
+        return r, h
+
+    def grad(self, dr=None, dh=None, r=None, y=None, w_y=None, gate=None, w_r=None, valid=None, dx=None, stream=None):
+        """(dx, dy, dw_y [d] fp32, dgate [gates][d] fp32, dw_r [d] fp32), None
+        where their part is; r: forward's r (with y None: x_scale x). valid
+        [rows] bool or uint8: other rows get zeros and add nothing to the
+        weights' gradients. dx may be given (dr itself, to update it in place)."""
+        import torch
+        rows, f32 = (self.T, self.d), torch.float32
+        io = self._io(y, w_y, gate, w_r)
+        io.r = self._arg("r", r, rows, self.dtype)
+        io.dr = self._arg("dr", dr, rows, self.dtype)
+        io.dh = self._arg("dh", dh, rows, self.dtype)
+        io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
+        if dx is None:
+            dx = self._buf("dx", rows, self.dtype)
+        io.dx = self._arg("dx", dx, rows, self.dtype)
+        dy = self._buf("dy", rows, self.dtype) if y is not None else None
+        dw_y = self._buf("dw_y", (self.d,), f32) if w_y is not None else None
+        dgate = self._buf("dgate", (self.G, self.d), f32) if gate is not None else None
+        dw_r = self._buf("dw_r", (self.d,), f32) if w_r is not None else None
+        io.dy, io.dw_y, io.dgate, io.dw_r = _address(dy), _address(dw_y), _address(dgate), _address(dw_r)
+        self._run(lib.pw_block_norm_grad, self.desc, io, stream, ws=True)
+        return dx, dy, dw_y, dgate, dw_r
+
+
+class MoEBlock:
+    """An MoE step inside a model's block, with its backward pass:
+
+        h = norm(x; w_in);  r = x_scale x + y_scale gate * norm(moe(h); w_out)
+
+    plus the router's balance loss. moe: an MoE with want_logits. w_out and
+    gate may be None. The experts' weights are packed when the MoE is built,
+    and the gradient of their products is the caller's, between grad_begin
+    and grad_end."""
+
+    def __init__(self, moe, w_in, w_out=None, gate=None, x_scale=1.0, y_scale=1.0, eps=1e-6, balance_coef=1e-2,
+                 z_coef=0.0):
+        if moe.logits is None:
+            raise PwError(PW_ERR_INVALID, "the balance loss needs an MoE with want_logits")
+        self.moe = moe
+        self.w_in, self.w_out, self.gate = w_in, w_out, gate
+        device = moe.out.device
+        gates = 0 if gate is None else gate.shape[0]
+        self.norm_in = BlockNorm(moe.T, moe.d, PW_BF16, eps=eps, device=device)
+        self.norm_out = BlockNorm(moe.T, moe.d, PW_BF16, gates, x_scale, y_scale, eps, device)
+        self.balance = RouterBalance(moe.T, moe.E, 2, balance_coef, z_coef, device)
+        self.grads = MoEGrad(moe.T, moe.d, moe.E, moe.static_rows, device)
+
+    def forward(self, x, valid=None, stream=None):
+        """(r, loss [2], counts [E + 1], future of the MoE step); x is kept for the
+        backward pass."""
+        m = self.moe
+        self.x, self.valid = x, valid
+        _, self.h = self.norm_in.forward(x, w_r=self.w_in, stream=stream)
+        f = m.step(self.h, stream)
+        counts, _, loss = self.balance.loss(m.logits, m.experts, valid, stream)
+        r, _ = self.norm_out.forward(x, y=m.out, w_y=self.w_out, gate=self.gate, stream=stream)
+        return r, loss, counts, f
+
+    def grad_begin(self, dr, stream=None):
+        """dy [rows][d], the gradient of the expert outputs moe.y, from dr, that of r."""
+        m = self.moe
+        self._dx, dout, self._dw_out, self._dgate, _ = self.norm_out.grad(dr, y=m.out, w_y=self.w_out, gate=self.gate,
+                                                                          valid=self.valid, stream=stream)
+        dy, self._dgates, _ = self.grads.combine(dout, m.y, m.gates, m.src_index, m.offsets, self.valid, stream=stream)
+        return dy
+
+    def grad_end(self, dxd, grad_loss=None, stream=None):
+        """{"x", "w_in", "w_out", "gate", "w_router"} gradients from dxd, that of the
+        dispatched rows moe.xd, and grad_loss [2], that of the losses (None: ones)."""
+        m = self.moe
+        dl = self.balance.grad(m.logits, m.experts, gates=m.gates, dgates=self._dgates, valid=self.valid,
+                               grad_loss=grad_loss, stream=stream)
+        dh, dw_router = self.grads.dispatch(dxd, dl, m.w[0], self.h, valid=self.valid, stream=stream)
+        dx, _, _, _, dw_in = self.norm_in.grad(self._dx, dh, self.x, w_r=self.w_in, valid=self.valid, stream=stream)
+        return {"x": dx, "w_in": dw_in, "w_out": self._dw_out, "gate": self._dgate, "w_router": dw_router}
 
 
 class Sched:

@@ -1,0 +1,521 @@
+// Gradients of a mixture-of-experts step's combine, dispatch and router.
+//
+// The step (moe.hip): row slot(t, s) of the dispatched rows holds token t for
+// its s-th expert (s = 0, 1; slot -1: dropped by the capacity);
+//   out_t = sum_s g_ts y[slot(t, s)],   xd[slot(t, s)] = x_t,   l_t = x_t W
+// Its gradients, with the experts' own products in between left to the
+// caller (from dy to dxd):
+//   dy[slot(t, s)] = g_ts dout_t        dg_ts = dout_t . y[slot(t, s)]
+//   dx_t = sum_s dxd[slot(t, s)] + dl_t W^T      dW = x^T dl
+#include "ops.h"
+
+#include <algorithm>
+
+namespace pw {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+
+struct CombineGradArgs {
+  const __bf16* dout;
+  const __bf16* y;
+  const float* gates;
+  const int32_t* src_index;
+  const int64_t* offsets;
+  const uint8_t* valid;
+  __bf16* dy;
+  float* dgates;
+  int32_t* slot_of;
+  uint64_t rows;
+  uint32_t tokens, d, E;
+};
+
+struct DispatchGradArgs {
+  const __bf16* dxd;
+  const float* dlogits;
+  const __bf16* w;
+  const __bf16* x;
+  const int32_t* slot_of;
+  const uint8_t* valid;
+  __bf16* dx;
+  float* dw;
+  float* part;         // [splits][d][Ep] partial sums of dw
+  uint64_t rows;
+  uint32_t tokens, d, E;
+  uint32_t splits;     // token ranges of dw
+  uint32_t split_tokens;
+};
+
+// ---- slot_of: the inverse of src_index ---------------------------------------
+
+constexpr uint32_t kSlotsAlone = 8192;  // tuples up to which one workgroup inverts the index
+
+__device__ __forceinline__ void put_slot(const CombineGradArgs& a, uint64_t i) {
+  const uint32_t g = (uint32_t)a.src_index[i];
+  if (g < 2 * a.tokens) a.slot_of[g] = (int32_t)i;
+}
+__device__ __forceinline__ uint64_t kept_rows(const CombineGradArgs& a) {
+  const int64_t n = a.offsets[a.E];
+  return n < 0 ? 0 : min((uint64_t)n, a.rows);
+}
+
+__global__ __launch_bounds__(1024) void k_slots_alone(CombineGradArgs a) {
+  for (uint32_t i = threadIdx.x; i < 2 * a.tokens; i += 1024) a.slot_of[i] = -1;
+  __syncthreads();  // the stores above have completed before any below
+  const uint64_t n = kept_rows(a);
+  for (uint64_t i = threadIdx.x; i < n; i += 1024) put_slot(a, i);
+}
+__global__ __launch_bounds__(256) void k_slots_clear(CombineGradArgs a) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i < 2 * a.tokens) a.slot_of[i] = -1;
+}
+__global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
+  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < kept_rows(a)) put_slot(a, i);
+}
+
+// ---- gradient of the combine ---------------------------------------------------
+// One wave handles kTokens tokens per pass, as the combine does: their slots
+// and gates in one round of loads, then every chunk of dout and of both y rows
+// in flight before any is used (a dropped tuple reads row 0 and is masked).
+constexpr uint32_t kCombineBlocks = 2048;
+constexpr int kTokens = 2;
+
+__global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t nch = a.d / 8;  // 16-byte chunks of a row
+  const u32x4* y = reinterpret_cast<const u32x4*>(a.y);
+  const u32x4* dout = reinterpret_cast<const u32x4*>(a.dout);
+  u32x4* dy = reinterpret_cast<u32x4*>(a.dy);
+  const uint32_t stride = gridDim.x * 4 * kTokens;
+  for (uint32_t t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += stride) {
+    int slot[kTokens][2];
+    float gate[kTokens][2], dot[kTokens][2] = {};
+    bool ok[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      const uint32_t t = min(t0 + k, a.tokens - 1);
+      const int2 s = *reinterpret_cast<const int2*>(a.slot_of + (uint64_t)t * 2);
+      const float2 g = *reinterpret_cast<const float2*>(a.gates + (uint64_t)t * 2);
+      const int s0 = __builtin_amdgcn_readfirstlane(s.x), s1 = __builtin_amdgcn_readfirstlane(s.y);
+      const bool here = t0 + k < a.tokens;
+      ok[k] = !a.valid || a.valid[t];
+      slot[k][0] = here ? s0 : -1;
+      slot[k][1] = here ? s1 : -1;
+      gate[k][0] = g.x;
+      gate[k][1] = g.y;
+    }
+    for (uint32_t c0 = 0; c0 < nch; c0 += 128) {
+      u32x4 vo[kTokens][2], vy[kTokens][2][2];  // [token][chunk], [token][tuple][chunk]
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t ch = min(c0 + lane + 64 * c, nch - 1);
+          vo[k][c] = __builtin_nontemporal_load(dout + (uint64_t)min(t0 + k, a.tokens - 1) * nch + ch);
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (a.rows) vy[k][s][c] = __builtin_nontemporal_load(y + (uint64_t)max(slot[k][s], 0) * nch + ch);
+        }
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t ch = c0 + lane + 64 * c;
+          const bool in = ch < nch;
+          const bf16x8 o = __builtin_bit_cast(bf16x8, vo[k][c]);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (slot[k][s] < 0) continue;  // wave-uniform
+            const bf16x8 v = __builtin_bit_cast(bf16x8, vy[k][s][c]);
+            bf16x8 r;
+            float p = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              p = fmaf((float)o[j], (float)v[j], p);
+              r[j] = ok[k] ? (__bf16)(gate[k][s] * (float)o[j]) : (__bf16)0.f;
+            }
+            if (in) {
+              dot[k][s] += p;
+              __builtin_nontemporal_store(__builtin_bit_cast(u32x4, r), dy + (uint64_t)slot[k][s] * nch + ch);
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k) {
+        dot[k][0] += __shfl_xor(dot[k][0], m);
+        dot[k][1] += __shfl_xor(dot[k][1], m);
+      }
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k)
+      if (lane == 0 && t0 + k < a.tokens) {
+        const float2 r = {ok[k] && slot[k][0] >= 0 ? dot[k][0] : 0.f, ok[k] && slot[k][1] >= 0 ? dot[k][1] : 0.f};
+        *reinterpret_cast<float2*>(a.dgates + (uint64_t)(t0 + k) * 2) = r;
+      }
+  }
+}
+
+// ---- gradient of dispatch and router, to the tokens ------------------------------
+// dx^T tile = W dl^T by v_mfma_f32_32x32x16_bf16, W's rows (columns of dx) as
+// the first operand and the tokens as the second: a lane holds one token. The
+// first operand's rows are dealt so that a lane's two accumulators hold 32
+// consecutive columns: row i of block b is column 32 h + 16 b + r, where
+// h = (i >> 2) & 1 is the half of the wave that receives it and
+// r = 4 (i >> 3) + (i & 3) the register. dl is split into two bf16 terms
+// (hi + lo, at most 2^-16 of the value is lost, below the rounding of dx to bf16 at
+// 2^-8), so the products are as exact as dx can show.
+constexpr int kDxTokens = 32;  // tokens of a wave
+
+__device__ __forceinline__ void split2(float v, __bf16& hi, __bf16& lo) {
+  hi = (__bf16)v;
+  lo = (__bf16)(v - (float)hi);
+}
+
+// W[c][e0 .. e0 + 7], zero where there is no expert.
+template <bool kWhole>
+__device__ __forceinline__ bf16x8 load_w(const DispatchGradArgs& a, uint32_t c, uint32_t e0) {
+  bf16x8 v = {};
+  if (kWhole) {
+    if (e0 < a.E) v = *reinterpret_cast<const bf16x8*>(a.w + (uint64_t)c * a.E + e0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e0 + j < a.E) v[j] = a.w[(uint64_t)c * a.E + e0 + j];
+  }
+  return v;
+}
+
+template <bool kWhole>  // whole chunks of 8 experts, 16-byte aligned
+__global__ __launch_bounds__(256) void k_dispatch_grad(DispatchGradArgs a) {
+  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
+  const uint32_t t0 = (blockIdx.x * 4 + w) * kDxTokens;
+  if (t0 >= a.tokens) return;
+  const bool live = t0 + i < a.tokens;
+  const uint32_t t = live ? t0 + i : a.tokens - 1;
+  const bool ok = !a.valid || a.valid[t];
+  // the token's logit gradients: experts 16 s + 8 h .. + 7 of step s
+  bf16x8 hi[4], lo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t e = 16 * s + 8 * h + j;
+      const float v = e < a.E ? a.dlogits[(uint64_t)t * a.E + e] : 0.f;
+      __bf16 p, q;
+      split2(v, p, q);
+      hi[s][j] = p;
+      lo[s][j] = q;
+    }
+  const int2 sl = *reinterpret_cast<const int2*>(a.slot_of + (uint64_t)t * 2);
+  const bool have[2] = {sl.x >= 0 && (uint64_t)sl.x < a.rows, sl.y >= 0 && (uint64_t)sl.y < a.rows};
+  const __bf16* row[2] = {a.dxd + (have[0] ? (uint64_t)sl.x : 0) * a.d + 32 * h,
+                          a.dxd + (have[1] ? (uint64_t)sl.y : 0) * a.d + 32 * h};
+  const uint32_t col = 32 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
+  for (uint32_t c0 = 0; c0 < a.d; c0 += 64) {
+    bf16x8 g[2][4];
+    if (a.rows) {  // uniform
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[s][q] = *reinterpret_cast<const bf16x8*>(row[s] + c0 + 8 * q);
+    }
+    f32x16 acc[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bf16x8 wv = load_w<kWhole>(a, c0 + col + 16 * b, 16 * s + 8 * h);
+        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, hi[s], acc[b], 0, 0, 0);
+        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, lo[s], acc[b], 0, 0, 0);
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float f = acc[q >> 1][(q & 1) * 8 + j];
+        if (have[0]) f += (float)g[0][q][j];
+        if (have[1]) f += (float)g[1][q][j];
+        o[j] = ok ? (__bf16)f : (__bf16)0.f;
+      }
+      if (live) *reinterpret_cast<bf16x8*>(a.dx + (uint64_t)t * a.d + c0 + 32 * h + 8 * q) = o;
+    }
+  }
+}
+
+// ---- gradient of the router's weights --------------------------------------------
+// dW = x^T dl over a range of tokens, by v_mfma_f32_32x32x16_bf16 with the
+// tokens as the inner index. A lane needs 8 tokens of one column: it loads 4
+// columns (8 bytes) of each of its 8 tokens and pairs the tokens with byte
+// permutes, so operand q holds columns 4 i + q. dl is split into three bf16
+// terms, which hold all 24 bits of it: every product is exact and the sums
+// are fp32. A workgroup covers 256 columns (2 waves of 128) with 4 waves of
+// tokens each, joined through LDS in a fixed order.
+constexpr uint32_t kDwThreads = 512;
+constexpr uint32_t kDwCols = 256;
+
+template <int NC>  // expert blocks of 32
+__global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
+  extern __shared__ float lds[];  // [kDwCols][32 NC]
+  constexpr uint32_t Ep = 32 * NC;
+  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
+  const uint32_t groups = a.d / kDwCols;
+  // the column groups of one token range run on one XCD (workgroup b runs on
+  // XCD b mod 8) and share its L2 for dl
+  const uint32_t k = blockIdx.x / 8, cg = k % groups, split = (k / groups) * 8 + blockIdx.x % 8;
+  if (split >= a.splits) return;  // whole workgroups
+  const uint32_t cw = w & 1, tw = w >> 1;
+  const uint32_t first = split * a.split_tokens, last = min(first + a.split_tokens, a.tokens);
+  const __bf16* x = a.x + cg * kDwCols + cw * 128 + 4 * i;
+  f32x16 acc[4][NC];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[q][c] = f32x16{};
+  for (uint32_t t0 = first + 16 * tw; t0 < last; t0 += 64) {
+    u32x2 v[8];
+    float dl[NC][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t tt = t0 + 8 * h + j, t = min(tt, last - 1);
+      v[j] = *reinterpret_cast<const u32x2*>(x + (uint64_t)t * a.d);
+      if (a.valid && !a.valid[t]) v[j] = u32x2{0, 0};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint32_t e = 32 * c + i;
+        const float f = a.dlogits[(uint64_t)t * a.E + min(e, a.E - 1)];
+        dl[c][j] = tt < last && e < a.E ? f : 0.f;
+      }
+    }
+    bf16x8 xa[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      u32x4 p;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // halves q & 1 of tokens 2 j and 2 j + 1
+        p[j] = __builtin_amdgcn_perm(v[2 * j + 1][q >> 1], v[2 * j][q >> 1], q & 1 ? 0x07060302u : 0x05040100u);
+      xa[q] = __builtin_bit_cast(bf16x8, p);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      bf16x8 d0, d1, d2;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __bf16 b0 = (__bf16)dl[c][j];
+        const float r1 = dl[c][j] - (float)b0;
+        const __bf16 b1 = (__bf16)r1;
+        d0[j] = b0;
+        d1[j] = b1;
+        d2[j] = (__bf16)(r1 - (float)b1);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d0, acc[q][c], 0, 0, 0);
+        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d1, acc[q][c], 0, 0, 0);
+        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d2, acc[q][c], 0, 0, 0);
+      }
+    }
+  }
+  for (uint32_t turn = 0; turn < 4; ++turn) {
+    if (tw == turn)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const uint32_t row = (r >> 2) * 8 + h * 4 + (r & 3);
+            float* p = lds + (cw * 128 + 4 * row + q) * Ep + 32 * c + i;
+            *p = turn ? *p + acc[q][c][r] : acc[q][c][r];
+          }
+    __syncthreads();
+  }
+  const uint32_t c0 = cg * kDwCols;
+  if (a.splits == 1) {
+    for (uint32_t o = threadIdx.x; o < kDwCols * Ep; o += kDwThreads)
+      if (o % Ep < a.E) a.dw[(uint64_t)(c0 + o / Ep) * a.E + o % Ep] = lds[o];
+  } else {
+    float* part = a.part + ((uint64_t)split * a.d + c0) * Ep;
+    for (uint32_t o = threadIdx.x; o < kDwCols * Ep; o += kDwThreads) part[o] = lds[o];
+  }
+}
+
+// Adds the partial sums of the token ranges, in order.
+template <int NC>
+__global__ __launch_bounds__(256) void k_router_dw_join(DispatchGradArgs a) {
+  constexpr uint32_t Ep = 32 * NC;
+  const uint32_t o = blockIdx.x * 256 + threadIdx.x;  // d is a multiple of 256: no rest
+  const uint64_t n = (uint64_t)a.d * Ep;
+  float s = 0.f;
+#pragma unroll 8
+  for (uint32_t i = 0; i < a.splits; ++i) s += a.part[i * n + o];
+  if (o % Ep < a.E) a.dw[(uint64_t)(o / Ep) * a.E + o % Ep] = s;
+}
+
+// Zeroes dw (a call without tokens).
+__global__ __launch_bounds__(256) void k_router_dw_zero(DispatchGradArgs a) {
+  const uint32_t o = blockIdx.x * 256 + threadIdx.x;
+  if (o < a.d * a.E) a.dw[o] = 0.f;
+}
+
+struct DwLayout {
+  uint32_t splits = 1, split_tokens = 64;
+  size_t total = 0;
+};
+
+constexpr uint32_t kDwGrid = 256;  // workgroups wanted: one per CU
+
+DwLayout dw_layout(const pw_moe_grad_desc& d) {
+  DwLayout l;
+  const uint32_t groups = d.d / kDwCols;
+  const uint64_t want = std::max<uint64_t>(1, kDwGrid / groups);
+  const uint64_t per = (d.tokens + want - 1) / want;
+  l.split_tokens = (uint32_t)std::max<uint64_t>(64, (per + 63) / 64 * 64);
+  l.splits = (uint32_t)std::max<uint64_t>(1, (d.tokens + l.split_tokens - 1) / l.split_tokens);
+  if (l.splits > 1) l.total = up256((size_t)l.splits * d.d * (d.num_experts > 32 ? 64 : 32) * 4);
+  return l;
+}
+
+int validate(const pw_moe_grad_desc* d) {
+  if (!d) return fail(PW_ERR_INVALID, "descriptor is NULL");
+  if (d->tokens > (1ull << 28)) return fail(PW_ERR_INVALID, "tokens must be at most 2^28");
+  if (d->rows > 2 * d->tokens) return fail(PW_ERR_INVALID, "rows must be at most 2 tokens");
+  if (d->d == 0 || d->d % 256 || d->d > 1280) return fail(PW_ERR_INVALID, "d must be a positive multiple of 256, <= 1280");
+  if (d->num_experts < 2 || d->num_experts > 64) return fail(PW_ERR_INVALID, "num_experts must be in [2, 64]");
+  if (d->top_k != 2) return fail(PW_ERR_UNSUPPORTED, "only top-2 routing is built");
+  if (d->dtype != PW_BF16) return fail(PW_ERR_INVALID, "rows and weights are bf16");
+  return PW_OK;
+}
+
+}  // namespace
+
+}  // namespace pw
+
+using namespace pw;
+
+extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_grad_io* io, void* stream) {
+  clear_error();
+  int st = validate(d);
+  if (st) return st;
+  if (!io) return fail(PW_ERR_INVALID, "io is NULL");
+  if (d->tokens == 0) return PW_OK;
+  if (!io->dout || !io->gates || !io->offsets || !io->dgates || !io->slot_of)
+    return fail(PW_ERR_INVALID, "dout, gates, offsets, dgates and slot_of are required");
+  if (d->rows && (!io->y || !io->src_index || !io->dy)) return fail(PW_ERR_INVALID, "y, src_index and dy are required");
+  if (((uintptr_t)io->dout | (uintptr_t)io->y | (uintptr_t)io->dy) % 16)
+    return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
+  if (((uintptr_t)io->gates | (uintptr_t)io->dgates | (uintptr_t)io->slot_of) % 8)
+    return fail(PW_ERR_INVALID, "gates, dgates and slot_of must be 8-byte aligned");
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = check_stream(s))) return st;
+  CombineGradArgs a{};
+  a.dout = static_cast<const __bf16*>(io->dout);
+  a.y = static_cast<const __bf16*>(io->y);
+  a.gates = io->gates;
+  a.src_index = io->src_index;
+  a.offsets = io->offsets;
+  a.valid = io->valid;
+  a.dy = static_cast<__bf16*>(io->dy);
+  a.dgates = io->dgates;
+  a.slot_of = io->slot_of;
+  a.rows = d->rows;
+  a.tokens = (uint32_t)d->tokens;
+  a.d = d->d;
+  a.E = d->num_experts;
+  hipError_t e;
+  if (2 * a.tokens <= kSlotsAlone) {
+    hipLaunchKernelGGL(k_slots_alone, dim3(1), dim3(1024), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots");
+  } else {
+    hipLaunchKernelGGL(k_slots_clear, dim3((2 * a.tokens + 255) / 256), dim3(256), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_clear");
+    if (a.rows) {
+      hipLaunchKernelGGL(k_slots_put, dim3((uint32_t)((a.rows + 255) / 256)), dim3(256), 0, s, a);
+      if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_put");
+    }
+  }
+  const uint32_t per = 4 * kTokens;
+  hipLaunchKernelGGL(k_combine_grad, dim3(std::min((a.tokens + per - 1) / per, kCombineBlocks)), dim3(256), 0, s, a);
+  e = hipGetLastError();
+  return e == hipSuccess ? PW_OK : hip_fail(e, "launch combine_grad");
+}
+
+extern "C" int pw_moe_dispatch_grad_workspace(const pw_moe_grad_desc* d, size_t* bytes) {
+  clear_error();
+  int st = validate(d);
+  if (st) return st;
+  if (!bytes) return fail(PW_ERR_INVALID, "bytes is NULL");
+  *bytes = dw_layout(*d).total;
+  return PW_OK;
+}
+
+extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch_grad_io* io, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  clear_error();
+  int st = validate(d);
+  if (st) return st;
+  if (!io) return fail(PW_ERR_INVALID, "io is NULL");
+  if (d->tokens && (!io->dlogits || !io->w_router || !io->slot_of || !io->dx))
+    return fail(PW_ERR_INVALID, "dlogits, w_router, slot_of and dx are required");
+  if (d->rows && !io->dxd) return fail(PW_ERR_INVALID, "dxd is required");
+  if (d->tokens && io->dw_router && !io->x) return fail(PW_ERR_INVALID, "dw_router needs x");
+  if (((uintptr_t)io->dxd | (uintptr_t)io->x | (uintptr_t)io->dx) % 16)
+    return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
+  if ((uintptr_t)io->slot_of % 8) return fail(PW_ERR_INVALID, "slot_of must be 8-byte aligned");
+  const DwLayout l = dw_layout(*d);
+  if (io->dw_router && (st = check_workspace(ws, ws_bytes, l.total))) return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if ((st = check_stream(s))) return st;
+  DispatchGradArgs a{};
+  a.dxd = static_cast<const __bf16*>(io->dxd);
+  a.dlogits = io->dlogits;
+  a.w = static_cast<const __bf16*>(io->w_router);
+  a.x = static_cast<const __bf16*>(io->x);
+  a.slot_of = io->slot_of;
+  a.valid = io->valid;
+  a.dx = static_cast<__bf16*>(io->dx);
+  a.dw = io->dw_router;
+  a.part = static_cast<float*>(ws);
+  a.rows = d->rows;
+  a.tokens = (uint32_t)d->tokens;
+  a.d = d->d;
+  a.E = d->num_experts;
+  a.splits = l.splits;
+  a.split_tokens = l.split_tokens;
+  hipError_t e;
+  if (a.tokens == 0) {
+    if (!a.dw) return PW_OK;
+    hipLaunchKernelGGL(k_router_dw_zero, dim3((a.d * a.E + 255) / 256), dim3(256), 0, s, a);
+    e = hipGetLastError();
+    return e == hipSuccess ? PW_OK : hip_fail(e, "launch router_dw_zero");
+  }
+  const bool whole = a.E % 8 == 0 && (uintptr_t)a.w % 16 == 0;
+  const uint32_t blocks = (a.tokens + 4 * kDxTokens - 1) / (4 * kDxTokens);
+  if (whole) hipLaunchKernelGGL(k_dispatch_grad<true>, dim3(blocks), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(k_dispatch_grad<false>, dim3(blocks), dim3(256), 0, s, a);
+  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch dispatch_grad");
+  if (!a.dw) return PW_OK;
+  const bool two = a.E > 32;
+  const uint32_t grid = 8 * (a.d / kDwCols) * ((a.splits + 7) / 8);
+  const size_t lds = (size_t)kDwCols * (two ? 64 : 32) * 4;
+  const void* fn = two ? (const void*)k_router_dw<2> : (const void*)k_router_dw<1>;
+  if ((e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)
+    return hip_fail(e, "router_dw: dynamic LDS");
+  if (two) hipLaunchKernelGGL(k_router_dw<2>, dim3(grid), dim3(kDwThreads), lds, s, a);
+  else hipLaunchKernelGGL(k_router_dw<1>, dim3(grid), dim3(kDwThreads), lds, s, a);
+  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw");
+  if (a.splits > 1) {
+    const uint32_t jb = a.d * (two ? 64 : 32) / 256;
+    if (two) hipLaunchKernelGGL(k_router_dw_join<2>, dim3(jb), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(k_router_dw_join<1>, dim3(jb), dim3(256), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw_join");
+  }
+  return PW_OK;
+}

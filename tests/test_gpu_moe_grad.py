@@ -1,0 +1,267 @@
+"""GPU parity of the gradients of an MoE step's combine, dispatch and router
+against the oracle in 64 bits, and a run of the whole block.
+
+Bars, u = 2^-24, bf16's half step 2^-8: dy is one fp32 product rounded once; a
+gate's gradient is an fp32 sum of d <= 1280 products, 24 in a lane and 6
+exchanges (64 u of its terms); dx adds a product whose dlogits keep 2^-16 of
+their value (two bf16 terms) and sum in fp32, and two rows; dw_router's
+products are exact and its sums fp32, at most 16 x 3 in an instruction chain of
+5000 / 64 steps, 4 waves and 64 partial sums: a relative error below 512 u of
+the terms' sum, since the chain is cut into token ranges of at most 512 here.
+"""
+import numpy as np
+import pytest
+import torch
+
+import pw_inputs
+from oracle import block as ob
+from oracle import moe as om
+
+pytestmark = pytest.mark.gpu
+U, HALF = 2.0 ** -24, 2.0 ** -8
+bf = torch.bfloat16
+
+CASES = [(1, 256, 2, 0), (1, 256, 64, 1), (7, 512, 5, 0), (33, 256, 33, 1), (300, 1280, 8, 0), (300, 512, 64, 6),
+         (1000, 256, 5, 350), (1003, 768, 12, 0), (4097, 1024, 64, 100), (5000, 256, 64, 0)]
+
+
+def make(T, d, E, cap, seed=0, masked=False):
+    rng = np.random.default_rng([T, d, E, cap, seed])
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    _, g, _, _, offsets, src = om.route(logits, E, 1, cap)
+    kept = src.size
+    rows = min(2 * T, E * cap) if cap else 2 * T
+    index = np.full(rows, -5, np.int32)
+    index[:kept] = src
+
+    def t(*shape, scale=1.0):
+        return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(bf)
+
+    s = dict(dout=t(T, d), y=t(rows, d), gates=torch.from_numpy(g.astype(np.float32)), src_index=torch.from_numpy(index),
+             offsets=torch.from_numpy(offsets.astype(np.int64)), dxd=t(rows, d), w_router=t(d, E, scale=d ** -0.5), x=t(T, d),
+             dlogits=torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)))
+    s["y"][kept:] = float("nan")                  # rows that hold nothing are not looked at
+    s["dxd"][kept:] = float("nan")
+    s["valid"] = torch.from_numpy(rng.random(T) < 0.7) if masked else None
+    return s, kept
+
+
+def f64(t):
+    return None if t is None else t.double().numpy()
+
+
+def check_combine(got, s, kept, before):
+    dy, dg, slot_of = (t.cpu() for t in got)
+    src = s["src_index"].numpy()
+    T = s["dout"].shape[0]
+    valid = None if s["valid"] is None else s["valid"].numpy()
+    want, dgw, size = ob.combine_grad(f64(s["dout"]), f64(s["y"]), f64(s["gates"]), src, kept, valid)
+    assert np.array_equal(slot_of.numpy(), ob.slots(src, kept, T))
+    assert np.all(np.abs(f64(dy[:kept]) - want) <= (HALF + 2 * U) * np.abs(want) + 1e-38)
+    assert torch.equal(dy[kept:], before[kept:])  # left as they were
+    assert np.all(np.abs(f64(dg) - dgw) <= 64 * U * size)
+
+
+def check_dispatch(got, s, kept):
+    slot_of = ob.slots(s["src_index"].numpy(), kept, s["x"].shape[0])
+    valid = None if s["valid"] is None else s["valid"].numpy()
+    dx, size, rows, dw, dws = ob.dispatch_grad(f64(s["dxd"]), f64(s["dlogits"]), f64(s["w_router"]), f64(s["x"]), slot_of, valid)
+    bound = (2.0 ** -16 + 200 * U) * size + 4 * U * rows
+    assert np.all(np.abs(f64(got[0].cpu()) - dx) <= bound + HALF * (np.abs(dx) + bound) + 1e-38)
+    if got[1] is not None:
+        assert np.all(np.abs(f64(got[1].cpu()) - dw) <= 512 * U * dws + 1e-38)
+
+
+def run(pw, s, f=None, stream=None):
+    c = {n: None if t is None else t.cuda() for n, t in s.items()}
+    T, d = s["x"].shape
+    f = f or pw.MoEGrad(T, d, s["w_router"].shape[1], rows=s["y"].shape[0])
+    dy = torch.full_like(c["y"], 3.0)
+    before = dy.cpu()
+    a = f.combine(c["dout"], c["y"], c["gates"], c["src_index"], c["offsets"], c["valid"], dy=dy, stream=stream)
+    b = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], c["x"], valid=c["valid"], stream=stream)
+    return a, b, before, c, f
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,d,E,cap", CASES)
+def test_combine_and_dispatch_gradients(gpu, T, d, E, cap, masked):
+    print(f"moe grad T={T} d={d} E={E} cap={cap} masked={masked}", flush=True)
+    s, kept = make(T, d, E, cap, masked=masked)
+    if masked:   # padding holds anything
+        bad = ~s["valid"]
+        s2 = {n: None if t is None else t.clone() for n, t in s.items()}
+        for n in ("dout", "x"):
+            s2[n][bad] = float("nan")
+        s2["gates"][bad] = float("inf")
+        s2["dlogits"][bad] = 0.0
+        s["dlogits"][bad] = 0.0
+        a, b, before, c, f = run(gpu, s2)
+    else:
+        a, b, before, c, f = run(gpu, s)
+    check_combine(a, s, kept, before)
+    check_dispatch(b, s, kept)
+    first = [t.clone() for t in b]
+    again = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], c["x"], valid=c["valid"])
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])   # equal inputs, equal bits
+    dx, none = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], valid=c["valid"])
+    assert none is None and torch.equal(dx, first[0])
+
+
+def test_everything_dropped_and_no_rows(gpu):
+    """No row kept (offsets all zero), and buffers without rows."""
+    for rows in (20, 0):
+        s, _ = make(10, 256, 4, 0)
+        s["offsets"].zero_()
+        for n in ("y", "dxd"):
+            s[n] = s[n][:rows].contiguous()
+        s["src_index"] = s["src_index"][:rows].contiguous()
+        a, b, before, _, _ = run(gpu, s)
+        assert torch.equal(a[0].cpu(), before) and not a[1].any() and torch.all(a[2] == -1)
+        check_dispatch(b, s, 0)
+
+
+def test_foreign_indices_are_dropped(gpu):
+    """Source indices outside [0, 2 T) and slots outside the rows touch nothing."""
+    s, kept = make(40, 256, 4, 0)
+    s["src_index"][5], s["src_index"][9] = -3, 1 << 30
+    a, b, before, c, f = run(gpu, s)
+    assert torch.all(a[2].cpu().view(-1)[s["src_index"][[0, 1, 2]].long()] >= 0)
+    assert torch.equal(a[0][[5, 9]].cpu(), before[[5, 9]])
+    slot = a[2].clone()
+    slot[0, 0], slot[1, 1] = 80, -9
+    dx, _ = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], slot_of=slot)
+    slot[0, 0], slot[1, 1] = -1, -1
+    want = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], slot_of=slot.clone())[0]
+    assert torch.equal(dx, want)
+
+
+def test_router_weights_that_are_not_16_byte_aligned(gpu):
+    s, kept = make(100, 256, 8, 0)
+    a, b, before, c, f = run(gpu, s)
+    flat = torch.zeros(256 * 8 + 1, dtype=bf, device="cuda")
+    w = flat[1:].view(256, 8)
+    w.copy_(c["w_router"])
+    check_dispatch(f.dispatch(c["dxd"], c["dlogits"], w, c["x"]), s, kept)
+
+
+def test_a_replayed_graph_and_another_stream(gpu):
+    T, d, E, cap = 6000, 512, 16, 700
+    data = [make(T, d, E, cap, seed) for seed in range(4)]
+    a, b, before, c, f = run(gpu, data[0][0])
+    dy = a[0]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        a = f.combine(c["dout"], c["y"], c["gates"], c["src_index"], c["offsets"], dy=dy)
+        b = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], c["x"])
+    for s, kept in data[1:] + data[:1]:
+        for n, t in s.items():
+            if t is not None:
+                c[n].copy_(t.cuda())
+        dy.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_combine(a, s, kept, before)
+        check_dispatch(b, s, kept)
+    side.wait_stream(torch.cuda.current_stream())
+    a = f.combine(c["dout"], c["y"], c["gates"], c["src_index"], c["offsets"], stream=side)
+    b = f.dispatch(c["dxd"], c["dlogits"], c["w_router"], c["x"], stream=side)
+    side.synchronize()
+    check_dispatch(b, s, kept)
+
+
+def test_refusals(gpu):
+    s, _ = make(16, 256, 4, 0)
+    f = gpu.MoEGrad(16, 256, 4)
+    c = {n: None if t is None else t.cuda() for n, t in s.items()}
+    args = ("dout", "y", "gates", "src_index", "offsets")
+    for n in args:
+        short = c[n][:, 1:] if n == "y" else c[n][1:]    # (fewer rows of y are another capacity's)
+        for bad in (c[n].cpu(), short, c[n].to(torch.float16)):
+            with pytest.raises(gpu.PwError):
+                f.combine(*[bad if m == n else c[m] for m in args])
+    with pytest.raises(gpu.PwError):
+        f.dispatch(c["dxd"], c["dlogits"], c["w_router"], c["x"])     # no slot_of yet
+    with pytest.raises(gpu.PwError):
+        gpu.MoEGrad(16, 320, 4)
+    with pytest.raises(gpu.PwError):
+        gpu.MoEGrad(16, 256, 4, rows=8).combine(*[c[m] for m in args])
+
+
+# ---- the whole block -----------------------------------------------------------------
+
+
+def expert_products(m, xd, w1, w2, dy, offs):
+    """Gradient of the experts' products, dy to dxd, as a caller runs it."""
+    dxd = torch.zeros_like(xd)
+    for e in range(m.E):
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        if hi > lo:
+            a = xd[lo:hi].float() @ w1[e].float()
+            a.requires_grad_(True)
+            with torch.enable_grad():
+                h = torch.nn.functional.gelu(a)
+            (da,) = torch.autograd.grad(h, a, dy[lo:hi].float() @ w2[e].float().t().contiguous())
+            dxd[lo:hi] = (da @ w1[e].float().t().contiguous()).to(bf)
+    return dxd
+
+
+@pytest.mark.parametrize("T,E,cap,masked", [(300, 8, 0, False), (300, 8, 40, True), (1, 4, 0, False)])
+def test_block_forward_and_backward(gpu, T, E, cap, masked):
+    """Norm, MoE step, norm with gate and residual, balance loss, and back, on
+    one stream with nothing waited for, against automatic differentiation of
+    the whole block in 64 bits with the routing that the GPU took.
+
+    Bar: relative 2-norms. About ten bf16 roundings (half a step, 2^-8, each at
+    most) lie on a gradient's way (h, hidden, y, out and r forward; dout, dy, dxd, dh,
+    dx back): 10 x 2^-8. dw_router sees two more, the norm's weights one."""
+    d, H, ax, ay, eps = 256, 256, 1.0, 0.5, 1e-5
+    inp = pw_inputs.moe(T, d, E, H)
+    wr, w1, w2 = inp.w_router.cuda(), inp.w1.cuda(), inp.w2.cuda()
+    rng = np.random.default_rng(T)
+    t = lambda *s, k=1.0, m=0.0: torch.from_numpy((rng.standard_normal(s) * k + m).astype(np.float32)).to(bf).cuda()  # noqa: E731
+    x, w_in, w_out, gate, dr = t(T, d), t(d, k=0.1, m=1.0), t(d, k=0.1, m=1.0), t(1, d, k=0.3, m=0.6), t(T, d)
+    valid = (torch.arange(T) % 5 != 2).cuda() if masked else None
+    if masked:
+        dr[~valid] = 0
+    up = torch.tensor([1.5, 0.5], device="cuda")
+    m = gpu.MoE(wr, w1, w2, T, num_src_shards=1, capacity=cap)
+    block = gpu.MoEBlock(m, w_in, w_out, gate, ax, ay, eps, balance_coef=0.1, z_coef=0.01)
+    r, loss, counts, fut = block.forward(x, valid)
+    dy = block.grad_begin(dr)
+    offs = m.offsets.cpu()
+    g = block.grad_end(expert_products(m, m.xd, w1, w2, dy, offs), up)
+    gpu.future_wait(fut, 60_000_000_000)
+
+    # the same block in 64 bits, routed as the GPU routed
+    D = lambda v: v.double().cpu().requires_grad_(True)  # noqa: E731
+    X, WI, WO, G, WR = D(x), D(w_in), D(w_out), D(gate), D(wr)
+    norm = lambda v, w: v / torch.sqrt(v.square().mean(1, True) + eps) * w  # noqa: E731
+    experts, src = m.experts.cpu().long(), m.src_index.cpu().numpy()
+    kept = int(offs[-1])
+    with torch.enable_grad():
+        h = norm(X, WI)
+        lg = h @ WR
+        gt = torch.softmax(torch.gather(lg, 1, experts), dim=1)
+        slot = torch.from_numpy(ob.slots(src, kept, T))
+        out = torch.zeros(T, d, dtype=torch.float64)
+        for s in range(2):
+            y = torch.stack([torch.nn.functional.gelu(h[i] @ w1[e].double().cpu()) @ w2[e].double().cpu()
+                             for i, e in enumerate(experts[:, s].tolist())])
+            out = out + torch.where(slot[:, s:s + 1] >= 0, gt[:, s:s + 1] * y, torch.zeros_like(y))
+        R = ax * X + ay * G * norm(out, WO)
+        v = torch.ones(T, dtype=torch.bool) if valid is None else valid.cpu()
+        n = int(v.sum())
+        p = torch.softmax(lg[v], dim=1)
+        c = counts.cpu().double()[:E]
+        L = torch.stack([0.1 * E * (c / (2 * n) * p.mean(0)).sum(), 0.01 * torch.logsumexp(lg[v], 1).square().mean()])
+        live = v.unsqueeze(1)
+        total = (torch.where(live, R, torch.zeros_like(R)) * dr.double().cpu()).sum() + (L * up.double().cpu()).sum()
+        want = torch.autograd.grad(total, [X, WI, WO, G, WR])
+    assert torch.equal(counts.cpu()[:E].long(), torch.bincount(experts[v].reshape(-1), minlength=E))
+    assert torch.allclose(loss.double().cpu(), L.detach(), rtol=2e-2, atol=0)
+    off = lambda a, b: float((a.double().cpu() - b).norm() / b.norm())  # noqa: E731
+    assert off(r[v.cuda()], R.detach()[v]) <= 6 * HALF
+    for name, b, k in zip(("x", "w_in", "w_out", "gate", "w_router"), want, (10, 11, 11, 11, 12)):
+        assert off(g[name], b.view_as(g[name].cpu())) <= k * HALF, (name, off(g[name], b))
