@@ -48,6 +48,8 @@ struct DispatchGradArgs {
   uint32_t tokens, d, E;
   uint32_t splits;     // token ranges of dw
   uint32_t split_tokens;
+  uint32_t col_groups; // workgroups that share the columns of dx
+  bool whole_w;        // rows of w are whole aligned chunks of 8 experts
 };
 
 // ---- slot_of: the inverse of src_index ---------------------------------------
@@ -163,26 +165,30 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
 }
 
 // ---- gradient of dispatch and router, to the tokens ------------------------------
-// dx^T tile = W dl^T by v_mfma_f32_32x32x16_bf16, W's rows (columns of dx) as
-// the first operand and the tokens as the second: a lane holds one token. The
-// first operand's rows are dealt so that a lane's two accumulators hold 32
-// consecutive columns: row i of block b is column 32 h + 16 b + r, where
-// h = (i >> 2) & 1 is the half of the wave that receives it and
-// r = 4 (i >> 3) + (i & 3) the register. dl is split into two bf16 terms
-// (hi + lo, at most 2^-16 of the value is lost, below the rounding of dx to bf16 at
-// 2^-8), so the products are as exact as dx can show.
-constexpr int kDxTokens = 32;  // tokens of a wave
+// A wave walks tiles of 16 tokens: dl W^T by v_mfma_f32_16x16x32_bf16 with the
+// tokens as the first operand's rows, 128 columns of dx at a time. W lies in
+// LDS in the order its operands are read (64 lanes of 16 bytes each). Column
+// block b of the second operand holds every eighth column (8 n + b for lane
+// n), so a lane's eight accumulators are 8 consecutive columns of its 4
+// tokens, and rows of dxd and dx are read and written 16 bytes a lane, 256
+// contiguous bytes a row. dl is split into two bf16 terms (hi + lo, at most
+// 2^-16 of the value is lost, below the rounding of dx to bf16 at 2^-8), so
+// the products are as exact as dx can show. 131072 tokens x 1024, 64 experts:
+// 159 us, 5.1 TB/s, the rate of a large copy; bound by HBM. (W in registers,
+// 128 columns a wave, 8 waves per CU: 223 us; one token a lane, 64 bytes of
+// its row: 306 us.)
+constexpr uint32_t kDxThreads = 1024;
+constexpr uint32_t kDxWaves = kDxThreads / 64;
+constexpr uint32_t kDxTokens = 16;
+constexpr uint32_t kDxCols = 128;
+constexpr uint32_t kDxGrid = 256;  // workgroups: one per CU
 
-__device__ __forceinline__ void split2(float v, __bf16& hi, __bf16& lo) {
-  hi = (__bf16)v;
-  lo = (__bf16)(v - (float)hi);
-}
+typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // W[c][e0 .. e0 + 7], zero where there is no expert.
-template <bool kWhole>
 __device__ __forceinline__ bf16x8 load_w(const DispatchGradArgs& a, uint32_t c, uint32_t e0) {
   bf16x8 v = {};
-  if (kWhole) {
+  if (a.whole_w) {  // uniform
     if (e0 < a.E) v = *reinterpret_cast<const bf16x8*>(a.w + (uint64_t)c * a.E + e0);
   } else {
 #pragma unroll
@@ -192,60 +198,92 @@ __device__ __forceinline__ bf16x8 load_w(const DispatchGradArgs& a, uint32_t c, 
   return v;
 }
 
-template <bool kWhole>  // whole chunks of 8 experts, 16-byte aligned
-__global__ __launch_bounds__(256) void k_dispatch_grad(DispatchGradArgs a) {
-  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
-  const uint32_t t0 = (blockIdx.x * 4 + w) * kDxTokens;
-  if (t0 >= a.tokens) return;
-  const bool live = t0 + i < a.tokens;
-  const uint32_t t = live ? t0 + i : a.tokens - 1;
-  const bool ok = !a.valid || a.valid[t];
-  // the token's logit gradients: experts 16 s + 8 h .. + 7 of step s
-  bf16x8 hi[4], lo[4];
+template <int KS, bool kVec>  // steps of 32 experts; whole aligned 16-byte chunks of a row of dl
+__global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a) {
+  extern __shared__ __attribute__((aligned(16))) bf16x8 lds_w[];  // [column block][b][s][64 lanes]
+  const uint32_t lane = threadIdx.x & 63, i = lane & 15, h = lane >> 4;
+  const uint32_t tiles = (a.tokens + kDxTokens - 1) / kDxTokens;
+  const uint32_t blocks = a.d / kDxCols / a.col_groups, block0 = blockIdx.x % a.col_groups * blocks;
+  const uint32_t streams = gridDim.x / a.col_groups * kDxWaves;
+  for (uint32_t o = threadIdx.x; o < blocks * 8 * KS * 64; o += kDxThreads) {
+    const uint32_t l = o & 63, f = o >> 6, s = f % KS, b = f / KS % 8, cb = block0 + f / (KS * 8);
+    lds_w[o] = load_w(a, cb * kDxCols + 8 * (l & 15) + b, 32 * s + 8 * (l >> 4));
+  }
+  __syncthreads();
+  for (uint32_t tile = blockIdx.x / a.col_groups * kDxWaves + (threadIdx.x >> 6); tile < tiles; tile += streams) {
+    // token i's logit gradients, experts 32 s + 8 h .. + 7, and its rows of dxd
+    const uint32_t ti = min(tile * kDxTokens + i, a.tokens - 1);
+    const int2 sl = *reinterpret_cast<const int2*>(a.slot_of + (uint64_t)ti * 2);
+    const float* row = a.dlogits + (uint64_t)ti * a.E;
+    bf16x8 hi[KS], lo[KS];
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t e0 = 32 * s + 8 * h;  // past the last expert: repeated values, against zeros of W
+      float v[8];
+      if (kVec) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t e = 16 * s + 8 * h + j;
-      const float v = e < a.E ? a.dlogits[(uint64_t)t * a.E + e] : 0.f;
-      __bf16 p, q;
-      split2(v, p, q);
-      hi[s][j] = p;
-      lo[s][j] = q;
-    }
-  const int2 sl = *reinterpret_cast<const int2*>(a.slot_of + (uint64_t)t * 2);
-  const bool have[2] = {sl.x >= 0 && (uint64_t)sl.x < a.rows, sl.y >= 0 && (uint64_t)sl.y < a.rows};
-  const __bf16* row[2] = {a.dxd + (have[0] ? (uint64_t)sl.x : 0) * a.d + 32 * h,
-                          a.dxd + (have[1] ? (uint64_t)sl.y : 0) * a.d + 32 * h};
-  const uint32_t col = 32 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
-  for (uint32_t c0 = 0; c0 < a.d; c0 += 64) {
-    bf16x8 g[2][4];
-    if (a.rows) {  // uniform
+        for (int q = 0; q < 2; ++q) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(row + min(e0 + 4 * q, a.E - 4));
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+          for (int j = 0; j < 4; ++j) v[4 * q + j] = x[j];
+        }
+      } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) g[s][q] = *reinterpret_cast<const bf16x8*>(row[s] + c0 + 8 * q);
-    }
-    f32x16 acc[2] = {f32x16{}, f32x16{}};
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bf16x8 wv = load_w<kWhole>(a, c0 + col + 16 * b, 16 * s + 8 * h);
-        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, hi[s], acc[b], 0, 0, 0);
-        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, lo[s], acc[b], 0, 0, 0);
+        for (int j = 0; j < 8; ++j) v[j] = row[min(e0 + j, a.E - 1)];
       }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      bf16x8 o;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float f = acc[q >> 1][(q & 1) * 8 + j];
-        if (have[0]) f += (float)g[0][q][j];
-        if (have[1]) f += (float)g[1][q][j];
-        o[j] = ok ? (__bf16)f : (__bf16)0.f;
+        hi[s][j] = (__bf16)v[j];
+        lo[s][j] = (__bf16)(v[j] - (float)hi[s][j]);
       }
-      if (live) *reinterpret_cast<bf16x8*>(a.dx + (uint64_t)t * a.d + c0 + 32 * h + 8 * q) = o;
+    }
+    const bool pad = a.valid && !a.valid[ti];
+    // of the lane's own 4 tokens (4 h + r): row, whether there is one, padding
+    const __bf16* src[2][4];
+    uint32_t have = 0;  // bit 4 s + r; bit 8 + r: padding
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int v = __shfl(s ? sl.y : sl.x, 4 * h + r);
+        const bool in = v >= 0 && (uint64_t)v < a.rows;
+        have |= (in ? 1u : 0u) << (4 * s + r);
+        src[s][r] = a.dxd + (uint64_t)(in ? (uint32_t)v : 0u) * a.d + block0 * kDxCols + 8 * i;
+      }
+      have |= (__shfl((int)pad, 4 * h + r) ? 1u : 0u) << (8 + r);
+    }
+    __bf16* out = a.dx + ((uint64_t)tile * kDxTokens + 4 * h) * a.d + block0 * kDxCols + 8 * i;
+    for (uint32_t cb = 0; cb < blocks; ++cb) {
+      bf16x8 g[2][4];
+      if (a.rows)  // uniform; a dropped tuple reads row 0, and does not use it
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) g[s][r] = *reinterpret_cast<const bf16x8*>(src[s][r] + cb * kDxCols);
+      f32x4 acc[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        acc[b] = f32x4{};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const bf16x8 w = lds_w[((cb * 8 + b) * KS + s) * 64 + lane];
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[s], w, acc[b], 0, 0, 0);
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[s], w, acc[b], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool have0 = have >> r & 1, have1 = have >> (4 + r) & 1, padding = have >> (8 + r) & 1;
+        bf16x8 o;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          float f = acc[b][r];
+          f += have0 ? (float)g[0][r][b] : 0.f;
+          f += have1 ? (float)g[1][r][b] : 0.f;
+          o[b] = (__bf16)(padding ? 0.f : f);
+        }
+        if (tile * kDxTokens + 4 * h + r < a.tokens) *reinterpret_cast<bf16x8*>(out + (uint64_t)r * a.d + cb * kDxCols) = o;
+      }
     }
   }
 }
@@ -256,10 +294,15 @@ __global__ __launch_bounds__(256) void k_dispatch_grad(DispatchGradArgs a) {
 // columns (8 bytes) of each of its 8 tokens and pairs the tokens with byte
 // permutes, so operand q holds columns 4 i + q. dl is split into three bf16
 // terms, which hold all 24 bits of it: every product is exact and the sums
-// are fp32. A workgroup covers 256 columns (2 waves of 128) with 4 waves of
-// tokens each, joined through LDS in a fixed order.
+// are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
+// of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
+// 131072 tokens x 1024, 64 experts: 80 us, 3.8 TB/s of reads, what sums and
+// maxima over 1 GiB reach; bound by reading x and dl once from HBM. (Sharing the split terms between the waves
+// through LDS, and requesting x two steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
+constexpr uint32_t kDwMaxTokens = 1u << 19;  // of a range: its rows of x (at most 2560 bytes) are one buffer
+constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, and below 2^32 with all that is added
 
 template <int NC>  // expert blocks of 32
 __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
@@ -273,55 +316,71 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   if (split >= a.splits) return;  // whole workgroups
   const uint32_t cw = w & 1, tw = w >> 1;
   const uint32_t first = split * a.split_tokens, last = min(first + a.split_tokens, a.tokens);
-  const __bf16* x = a.x + cg * kDwCols + cw * 128 + 4 * i;
   f32x16 acc[4][NC];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[q][c] = f32x16{};
-  for (uint32_t t0 = first + 16 * tw; t0 < last; t0 += 64) {
-    u32x2 v[8];
+  struct Step {
+    u32x2 v[8];        // 4 columns of 8 tokens
     float dl[NC][8];
+  };
+  // The range's rows of x and dl as buffers: past its end, and for experts
+  // that are none (a distant offset), a load returns zero.
+  const uint32_t n = last - first, xrow = a.d * 2, drow = a.E * 4;
+  const auto xb = raw_buffer(a.x + (uint64_t)first * a.d, n * xrow);
+  const auto db = raw_buffer(a.dlogits + (uint64_t)first * a.E, n * drow);
+  const uint32_t xoff = (16 * tw + 8 * h) * xrow + (cg * kDwCols + cw * 128 + 4 * i) * 2;
+  uint32_t doff[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) doff[c] = (16 * tw + 8 * h) * drow + (32 * c + i < a.E ? (32 * c + i) * 4 : kDistant);
+  auto fetch = [&](Step& s, uint32_t t) {  // tokens t + 16 tw + 8 h + j of the range
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t tt = t0 + 8 * h + j, t = min(tt, last - 1);
-      v[j] = *reinterpret_cast<const u32x2*>(x + (uint64_t)t * a.d);
-      if (a.valid && !a.valid[t]) v[j] = u32x2{0, 0};
+      s.v[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(xb, xoff + (t + j) * xrow, 0, 0));
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const uint32_t e = 32 * c + i;
-        const float f = a.dlogits[(uint64_t)t * a.E + min(e, a.E - 1)];
-        dl[c][j] = tt < last && e < a.E ? f : 0.f;
-      }
+      for (int c = 0; c < NC; ++c)
+        s.dl[c][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(db, doff[c] + (t + j) * drow, 0, 0));
     }
-    bf16x8 xa[4];
+  };
+  // A step's operands are made from its loads, the next step's loads requested
+  // into the same registers, and then its products run.
+  Step s;
+  fetch(s, 0);
+  for (uint32_t t = 0; t < n; t += 64) {
+    if (a.valid)  // uniform
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!a.valid[first + min(t + 16 * tw + 8 * h + j, n - 1)]) s.v[j] = u32x2{0, 0};
+    bf16x8 xa[4], dt[NC][3];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       u32x4 p;
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // halves q & 1 of tokens 2 j and 2 j + 1
-        p[j] = __builtin_amdgcn_perm(v[2 * j + 1][q >> 1], v[2 * j][q >> 1], q & 1 ? 0x07060302u : 0x05040100u);
+        p[j] = __builtin_amdgcn_perm(s.v[2 * j + 1][q >> 1], s.v[2 * j][q >> 1], q & 1 ? 0x07060302u : 0x05040100u);
       xa[q] = __builtin_bit_cast(bf16x8, p);
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      bf16x8 d0, d1, d2;
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __bf16 b0 = (__bf16)dl[c][j];
-        const float r1 = dl[c][j] - (float)b0;
-        const __bf16 b1 = (__bf16)r1;
-        d0[j] = b0;
-        d1[j] = b1;
-        d2[j] = (__bf16)(r1 - (float)b1);
+        const float f = s.dl[c][j];
+        dt[c][0][j] = (__bf16)f;
+        const float r1 = f - (float)dt[c][0][j];
+        dt[c][1][j] = (__bf16)r1;
+        dt[c][2][j] = (__bf16)(r1 - (float)dt[c][1][j]);
       }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(s, t + 64);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d0, acc[q][c], 0, 0, 0);
-        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d1, acc[q][c], 0, 0, 0);
-        acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], d2, acc[q][c], 0, 0, 0);
-      }
-    }
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], dt[c][m], acc[q][c], 0, 0, 0);
   }
   for (uint32_t turn = 0; turn < 4; ++turn) {
     if (tw == turn)
@@ -365,6 +424,28 @@ __global__ __launch_bounds__(256) void k_router_dw_zero(DispatchGradArgs a) {
   if (o < a.d * a.E) a.dw[o] = 0.f;
 }
 
+template <int KS, bool kVec>
+hipError_t launch_dx_steps(const DispatchGradArgs& a, uint32_t grid, hipStream_t s) {
+  const size_t lds = (size_t)a.d / a.col_groups * KS * 64;
+  const void* fn = (const void*)k_dispatch_grad<KS, kVec>;
+  const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_dispatch_grad<KS, kVec>), dim3(grid), dim3(kDxThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dx(DispatchGradArgs& a, hipStream_t s) {
+  const uint32_t tiles = (a.tokens + kDxTokens - 1) / kDxTokens, blocks = a.d / kDxCols;
+  // With a tile for every wave of the GPU a workgroup keeps all of W and a wave
+  // takes whole rows; below that the column blocks go to different workgroups.
+  a.col_groups = tiles >= kDxGrid * kDxWaves ? 1 : blocks;
+  const uint32_t grid = std::min(kDxGrid * (a.col_groups > 1 ? 2 : 1) / a.col_groups, (tiles + kDxWaves - 1) / kDxWaves) * a.col_groups;
+  a.whole_w = a.E % 8 == 0 && (uintptr_t)a.w % 16 == 0;
+  const bool vec = a.E % 4 == 0 && (uintptr_t)a.dlogits % 16 == 0;
+  if (a.E <= 32) return vec ? launch_dx_steps<1, true>(a, grid, s) : launch_dx_steps<1, false>(a, grid, s);
+  return vec ? launch_dx_steps<2, true>(a, grid, s) : launch_dx_steps<2, false>(a, grid, s);
+}
+
 struct DwLayout {
   uint32_t splits = 1, split_tokens = 64;
   size_t total = 0;
@@ -377,7 +458,7 @@ DwLayout dw_layout(const pw_moe_grad_desc& d) {
   const uint32_t groups = d.d / kDwCols;
   const uint64_t want = std::max<uint64_t>(1, kDwGrid / groups);
   const uint64_t per = (d.tokens + want - 1) / want;
-  l.split_tokens = (uint32_t)std::max<uint64_t>(64, (per + 63) / 64 * 64);
+  l.split_tokens = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(64, (per + 63) / 64 * 64), kDwMaxTokens);
   l.splits = (uint32_t)std::max<uint64_t>(1, (d.tokens + l.split_tokens - 1) / l.split_tokens);
   if (l.splits > 1) l.total = up256((size_t)l.splits * d.d * (d.num_experts > 32 ? 64 : 32) * 4);
   return l;
@@ -496,11 +577,7 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
     e = hipGetLastError();
     return e == hipSuccess ? PW_OK : hip_fail(e, "launch router_dw_zero");
   }
-  const bool whole = a.E % 8 == 0 && (uintptr_t)a.w % 16 == 0;
-  const uint32_t blocks = (a.tokens + 4 * kDxTokens - 1) / (4 * kDxTokens);
-  if (whole) hipLaunchKernelGGL(k_dispatch_grad<true>, dim3(blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_dispatch_grad<false>, dim3(blocks), dim3(256), 0, s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch dispatch_grad");
+  if ((e = launch_dx(a, s)) != hipSuccess) return hip_fail(e, "launch dispatch_grad");
   if (!a.dw) return PW_OK;
   const bool two = a.E > 32;
   const uint32_t grid = 8 * (a.d / kDwCols) * ((a.splits + 7) / 8);
