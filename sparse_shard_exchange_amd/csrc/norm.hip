@@ -12,9 +12,12 @@
 //   Q_g = sum over g's rows of D y t     dgate_g = ay wy Q_g
 //   dwy = ay sum_g gate_g Q_g            dwr = sum dh r s
 //
-// A row lives in the registers of its team (one wave for narrow rows, the
-// whole workgroup for wide ones) from its only read to its only write, so the
-// passes move 4 and 6 row tensors and nothing else; the bound is HBM.
+// A row lives in the registers of its team (one wave up to 512 elements, up to
+// 16 waves for the widest) from its only read to its only write, so the passes
+// move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
+// bf16, all parts: forward 204 us (5.3 TB/s), backward 336 + 6 us (4.8 TB/s); a
+// large copy reaches 5.2. (Nontemporal loads and stores: 199 and 325 us, but
+// the next operator reads these rows, where they are small from the caches.)
 #include "ops.h"
 
 #include <algorithm>
@@ -23,8 +26,9 @@ namespace pw {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a workgroup, or a wider team's
 constexpr uint32_t kMaxWidth = 8192;
+constexpr int threads_of(int team) { return team > kThreads ? team : kThreads; }
 
 struct NormArgs {
   const void* x;
@@ -88,38 +92,57 @@ __device__ __forceinline__ void store(void* base, uint64_t off, const Chunk<T, V
   *reinterpret_cast<Chunk<T, V>*>(static_cast<T*>(base) + off) = c;
 }
 
-// Sums a and b over the team; every thread of the team gets both. Teams of a
-// workgroup exchange through LDS (two barriers: before the first write the
-// previous sums have been read).
+// A chunk of a row vector that every row uses (a weight or a gate). Chunks of
+// bf16 the compiler may keep in registers for all rows; wider elements are
+// loaded again for each row, from the caches (the empty asm statement hides
+// that the address is the same): as many more registers would halve the waves.
+template <typename T, int V>
+__device__ __forceinline__ Chunk<T, V> load_shared(const void* p, uint64_t off) {
+  if constexpr (V < 8) asm volatile("" : "+s"(p));
+  return load<T, V>(p, off);
+}
+
+// The waves' sums of one exchange, by wave. A workgroup alternates between two
+// of them, so one barrier an exchange is enough: whoever writes one again has
+// passed the barrier of the other, which every wave reaches after it has read
+// the first.
 template <int TEAM>
-__device__ __forceinline__ void team_sum(float& a, float& b, float (*red)[2]) {
+struct Exchange {
+  float sums[2][threads_of(TEAM) / 64][3];
+};
+
+// Sums N values over the team; every thread of the team gets them.
+template <int TEAM, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint32_t& turn) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    a += __shfl_xor(a, m);
-    b += __shfl_xor(b, m);
-  }
+  for (int m = 1; m < 64; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
   if constexpr (TEAM > 64) {
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) {
-      red[threadIdx.x / 64][0] = a;
-      red[threadIdx.x / 64][1] = b;
-    }
-    __syncthreads();
-    a = b = 0.f;
+    constexpr int W = TEAM / 64;
+    auto& sums = x.sums[turn];
+    turn ^= 1;
+    if (threadIdx.x % 64 == 0)
 #pragma unroll
-    for (int w = 0; w < TEAM / 64; ++w) {
-      a += red[w][0];
-      b += red[w][1];
-    }
+      for (int i = 0; i < N; ++i) sums[threadIdx.x / 64][i] = v[i];
+    __syncthreads();
+    const int w = threadIdx.x / TEAM * W + threadIdx.x % W;  // each lane a wave's sums, then across W lanes
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = sums[w][i];
+#pragma unroll
+    for (int m = 1; m < W; m <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
   }
 }
 
 // C chunks of V elements per thread of a team of TEAM threads.
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
-__global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
-  __shared__ float red[kThreads / 64][2];
+__global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
+  __shared__ Exchange<TEAM> ex;
+  uint32_t turn = 0;
   const uint32_t lane = threadIdx.x % TEAM, nch = a.d / V;
-  constexpr uint32_t kTeams = kThreads / TEAM;
+  constexpr uint32_t kTeams = threads_of(TEAM) / TEAM;
   const bool norm_y = kY && a.w_y, gated = kY && a.gate;
   // the trip count is the same for all threads of a workgroup (barriers inside)
   for (uint32_t row0 = blockIdx.x * kTeams; row0 < a.rows; row0 += gridDim.x * kTeams) {
@@ -135,17 +158,17 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
     }
     float ty = a.y_scale;
     if (norm_y) {
-      float ss = 0.f, none = 0.f;
+      float ss[1] = {0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c)
         if (lane + c * TEAM < nch)
 #pragma unroll
-          for (int v = 0; v < V; ++v) ss = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss);
-      team_sum<TEAM>(ss, none, red);
-      ty = a.y_scale * rsqrtf(fmaf(ss, a.inv_d, a.eps));
+          for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
+      team_sum(ss, ex, turn);
+      ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
     }
     const uint64_t gbase = gated ? (uint64_t)((live ? row : a.rows - 1) / a.group) * a.d : 0;
-    float r[C][V], ss = 0.f, none = 0.f;
+    float r[C][V], ss[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t ch = min(lane + c * TEAM, nch - 1);
@@ -161,13 +184,13 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
           f = gated ? fmaf(n, at<T, V>(g, v), f) : f + n;
         }
         r[c][v] = f;
-        if (kH && lane + c * TEAM < nch) ss = fmaf(f, f, ss);
+        if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
       }
     }
     float s = 0.f;
     if (kH) {
-      team_sum<TEAM>(ss, none, red);
-      s = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+      team_sum(ss, ex, turn);
+      s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -197,12 +220,14 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a) {
 // the whole group, else to part_q; and gate Q to the running sum P of dw_y.
 // W and P end in one partial row per workgroup; k_norm_join adds the rows.
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
-__global__ __launch_bounds__(kThreads) void k_norm_grad(NormArgs a) {
-  extern __shared__ float lds[];  // TEAM 64: [teams][d] sums of the teams
-  __shared__ float red[kThreads / 64][2];
+__global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) void k_norm_grad(NormArgs a) {
+  constexpr int NT = threads_of(TEAM);
+  extern __shared__ float lds[];  // several teams: [teams][d] their sums
+  __shared__ Exchange<TEAM> ex;
+  uint32_t turn = 0;
   const uint32_t lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, nch = a.d / V;
-  constexpr uint32_t kTeams = kThreads / TEAM;
-  constexpr int kOwn = (C * V * TEAM + kThreads - 1) / kThreads;  // columns of a thread at the end of a segment
+  constexpr uint32_t kTeams = NT / TEAM;
+  constexpr int kOwn = C * V / (int)kTeams;  // columns of a thread at the end of a segment
   const bool norm_y = kY && a.w_y, gated = kY && a.gate, sums_y = norm_y || gated;
   float Q[C][V], W[C][V], P[kOwn];
 #pragma unroll
@@ -214,11 +239,11 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(NormArgs a) {
 
   // Column i of this thread at a segment's end, and its sum over the teams.
   auto column = [&](int i) -> uint32_t {
-    if constexpr (TEAM == kThreads) return (lane + (i / V) * TEAM) * V + i % V;
-    return threadIdx.x + i * kThreads;
+    if constexpr (kTeams == 1) return (lane + (i / V) * TEAM) * V + i % V;
+    return threadIdx.x + i * NT;
   };
   auto gather = [&](const float (&s)[C][V], float (&out)[kOwn]) {
-    if constexpr (TEAM == kThreads) {
+    if constexpr (kTeams == 1) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) out[i] = s[i / V][i % V];
     } else {
@@ -262,42 +287,39 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(NormArgs a) {
         if (kY) y[c] = load<T, V>(a.y, o);
       }
       float D[C][V];
-      float rr = 0.f, gr = 0.f, yy = 0.f, none = 0.f;
+      float sum[3] = {0.f, 0.f, 0.f};  // r^2, G r, y^2
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const bool in = lane + c * TEAM < nch;
         Chunk<T, V> w;
-        if (kH) w = load<T, V>(a.w_r, (uint64_t)min(lane + c * TEAM, nch - 1) * V);
+        if (kH) w = load_shared<T, V>(a.w_r, (uint64_t)min(lane + c * TEAM, nch - 1) * V);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (kH) {
             D[c][v] = at<T, V>(dh[c], v) * at<T, V>(w, v);
             if (in) {
-              rr = fmaf(at<T, V>(r[c], v), at<T, V>(r[c], v), rr);
-              gr = fmaf(D[c][v], at<T, V>(r[c], v), gr);
+              sum[0] = fmaf(at<T, V>(r[c], v), at<T, V>(r[c], v), sum[0]);
+              sum[1] = fmaf(D[c][v], at<T, V>(r[c], v), sum[1]);
             }
           }
-          if (norm_y && in) yy = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), yy);
+          if (norm_y && in) sum[2] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), sum[2]);
         }
       }
       float s = 0.f, m = 0.f, t = 1.f;
+      if (kH || norm_y) team_sum(sum, ex, turn);  // uniform
       if (kH) {
-        team_sum<TEAM>(rr, gr, red);
-        s = rsqrtf(fmaf(rr, a.inv_d, a.eps));
-        m = s * s * gr * a.inv_d;
+        s = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
+        m = s * s * sum[1] * a.inv_d;
       }
-      if (norm_y) {
-        team_sum<TEAM>(yy, none, red);
-        t = rsqrtf(fmaf(yy, a.inv_d, a.eps));
-      }
-      float qy = 0.f;
+      if (norm_y) t = rsqrtf(fmaf(sum[2], a.inv_d, a.eps));
+      float qy[1] = {0.f};
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const uint32_t ch = lane + c * TEAM;
         const bool in = ok && ch < nch;
         Chunk<T, V> o, wy, gt;
-        if (norm_y) wy = load<T, V>(a.w_y, (uint64_t)min(ch, nch - 1) * V);
-        if (gated) gt = load<T, V>(a.gate, gbase + (uint64_t)min(ch, nch - 1) * V);
+        if (norm_y) wy = load_shared<T, V>(a.w_y, (uint64_t)min(ch, nch - 1) * V);
+        if (gated) gt = load_shared<T, V>(a.gate, gbase + (uint64_t)min(ch, nch - 1) * V);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float f = a.dr ? at<T, V>(dr[c], v) : 0.f;
@@ -314,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(NormArgs a) {
             if (gated) f *= at<T, V>(gt, v);
             if (norm_y) {
               f *= at<T, V>(wy, v);
-              if (ch < nch) qy = fmaf(f, yv, qy);
+              if (ch < nch) qy[0] = fmaf(f, yv, qy[0]);
             }
           }
           D[c][v] = f;
@@ -324,8 +346,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_grad(NormArgs a) {
       if (kY) {
         float m2 = 0.f;
         if (norm_y) {
-          team_sum<TEAM>(qy, none, red);
-          m2 = t * t * qy * a.inv_d;
+          team_sum(qy, ex, turn);
+          m2 = t * t * qy[0] * a.inv_d;
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -381,6 +403,7 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a) {
   if ((what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;
   float v = 0.f;
   if (col < a.d)
+#pragma unroll 8
     for (uint32_t i = slice; i < n; i += 16) v += part[(uint64_t)i * a.d + col];
   s[slice][c] = v;
   __syncthreads();
@@ -403,8 +426,13 @@ __global__ __launch_bounds__(kThreads) void k_norm_zero(NormArgs a) {
 }
 
 // The kernel variant of a row: elements per chunk, chunks per thread, threads
-// per row. One wave per row while the row fits 4 chunks a lane (no barrier in
-// the row sums), else the workgroup. Rows that are not whole aligned 16-byte
+// per row. At most 8 elements a thread, so that the gradient's registers (rows,
+// sums, weights) leave room for 4 waves per SIMD (131072 x 1024 bf16 with 16
+// elements and one wave a row: the same 340 us, with 192 registers; 2047 x 1001
+// fp32 with 256 threads: 42 us against 16). From 4096 on rows of 4-byte chunks
+// take 16 elements by 512 threads (8192 x 8192 fp32 back: 405 us against 570 by
+// 1024 threads of 8, 4000 x 8191 bf16: 221 against 507; 16384 x 8192 bf16 in
+// whole chunks: 505 against 477). Rows that are not whole aligned 16-byte
 // chunks go by single elements.
 struct Shape {
   int V, C, team;
@@ -412,18 +440,12 @@ struct Shape {
 
 Shape shape_of(uint32_t d, bool f32, bool aligned) {
   const int V = aligned ? (f32 ? 4 : 8) : 1;
-  const uint32_t nch = d / V;
-  if (V > 1) {
-    if (nch <= 64) return {V, 1, 64};
-    if (nch <= 128) return {V, 2, 64};
-    if (nch <= 256) return {V, 4, 64};
-    if (nch <= 512) return {V, 2, 256};
-    if (nch <= 1024) return {V, 4, 256};
-    return {V, 8, 256};
-  }
-  if (nch <= 256) return {1, 4, 64};
-  if (nch <= 2048) return {1, 8, 256};
-  return {1, 32, 256};
+  if (d > 4096) return V == 8 ? Shape{8, 1, 1024} : Shape{V, 16 / V, 512};
+  if (d > 2048) return {V, 8 / V, 512};
+  if (d > 1024) return {V, 8 / V, 256};
+  if (d > 512) return {V, 8 / V, 128};
+  if (d > 256 || V == 8) return {V, 8 / V, 64};
+  return {V, 4 / V, 64};
 }
 
 struct Segments {
@@ -431,14 +453,16 @@ struct Segments {
 };
 
 constexpr uint32_t kSegments = 1024;  // segments wanted: 4 workgroups per CU
+constexpr uint32_t kSegmentRows = 4;  // of a segment at least, where a group has them
 
-// Enough segments to fill the GPU, none below 16 rows where a group has more.
+// Enough segments to fill the GPU, but none so short that its partial sums
+// (two or three fp32 rows written and read) cost as much as its rows.
 Segments segments(uint32_t rows, uint32_t gates) {
   Segments s;
   const uint32_t groups = std::max(1u, gates);
   s.group = rows / groups;
   const uint32_t want = std::max(1u, kSegments / groups);
-  s.seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, 16u));
+  s.seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, kSegmentRows));
   s.segs = (s.group + s.seg_rows - 1) / s.seg_rows;
   s.num_segs = s.segs * groups;
   s.grid = std::min(s.num_segs, kSegments);
@@ -522,13 +546,13 @@ constexpr uint32_t kForwardGrid = 256 * 16;  // workgroups of k_norm at most
 
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
 void launch(const NormArgs& a, bool grad, hipStream_t s) {
+  constexpr uint32_t NT = threads_of(TEAM), teams = NT / TEAM;
   if (grad) {
-    const size_t lds = TEAM < kThreads ? (size_t)(kThreads / TEAM) * a.d * 4 : 0;
-    hipLaunchKernelGGL((k_norm_grad<T, V, C, TEAM, kY, kH>), dim3(a.grid), dim3(kThreads), lds, s, a);
+    const size_t lds = teams > 1 ? (size_t)teams * a.d * 4 : 0;
+    hipLaunchKernelGGL((k_norm_grad<T, V, C, TEAM, kY, kH>), dim3(a.grid), dim3(NT), lds, s, a);
   } else {
-    const uint32_t teams = kThreads / TEAM;
     const uint32_t blocks = (uint32_t)std::min<uint64_t>(((uint64_t)a.rows + teams - 1) / teams, kForwardGrid);
-    hipLaunchKernelGGL((k_norm<T, V, C, TEAM, kY, kH>), dim3(blocks), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_norm<T, V, C, TEAM, kY, kH>), dim3(blocks), dim3(NT), 0, s, a);
   }
 }
 
@@ -541,21 +565,18 @@ void launch_parts(const NormArgs& a, bool grad, hipStream_t s) {
 
 template <typename T, int V>
 void launch_shape(const NormArgs& a, const Shape& sh, bool grad, hipStream_t s) {
-  if constexpr (V > 1) {
-    if (sh.team == 64) {
-      if (sh.C == 1) launch_parts<T, V, 1, 64>(a, grad, s);
-      else if (sh.C == 2) launch_parts<T, V, 2, 64>(a, grad, s);
-      else launch_parts<T, V, 4, 64>(a, grad, s);
-    } else {
-      if (sh.C == 2) launch_parts<T, V, 2, 256>(a, grad, s);
-      else if (sh.C == 4) launch_parts<T, V, 4, 256>(a, grad, s);
-      else if constexpr (V == 4) launch_parts<T, V, 8, 256>(a, grad, s);  // 8192 fp32; bf16 ends at 4
-    }
-  } else {
-    if (sh.team == 64) launch_parts<T, 1, 4, 64>(a, grad, s);
-    else if (sh.C == 8) launch_parts<T, 1, 8, 256>(a, grad, s);
-    else launch_parts<T, 1, 32, 256>(a, grad, s);
+  switch (sh.team) {
+    case 1024:
+      if constexpr (V == 8) return launch_parts<T, 8, 1, 1024>(a, grad, s);
+    case 512:
+      if constexpr (V < 8)
+        if (sh.C * V == 16) return launch_parts<T, V, 16 / V, 512>(a, grad, s);
+      return launch_parts<T, V, 8 / V, 512>(a, grad, s);
+    case 256: return launch_parts<T, V, 8 / V, 256>(a, grad, s);
+    case 128: return launch_parts<T, V, 8 / V, 128>(a, grad, s);
   }
+  if (sh.C * V == 8) return launch_parts<T, V, 8 / V, 64>(a, grad, s);
+  if constexpr (V < 8) launch_parts<T, V, 4 / V, 64>(a, grad, s);
 }
 
 hipError_t launch_any(const NormArgs& a, const pw_norm_desc& d, bool aligned, bool grad, hipStream_t s) {
