@@ -18,11 +18,14 @@ namespace pw {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;     // k_balance, its join
+constexpr int kGradThreads = 256;  // k_router_grad
 constexpr uint32_t kMaxBalanceExperts = 256;
-constexpr uint32_t kParts = 256;        // partial sums at most (workgroups of k_balance)
+constexpr int kRed = 256;          // threads of the loss' last sum: one per expert
+constexpr uint32_t kParts = 256;        // partial sums at most: a workgroup of 16 waves per CU
 constexpr uint32_t kAlone = 2048;       // tokens up to which one workgroup does all
 constexpr uint32_t kRows = 4;           // rows of a group in flight
+constexpr uint32_t kGradWide = 2048;    // workgroups up to which k_router_grad takes one row a group
 
 struct BalanceArgs {
   const float* logits;
@@ -35,9 +38,7 @@ struct BalanceArgs {
   const float* dgates;
   const float* grad_loss;
   float* dlogits;
-  float* part_p;    // [parts][E] sums of probabilities
-  int32_t* part_c;  // [parts][E + 1] tuples per expert; valid tokens
-  float* part_z;    // [parts] sums of squared logarithms
+  uint2* part;      // [parts][E + 1] sums of probabilities (fp32 bits), tuples; last: squared logarithms, valid tokens
   uint32_t parts;
   uint32_t tokens, E, k;
   float balance_coef, z_coef;
@@ -58,24 +59,11 @@ __device__ __forceinline__ void load4(const float* row, uint32_t e0, uint32_t E,
   }
 }
 
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
 // Probabilities of a row (in place) and its logarithm of the sum of
 // exponentials. A row of -infinity alone gives zeros; NaN stays NaN.
 template <int L>
 __device__ __forceinline__ float softmax_row(float (&v)[4]) {
-  const float top = group_max<L>(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+  const float top = lanes_max<L>(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
   const float m = top == -INFINITY ? 0.f : top;
   float s = 0.f;
 #pragma unroll
@@ -83,32 +71,39 @@ __device__ __forceinline__ float softmax_row(float (&v)[4]) {
     v[j] = expf(v[j] - m);
     s += v[j];
   }
-  s = group_sum<L>(s);
+  s = lanes_sum<L>(s);
   const float inv = s == 0.f ? 0.f : 1.0f / s;
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] *= inv;
   return s == 0.f ? 0.f : m + logf(s);
 }
 
-// The losses from whole sums; all threads of the workgroup (kThreads or more)
-// call it, thread e holding expert e's sums. red: kThreads doubles.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// The losses from whole sums; all threads of the workgroup call it, thread e
+// holding expert e's sums. red: kRed / 64 doubles.
 __device__ __forceinline__ void finish(const BalanceArgs& a, double p, int c, double z, int n, double* red) {
   const uint32_t t = threadIdx.x;
   const double inv = n > 0 ? 1.0 / n : 0.0;
   const double mean = p * inv;
-  if (t < (uint32_t)kThreads) red[t] = t < a.E ? (double)c * mean : 0.0;
-  __syncthreads();
-  for (uint32_t m = kThreads / 2; m > 0; m >>= 1) {
-    if (t < m) red[t] += red[t + m];
-    __syncthreads();
+  if (t < (uint32_t)kRed) {  // whole waves
+    const double s = wave_sum(t < a.E ? (double)c * mean : 0.0);
+    if (t % 64 == 0) red[t / 64] = s;
   }
+  __syncthreads();
   if (t < a.E) {
     a.counts[t] = c;
     if (a.prob_mean) a.prob_mean[t] = (float)mean;
   }
   if (t == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kRed / 64; ++w) s += red[w];
     a.counts[a.E] = n;
-    a.loss[0] = (float)((double)a.balance_coef * a.E * red[0] * inv / a.k);
+    a.loss[0] = (float)((double)a.balance_coef * a.E * s * inv / a.k);
     a.loss[1] = (float)((double)a.z_coef * z * inv);
   }
 }
@@ -123,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   __shared__ int s_cnt[kMaxBalanceExperts + 1];
   __shared__ float s_p[kThreads / 64][4 * L];
   __shared__ float s_z[kThreads / 64];
-  __shared__ double s_red[kLast ? kThreads : 1];
+  __shared__ double s_red[kRed / 64];
   const uint32_t tid = threadIdx.x, lane = tid % L, grp = tid / L;
   for (uint32_t i = tid; i <= a.E; i += kThreads) s_cnt[i] = 0;
   __syncthreads();
@@ -164,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     for (int m = L; m < 64; m <<= 1) p[j] += __shfl_xor(p[j], m);
-  for (int m = 1; m < 64; m <<= 1) z += __shfl_xor(z, m);
+  z = lanes_sum<64>(z);
   const uint32_t w = tid / 64, l = tid % 64;
   if (l < L)
 #pragma unroll
@@ -179,68 +174,93 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   if (kLast) {
     finish(a, (double)sp, tid < a.E ? s_cnt[tid] : 0, (double)sz, s_cnt[a.E], s_red);
   } else {
-    if (tid < a.E) a.part_p[blockIdx.x * a.E + tid] = sp;
-    for (uint32_t i = tid; i <= a.E; i += kThreads) a.part_c[blockIdx.x * (a.E + 1) + i] = s_cnt[i];
-    if (tid == 0) a.part_z[blockIdx.x] = sz;
+    uint2* part = a.part + (uint64_t)blockIdx.x * (a.E + 1);
+    if (tid <= a.E) part[tid] = uint2{__builtin_bit_cast(uint32_t, tid < a.E ? sp : sz), (uint32_t)s_cnt[tid]};
   }
 }
 
-// Joins the partial sums: thread (r, e) adds every R-th partial of expert e
-// in double, then the R slices are added in order.
-__global__ __launch_bounds__(1024) void k_balance_join(BalanceArgs a) {
-  __shared__ double s_p[1024];
-  __shared__ int s_c[1024];
-  __shared__ double s_z[kThreads];
-  __shared__ int s_n[kThreads];
-  __shared__ double s_red[kThreads];
-  const uint32_t tid = threadIdx.x;
-  const uint32_t W = a.E <= 64 ? 64 : 256, R = 1024 / W;
-  const uint32_t e = tid % W, r = tid / W;
-  double p = 0.0;
+// Joins the partial sums: thread (r, e) adds every R-th partial of column e,
+// then the R slices are added in order; the last column goes to 16 threads.
+// 16 loads of a thread in flight and no branch between them: the kernel is a
+// few memory latencies long, whatever it adds.
+__device__ __forceinline__ void add_parts(const BalanceArgs& a, uint32_t e, uint32_t i0, uint32_t step, float& p, int& c) {
+  uint2 v[16];
+#pragma unroll
+  for (uint32_t q = 0; q < 16; ++q) v[q] = a.part[min(i0 + q * step, a.parts - 1) * (a.E + 1) + e];
+#pragma unroll
+  for (uint32_t q = 0; q < 16; ++q) {
+    const bool in = i0 + q * step < a.parts;
+    p += in ? __builtin_bit_cast(float, v[q].x) : 0.f;
+    c += in ? (int)v[q].y : 0;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs a) {
+  static_assert(kParts == 256, "16 slices of 16 partial sums, or 4 of 64");
+  __shared__ float s_p[kThreads], s_z[16];
+  __shared__ int s_c[kThreads], s_n[16];
+  __shared__ double s_red[kRed / 64];
+  const uint32_t tid = threadIdx.x, W = a.E <= 64 ? 64 : 256, R = kThreads / W;
+  float p = 0.f;
   int c = 0;
-  if (e < a.E)
-    for (uint32_t i = r; i < a.parts; i += R) {
-      p += (double)a.part_p[i * a.E + e];
-      c += a.part_c[i * (a.E + 1) + e];
-    }
+  for (uint32_t i = 0; i < kParts / R; i += 16) add_parts(a, min(tid % W, a.E), tid / W + i * R, R, p, c);
   s_p[tid] = p;
   s_c[tid] = c;
-  if (tid < kThreads) {
-    double z = 0.0;
-    int n = 0;
-    for (uint32_t i = tid; i < a.parts; i += kThreads) {
-      z += (double)a.part_z[i];
-      n += a.part_c[i * (a.E + 1) + a.E];
-    }
-    s_z[tid] = z;
-    s_n[tid] = n;
+  if (tid < 16) {
+    p = 0.f;
+    c = 0;
+    add_parts(a, a.E, tid, 16, p, c);
+    s_z[tid] = p;
+    s_n[tid] = c;
   }
   __syncthreads();
-  for (uint32_t m = kThreads / 2; m > 0; m >>= 1) {
-    if (tid < m) {
-      s_z[tid] += s_z[tid + m];
-      s_n[tid] += s_n[tid + m];
-    }
-    __syncthreads();
-  }
-  p = 0.0;
-  c = 0;
+  double sum = 0.0, z = 0.0;
+  int count = 0, n = 0;
   if (tid < a.E)
     for (uint32_t i = 0; i < R; ++i) {
-      p += s_p[i * W + tid];
-      c += s_c[i * W + tid];
+      sum += (double)s_p[i * W + tid];
+      count += s_c[i * W + tid];
     }
-  finish(a, p, c, s_z[0], s_n[0], s_red);
+  for (uint32_t i = 0; i < 16; ++i) {
+    z += (double)s_z[i];
+    n += s_n[i];
+  }
+  finish(a, sum, count, z, n, s_red);
 }
 
-// The gradient of the logits, one row per group. The counts enter centred on
-// their mean k n / E, a difference of whole numbers (the probabilities sum to one,
-// so a common part has no gradient): nearly even loads lose nothing in
-// c_e - sum_j c_j p_j.
-template <int L, bool kVec>
-__global__ __launch_bounds__(kThreads) void k_router_grad(BalanceArgs a) {
-  constexpr uint32_t G = kThreads / L;
+// The gradient of the logits, kRows rows per group in flight. The counts enter centred on
+// their mean k n / E, a difference of whole numbers (the probabilities sum to
+// one, so a common part has no gradient): nearly even loads lose nothing in
+// c_e - sum_j c_j p_j. A row's gates are loaded by its group's first k lanes and
+// handed round.
+template <int L, bool kVec, uint32_t kRows>
+__global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
+  constexpr uint32_t G = kGradThreads / L, S = L < 8 ? L : 8;  // lanes that hold gates
+  constexpr uint32_t kOf = 8 / S;                              // gates of such a lane
   const uint32_t tid = threadIdx.x, lane = tid % L, grp = tid / L;
+  const uint32_t t0 = blockIdx.x * G * kRows + grp;
+  float v[kRows][4], g[kRows][kOf], dg[kRows][kOf];
+  uint32_t ex[kRows][kOf];
+  bool ok[kRows];
+#pragma unroll
+  for (uint32_t u = 0; u < kRows; ++u) {
+    const uint32_t t = min(t0 + u * G, a.tokens - 1);
+    load4<kVec>(a.logits + (uint64_t)t * a.E, lane * 4, a.E, v[u]);
+    ok[u] = true;
+  }
+  if (a.gates)  // uniform
+#pragma unroll
+    for (uint32_t u = 0; u < kRows; ++u)
+#pragma unroll
+      for (uint32_t q = 0; q < kOf; ++q) {
+        const uint64_t o = (uint64_t)min(t0 + u * G, a.tokens - 1) * a.k + min(lane * kOf + q, a.k - 1);
+        g[u][q] = a.gates[o];
+        dg[u][q] = a.dgates[o];
+        ex[u][q] = (uint32_t)a.experts[o];
+      }
+  if (a.valid)  // uniform
+#pragma unroll
+    for (uint32_t u = 0; u < kRows; ++u) ok[u] = a.valid[min(t0 + u * G, a.tokens - 1)];
   const int n = a.counts[a.E];
   const float inv = n > 0 ? 1.0f / (float)n : 0.f;
   const float u0 = a.grad_loss ? a.grad_loss[0] : 1.f, u1 = a.grad_loss ? a.grad_loss[1] : 1.f;
@@ -251,44 +271,53 @@ __global__ __launch_bounds__(kThreads) void k_router_grad(BalanceArgs a) {
     const uint32_t e = lane * 4 + j;
     c[j] = e < a.E ? (float)((int64_t)a.counts[e] * a.E - (int64_t)a.k * n) * (inv / (float)a.E) : 0.f;
   }
-  const uint32_t t = blockIdx.x * G + grp;
-  if (t >= a.tokens) return;  // whole groups leave: the exchanges below stay inside a group
-  float v[4];
-  load4<kVec>(a.logits + (uint64_t)t * a.E, lane * 4, a.E, v);
-  const bool ok = !a.valid || a.valid[t];
-  const float lse = softmax_row<L>(v);
-  const float mean = group_sum<L>(fmaf(c[0], v[0], fmaf(c[1], v[1], fmaf(c[2], v[2], c[3] * v[3]))));
-  float o[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = v[j] * fmaf(cb, c[j] - mean, cz * lse);
-  if (a.gates) {
-    const float* g = a.gates + (uint64_t)t * a.k;
-    const float* dg = a.dgates + (uint64_t)t * a.k;
-    const int32_t* ex = a.experts + (uint64_t)t * a.k;
-    float dot = 0.f;
-    for (uint32_t s = 0; s < a.k; ++s) dot = fmaf(g[s], dg[s], dot);
-    for (uint32_t s = 0; s < a.k; ++s) {
-      const uint32_t e = (uint32_t)ex[s] - lane * 4;
-      const float part = g[s] * (dg[s] - dot);
+  for (uint32_t u = 0; u < kRows; ++u) {
+    const uint32_t t = t0 + u * G;
+    const float lse = softmax_row<L>(v[u]);
+    const float mean = lanes_sum<L>(fmaf(c[0], v[u][0], fmaf(c[1], v[u][1], fmaf(c[2], v[u][2], c[3] * v[u][3]))));
+    float o[4];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j)
-        if (e == j) o[j] += part;
+    for (int j = 0; j < 4; ++j) o[j] = v[u][j] * fmaf(cb, c[j] - mean, cz * lse);
+    if (a.gates) {  // uniform
+      float dot = 0.f, part[kOf];
+#pragma unroll
+      for (uint32_t q = 0; q < kOf; ++q)
+        if (lane * kOf + q < a.k) dot = fmaf(g[u][q], dg[u][q], dot);
+      dot = lanes_sum<S>(dot);
+#pragma unroll
+      for (uint32_t q = 0; q < kOf; ++q) part[q] = g[u][q] * (dg[u][q] - dot);
+      for (uint32_t s = 0; s < a.k; ++s) {
+        const int from = (int)(tid % 64 - lane + s / kOf);
+        float p = part[0];
+        uint32_t e = ex[u][0];
+        if (kOf > 1 && s % kOf) {
+          p = part[kOf - 1];
+          e = ex[u][kOf - 1];
+        }
+        p = __shfl(p, from);
+        e = (uint32_t)__shfl((int)e, from) - lane * 4;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j)
+          if (e == j) o[j] += p;
+      }
     }
-  }
-  float* out = a.dlogits + (uint64_t)t * a.E;
-  if (kVec) {
-    typedef __attribute__((ext_vector_type(4))) float f32x4;
-    const f32x4 q = {ok ? o[0] : 0.f, ok ? o[1] : 0.f, ok ? o[2] : 0.f, ok ? o[3] : 0.f};
-    if (lane * 4 < a.E) *reinterpret_cast<f32x4*>(out + lane * 4) = q;
-  } else {
+    if (t >= a.tokens) continue;
+    float* out = a.dlogits + (uint64_t)t * a.E;
+    if (kVec) {
+      typedef __attribute__((ext_vector_type(4))) float f32x4;
+      const f32x4 q = {ok[u] ? o[0] : 0.f, ok[u] ? o[1] : 0.f, ok[u] ? o[2] : 0.f, ok[u] ? o[3] : 0.f};
+      if (lane * 4 < a.E) *reinterpret_cast<f32x4*>(out + lane * 4) = q;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane * 4 + j < a.E) out[lane * 4 + j] = ok ? o[j] : 0.f;
+      for (int j = 0; j < 4; ++j)
+        if (lane * 4 + j < a.E) out[lane * 4 + j] = ok[u] ? o[j] : 0.f;
+    }
   }
 }
 
 struct BalanceLayout {
-  size_t p = 0, c = 0, z = 0, total = 0;
+  size_t total = 0;
   uint32_t parts = 0;  // 1: one workgroup, no partial sums
 };
 
@@ -299,11 +328,7 @@ BalanceLayout balance_layout(const pw_balance_desc& d) {
   const uint32_t rows = kThreads / group_lanes(d.num_experts) * kRows;
   const uint64_t blocks = (d.tokens + rows - 1) / rows;
   l.parts = d.tokens <= kAlone ? 1u : (uint32_t)std::min<uint64_t>(blocks, kParts);
-  if (l.parts <= 1) return l;
-  l.p = 0;
-  l.c = up256((size_t)l.parts * d.num_experts * 4);
-  l.z = l.c + up256((size_t)l.parts * (d.num_experts + 1) * 4);
-  l.total = l.z + up256((size_t)l.parts * 4);
+  if (l.parts > 1) l.total = up256((size_t)l.parts * (d.num_experts + 1) * sizeof(uint2));
   return l;
 }
 
@@ -350,8 +375,10 @@ void launch_balance(const BalanceArgs& a, hipStream_t s) {
 
 template <int L, bool kVec>
 void launch_grad(const BalanceArgs& a, hipStream_t s) {
-  constexpr uint32_t G = kThreads / L;
-  hipLaunchKernelGGL((k_router_grad<L, kVec>), dim3((a.tokens + G - 1) / G), dim3(kThreads), 0, s, a);
+  constexpr uint32_t G = kGradThreads / L;
+  const uint32_t groups = (a.tokens + G - 1) / G;
+  if (groups <= kGradWide) hipLaunchKernelGGL((k_router_grad<L, kVec, 1>), dim3(groups), dim3(kGradThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_router_grad<L, kVec, 4>), dim3((groups + 3) / 4), dim3(kGradThreads), 0, s, a);
 }
 
 #define PW_BY_EXPERTS(fn, a, vec, s)                                \
@@ -389,19 +416,14 @@ extern "C" int pw_router_balance(const pw_balance_desc* d, const pw_balance_io* 
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = check_stream(s))) return st;
   BalanceArgs a = args(*d, *io);
-  unsigned char* base = static_cast<unsigned char*>(ws);
   a.parts = l.parts;
-  if (l.parts > 1) {
-    a.part_p = reinterpret_cast<float*>(base + l.p);
-    a.part_c = reinterpret_cast<int32_t*>(base + l.c);
-    a.part_z = reinterpret_cast<float*>(base + l.z);
-  }
+  a.part = static_cast<uint2*>(ws);
   const bool vec = a.E % 4 == 0 && (uintptr_t)a.logits % 16 == 0;
   PW_BY_EXPERTS(launch_balance, a, vec, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e, "launch balance");
   if (l.parts > 1) {
-    hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(kThreads), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch balance_join");
   }
   return PW_OK;

@@ -149,12 +149,10 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
         }
     }
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-#pragma unroll
-      for (int k = 0; k < kTokens; ++k) {
-        dot[k][0] += __shfl_xor(dot[k][0], m);
-        dot[k][1] += __shfl_xor(dot[k][1], m);
-      }
+    for (int k = 0; k < kTokens; ++k) {
+      dot[k][0] = lanes_sum<64>(dot[k][0]);
+      dot[k][1] = lanes_sum<64>(dot[k][1]);
+    }
 #pragma unroll
     for (int k = 0; k < kTokens; ++k)
       if (lane == 0 && t0 + k < a.tokens) {

@@ -115,9 +115,7 @@ struct Exchange {
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint32_t& turn) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
+  for (int i = 0; i < N; ++i) v[i] = lanes_sum<64>(v[i]);
   if constexpr (TEAM > 64) {
     constexpr int W = TEAM / 64;
     auto& sums = x.sums[turn];
@@ -128,11 +126,7 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint3
     __syncthreads();
     const int w = threadIdx.x / TEAM * W + threadIdx.x % W;  // each lane a wave's sums, then across W lanes
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = sums[w][i];
-#pragma unroll
-    for (int m = 1; m < W; m <<= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], m);
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<W>(sums[w][i]);
   }
 }
 

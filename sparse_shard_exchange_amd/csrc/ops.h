@@ -9,6 +9,29 @@
 
 namespace pw {
 
+// The value of the lane that differs in bit M of its number, once the lanes
+// below have been joined (all lanes of an aligned group of M agree): quad
+// permutes and row mirrors inside 16 lanes, an LDS exchange beyond. All lanes of
+// the aligned group of 2 M are active.
+template <int M>
+__device__ __forceinline__ float across(float v) {
+  if constexpr (M >= 16) return __shfl_xor(v, M);
+  constexpr int ctrl = M == 1 ? 0xB1 : M == 2 ? 0x4E : M == 4 ? 0x141 : 0x140;
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xf, 0xf, true));
+}
+
+// Sum over each aligned group of L lanes; every lane gets it.
+template <int L, int M = 1>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (M < L) return lanes_sum<L, 2 * M>(v + across<M>(v));
+  return v;
+}
+template <int L, int M = 1>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (M < L) return lanes_max<L, 2 * M>(fmaxf(v, across<M>(v)));
+  return v;
+}
+
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // The caller's workspace holds `need` bytes (need 0: none is looked at).
