@@ -9,7 +9,9 @@
 // Both kernels read each logit once: a token's row is spread over a group of
 // L lanes of 4 experts each (L = 4, 16, 64 for E <= 16, 64, 256), so a wave's
 // load covers 64 / L whole rows, and the row's maximum, sum and dot product
-// are lane exchanges inside the group.
+// are lane exchanges inside the group. 131072 x 64: loss 13.7 + 4.4 us, bound by
+// reading (35 MB, 2.5 TB/s, of which the first and last loads' latency is half),
+// gradient 20 us (70 MB, 3.5 TB/s). 48 x 8: 4.2 us, a few memory latencies.
 #include "ops.h"
 
 #include <algorithm>
@@ -23,9 +25,14 @@ constexpr int kGradThreads = 256;  // k_router_grad
 constexpr uint32_t kMaxBalanceExperts = 256;
 constexpr int kRed = 256;          // threads of the loss' last sum: one per expert
 constexpr uint32_t kParts = 256;        // partial sums at most: a workgroup of 16 waves per CU
-constexpr uint32_t kAlone = 2048;       // tokens up to which one workgroup does all
-constexpr uint32_t kRows = 4;           // rows of a group in flight
-constexpr uint32_t kGradWide = 2048;    // workgroups up to which k_router_grad takes one row a group
+// Rows of a group up to which one workgroup does all, in one launch (E = 64, 512
+// tokens: 9.5 us against 10.7 for two launches; 1024 tokens: 16.0 against 10.7;
+// E = 8 and 256 cross over at the same count of 8 rows).
+constexpr uint32_t kAlone = 8;
+constexpr uint32_t rows_of(bool last) { return last ? 2 : 4; }  // rows of a group of k_balance in flight
+// Workgroups up to which k_router_grad takes one row a group (999 x 5: 5.8 us
+// against 8.6 with 4; 131072 x 64, 8192 workgroups: 24.7 us against 20).
+constexpr uint32_t kGradWide = 2048;
 
 struct BalanceArgs {
   const float* logits;
@@ -114,7 +121,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, double p, int c, do
 // kLast the one workgroup writes the results, else its partial sums.
 template <int L, bool kVec, bool kLast>
 __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
-  constexpr uint32_t G = kThreads / L;  // groups: rows of one pass
+  constexpr uint32_t G = kThreads / L, kRows = rows_of(kLast);  // groups: rows of one pass
   __shared__ int s_cnt[kMaxBalanceExperts + 1];
   __shared__ float s_p[kThreads / 64][4 * L];
   __shared__ float s_z[kThreads / 64];
@@ -325,9 +332,9 @@ int group_lanes(uint32_t E) { return E <= 16 ? 4 : E <= 64 ? 16 : 64; }
 
 BalanceLayout balance_layout(const pw_balance_desc& d) {
   BalanceLayout l;
-  const uint32_t rows = kThreads / group_lanes(d.num_experts) * kRows;
+  const uint32_t G = kThreads / group_lanes(d.num_experts), rows = G * rows_of(false);
   const uint64_t blocks = (d.tokens + rows - 1) / rows;
-  l.parts = d.tokens <= kAlone ? 1u : (uint32_t)std::min<uint64_t>(blocks, kParts);
+  l.parts = d.tokens <= kAlone * G ? 1u : (uint32_t)std::min<uint64_t>(blocks, kParts);
   if (l.parts > 1) l.total = up256((size_t)l.parts * (d.num_experts + 1) * sizeof(uint2));
   return l;
 }

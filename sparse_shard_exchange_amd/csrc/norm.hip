@@ -397,7 +397,7 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a) {
   if ((what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;
   float v = 0.f;
   if (col < a.d)
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t i = slice; i < n; i += 16) v += part[(uint64_t)i * a.d + col];
   s[slice][c] = v;
   __syncthreads();
