@@ -417,7 +417,7 @@ int pw_plan_reset_times(pw_plan_t plan);
  *   prob_mean[e] = 1/n sum_t p[t][e]
  *   loss[0]      = balance_coef E sum_e counts[e] / (k n) prob_mean[e]
  *   loss[1]      = z_coef / n sum_t (log sum_e exp logits[t][e])^2
- * and zeros if n == 0. Tokens with valid[t] == 0 are not looked at. An expert
+ * and zeros if n == 0 (loss[1] also if z_coef is). Tokens with valid[t] == 0 are not looked at. An expert
  * id outside [0, E) is no tuple. A token whose logits are all -infinity has
  * zero probabilities and a zero logarithm. */
 typedef struct {
@@ -505,7 +505,8 @@ int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch_grad_io* i
  * with gate [gates][d], each row shared by rows / gates consecutive rows.
  * Parts that are NULL drop out: y (r = x_scale x), w_y (y as it is), gate
  * (ones), w_r with h (no next norm). Intermediate values stay fp32; r and h
- * are each rounded once (h is the norm of r before its rounding). */
+ * are each rounded once (h is the norm of r before its rounding). The gradient
+ * takes r as it was stored. */
 typedef struct {
   uint64_t rows;     /* at most 2^31 - 1; a multiple of gates                   */
   uint32_t d;        /* 1..8192                                                 */

@@ -16,7 +16,7 @@ import os
 # of that runtime under the same soname. Loaded after torch, our dependency
 # resolves to torch's copy; loaded before, the process would end up with two
 # HIP runtimes, and ours would find no device once torch's had claimed it.
-import torch  # noqa: F401  (load order only)
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpw.so")
@@ -536,46 +536,46 @@ def _address(t):
 class _Operator:
     """What the plan-less operators share: the device, the workspace, checked
     arguments, and output buffers, made by the first call that needs them and
-    kept (so every call returns the same tensors; make one call before
-    capturing a HIP graph). Calls of one object share its buffers: order them."""
+    kept (so every call returns the same tensors; a call that would make them
+    under HIP graph capture is refused: make one call before). Calls of one
+    object share its buffers: order them."""
 
     def __init__(self, device):
-        import torch
         dev = torch.device(device)
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self._index = self.device.index
         self._buffers = {}
-        self._ws = None
+        self._ws_args = (None, 0)  # address and bytes of the workspace
 
     def _buf(self, name, shape, dtype):
-        import torch
         b = self._buffers.get(name)
         if b is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise PwError(PW_ERR_STATE, f"the buffer for {name} is made by the first call: make it before capturing")
             b = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.device)
         return b
 
     def _workspace(self, sizer, d):
-        import torch
         need = C.c_size_t(0)
         check(sizer(C.byref(d), C.byref(need)))
-        if need.value and (self._ws is None or self._ws.numel() < need.value):
+        if need.value:
             self._ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+            self._ws_args = (self._ws.data_ptr(), need.value)
 
-    def _arg(self, name, t, shape, *dtypes):
+    def _arg(self, name, t, shape, dtype, or_dtype=None):
         """The address of a tensor that must be contiguous, on this device, of
-        this shape and of one of these types; None stays None."""
+        this shape and type; None stays None."""
         if t is None:
             return None
-        if (t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != self._index):
-            raise PwError(PW_ERR_INVALID, f"{name} must be a contiguous {' or '.join(str(x) for x in dtypes)} tensor of shape "
-                                          f"{shape} on {self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return _address(t)
+        if (t.shape == shape and (t.dtype is dtype or t.dtype is or_dtype) and t.is_contiguous()
+                and t.get_device() == self._index):
+            return t.data_ptr() or 256  # (see _address)
+        raise PwError(PW_ERR_INVALID, f"{name} must be a contiguous {dtype} tensor of shape {shape} on {self.device}, "
+                                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _run(self, fn, d, io, stream, ws=False):
-        import torch
-        args = (C.c_void_p(self._ws.data_ptr()) if self._ws is not None else None,
-                self._ws.numel() if self._ws is not None else 0) if ws else ()
-        s = C.c_void_p((stream if stream is not None else torch.cuda.current_stream(self._index)).cuda_stream)
+        args = self._ws_args if ws else ()
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
         if torch.cuda.current_device() == self._index:
             check(fn(C.byref(d), C.byref(io), *args, s))
         else:
@@ -597,7 +597,6 @@ class RouterBalance(_Operator):
         self._workspace(lib.pw_router_balance_workspace, self.desc)
 
     def _io(self, logits, experts, valid):
-        import torch
         io = pw_balance_io()
         io.logits = self._arg("logits", logits, (self.T, self.E), torch.float32)
         io.experts = self._arg("experts", experts, (self.T, self.k), torch.int32)
@@ -607,7 +606,6 @@ class RouterBalance(_Operator):
     def loss(self, logits, experts, valid=None, stream=None):
         """(counts [E + 1] int32: tuples per expert, then tokens counted;
         prob_mean [E]; loss [2]: balance, z)."""
-        import torch
         io = self._io(logits, experts, valid)
         counts = self._buf("counts", (self.E + 1,), torch.int32)
         mean = self._buf("prob_mean", (self.E,), torch.float32)
@@ -620,7 +618,6 @@ class RouterBalance(_Operator):
     def grad(self, logits, experts=None, counts=None, gates=None, dgates=None, valid=None, grad_loss=None, stream=None):
         """dlogits [tokens][E]: of both losses (grad_loss [2], None: ones; counts
         None: those of the last loss() call) and of the gates, if given."""
-        import torch
         io = self._io(logits, experts, valid)
         if counts is None:
             counts = self._counts
@@ -660,7 +657,6 @@ class MoEGrad(_Operator):
         """(dy like y, dgates [tokens][2] fp32, slot_of [tokens][2] int32) from
         the step's y, gates, src_index and offsets. Rows of dy behind
         offsets[E] are left as they are; dy=None: a kept buffer."""
-        import torch
         n = self._rows(y)
         bf = torch.bfloat16
         if dy is None:
@@ -685,7 +681,6 @@ class MoEGrad(_Operator):
     def dispatch(self, dxd, dlogits, w_router, x=None, slot_of=None, valid=None, stream=None):
         """(dx [tokens][d] bf16, dw_router [d][E] fp32); slot_of None: that of
         the last combine() call; x None: dx alone (dw_router None)."""
-        import torch
         n = self._rows(dxd)
         bf = torch.bfloat16
         if slot_of is None:
@@ -713,7 +708,6 @@ class BlockNorm(_Operator):
     gate rows, each for rows / gates consecutive rows (0: no gate)."""
 
     def __init__(self, rows, d, dtype=PW_BF16, gates=0, x_scale=1.0, y_scale=1.0, eps=1e-6, device="cuda"):
-        import torch
         super().__init__(device)
         self.T, self.d, self.G = rows, d, gates
         self.dtype = torch.float32 if dtype == PW_F32 else torch.bfloat16
@@ -748,7 +742,6 @@ class BlockNorm(_Operator):
         where their part is; r: forward's r (with y None: x_scale x). valid
         [rows] bool or uint8: other rows get zeros and add nothing to the
         weights' gradients. dx may be given (dr itself, to update it in place)."""
-        import torch
         rows, f32 = (self.T, self.d), torch.float32
         io = self._io(y, w_y, gate, w_r)
         io.r = self._arg("r", r, rows, self.dtype)

@@ -111,7 +111,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, double p, int c, do
     for (int w = 0; w < kRed / 64; ++w) s += red[w];
     a.counts[a.E] = n;
     a.loss[0] = (float)((double)a.balance_coef * a.E * s * inv / a.k);
-    a.loss[1] = (float)((double)a.z_coef * z * inv);
+    a.loss[1] = a.z_coef == 0.f ? 0.f : (float)((double)a.z_coef * z * inv);  // (z may have overflowed)
   }
 }
 

@@ -72,8 +72,8 @@ __global__ __launch_bounds__(1024) void k_slots_alone(CombineGradArgs a) {
   for (uint64_t i = threadIdx.x; i < n; i += 1024) put_slot(a, i);
 }
 __global__ __launch_bounds__(256) void k_slots_clear(CombineGradArgs a) {
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i < 2 * a.tokens) a.slot_of[i] = -1;
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x;
+  if (t < a.tokens) reinterpret_cast<int2*>(a.slot_of)[t] = int2{-1, -1};
 }
 __global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
   const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
@@ -513,7 +513,7 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
     hipLaunchKernelGGL(k_slots_alone, dim3(1), dim3(1024), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots");
   } else {
-    hipLaunchKernelGGL(k_slots_clear, dim3((2 * a.tokens + 255) / 256), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_slots_clear, dim3((a.tokens + 255) / 256), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_clear");
     if (a.rows) {
       hipLaunchKernelGGL(k_slots_put, dim3((uint32_t)((a.rows + 255) / 256)), dim3(256), 0, s, a);
