@@ -52,6 +52,21 @@ struct DispatchGradArgs {
   bool whole_w;        // rows of w are whole aligned chunks of 8 experts
 };
 
+// Row loads bypass the caches (kStream) where the call's rows are twice the
+// last-level cache (256 MiB) or more, so that none can still be there: combine,
+// 131072 tokens x 1024, 271 us against 276 with plain loads, dispatch 233
+// against 239; below, rows that the caches hold are read from them (16384
+// tokens: combine 31 us against 37, dispatch 45 against 55). Rows are always
+// stored nontemporally: written plainly, they are written back during the reads
+// of the next kernel (dW after dx: 72 us against 81).
+constexpr uint64_t kStreamBytes = 512ull << 20;
+
+template <bool kStream, typename V>
+__device__ __forceinline__ V load_row(const V* p) {
+  if constexpr (kStream) return __builtin_nontemporal_load(p);
+  return *p;
+}
+
 // ---- slot_of: the inverse of src_index ---------------------------------------
 
 // Up to kSlotsInside tuples the combine's kernel inverts the index itself: each
@@ -83,7 +98,7 @@ __global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
 constexpr uint32_t kCombineBlocks = 2048;
 constexpr int kTokens = 2;
 
-template <bool kInside>  // the slots of the workgroup's 4 kTokens tokens are found here (one pass)
+template <bool kInside, bool kStream>  // kInside: the slots of the workgroup's 4 kTokens tokens are found here (one pass)
 __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
   __shared__ int own[kInside ? 8 * kTokens : 1];
   if (kInside) {
@@ -130,10 +145,10 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t ch = min(c0 + lane + 64 * c, nch - 1);
-          vo[k][c] = __builtin_nontemporal_load(dout + (uint64_t)min(t0 + k, a.tokens - 1) * nch + ch);
+          vo[k][c] = load_row<kStream>(dout + (uint64_t)min(t0 + k, a.tokens - 1) * nch + ch);
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (a.rows) vy[k][s][c] = __builtin_nontemporal_load(y + (uint64_t)max(slot[k][s], 0) * nch + ch);
+            if (a.rows) vy[k][s][c] = load_row<kStream>(y + (uint64_t)max(slot[k][s], 0) * nch + ch);
         }
 #pragma unroll
       for (int k = 0; k < kTokens; ++k)
@@ -184,7 +199,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
 // contiguous bytes a row. dl is split into two bf16 terms (hi + lo, at most
 // 2^-16 of the value is lost, below the rounding of dx to bf16 at 2^-8), so
 // the products are as exact as dx can show. 131072 tokens x 1024, 64 experts:
-// 159 us, 5.1 TB/s, the rate of a large copy; bound by HBM. (W in registers,
+// 155 us, 5.2 TB/s, the rate of a large copy; bound by HBM. (W in registers,
 // 128 columns a wave, 8 waves per CU: 223 us; one token a lane, 64 bytes of
 // its row: 306 us.)
 constexpr uint32_t kDxThreads = 1024;
@@ -208,7 +223,7 @@ __device__ __forceinline__ bf16x8 load_w(const DispatchGradArgs& a, uint32_t c, 
   return v;
 }
 
-template <int KS, bool kVec>  // steps of 32 experts; whole aligned 16-byte chunks of a row of dl
+template <int KS, bool kVec, bool kStream>  // steps of 32 experts; whole aligned 16-byte chunks of a row of dl
 __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a) {
   extern __shared__ __attribute__((aligned(16))) bf16x8 lds_w[];  // [column block][b][s][64 lanes]
   const uint32_t lane = threadIdx.x & 63, i = lane & 15, h = lane >> 4;
@@ -269,7 +284,8 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) g[s][r] = *reinterpret_cast<const bf16x8*>(src[s][r] + cb * kDxCols);
+          for (int s = 0; s < 2; ++s) 
+            g[s][r] = load_row<kStream>(reinterpret_cast<const bf16x8*>(src[s][r] + cb * kDxCols));
       f32x4 acc[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -292,7 +308,8 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
           f += have1 ? (float)g[1][r][b] : 0.f;
           o[b] = (__bf16)(padding ? 0.f : f);
         }
-        if (tile * kDxTokens + 4 * h + r < a.tokens) *reinterpret_cast<bf16x8*>(out + (uint64_t)r * a.d + cb * kDxCols) = o;
+        if (tile * kDxTokens + 4 * h + r < a.tokens)
+          __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(out + (uint64_t)r * a.d + cb * kDxCols));
       }
     }
   }
@@ -306,15 +323,16 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 // terms, which hold all 24 bits of it: every product is exact and the sums
 // are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
 // of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
-// 131072 tokens x 1024, 64 experts: 80 us, 3.8 TB/s of reads, what sums and
-// maxima over 1 GiB reach; bound by reading x and dl once from HBM. (Sharing the split terms between the waves
+// 131072 tokens x 1024, 64 experts: 72 us, 4.2 TB/s; bound by reading x and dl
+// once from HBM. (Sharing the split terms between the waves
 // through LDS, and requesting x two steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
+constexpr int kNontemporal = 2;  // nt in the cache-policy operand of buffer instructions
 constexpr uint32_t kDwMaxTokens = 1u << 19;  // of a range: its rows of x (at most 2560 bytes) are one buffer
 constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, and below 2^32 with all that is added
 
-template <int NC>  // expert blocks of 32
+template <int NC, bool kStream>  // expert blocks of 32
 __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   extern __shared__ float lds[];  // [kDwCols][32 NC]
   constexpr uint32_t Ep = 32 * NC;
@@ -347,7 +365,7 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   auto fetch = [&](Step& s, uint32_t t) {  // tokens t + 16 tw + 8 h + j of the range
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      s.v[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(xb, xoff + (t + j) * xrow, 0, 0));
+      s.v[j] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(xb, xoff + (t + j) * xrow, 0, kStream ? kNontemporal : 0));
 #pragma unroll
       for (int c = 0; c < NC; ++c)
         s.dl[c][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(db, doff[c] + (t + j) * drow, 0, 0));
@@ -436,19 +454,24 @@ __global__ __launch_bounds__(256) void k_router_dw_zero(DispatchGradArgs a) {
 
 constexpr size_t kDefaultLds = 64 << 10;  // what a kernel may use without asking
 
-template <int KS, bool kVec>
+template <int KS, bool kVec, bool kStream>
 hipError_t launch_dx_steps(const DispatchGradArgs& a, uint32_t grid, hipStream_t s) {
   const size_t lds = (size_t)a.d / a.col_groups * KS * 64;
   if (lds > kDefaultLds) {
-    const hipError_t e = hipFuncSetAttribute((const void*)k_dispatch_grad<KS, kVec>,
+    const hipError_t e = hipFuncSetAttribute((const void*)k_dispatch_grad<KS, kVec, kStream>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_dispatch_grad<KS, kVec>), dim3(grid), dim3(kDxThreads), lds, s, a);
+  hipLaunchKernelGGL((k_dispatch_grad<KS, kVec, kStream>), dim3(grid), dim3(kDxThreads), lds, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_dx(DispatchGradArgs& a, hipStream_t s) {
+template <int KS, bool kVec>
+hipError_t launch_dx_loads(const DispatchGradArgs& a, uint32_t grid, bool stream, hipStream_t s) {
+  return stream ? launch_dx_steps<KS, kVec, true>(a, grid, s) : launch_dx_steps<KS, kVec, false>(a, grid, s);
+}
+
+hipError_t launch_dx(DispatchGradArgs& a, bool stream, hipStream_t s) {
   const uint32_t tiles = (a.tokens + kDxTokens - 1) / kDxTokens, blocks = a.d / kDxCols;
   // With a tile for every wave of the GPU a workgroup keeps all of W and a wave
   // takes whole rows; below that the column blocks go to different workgroups.
@@ -456,8 +479,8 @@ hipError_t launch_dx(DispatchGradArgs& a, hipStream_t s) {
   const uint32_t grid = std::min(kDxGrid * (a.col_groups > 1 ? 2 : 1) / a.col_groups, (tiles + kDxWaves - 1) / kDxWaves) * a.col_groups;
   a.whole_w = a.E % 8 == 0 && (uintptr_t)a.w % 16 == 0;
   const bool vec = a.E % 4 == 0 && (uintptr_t)a.dlogits % 16 == 0;
-  if (a.E <= 32) return vec ? launch_dx_steps<1, true>(a, grid, s) : launch_dx_steps<1, false>(a, grid, s);
-  return vec ? launch_dx_steps<2, true>(a, grid, s) : launch_dx_steps<2, false>(a, grid, s);
+  if (a.E <= 32) return vec ? launch_dx_loads<1, true>(a, grid, stream, s) : launch_dx_loads<1, false>(a, grid, stream, s);
+  return vec ? launch_dx_loads<2, true>(a, grid, stream, s) : launch_dx_loads<2, false>(a, grid, stream, s);
 }
 
 struct DwLayout {
@@ -527,7 +550,7 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
   hipError_t e;
   const uint32_t per = 4 * kTokens;
   if (2 * a.tokens <= kSlotsInside) {
-    hipLaunchKernelGGL(k_combine_grad<true>, dim3((a.tokens + per - 1) / per), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_combine_grad<true, false>), dim3((a.tokens + per - 1) / per), dim3(256), 0, s, a);
     e = hipGetLastError();
     return e == hipSuccess ? PW_OK : hip_fail(e, "launch combine_grad");
   }
@@ -537,7 +560,11 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
     hipLaunchKernelGGL(k_slots_put, dim3((uint32_t)((a.rows + 255) / 256)), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_put");
   }
-  hipLaunchKernelGGL(k_combine_grad<false>, dim3(std::min((a.tokens + per - 1) / per, kCombineBlocks)), dim3(256), 0, s, a);
+  const dim3 grid(std::min((a.tokens + per - 1) / per, kCombineBlocks));
+  if (((uint64_t)a.tokens + 2 * a.rows) * a.d * 2 >= kStreamBytes)
+    hipLaunchKernelGGL((k_combine_grad<false, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_combine_grad<false, false>), grid, dim3(256), 0, s, a);
   e = hipGetLastError();
   return e == hipSuccess ? PW_OK : hip_fail(e, "launch combine_grad");
 }
@@ -584,6 +611,7 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
   a.E = d->num_experts;
   a.splits = l.splits;
   a.split_tokens = l.split_tokens;
+  const bool stream_rows = ((uint64_t)a.tokens * (a.dw ? 2 : 1) + a.rows) * a.d * 2 >= kStreamBytes;
   hipError_t e;
   if (a.tokens == 0) {
     if (!a.dw) return PW_OK;
@@ -591,14 +619,16 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
     e = hipGetLastError();
     return e == hipSuccess ? PW_OK : hip_fail(e, "launch router_dw_zero");
   }
-  if ((e = launch_dx(a, s)) != hipSuccess) return hip_fail(e, "launch dispatch_grad");
+  if ((e = launch_dx(a, stream_rows, s)) != hipSuccess) return hip_fail(e, "launch dispatch_grad");
   if (!a.dw) return PW_OK;
   const bool two = a.E > 32;
   const uint32_t grid = 8 * (a.d / kDwCols) * ((a.splits + 7) / 8);
   const size_t lds = (size_t)kDwCols * (two ? 64 : 32) * 4;
   static_assert(kDwCols * 64 * 4 <= kDefaultLds, "no larger dynamic LDS to ask for");
-  if (two) hipLaunchKernelGGL(k_router_dw<2>, dim3(grid), dim3(kDwThreads), lds, s, a);
-  else hipLaunchKernelGGL(k_router_dw<1>, dim3(grid), dim3(kDwThreads), lds, s, a);
+  if (two && stream_rows) hipLaunchKernelGGL((k_router_dw<2, true>), dim3(grid), dim3(kDwThreads), lds, s, a);
+  else if (two) hipLaunchKernelGGL((k_router_dw<2, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
+  else if (stream_rows) hipLaunchKernelGGL((k_router_dw<1, true>), dim3(grid), dim3(kDwThreads), lds, s, a);
+  else hipLaunchKernelGGL((k_router_dw<1, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw");
   if (a.splits > 1) {
     const uint32_t jb = a.d * (two ? 64 : 32) / 256;

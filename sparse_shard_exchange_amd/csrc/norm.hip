@@ -15,9 +15,12 @@
 // A row lives in the registers of its team (one wave up to 512 elements, up to
 // 16 waves for the widest) from its only read to its only write, so the passes
 // move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
-// bf16, all parts: forward 204 us (5.3 TB/s), backward 336 + 6 us (4.8 TB/s); a
-// large copy reaches 5.2. (Nontemporal loads and stores: 199 and 325 us, but
-// the next operator reads these rows, where they are small from the caches.)
+// bf16, all parts: forward 198 us (5.4 TB/s), backward 326 + 6 us (4.9 TB/s); a
+// large copy reaches 5.2. Rows are stored nontemporally: written plainly, they
+// are written back during the next operator's reads (forward and backward in
+// turn, 131072 rows 527 us against 542, 32768 rows 126 against 135, 16384 rows,
+// where the last-level cache would hold them, 70 against 67). They are loaded
+// plainly: nontemporal loads take 3% less at 131072 rows, 10% more below 65536.
 #include "ops.h"
 
 #include <algorithm>
@@ -89,7 +92,9 @@ __device__ __forceinline__ void put(Chunk<T, V>& c, int v, float f) {
 }
 template <typename T, int V>
 __device__ __forceinline__ void store(void* base, uint64_t off, const Chunk<T, V>& c) {
-  *reinterpret_cast<Chunk<T, V>*>(static_cast<T*>(base) + off) = c;
+  T* p = static_cast<T*>(base) + off;
+  if constexpr (V > 1) __builtin_nontemporal_store(c.q, reinterpret_cast<decltype(Chunk<T, V>::q)*>(p));
+  else *p = c.q;
 }
 
 // A chunk of a row vector that every row uses (a weight or a gate). Chunks of
