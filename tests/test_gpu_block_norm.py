@@ -148,6 +148,34 @@ def test_padding_holds_anything(gpu):
         assert not got[0][~valid.cuda()].any() and not got[1][~valid.cuda()].any() and not got[3][1].any()
 
 
+def test_offsets_past_32_bits(gpu):
+    """More than 2^32 elements a tensor: the last rows as in a call of their own."""
+    rows, d, k = 1060000, 4104, 24
+    assert rows * d > 1 << 32
+    s = make(k, d, "bf16", 0, "ywh")
+    c = {n: cuda(t) for n, t in s.items()}
+    kw = dict(w_y=c["w_y"], w_r=c["w_r"])
+
+    def long(t):
+        z = torch.zeros(rows, d, dtype=t.dtype, device="cuda")
+        z[-k:] = t
+        return z
+
+    big, small = gpu.BlockNorm(rows, d, eps=EPS), gpu.BlockNorm(k, d, eps=EPS)
+    x, y = long(c["x"]), long(c["y"])
+    r, h = big.forward(x, y=y, r=x, **kw)
+    r2, h2 = small.forward(c["x"], y=c["y"], **kw)
+    assert torch.equal(r[-k:], r2) and torch.equal(h[-k:], h2) and not h[:rows - k].any()
+    h.zero_()
+    h[-k:] = c["dh"]
+    dr = long(c["dr"])
+    got = big.grad(dr, h, r, y=y, dx=dr, **kw)
+    one = small.grad(c["dr"], c["dh"], r2, y=c["y"], **kw)
+    assert torch.equal(got[0][-k:], one[0]) and torch.equal(got[1][-k:], one[1]) and not got[1][:rows - k].any()
+    s["gate"] = None
+    check_grad((one[0], one[1], got[2], None, got[4]), s, r2.cpu(), 1.0, 1.0)
+
+
 def test_zero_rows_and_zero_vectors(gpu):
     f = gpu.BlockNorm(0, 64, gpu.PW_F32, 2)
     e, w, g = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda"), torch.ones(2, 64, device="cuda")

@@ -174,6 +174,71 @@ def test_a_replayed_graph_and_another_stream(gpu):
     check_dispatch(b, s, kept)
 
 
+@pytest.mark.parametrize("T,d,E", [(60001, 1280, 37), (70000, 1024, 24)])
+def test_rows_beyond_the_caches(gpu, T, d, E):
+    """512 MiB of rows and more, read past the caches; 64-bit sums on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    src = torch.randperm(2 * T, generator=g, device="cuda").int()
+    n = 2 * T
+    offsets = torch.full((E + 1,), n, dtype=torch.int64, device="cuda")
+    dout, y, gates = rnd(T, d).to(bf), rnd(n, d).to(bf), torch.rand(T, 2, generator=g, device="cuda")
+    f = gpu.MoEGrad(T, d, E)
+    dy, dg, slot_of = f.combine(dout, y, gates, src, offsets)
+    assert torch.equal(src[slot_of.view(-1).long()], torch.arange(n, device="cuda", dtype=torch.int32))
+    dl, w, x = rnd(T, E), (rnd(d, E) * d ** -0.5).to(bf), rnd(T, d).to(bf)
+    dx, dw = f.dispatch(y, dl, w, x)
+    want_dw, terms = torch.zeros(d, E, dtype=torch.float64, device="cuda"), torch.zeros(d, E, dtype=torch.float64, device="cuda")
+    for lo in range(0, T, 16384):
+        hi = min(lo + 16384, T)
+        o, s = dout[lo:hi].double(), slot_of[lo:hi].long()
+        dl64, x64 = dl[lo:hi].double(), x[lo:hi].double()
+        part, size = dl64 @ w.double().t().contiguous(), dl64.abs() @ w.double().abs().t().contiguous()
+        rows = torch.zeros_like(part)
+        for j in range(2):
+            yj = y[s[:, j]].double()
+            want = gates[lo:hi, j:j + 1].double() * o
+            assert bool(((dy[s[:, j]].double() - want).abs() <= (HALF + 2 * U) * want.abs() + 1e-38).all())
+            assert bool(((dg[lo:hi, j].double() - (o * yj).sum(1)).abs() <= 64 * U * (o * yj).abs().sum(1)).all())
+            part += yj
+            rows += yj.abs()
+        bound = (2.0 ** -16 + 200 * U) * size + 4 * U * rows
+        assert bool(((dx[lo:hi].double() - part).abs() <= bound + HALF * (part.abs() + bound) + 1e-38).all())
+        want_dw += x64.t().contiguous() @ dl64
+        terms += x64.abs().t().contiguous() @ dl64.abs()
+    span = -(-max(64, -(-T // (256 // (d // 256)))) // 64) * 64
+    assert bool(((dw.double() - want_dw).abs() <= (48 * span // 64 + -(-T // span) + 8) * U * terms).all())
+
+
+def test_offsets_past_32_bits(gpu):
+    """More than 2^32 elements of dispatched rows: the last tokens as in a call of their own."""
+    T, d, E, k = 1700000, 1280, 8, 40
+    assert 2 * T * d > 1 << 32
+    dev = "cuda"
+    src = torch.arange(2 * T, dtype=torch.int32, device=dev)
+    offsets = torch.full((E + 1,), 2 * T, dtype=torch.int64, device=dev)
+    g = torch.Generator(device=dev).manual_seed(3)
+    tail = lambda n, *s, dt=bf: torch.randn(n, *s, generator=g, device=dev).to(dt)  # noqa: E731
+
+    def long(n, last, dt=bf):
+        t = torch.zeros(n, last.shape[1], dtype=dt, device=dev)
+        t[-last.shape[0]:] = last
+        return t
+
+    dout, y, gates, dl, x, w = tail(k, d), tail(2 * k, d), tail(k, 2, dt=torch.float32), tail(k, E, dt=torch.float32), tail(k, d), tail(d, E)
+    big, small = gpu.MoEGrad(T, d, E), gpu.MoEGrad(k, d, E)
+    Y = long(2 * T, y)
+    a = big.combine(long(T, dout), Y, long(T, gates, torch.float32), src, offsets)
+    b = small.combine(dout, y, gates, src[:2 * k].contiguous(), torch.full_like(offsets, 2 * k))
+    assert torch.equal(a[0][-2 * k:], b[0]) and torch.equal(a[1][-k:], b[1])
+    assert torch.equal(a[2].view(-1), src) and not a[0][:2 * (T - k)].any()
+    p = big.dispatch(Y, long(T, dl, torch.float32), w, long(T, x))
+    q = small.dispatch(y, dl, w, x)
+    assert torch.equal(p[0][-k:], q[0]) and not p[0][:T - k].any()
+    size = x.double().abs().t().contiguous() @ dl.double().abs()
+    assert bool(((p[1].double() - x.double().t().contiguous() @ dl.double()).abs() <= 200 * U * size).all())
+
+
 def test_refusals(gpu):
     s, _ = make(16, 256, 4, 0)
     f = gpu.MoEGrad(16, 256, 4)

@@ -115,6 +115,28 @@ def test_masked_rows_hold_anything(gpu):
     assert np.all(np.abs(d - want) <= 200 * U * size)
 
 
+def test_offsets_past_32_bits(gpu):
+    """More than 2^32 logits: the last tokens alone are valid."""
+    T, E, k, n = 17000000, 256, 2, 300
+    assert T * E > 1 << 32
+    l, ex, g, dg, _, u = make(n, E, k, None)
+
+    def long(a, dtype):
+        t = torch.zeros(T, a.shape[1], dtype=dtype, device="cuda")
+        t[-n:] = dev(a)
+        return t
+
+    f = gpu.RouterBalance(T, E, k, BAL, Z)
+    L, X = long(l, torch.float32), long(ex, torch.int32)
+    valid = torch.zeros(T, dtype=torch.bool, device="cuda")
+    valid[-n:] = True
+    got = f.loss(L, X, valid=valid)
+    check_loss(got, l, ex, None)
+    d = f.grad(L, X, gates=long(g, torch.float32), dgates=long(dg, torch.float32), valid=valid, grad_loss=dev(u))
+    check_grad(d[-n:].cpu().numpy(), l, ex, got[0].cpu().numpy(), g, dg, None, u)
+    assert not d[:T - n].any()
+
+
 def test_no_tokens(gpu):
     f = gpu.RouterBalance(0, 4, 2)
     e = torch.empty((0, 4), device="cuda")
