@@ -9,9 +9,10 @@
 // Both kernels read each logit once: a token's row is spread over a group of
 // L lanes of 4 experts each (L = 4, 16, 64 for E <= 16, 64, 256), so a wave's
 // load covers 64 / L whole rows, and the row's maximum, sum and dot product
-// are lane exchanges inside the group. 131072 x 64: loss 13.7 + 4.4 us, bound by
-// reading (35 MB, 2.5 TB/s, of which the first and last loads' latency is half),
-// gradient 20 us (70 MB, 3.5 TB/s). 48 x 8: 4.2 us, a few memory latencies.
+// are lane exchanges inside the group. 131072 x 64: loss 12.1 + 4.5 us (35 MB, 2.9
+// TB/s), gradient 18.1 us (70 MB, 3.9 TB/s): reading, with the first loads', the
+// arithmetic's (a quarter) and the launches' latency on top. 48 x 8: 4.2 us, a few
+// memory latencies.
 #include "ops.h"
 
 #include <algorithm>
@@ -66,6 +67,19 @@ __device__ __forceinline__ void load4(const float* row, uint32_t e0, uint32_t E,
   }
 }
 
+// e^x for x <= 0 (and NaN): the hardware's 2^t with t = x log2(e), and what the
+// product's rounding and log2(e)'s own left out put back to first order, so the
+// result is off by the rounding of x and two units in the last place. 8
+// instructions where expf takes 14; half of both kernels' arithmetic is this.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e430p-1f;
+  x = x < -150.f ? -150.f : x;  // e^-150 is zero in fp32; keeps -infinity out of the rest
+  const float t = x * kLog2e;
+  const float rest = fmaf(x, kLog2e, -t) + x * kRest;
+  const float y = __builtin_amdgcn_exp2f(t);
+  return fmaf(y, rest * kLn2, y);
+}
+
 // Probabilities of a row (in place) and its logarithm of the sum of
 // exponentials. A row of -infinity alone gives zeros; NaN stays NaN.
 template <int L>
@@ -75,14 +89,14 @@ __device__ __forceinline__ float softmax_row(float (&v)[4]) {
   float s = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[j] = expf(v[j] - m);
+    v[j] = exp_neg(v[j] - m);
     s += v[j];
   }
   s = lanes_sum<L>(s);
-  const float inv = s == 0.f ? 0.f : 1.0f / s;
+  const float inv = s == 0.f ? 0.f : __builtin_amdgcn_rcpf(s);  // s is in [1, E]: a unit in the last place
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] *= inv;
-  return s == 0.f ? 0.f : m + logf(s);
+  return s == 0.f ? 0.f : fmaf(__builtin_amdgcn_logf(s), 0x1.62e430p-1f, m);  // log2(s) ln 2
 }
 
 __device__ __forceinline__ double wave_sum(double v) {

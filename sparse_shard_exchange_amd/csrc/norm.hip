@@ -451,17 +451,24 @@ struct Segments {
   uint32_t group, segs, seg_rows, num_segs, grid;
 };
 
-constexpr uint32_t kSegments = 1024;  // segments wanted: 4 workgroups per CU
-constexpr uint32_t kSegmentRows = 4;  // of a segment at least, where a group has them
+// Segments wanted: 4 workgroups per CU for long batches; for short ones half as
+// many of up to 8 rows, since a segment's partial sums (two or three fp32 rows
+// written and read back) weigh against its rows, and a row's turn is a few
+// memory latencies (backward, bf16: 64 x 1024 8.2 us with 4 rows a segment, 7.1
+// with 2; 4096 x 1024 20.2 with 4, 18.3 with 8; 64 x 8192 25.8 and 20.0 with 4
+// and 2).
+constexpr uint32_t kSegments = 1024;
+constexpr uint32_t kShortRows = 8;
 
-// Enough segments to fill the GPU, but none so short that its partial sums
-// (two or three fp32 rows written and read) cost as much as its rows.
 Segments segments(uint32_t rows, uint32_t gates) {
   Segments s;
   const uint32_t groups = std::max(1u, gates);
   s.group = rows / groups;
   const uint32_t want = std::max(1u, kSegments / groups);
-  s.seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, kSegmentRows));
+  uint32_t short_rows = 1;  // a power of two: whole turns of the teams
+  while (short_rows < kShortRows && (uint64_t)short_rows * (kSegments / 2) < rows) short_rows *= 2;
+  s.seg_rows = std::max((s.group + want - 1) / want,
+                        std::min(s.group, short_rows));
   s.segs = (s.group + s.seg_rows - 1) / s.seg_rows;
   s.num_segs = s.segs * groups;
   s.grid = std::min(s.num_segs, kSegments);
