@@ -95,7 +95,6 @@ __global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
 // One wave handles kTokens tokens per pass, as the combine does: their slots
 // and gates in one round of loads, then every chunk of dout and of both y rows
 // in flight before any is used (a dropped tuple reads row 0 and is masked).
-constexpr uint32_t kCombineBlocks = 2048;
 constexpr int kTokens = 2;
 
 template <bool kInside, bool kStream>  // kInside: the slots of the workgroup's 4 kTokens tokens are found here (one pass)
@@ -118,8 +117,14 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
   const u32x4* y = reinterpret_cast<const u32x4*>(a.y);
   const u32x4* dout = reinterpret_cast<const u32x4*>(a.dout);
   u32x4* dy = reinterpret_cast<u32x4*>(a.dy);
-  const uint32_t stride = gridDim.x * 4 * kTokens;
-  for (uint32_t t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += stride) {
+#ifdef XC
+  const uint32_t blk = kInside ? blockIdx.x : xcd_contiguous(blockIdx.x, gridDim.x);
+#else
+  const uint32_t blk = blockIdx.x;
+#endif
+  const uint32_t t0 = (blk * 4 + (threadIdx.x >> 6)) * kTokens;
+  if (t0 >= a.tokens) return;  // whole waves, no barriers below
+  {
     int slot[kTokens][2];
     float gate[kTokens][2], dot[kTokens][2] = {};
     bool ok[kTokens];
@@ -560,7 +565,7 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
     hipLaunchKernelGGL(k_slots_put, dim3((uint32_t)((a.rows + 255) / 256)), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_put");
   }
-  const dim3 grid(std::min((a.tokens + per - 1) / per, kCombineBlocks));
+  const dim3 grid((a.tokens + per - 1) / per);
   if (((uint64_t)a.tokens + 2 * a.rows) * a.d * 2 >= kStreamBytes)
     hipLaunchKernelGGL((k_combine_grad<false, true>), grid, dim3(256), 0, s, a);
   else

@@ -55,8 +55,7 @@ struct NormArgs {
   float* part_q;   // [segments][d] sums of D y t of each segment
   uint32_t rows, d, gates;
   uint32_t group;      // rows that share a gate row (rows if there is one gate or none)
-  uint32_t seg_rows;   // rows of a segment; segments do not cross groups
-  uint32_t segs;       // segments of a group
+  uint32_t segs;       // segments of a group: every segs-th turn of its rows
   uint32_t num_segs;   // groups x segs
   uint32_t grid;       // workgroups of k_norm_grad
   float x_scale, y_scale, eps, inv_d;
@@ -135,7 +134,10 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint3
   }
 }
 
-// C chunks of V elements per thread of a team of TEAM threads.
+// C chunks of V elements per thread of a team of TEAM threads; a workgroup takes
+// one row per team and ends (131072 x 1024 bf16: 178 us; walking the rows with
+// 4096 workgroups 200, with 1024 224: rows that run at the same time are
+// neighbours, and the next workgroup's loads overlap this one's stores).
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
 __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
   __shared__ Exchange<TEAM> ex;
@@ -143,81 +145,77 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
   const uint32_t lane = threadIdx.x % TEAM, nch = a.d / V;
   constexpr uint32_t kTeams = threads_of(TEAM) / TEAM;
   const bool norm_y = kY && a.w_y, gated = kY && a.gate;
-  // the trip count is the same for all threads of a workgroup (barriers inside)
-  for (uint32_t row0 = blockIdx.x * kTeams; row0 < a.rows; row0 += gridDim.x * kTeams) {
-    const uint32_t row = row0 + threadIdx.x / TEAM;
-    const bool live = row < a.rows;
-    const uint64_t base = (uint64_t)(live ? row : a.rows - 1) * a.d;
-    Chunk<T, V> x[C], y[C];
+  const uint32_t row = blockIdx.x * kTeams + threadIdx.x / TEAM;
+  const bool live = row < a.rows;  // every thread stays: barriers inside
+  const uint64_t base = (uint64_t)min(row, a.rows - 1) * a.d;
+  const uint64_t gbase = gated ? (uint64_t)(min(row, a.rows - 1) / a.group) * a.d : 0;
+  Chunk<T, V> x[C], y[C], wy[C], g[C], wr[C];  // all requested before any is used
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint32_t ch = min(lane + c * TEAM, nch - 1);
-      x[c] = load<T, V>(a.x, base + (uint64_t)ch * V);
-      if (kY) y[c] = load<T, V>(a.y, base + (uint64_t)ch * V);
-    }
-    float ty = a.y_scale;
-    if (norm_y) {
-      float ss[1] = {0.f};
+  for (int c = 0; c < C; ++c) {
+    const uint64_t ch = (uint64_t)min(lane + c * TEAM, nch - 1) * V;
+    x[c] = load<T, V>(a.x, base + ch);
+    if (kY) y[c] = load<T, V>(a.y, base + ch);
+    if (norm_y) wy[c] = load<T, V>(a.w_y, ch);
+    if (gated) g[c] = load<T, V>(a.gate, gbase + ch);
+    if (kH) wr[c] = load<T, V>(a.w_r, ch);
+  }
+  float ty = a.y_scale;
+  if (norm_y) {
+    float ss[1] = {0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (lane + c * TEAM < nch)
+    for (int c = 0; c < C; ++c)
+      if (lane + c * TEAM < nch)
 #pragma unroll
-          for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
-      team_sum(ss, ex, turn);
-      ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
-    }
-    const uint64_t gbase = gated ? (uint64_t)((live ? row : a.rows - 1) / a.group) * a.d : 0;
-    float r[C][V], ss[1] = {0.f};
+        for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
+    team_sum(ss, ex, turn);
+    ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+  }
+  float r[C][V], ss[1] = {0.f};
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint32_t ch = min(lane + c * TEAM, nch - 1);
-      Chunk<T, V> wy, g;
-      if (norm_y) wy = load<T, V>(a.w_y, (uint64_t)ch * V);
-      if (gated) g = load<T, V>(a.gate, gbase + (uint64_t)ch * V);
+  for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float f = a.x_scale * at<T, V>(x[c], v);
-        if (kY) {
-          float n = ty * at<T, V>(y[c], v);
-          if (norm_y) n *= at<T, V>(wy, v);
-          f = gated ? fmaf(n, at<T, V>(g, v), f) : f + n;
-        }
-        r[c][v] = f;
-        if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
+    for (int v = 0; v < V; ++v) {
+      float f = a.x_scale * at<T, V>(x[c], v);
+      if (kY) {
+        float n = ty * at<T, V>(y[c], v);
+        if (norm_y) n *= at<T, V>(wy[c], v);
+        f = gated ? fmaf(n, at<T, V>(g[c], v), f) : f + n;
       }
+      r[c][v] = f;
+      if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
     }
-    float s = 0.f;
+  }
+  float s = 0.f;
+  if (kH) {
+    team_sum(ss, ex, turn);
+    s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t ch = lane + c * TEAM;
+    if (!live || ch >= nch) continue;
+    Chunk<T, V> o;
+    if (a.r) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v]);
+      store<T, V>(a.r, base + (uint64_t)ch * V, o);
+    }
     if (kH) {
-      team_sum(ss, ex, turn);
-      s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
-    }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint32_t ch = lane + c * TEAM;
-      if (!live || ch >= nch) continue;
-      Chunk<T, V> o;
-      if (a.r) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v]);
-        store<T, V>(a.r, base + (uint64_t)ch * V, o);
-      }
-      if (kH) {
-        const Chunk<T, V> w = load<T, V>(a.w_r, (uint64_t)ch * V);
-#pragma unroll
-        for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v] * s * at<T, V>(w, v));
-        store<T, V>(a.h, base + (uint64_t)ch * V, o);
-      }
+      for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v] * s * at<T, V>(wr[c], v));
+      store<T, V>(a.h, base + (uint64_t)ch * V, o);
     }
   }
 }
 
-// Backward. The rows are cut into segments of consecutive rows of one gate
-// group; a workgroup walks segments, its teams taking the segment's rows in
-// turn, and keeps in registers, for its columns, the running sums of D y t
-// (Q, until the end of the segment) and dh r s (W, until its own end). At a
-// segment's end Q goes, summed over the teams, to dgate where the segment is
-// the whole group, else to part_q; and gate Q to the running sum P of dw_y.
-// W and P end in one partial row per workgroup; k_norm_join adds the rows.
+// Backward. The rows of a gate group are dealt to its segments in turn (a row
+// for each team, segment after segment), so that workgroups running at the same
+// time read neighbouring rows. A workgroup walks segments and keeps in
+// registers, for its columns, the running sums of D y t (Q, until the end of
+// the segment) and dh r s (W, until its own end). At a segment's end Q goes,
+// summed over the teams, to dgate where the segment is the whole group, else to
+// part_q; and gate Q to the running sum P of dw_y. W and P end in one partial
+// row per workgroup; k_norm_join adds the rows.
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
 __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) void k_norm_grad(NormArgs a) {
   constexpr int NT = threads_of(TEAM);
@@ -264,15 +262,14 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
 
   for (uint32_t sg = blockIdx.x; sg < a.num_segs; sg += gridDim.x) {
     const uint32_t g = sg / a.segs, k = sg % a.segs;
-    const uint32_t lo = k * a.seg_rows, hi = min(lo + a.seg_rows, a.group);  // rows of the group
     const uint64_t gbase = (uint64_t)g * a.d;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int v = 0; v < V; ++v) Q[c][v] = 0.f;
-    for (uint32_t i0 = lo; i0 < hi; i0 += kTeams) {
-      const bool live = i0 + team < hi;
-      const uint64_t row = (uint64_t)g * a.group + (live ? i0 + team : hi - 1), base = row * a.d;
+    for (uint32_t i0 = k * kTeams; i0 < a.group; i0 += a.segs * kTeams) {
+      const bool live = i0 + team < a.group;
+      const uint64_t row = (uint64_t)g * a.group + min(i0 + team, a.group - 1), base = row * a.d;
       const bool ok = live && (!a.valid || a.valid[row]);
       Chunk<T, V> dr[C], dh[C], r[C], y[C];
 #pragma unroll
@@ -447,8 +444,14 @@ Shape shape_of(uint32_t d, bool f32, bool aligned) {
   return {V, 4 / V, 64};
 }
 
+// Rows a workgroup takes at a time.
+uint32_t teams_of(uint32_t d) {
+  const uint32_t team = shape_of(d, false, true).team;  // the same for every type and alignment
+  return threads_of(team) / team;
+}
+
 struct Segments {
-  uint32_t group, segs, seg_rows, num_segs, grid;
+  uint32_t group, segs, num_segs, grid;
 };
 
 // Segments wanted: 4 workgroups per CU for long batches; for short ones half as
@@ -460,16 +463,15 @@ struct Segments {
 constexpr uint32_t kSegments = 1024;
 constexpr uint32_t kShortRows = 8;
 
-Segments segments(uint32_t rows, uint32_t gates) {
+Segments segments(uint32_t rows, uint32_t gates, uint32_t d) {
   Segments s;
   const uint32_t groups = std::max(1u, gates);
   s.group = rows / groups;
   const uint32_t want = std::max(1u, kSegments / groups);
-  uint32_t short_rows = 1;  // a power of two: whole turns of the teams
+  uint32_t short_rows = teams_of(d);  // a power of two: whole turns of the teams
   while (short_rows < kShortRows && (uint64_t)short_rows * (kSegments / 2) < rows) short_rows *= 2;
-  s.seg_rows = std::max((s.group + want - 1) / want,
-                        std::min(s.group, short_rows));
-  s.segs = (s.group + s.seg_rows - 1) / s.seg_rows;
+  const uint32_t seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, short_rows));
+  s.segs = (s.group + seg_rows - 1) / seg_rows;
   s.num_segs = s.segs * groups;
   s.grid = std::min(s.num_segs, kSegments);
   return s;
@@ -482,7 +484,7 @@ struct GradLayout {
 GradLayout grad_layout(const pw_norm_desc& d) {
   GradLayout l;
   if (d.rows == 0) return l;
-  const Segments s = segments((uint32_t)d.rows, d.gates);
+  const Segments s = segments((uint32_t)d.rows, d.gates, d.d);
   const size_t row = (size_t)d.d * 4;
   if (s.grid > 1) {
     l.p = up256(s.grid * row);
@@ -548,8 +550,6 @@ NormArgs args(const pw_norm_desc& d, const pw_norm_io& io) {
   return a;
 }
 
-constexpr uint32_t kForwardGrid = 256 * 16;  // workgroups of k_norm at most
-
 template <typename T, int V, int C, int TEAM, bool kY, bool kH>
 void launch(const NormArgs& a, bool grad, hipStream_t s) {
   constexpr uint32_t NT = threads_of(TEAM), teams = NT / TEAM;
@@ -557,7 +557,7 @@ void launch(const NormArgs& a, bool grad, hipStream_t s) {
     const size_t lds = teams > 1 ? (size_t)teams * a.d * 4 : 0;
     hipLaunchKernelGGL((k_norm_grad<T, V, C, TEAM, kY, kH>), dim3(a.grid), dim3(NT), lds, s, a);
   } else {
-    const uint32_t blocks = (uint32_t)std::min<uint64_t>(((uint64_t)a.rows + teams - 1) / teams, kForwardGrid);
+    const uint32_t blocks = (a.rows + teams - 1) / teams;
     hipLaunchKernelGGL((k_norm<T, V, C, TEAM, kY, kH>), dim3(blocks), dim3(NT), 0, s, a);
   }
 }
@@ -648,10 +648,9 @@ extern "C" int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, v
     e = hipGetLastError();
     return e == hipSuccess ? PW_OK : hip_fail(e, "launch norm_zero");
   }
-  const Segments sg = segments(a.rows, a.gates);
+  const Segments sg = segments(a.rows, a.gates, a.d);
   a.group = sg.group;
   a.segs = sg.segs;
-  a.seg_rows = sg.seg_rows;
   a.num_segs = sg.num_segs;
   a.grid = sg.grid;
   unsigned char* base = static_cast<unsigned char*>(ws);
