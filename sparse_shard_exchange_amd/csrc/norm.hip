@@ -15,7 +15,7 @@
 // A row lives in the registers of its team (one wave up to 512 elements, up to
 // 16 waves for the widest) from its only read to its only write, so the passes
 // move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
-// bf16, all parts: forward 198 us (5.4 TB/s), backward 326 + 6 us (4.9 TB/s); a
+// bf16, all parts: forward 176 us (6.1 TB/s), backward 310 + 11 us (5.0 TB/s); a
 // large copy reaches 5.2. Rows are stored nontemporally: written plainly, they
 // are written back during the next operator's reads (forward and backward in
 // turn, 131072 rows 527 us against 542, 32768 rows 126 against 135, 16384 rows,
@@ -388,24 +388,27 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
 }
 
 // Adds the partial rows: blockIdx.y 0: dw_r, 1: dw_y, 2 + g: dgate of group
-// g. 64 columns per workgroup, 16 slices of rows, added in a fixed order.
+// g. 32 columns per workgroup, 32 slices of rows, added in a fixed order.
+constexpr uint32_t kJoinCols = 32, kJoinSlices = 1024 / kJoinCols;
+
 template <typename T>
 __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a) {
-  __shared__ float s[16][64];
-  const uint32_t c = threadIdx.x % 64, slice = threadIdx.x / 64, col = blockIdx.x * 64 + c;
+  __shared__ float s[kJoinSlices][kJoinCols];
+  const uint32_t c = threadIdx.x % kJoinCols, slice = threadIdx.x / kJoinCols, col = blockIdx.x * kJoinCols + c;
   const uint32_t what = blockIdx.y;
+  if ((what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;  // whole workgroups
   const float* part = what == 0 ? a.part_w : what == 1 ? a.part_p : a.part_q + (uint64_t)(what - 2) * a.segs * a.d;
   const uint32_t n = what < 2 ? a.grid : a.segs;
-  if ((what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;
   float v = 0.f;
   if (col < a.d)
 #pragma unroll 16
-    for (uint32_t i = slice; i < n; i += 16) v += part[(uint64_t)i * a.d + col];
+    for (uint32_t i = slice; i < n; i += kJoinSlices) v += part[(uint64_t)i * a.d + col];
   s[slice][c] = v;
   __syncthreads();
   if (slice != 0 || col >= a.d) return;
   v = 0.f;
-  for (int i = 0; i < 16; ++i) v += s[i][c];
+#pragma unroll
+  for (uint32_t i = 0; i < kJoinSlices; ++i) v += s[i][c];
   if (what == 0) a.dw_r[col] = v;
   else if (what == 1) a.dw_y[col] = v * a.y_scale;
   else a.dgate[(uint64_t)(what - 2) * a.d + col] = v * a.y_scale * (a.w_y ? (float)static_cast<const T*>(a.w_y)[col] : 1.f);
@@ -454,26 +457,31 @@ struct Segments {
   uint32_t group, segs, num_segs, grid;
 };
 
-// Segments wanted: 4 workgroups per CU for long batches; for short ones half as
-// many of up to 8 rows, since a segment's partial sums (two or three fp32 rows
+// Segments wanted: 8 workgroups per CU for long batches (131072 x 1024 bf16 back:
+// 318 us with the join, with 1024 segments 338: the second half of the
+// workgroups starts as the first ends, and evens out their ends), 4 where a
+// workgroup takes one row at a time (16384 x 8192: 422 and 373 us); for short
+// batches up to 512 of up to 8 rows, since a segment's partial sums (two or three fp32 rows
 // written and read back) weigh against its rows, and a row's turn is a few
 // memory latencies (backward, bf16: 64 x 1024 8.2 us with 4 rows a segment, 7.1
 // with 2; 4096 x 1024 20.2 with 4, 18.3 with 8; 64 x 8192 25.8 and 20.0 with 4
 // and 2).
-constexpr uint32_t kSegments = 1024;
+constexpr uint32_t kSegments = 2048;
+constexpr uint32_t kShortSegments = 512;
 constexpr uint32_t kShortRows = 8;
 
 Segments segments(uint32_t rows, uint32_t gates, uint32_t d) {
   Segments s;
   const uint32_t groups = std::max(1u, gates);
   s.group = rows / groups;
-  const uint32_t want = std::max(1u, kSegments / groups);
+  const uint32_t most = teams_of(d) > 1 ? kSegments : kSegments / 2;
+  const uint32_t want = std::max(1u, most / groups);
   uint32_t short_rows = teams_of(d);  // a power of two: whole turns of the teams
-  while (short_rows < kShortRows && (uint64_t)short_rows * (kSegments / 2) < rows) short_rows *= 2;
+  while (short_rows < kShortRows && (uint64_t)short_rows * kShortSegments < rows) short_rows *= 2;
   const uint32_t seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, short_rows));
   s.segs = (s.group + seg_rows - 1) / seg_rows;
   s.num_segs = s.segs * groups;
-  s.grid = std::min(s.num_segs, kSegments);
+  s.grid = std::min(s.num_segs, most);
   return s;
 }
 
@@ -665,7 +673,7 @@ extern "C" int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, v
   if (e != hipSuccess) return hip_fail(e, "launch norm_grad");
   const bool gates = a.gate && a.segs > 1;
   if ((a.grid > 1 && (a.dw_r || a.dw_y)) || gates) {
-    const dim3 grid((a.d + 63) / 64, 2 + (gates ? a.gates : 0));
+    const dim3 grid((a.d + kJoinCols - 1) / kJoinCols, 2 + (gates ? a.gates : 0));
     if (d->dtype == PW_F32) hipLaunchKernelGGL(k_norm_join<float>, grid, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL(k_norm_join<__bf16>, grid, dim3(1024), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch norm_join");
