@@ -406,8 +406,9 @@ int pw_plan_reset_times(pw_plan_t plan);
  * between calls, so calls that are ordered may share one; calls that overlap
  * must not). They enqueue kernel launches only, so they can be captured into
  * HIP graphs and replayed. All buffers and the stream must belong to the
- * current device. Buffers are contiguous; outputs must not overlap inputs or
- * each other except where said. Sums are fp32 or wider and in a fixed order:
+ * current device. Buffers are contiguous and aligned to their elements (those
+ * of the MOE gradients' rows to 16 bytes, their gates, slots and offsets to
+ * 8); outputs must not overlap inputs or each other except where said. Sums are fp32 or wider and in a fixed order:
  * equal inputs give equal bits.
  * ======================================================================== */
 
@@ -486,7 +487,8 @@ typedef struct {
   const void* x;            /* [tokens][d] the step's tokens (with dw_router)   */
   const int32_t* slot_of;   /* [tokens][2] (pw_moe_combine_grad)                */
   const uint8_t* valid;     /* [tokens], nullable: where 0 (padding), dx is zero
-                               and x adds nothing to dw_router                  */
+                               and the token adds nothing to dw_router, whatever
+                               it holds                                         */
   void* dx;                 /* [tokens][d]: both tuples' dxd rows + dlogits . w_router^T */
   float* dw_router;         /* [d][E] fp32: x^T . dlogits; nullable             */
 } pw_dispatch_grad_io;

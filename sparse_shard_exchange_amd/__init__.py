@@ -768,7 +768,7 @@ class MoEBlock:
     plus the router's balance loss. moe: an MoE with want_logits. w_out and
     gate may be None. The experts' weights are packed when the MoE is built,
     and the gradient of their products is the caller's, between grad_begin
-    and grad_end."""
+    and grad_end. One forward, then its backward: the buffers are the object's."""
 
     def __init__(self, moe, w_in, w_out=None, gate=None, x_scale=1.0, y_scale=1.0, eps=1e-6, balance_coef=1e-2,
                  z_coef=0.0):

@@ -259,80 +259,81 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
   constexpr uint32_t G = kGradThreads / L, S = L < 8 ? L : 8;  // lanes that hold gates
   constexpr uint32_t kOf = 8 / S;                              // gates of such a lane
   const uint32_t tid = threadIdx.x, lane = tid % L, grp = tid / L;
-  const uint32_t t0 = blockIdx.x * G * kRows + grp;
-  float v[kRows][4], g[kRows][kOf], dg[kRows][kOf];
-  uint32_t ex[kRows][kOf];
-  bool ok[kRows];
+  for (uint32_t t0 = blockIdx.x * G * kRows + grp; t0 - grp < a.tokens; t0 += gridDim.x * G * kRows) {
+    float v[kRows][4], g[kRows][kOf], dg[kRows][kOf];
+    uint32_t ex[kRows][kOf];
+    bool ok[kRows];
 #pragma unroll
-  for (uint32_t u = 0; u < kRows; ++u) {
-    const uint32_t t = min(t0 + u * G, a.tokens - 1);
-    load4<kVec>(a.logits + (uint64_t)t * a.E, lane * 4, a.E, v[u]);
-    ok[u] = true;
-  }
-  if (a.gates)  // uniform
-#pragma unroll
-    for (uint32_t u = 0; u < kRows; ++u)
-#pragma unroll
-      for (uint32_t q = 0; q < kOf; ++q) {
-        const uint64_t o = (uint64_t)min(t0 + u * G, a.tokens - 1) * a.k + min(lane * kOf + q, a.k - 1);
-        g[u][q] = a.gates[o];
-        dg[u][q] = a.dgates[o];
-        ex[u][q] = (uint32_t)a.experts[o];
-      }
-  if (a.valid)  // uniform
-#pragma unroll
-    for (uint32_t u = 0; u < kRows; ++u) ok[u] = a.valid[min(t0 + u * G, a.tokens - 1)];
-  const int n = a.counts[a.E];
-  const float inv = n > 0 ? 1.0f / (float)n : 0.f;
-  const float u0 = a.grad_loss ? a.grad_loss[0] : 1.f, u1 = a.grad_loss ? a.grad_loss[1] : 1.f;
-  const float cb = u0 * a.balance_coef * (float)a.E / (float)a.k * inv, cz = u1 * 2.f * a.z_coef * inv;
-  float c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t e = lane * 4 + j;
-    c[j] = e < a.E ? (float)((int64_t)a.counts[e] * a.E - (int64_t)a.k * n) * (inv / (float)a.E) : 0.f;
-  }
-#pragma unroll
-  for (uint32_t u = 0; u < kRows; ++u) {
-    const uint32_t t = t0 + u * G;
-    const float lse = softmax_row<L>(v[u]);
-    const float mean = lanes_sum<L>(fmaf(c[0], v[u][0], fmaf(c[1], v[u][1], fmaf(c[2], v[u][2], c[3] * v[u][3]))));
-    float o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = v[u][j] * fmaf(cb, c[j] - mean, cz * lse);
-    if (a.gates) {  // uniform
-      float dot = 0.f, part[kOf];
-#pragma unroll
-      for (uint32_t q = 0; q < kOf; ++q)
-        if (lane * kOf + q < a.k) dot = fmaf(g[u][q], dg[u][q], dot);
-      dot = lanes_sum<S>(dot);
-#pragma unroll
-      for (uint32_t q = 0; q < kOf; ++q) part[q] = g[u][q] * (dg[u][q] - dot);
-      for (uint32_t s = 0; s < a.k; ++s) {
-        const int from = (int)(tid % 64 - lane + s / kOf);
-        float p = part[0];
-        uint32_t e = ex[u][0];
-        if (kOf > 1 && s % kOf) {
-          p = part[kOf - 1];
-          e = ex[u][kOf - 1];
-        }
-        p = __shfl(p, from);
-        e = (uint32_t)__shfl((int)e, from) - lane * 4;
-#pragma unroll
-        for (uint32_t j = 0; j < 4; ++j)
-          if (e == j) o[j] += p;
-      }
+    for (uint32_t u = 0; u < kRows; ++u) {
+      const uint32_t t = min(t0 + u * G, a.tokens - 1);
+      load4<kVec>(a.logits + (uint64_t)t * a.E, lane * 4, a.E, v[u]);
+      ok[u] = true;
     }
-    if (t >= a.tokens) continue;
-    float* out = a.dlogits + (uint64_t)t * a.E;
-    if (kVec) {
-      typedef __attribute__((ext_vector_type(4))) float f32x4;
-      const f32x4 q = {ok[u] ? o[0] : 0.f, ok[u] ? o[1] : 0.f, ok[u] ? o[2] : 0.f, ok[u] ? o[3] : 0.f};
-      if (lane * 4 < a.E) *reinterpret_cast<f32x4*>(out + lane * 4) = q;
-    } else {
+    if (a.gates)  // uniform
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (lane * 4 + j < a.E) out[lane * 4 + j] = ok[u] ? o[j] : 0.f;
+      for (uint32_t u = 0; u < kRows; ++u)
+#pragma unroll
+        for (uint32_t q = 0; q < kOf; ++q) {
+          const uint64_t o = (uint64_t)min(t0 + u * G, a.tokens - 1) * a.k + min(lane * kOf + q, a.k - 1);
+          g[u][q] = a.gates[o];
+          dg[u][q] = a.dgates[o];
+          ex[u][q] = (uint32_t)a.experts[o];
+        }
+    if (a.valid)  // uniform
+#pragma unroll
+      for (uint32_t u = 0; u < kRows; ++u) ok[u] = a.valid[min(t0 + u * G, a.tokens - 1)];
+    const int n = a.counts[a.E];
+    const float inv = n > 0 ? 1.0f / (float)n : 0.f;
+    const float u0 = a.grad_loss ? a.grad_loss[0] : 1.f, u1 = a.grad_loss ? a.grad_loss[1] : 1.f;
+    const float cb = u0 * a.balance_coef * (float)a.E / (float)a.k * inv, cz = u1 * 2.f * a.z_coef * inv;
+    float c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t e = lane * 4 + j;
+      c[j] = e < a.E ? (float)((int64_t)a.counts[e] * a.E - (int64_t)a.k * n) * (inv / (float)a.E) : 0.f;
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kRows; ++u) {
+      const uint32_t t = t0 + u * G;
+      const float lse = softmax_row<L>(v[u]);
+      const float mean = lanes_sum<L>(fmaf(c[0], v[u][0], fmaf(c[1], v[u][1], fmaf(c[2], v[u][2], c[3] * v[u][3]))));
+      float o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = v[u][j] * fmaf(cb, c[j] - mean, cz * lse);
+      if (a.gates) {  // uniform
+        float dot = 0.f, part[kOf];
+#pragma unroll
+        for (uint32_t q = 0; q < kOf; ++q)
+          if (lane * kOf + q < a.k) dot = fmaf(g[u][q], dg[u][q], dot);
+        dot = lanes_sum<S>(dot);
+#pragma unroll
+        for (uint32_t q = 0; q < kOf; ++q) part[q] = g[u][q] * (dg[u][q] - dot);
+        for (uint32_t s = 0; s < a.k; ++s) {
+          const int from = (int)(tid % 64 - lane + s / kOf);
+          float p = part[0];
+          uint32_t e = ex[u][0];
+          if (kOf > 1 && s % kOf) {
+            p = part[kOf - 1];
+            e = ex[u][kOf - 1];
+          }
+          p = __shfl(p, from);
+          e = (uint32_t)__shfl((int)e, from) - lane * 4;
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j)
+            if (e == j) o[j] += p;
+        }
+      }
+      if (t >= a.tokens) continue;
+      float* out = a.dlogits + (uint64_t)t * a.E;
+      if (kVec) {
+        typedef __attribute__((ext_vector_type(4))) float f32x4;
+        const f32x4 q = {ok[u] ? o[0] : 0.f, ok[u] ? o[1] : 0.f, ok[u] ? o[2] : 0.f, ok[u] ? o[3] : 0.f};
+        if (lane * 4 < a.E) *reinterpret_cast<f32x4*>(out + lane * 4) = q;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (lane * 4 + j < a.E) out[lane * 4 + j] = ok[u] ? o[j] : 0.f;
+      }
     }
   }
 }
@@ -362,6 +363,13 @@ int validate(const pw_balance_desc* d) {
     return fail(PW_ERR_INVALID, "top_k must be in [1, 8] and at most num_experts");
   if (d->tokens * d->top_k > 0x7fffffffull) return fail(PW_ERR_INVALID, "tokens x top_k must stay below 2^31");
   if (!isfinite(d->balance_coef) || !isfinite(d->z_coef)) return fail(PW_ERR_INVALID, "the coefficients must be finite");
+  return PW_OK;
+}
+
+int check_aligned(const pw_balance_io& io) {
+  if (misaligned({io.logits, io.experts, io.counts, io.prob_mean, io.loss, io.gates, io.dgates, io.grad_loss,
+                  io.dlogits}, 4))
+    return fail(PW_ERR_INVALID, "a buffer is not aligned to its elements");
   return PW_OK;
 }
 
@@ -399,7 +407,7 @@ void launch_grad(const BalanceArgs& a, hipStream_t s) {
   constexpr uint32_t G = kGradThreads / L;
   const uint32_t groups = (a.tokens + G - 1) / G;
   if (groups <= kGradWide) hipLaunchKernelGGL((k_router_grad<L, kVec, 1>), dim3(groups), dim3(kGradThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_router_grad<L, kVec, 4>), dim3((groups + 3) / 4), dim3(kGradThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_router_grad<L, kVec, 4>), dim3(std::min((groups + 3) / 4, kMaxGrid)), dim3(kGradThreads), 0, s, a);
 }
 
 #define PW_BY_EXPERTS(fn, a, vec, s)                                \
@@ -432,6 +440,7 @@ extern "C" int pw_router_balance(const pw_balance_desc* d, const pw_balance_io* 
   if (st) return st;
   if (!io || !io->counts || !io->loss) return fail(PW_ERR_INVALID, "counts and loss are required");
   if (d->tokens && (!io->logits || !io->experts)) return fail(PW_ERR_INVALID, "logits and experts are required");
+  if ((st = check_aligned(*io))) return st;
   const BalanceLayout l = balance_layout(*d);
   if ((st = check_workspace(ws, ws_bytes, l.total))) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -459,6 +468,7 @@ extern "C" int pw_router_grad(const pw_balance_desc* d, const pw_balance_io* io,
   if (!io->logits || !io->counts || !io->dlogits) return fail(PW_ERR_INVALID, "logits, counts and dlogits are required");
   if (!io->gates != !io->dgates) return fail(PW_ERR_INVALID, "gates and dgates are given together or not at all");
   if (io->gates && !io->experts) return fail(PW_ERR_INVALID, "gates need experts");
+  if ((st = check_aligned(*io))) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = check_stream(s))) return st;
   const BalanceArgs a = args(*d, *io);

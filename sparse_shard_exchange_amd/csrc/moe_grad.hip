@@ -92,12 +92,14 @@ __global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
 }
 
 // ---- gradient of the combine ---------------------------------------------------
-// One wave handles kTokens tokens per pass, as the combine does: their slots
-// and gates in one round of loads, then every chunk of dout and of both y rows
-// in flight before any is used (a dropped tuple reads row 0 and is masked).
+// One wave handles kTokens tokens: their slots and gates in one round of loads,
+// then every chunk of dout and of both y rows in flight before any is used (a
+// dropped tuple reads row 0 and is masked). A workgroup takes its 8 tokens and
+// ends: 131072 tokens x 1024, 253 us, 5.3 TB/s on random rows of 2 KiB, against
+// 264 us with 2048 workgroups that walk the tokens. Bound by HBM.
 constexpr int kTokens = 2;
 
-template <bool kInside, bool kStream>  // kInside: the slots of the workgroup's 4 kTokens tokens are found here (one pass)
+template <bool kInside, bool kStream>  // kInside: the slots of the workgroup's 4 kTokens tokens are found here
 __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
   __shared__ int own[kInside ? 8 * kTokens : 1];
   if (kInside) {
@@ -117,14 +119,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
   const u32x4* y = reinterpret_cast<const u32x4*>(a.y);
   const u32x4* dout = reinterpret_cast<const u32x4*>(a.dout);
   u32x4* dy = reinterpret_cast<u32x4*>(a.dy);
-#ifdef XC
-  const uint32_t blk = kInside ? blockIdx.x : xcd_contiguous(blockIdx.x, gridDim.x);
-#else
-  const uint32_t blk = blockIdx.x;
-#endif
-  const uint32_t t0 = (blk * 4 + (threadIdx.x >> 6)) * kTokens;
-  if (t0 >= a.tokens) return;  // whole waves, no barriers below
-  {
+  for (uint32_t t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * kTokens; t0 < a.tokens; t0 += gridDim.x * 4 * kTokens) {
     int slot[kTokens][2];
     float gate[kTokens][2], dot[kTokens][2] = {};
     bool ok[kTokens];
@@ -204,7 +199,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
 // contiguous bytes a row. dl is split into two bf16 terms (hi + lo, at most
 // 2^-16 of the value is lost, below the rounding of dx to bf16 at 2^-8), so
 // the products are as exact as dx can show. 131072 tokens x 1024, 64 experts:
-// 155 us, 5.2 TB/s, the rate of a large copy; bound by HBM. (W in registers,
+// 154 us, 5.5 TB/s, the rate of a large copy; bound by HBM. (W in registers,
 // 128 columns a wave, 8 waves per CU: 223 us; one token a lane, 64 bytes of
 // its row: 306 us.)
 constexpr uint32_t kDxThreads = 1024;
@@ -289,7 +284,7 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) 
+          for (int s = 0; s < 2; ++s)
             g[s][r] = load_row<kStream>(reinterpret_cast<const bf16x8*>(src[s][r] + cb * kDxCols));
       f32x4 acc[8];
 #pragma unroll
@@ -328,9 +323,9 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 // terms, which hold all 24 bits of it: every product is exact and the sums
 // are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
 // of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
-// 131072 tokens x 1024, 64 experts: 72 us, 4.2 TB/s; bound by reading x and dl
-// once from HBM. (Sharing the split terms between the waves
-// through LDS, and requesting x two steps ahead, measured no faster.)
+// 131072 tokens x 1024, 64 experts: 70 us, 4.3 TB/s; bound by reading x and dl
+// once from HBM. (Sharing the split terms between the waves through LDS, and
+// requesting x two steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
 constexpr int kNontemporal = 2;  // nt in the cache-policy operand of buffer instructions
@@ -384,7 +379,11 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
     if (a.valid)  // uniform
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (!a.valid[first + min(t + 16 * tw + 8 * h + j, n - 1)]) s.v[j] = u32x2{0, 0};
+        if (!a.valid[first + min(t + 16 * tw + 8 * h + j, n - 1)]) {
+          s.v[j] = u32x2{0, 0};
+#pragma unroll
+          for (int c = 0; c < NC; ++c) s.dl[c][j] = 0.f;
+        }
     bf16x8 xa[4], dt[NC][3];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -532,10 +531,9 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
   if (!io->dout || !io->gates || !io->offsets || !io->dgates || !io->slot_of)
     return fail(PW_ERR_INVALID, "dout, gates, offsets, dgates and slot_of are required");
   if (d->rows && (!io->y || !io->src_index || !io->dy)) return fail(PW_ERR_INVALID, "y, src_index and dy are required");
-  if (((uintptr_t)io->dout | (uintptr_t)io->y | (uintptr_t)io->dy) % 16)
-    return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
-  if (((uintptr_t)io->gates | (uintptr_t)io->dgates | (uintptr_t)io->slot_of) % 8)
-    return fail(PW_ERR_INVALID, "gates, dgates and slot_of must be 8-byte aligned");
+  if (misaligned({io->dout, io->y, io->dy}, 16)) return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
+  if (misaligned({io->gates, io->dgates, io->slot_of, io->offsets}, 8) || misaligned({io->src_index}, 4))
+    return fail(PW_ERR_INVALID, "gates, dgates, slot_of and offsets must be 8-byte aligned, src_index 4-byte");
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = check_stream(s))) return st;
   CombineGradArgs a{};
@@ -565,7 +563,7 @@ extern "C" int pw_moe_combine_grad(const pw_moe_grad_desc* d, const pw_combine_g
     hipLaunchKernelGGL(k_slots_put, dim3((uint32_t)((a.rows + 255) / 256)), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch slots_put");
   }
-  const dim3 grid((a.tokens + per - 1) / per);
+  const dim3 grid(std::min((a.tokens + per - 1) / per, kMaxGrid));
   if (((uint64_t)a.tokens + 2 * a.rows) * a.d * 2 >= kStreamBytes)
     hipLaunchKernelGGL((k_combine_grad<false, true>), grid, dim3(256), 0, s, a);
   else
@@ -593,9 +591,9 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
     return fail(PW_ERR_INVALID, "dlogits, w_router, slot_of and dx are required");
   if (d->rows && !io->dxd) return fail(PW_ERR_INVALID, "dxd is required");
   if (d->tokens && io->dw_router && !io->x) return fail(PW_ERR_INVALID, "dw_router needs x");
-  if (((uintptr_t)io->dxd | (uintptr_t)io->x | (uintptr_t)io->dx) % 16)
-    return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
-  if ((uintptr_t)io->slot_of % 8) return fail(PW_ERR_INVALID, "slot_of must be 8-byte aligned");
+  if (misaligned({io->dxd, io->x, io->dx}, 16)) return fail(PW_ERR_INVALID, "row buffers must be 16-byte aligned");
+  if (misaligned({io->slot_of}, 8) || misaligned({io->dlogits, io->dw_router}, 4) || misaligned({io->w_router}, 2))
+    return fail(PW_ERR_INVALID, "slot_of must be 8-byte aligned, dlogits and dw_router 4-byte, w_router 2-byte");
   const DwLayout l = dw_layout(*d);
   if (io->dw_router && (st = check_workspace(ws, ws_bytes, l.total))) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);

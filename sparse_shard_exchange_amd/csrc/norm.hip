@@ -145,65 +145,67 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
   const uint32_t lane = threadIdx.x % TEAM, nch = a.d / V;
   constexpr uint32_t kTeams = threads_of(TEAM) / TEAM;
   const bool norm_y = kY && a.w_y, gated = kY && a.gate;
-  const uint32_t row = blockIdx.x * kTeams + threadIdx.x / TEAM;
-  const bool live = row < a.rows;  // every thread stays: barriers inside
-  const uint64_t base = (uint64_t)min(row, a.rows - 1) * a.d;
-  const uint64_t gbase = gated ? (uint64_t)(min(row, a.rows - 1) / a.group) * a.d : 0;
-  Chunk<T, V> x[C], y[C], wy[C], g[C], wr[C];  // all requested before any is used
+  for (uint32_t row0 = blockIdx.x * kTeams; row0 < a.rows; row0 += gridDim.x * kTeams) {  // (one turn: see kMaxGrid)
+    const uint32_t row = row0 + threadIdx.x / TEAM;
+    const bool live = row < a.rows;  // every thread stays: barriers inside
+    const uint64_t base = (uint64_t)min(row, a.rows - 1) * a.d;
+    const uint64_t gbase = gated ? (uint64_t)(min(row, a.rows - 1) / a.group) * a.d : 0;
+    Chunk<T, V> x[C], y[C], wy[C], g[C], wr[C];  // all requested before any is used
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const uint64_t ch = (uint64_t)min(lane + c * TEAM, nch - 1) * V;
-    x[c] = load<T, V>(a.x, base + ch);
-    if (kY) y[c] = load<T, V>(a.y, base + ch);
-    if (norm_y) wy[c] = load<T, V>(a.w_y, ch);
-    if (gated) g[c] = load<T, V>(a.gate, gbase + ch);
-    if (kH) wr[c] = load<T, V>(a.w_r, ch);
-  }
-  float ty = a.y_scale;
-  if (norm_y) {
-    float ss[1] = {0.f};
+    for (int c = 0; c < C; ++c) {
+      const uint64_t ch = (uint64_t)min(lane + c * TEAM, nch - 1) * V;
+      x[c] = load<T, V>(a.x, base + ch);
+      if (kY) y[c] = load<T, V>(a.y, base + ch);
+      if (norm_y) wy[c] = load<T, V>(a.w_y, ch);
+      if (gated) g[c] = load<T, V>(a.gate, gbase + ch);
+      if (kH) wr[c] = load<T, V>(a.w_r, ch);
+    }
+    float ty = a.y_scale;
+    if (norm_y) {
+      float ss[1] = {0.f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (lane + c * TEAM < nch)
+      for (int c = 0; c < C; ++c)
+        if (lane + c * TEAM < nch)
 #pragma unroll
-        for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
-    team_sum(ss, ex, turn);
-    ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
-  }
-  float r[C][V], ss[1] = {0.f};
+          for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
+      team_sum(ss, ex, turn);
+      ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+    }
+    float r[C][V], ss[1] = {0.f};
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float f = a.x_scale * at<T, V>(x[c], v);
-      if (kY) {
-        float n = ty * at<T, V>(y[c], v);
-        if (norm_y) n *= at<T, V>(wy[c], v);
-        f = gated ? fmaf(n, at<T, V>(g[c], v), f) : f + n;
+      for (int v = 0; v < V; ++v) {
+        float f = a.x_scale * at<T, V>(x[c], v);
+        if (kY) {
+          float n = ty * at<T, V>(y[c], v);
+          if (norm_y) n *= at<T, V>(wy[c], v);
+          f = gated ? fmaf(n, at<T, V>(g[c], v), f) : f + n;
+        }
+        r[c][v] = f;
+        if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
       }
-      r[c][v] = f;
-      if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
     }
-  }
-  float s = 0.f;
-  if (kH) {
-    team_sum(ss, ex, turn);
-    s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const uint32_t ch = lane + c * TEAM;
-    if (!live || ch >= nch) continue;
-    Chunk<T, V> o;
-    if (a.r) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v]);
-      store<T, V>(a.r, base + (uint64_t)ch * V, o);
-    }
+    float s = 0.f;
     if (kH) {
+      team_sum(ss, ex, turn);
+      s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+    }
 #pragma unroll
-      for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v] * s * at<T, V>(wr[c], v));
-      store<T, V>(a.h, base + (uint64_t)ch * V, o);
+    for (int c = 0; c < C; ++c) {
+      const uint32_t ch = lane + c * TEAM;
+      if (!live || ch >= nch) continue;
+      Chunk<T, V> o;
+      if (a.r) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v]);
+        store<T, V>(a.r, base + (uint64_t)ch * V, o);
+      }
+      if (kH) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v] * s * at<T, V>(wr[c], v));
+        store<T, V>(a.h, base + (uint64_t)ch * V, o);
+      }
     }
   }
 }
@@ -411,7 +413,9 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a) {
   for (uint32_t i = 0; i < kJoinSlices; ++i) v += s[i][c];
   if (what == 0) a.dw_r[col] = v;
   else if (what == 1) a.dw_y[col] = v * a.y_scale;
-  else a.dgate[(uint64_t)(what - 2) * a.d + col] = v * a.y_scale * (a.w_y ? (float)static_cast<const T*>(a.w_y)[col] : 1.f);
+  else
+    a.dgate[(uint64_t)(what - 2) * a.d + col] =
+        v * a.y_scale * (a.w_y ? (float)static_cast<const T*>(a.w_y)[col] : 1.f);
 }
 
 // Zeroes the parameter gradients of a call without rows.
@@ -520,13 +524,10 @@ int validate_parts(const pw_norm_desc& d, const pw_norm_io* io) {
   if (!io->y && (io->w_y || io->gate)) return fail(PW_ERR_INVALID, "w_y and gate need y");
   if (!io->gate != !d.gates) return fail(PW_ERR_INVALID, "gate is given if and only if gates is above zero");
   if (!io->y && !io->w_r) return fail(PW_ERR_INVALID, "nothing to do: neither y nor w_r is given");
+  if (misaligned({io->x, io->y, io->w_y, io->gate, io->w_r, io->r, io->h, io->dr, io->dh, io->dx, io->dy},
+                 d.dtype == PW_F32 ? 4 : 2) || misaligned({io->dw_y, io->dgate, io->dw_r}, 4))
+    return fail(PW_ERR_INVALID, "a buffer is not aligned to its elements");
   return PW_OK;
-}
-
-bool aligned16(std::initializer_list<const void*> ps) {
-  uintptr_t v = 0;
-  for (const void* p : ps) v |= (uintptr_t)p;
-  return v % 16 == 0;
 }
 
 NormArgs args(const pw_norm_desc& d, const pw_norm_io& io) {
@@ -565,7 +566,7 @@ void launch(const NormArgs& a, bool grad, hipStream_t s) {
     const size_t lds = teams > 1 ? (size_t)teams * a.d * 4 : 0;
     hipLaunchKernelGGL((k_norm_grad<T, V, C, TEAM, kY, kH>), dim3(a.grid), dim3(NT), lds, s, a);
   } else {
-    const uint32_t blocks = (a.rows + teams - 1) / teams;
+    const uint32_t blocks = std::min((a.rows + teams - 1) / teams, kMaxGrid);
     hipLaunchKernelGGL((k_norm<T, V, C, TEAM, kY, kH>), dim3(blocks), dim3(NT), 0, s, a);
   }
 }
@@ -619,7 +620,7 @@ extern "C" int pw_block_norm(const pw_norm_desc* d, const pw_norm_io* io, void* 
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = check_stream(s))) return st;
   const NormArgs a = args(*d, *io);
-  const hipError_t e = launch_any(a, *d, aligned16({a.x, a.y, a.w_y, a.gate, a.w_r, a.r, a.h}), false, s);
+  const hipError_t e = launch_any(a, *d, !misaligned({a.x, a.y, a.w_y, a.gate, a.w_r, a.r, a.h}, 16), false, s);
   return e == hipSuccess ? PW_OK : hip_fail(e, "launch norm");
 }
 
@@ -668,8 +669,9 @@ extern "C" int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, v
     a.part_q = reinterpret_cast<float*>(base + l.q);
   }
   // without a next norm the gradient of h plays no part
-  e = launch_any(a, *d, aligned16({a.y, a.w_y, a.gate, a.w_r, a.w_r ? a.r_in : nullptr, a.dr, a.w_r ? a.dh : nullptr,
-                                   a.dx, a.dy}), true, s);
+  const bool aligned = !misaligned({a.y, a.w_y, a.gate, a.w_r, a.w_r ? a.r_in : nullptr, a.dr,
+                                    a.w_r ? a.dh : nullptr, a.dx, a.dy}, 16);
+  e = launch_any(a, *d, aligned, true, s);
   if (e != hipSuccess) return hip_fail(e, "launch norm_grad");
   const bool gates = a.gate && a.segs > 1;
   if ((a.grid > 1 && (a.dw_r || a.dw_y)) || gates) {

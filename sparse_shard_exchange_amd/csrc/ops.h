@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <initializer_list>
+
 #include "device.h"
 #include "runtime.h"
 
@@ -32,7 +34,19 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+// Workgroups of a launch at most: a dimension of the grid holds fewer than 2^32
+// threads, of workgroups of up to 1024. Kernels that are launched with one
+// workgroup for each piece of work walk on from there in steps of the grid.
+constexpr uint32_t kMaxGrid = 1u << 21;
+
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Whether an address is no multiple of `bytes` (NULL is one).
+inline bool misaligned(std::initializer_list<const void*> ps, uintptr_t bytes) {
+  uintptr_t v = 0;
+  for (const void* p : ps) v |= (uintptr_t)p;
+  return v % bytes != 0;
+}
 
 // The caller's workspace holds `need` bytes (need 0: none is looked at).
 inline int check_workspace(const void* ws, size_t ws_bytes, size_t need) {

@@ -176,6 +176,19 @@ def test_offsets_past_32_bits(gpu):
     check_grad((one[0], one[1], got[2], None, got[4]), s, r2.cpu(), 1.0, 1.0)
 
 
+def test_more_rows_than_a_grid_has_threads(gpu):
+    """70 million short rows: the workgroups walk on."""
+    rows, d = 70_000_000, 2
+    assert rows // 4 * 256 >= 1 << 32
+    s = make(1000, d, "bf16", 0, "ywh")
+    c = {n: cuda(t) for n, t in s.items()}
+    x, y = c["x"].repeat(rows // 1000, 1), c["y"].repeat(rows // 1000, 1)
+    r, h = gpu.BlockNorm(rows, d, eps=EPS).forward(x, y=y, w_y=c["w_y"], w_r=c["w_r"])
+    r2, h2 = gpu.BlockNorm(1000, d, eps=EPS).forward(c["x"], y=c["y"], w_y=c["w_y"], w_r=c["w_r"])
+    check_forward((r2, h2), s, 1.0, 1.0)
+    assert bool((r.view(-1, 1000, d) == r2).all()) and bool((h.view(-1, 1000, d) == h2).all())
+
+
 def test_zero_rows_and_zero_vectors(gpu):
     f = gpu.BlockNorm(0, 64, gpu.PW_F32, 2)
     e, w, g = torch.empty(0, 64, device="cuda"), torch.ones(64, device="cuda"), torch.ones(2, 64, device="cuda")

@@ -97,7 +97,7 @@ def test_combine_and_dispatch_gradients(gpu, T, d, E, cap, masked):
         for n in ("dout", "x"):
             s2[n][bad] = float("nan")
         s2["gates"][bad] = float("inf")
-        s2["dlogits"][bad] = 0.0
+        s2["dlogits"][bad] = float("nan")
         s["dlogits"][bad] = 0.0
         a, b, before, c, f = run(gpu, s2)
     else:
@@ -237,6 +237,27 @@ def test_offsets_past_32_bits(gpu):
     assert torch.equal(p[0][-k:], q[0]) and not p[0][:T - k].any()
     size = x.double().abs().t().contiguous() @ dl.double().abs()
     assert bool(((p[1].double() - x.double().t().contiguous() @ dl.double()).abs() <= 200 * U * size).all())
+
+
+def test_more_tokens_than_a_grid_has_threads(gpu):
+    """2^27 tokens of a few kept tuples: the workgroups walk on."""
+    T, d, E, k = (1 << 27) + 40, 256, 4, 24
+    assert (T + 7) // 8 * 256 >= 1 << 32
+    rng = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=rng, device="cuda")  # noqa: E731
+    src = torch.cat([torch.arange(0, k // 2), torch.arange(2 * T - k // 2, 2 * T)]).int().cuda()  # the first and last tokens
+    offsets = torch.full((E + 1,), k, dtype=torch.int64, device="cuda")
+    y, ends = rnd(k, d).to(bf), rnd(k // 2, d).to(bf)
+    dout = torch.zeros(T, d, dtype=bf, device="cuda")
+    dout[:k // 4], dout[-(k // 4):] = ends[:k // 4], ends[k // 4:]
+    gates = torch.full((T, 2), 0.5, device="cuda")
+    dy, dg, slot_of = gpu.MoEGrad(T, d, E, rows=k).combine(dout, y, gates, src, offsets)
+    per_row = ends.repeat_interleave(2, dim=0)
+    assert torch.equal(dy, (per_row.float() * 0.5).to(bf))
+    want = (per_row.double() * y.double()).sum(1)
+    got = torch.cat([dg[:k // 4].view(-1), dg[-(k // 4):].view(-1)]).double()
+    assert bool(((got - want).abs() <= 64 * U * (per_row.double() * y.double()).abs().sum(1)).all())
+    assert not dg[k // 4:-(k // 4)].any() and bool((slot_of[k // 4:-(k // 4)] == -1).all())
 
 
 def test_refusals(gpu):

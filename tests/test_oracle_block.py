@@ -148,6 +148,15 @@ def test_balance_buffer_errors():
     assert pw.lib.pw_router_grad(C.byref(d), C.byref(io), None) == INV   # gates without experts
 
 
+@pytest.mark.parametrize("name", ["logits", "experts", "counts", "loss", "gates", "dgates", "grad_loss", "dlogits"])
+def test_balance_refuses_split_elements(name):
+    io = pw.pw_balance_io(*([P] * 10))
+    io.valid = None
+    setattr(io, name, P + 2)
+    assert pw.lib.pw_router_balance(C.byref(bal()), C.byref(io), P, 1 << 30, None) == INV
+    assert pw.lib.pw_router_grad(C.byref(bal()), C.byref(io), None) == INV
+
+
 def moe(**kw):
     base = dict(tokens=512, rows=1024, d=512, num_experts=8, top_k=2, dtype=pw.PW_BF16)
     base.update(kw)
@@ -222,6 +231,16 @@ def test_norm_grad_buffer_errors(drop):
     io.valid = None
     setattr(io, drop, None)
     assert pw.lib.pw_block_norm_grad(C.byref(norm(gates=2)), C.byref(io), P, 1 << 30, None) == INV
+
+
+@pytest.mark.parametrize("name,dtype,off", [("x", pw.PW_BF16, 1), ("w_r", pw.PW_F32, 2), ("dh", pw.PW_F32, 2),
+                                            ("dw_y", pw.PW_BF16, 2), ("dx", pw.PW_BF16, 1)])
+def test_norm_refuses_split_elements(name, dtype, off):
+    io = pw.pw_norm_io(*([P] * 15))
+    io.valid = None
+    setattr(io, name, P + off)
+    assert pw.lib.pw_block_norm_grad(C.byref(norm(gates=2, dtype=dtype)), C.byref(io), P, 1 << 30, None) == INV
+    assert pw.lib.pw_block_norm(C.byref(norm(gates=2, dtype=dtype)), C.byref(io), None) == INV
 
 
 def test_norm_grad_workspace_errors():
