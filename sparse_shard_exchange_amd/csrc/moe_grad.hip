@@ -43,7 +43,7 @@ struct DispatchGradArgs {
   const uint8_t* valid;
   __bf16* dx;
   float* dw;
-  float* part;         // [splits][d][Ep] partial sums of dw
+  float* part;         // [splits][d / 256][Ep][256] partial sums of dw
   uint64_t rows;
   uint32_t tokens, d, E;
   uint32_t splits;     // token ranges of dw
@@ -209,21 +209,37 @@ constexpr uint32_t kDxCols = 128;
 constexpr uint32_t kDxGrid = 256;  // workgroups: one per CU
 
 typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4_at4;  // loads of 16 bytes need 4-byte alignment
 
-// W[c][e0 .. e0 + 7], zero where there is no expert.
+// Where the four inner positions from e on begin: experts past the last are
+// reached by moving back (positions already covered get zeros of W), so that a
+// row of dl is read in whole 16-byte loads, however many experts there are.
+__device__ __forceinline__ uint32_t four_from(uint32_t e, uint32_t E) { return min(e, E - 4); }
+
+// W[c] at the inner positions e0 .. e0 + 7, zero where there is no expert or
+// an earlier position holds it.
+template <bool kFour>
 __device__ __forceinline__ bf16x8 load_w(const DispatchGradArgs& a, uint32_t c, uint32_t e0) {
+  const __bf16* row = a.w + (uint64_t)c * a.E;
   bf16x8 v = {};
   if (a.whole_w) {  // uniform
-    if (e0 < a.E) v = *reinterpret_cast<const bf16x8*>(a.w + (uint64_t)c * a.E + e0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e0 + j < a.E) v[j] = a.w[(uint64_t)c * a.E + e0 + j];
+    if (e0 < a.E) v = *reinterpret_cast<const bf16x8*>(row + e0);
+    return v;
   }
+  uint32_t at[8];
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j) {
+    const uint32_t e = e0 + (j & ~3u);
+    at[j] = kFour ? four_from(e, a.E) + (j & 3) : min(e0 + j, a.E - 1);
+    v[j] = row[at[j]];
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < 8; ++j)
+    if (kFour ? at[j] < e0 + (j & ~3u) : e0 + j >= a.E) v[j] = (__bf16)0.f;
   return v;
 }
 
-template <int KS, bool kVec, bool kStream>  // steps of 32 experts; whole aligned 16-byte chunks of a row of dl
+template <int KS, bool kFour, bool kStream>  // steps of 32 experts; at least 4 experts
 __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a) {
   extern __shared__ __attribute__((aligned(16))) bf16x8 lds_w[];  // [column block][b][s][64 lanes]
   const uint32_t lane = threadIdx.x & 63, i = lane & 15, h = lane >> 4;
@@ -232,7 +248,7 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
   const uint32_t streams = gridDim.x / a.col_groups * kDxWaves;
   for (uint32_t o = threadIdx.x; o < blocks * 8 * KS * 64; o += kDxThreads) {
     const uint32_t l = o & 63, f = o >> 6, s = f % KS, b = f / KS % 8, cb = block0 + f / (KS * 8);
-    lds_w[o] = load_w(a, cb * kDxCols + 8 * (l & 15) + b, 32 * s + 8 * (l >> 4));
+    lds_w[o] = load_w<kFour>(a, cb * kDxCols + 8 * (l & 15) + b, 32 * s + 8 * (l >> 4));
   }
   __syncthreads();
   for (uint32_t tile = blockIdx.x / a.col_groups * kDxWaves + (threadIdx.x >> 6); tile < tiles; tile += streams) {
@@ -245,10 +261,10 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
     for (int s = 0; s < KS; ++s) {
       const uint32_t e0 = 32 * s + 8 * h;  // past the last expert: repeated values, against zeros of W
       float v[8];
-      if (kVec) {
+      if (kFour) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(row + min(e0 + 4 * q, a.E - 4));
+          const f32x4 x = *reinterpret_cast<const f32x4_at4*>(row + four_from(e0 + 4 * q, a.E));
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[4 * q + j] = x[j];
         }
@@ -334,7 +350,7 @@ constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, 
 
 template <int NC, bool kStream>  // expert blocks of 32
 __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
-  extern __shared__ float lds[];  // [kDwCols][32 NC]
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // [32 NC][kDwCols]
   constexpr uint32_t Ep = 32 * NC;
   const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
   const uint32_t groups = a.d / kDwCols;
@@ -414,40 +430,50 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
         for (int q = 0; q < 4; ++q)
           acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], dt[c][m], acc[q][c], 0, 0, 0);
   }
+  // The token waves add up in LDS, [expert][256 columns], one after the other. A
+  // lane's four operands of one register are 4 consecutive columns: 16-byte
+  // accesses, their chunks permuted by expert so that 16 lanes meet 64 banks.
+  auto chunk = [&](uint32_t e, uint32_t c) { return reinterpret_cast<f32x4*>(lds + e * kDwCols + 4 * (c ^ (e & 15))); };
   for (uint32_t turn = 0; turn < 4; ++turn) {
     if (tw == turn)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const uint32_t row = (r >> 2) * 8 + h * 4 + (r & 3);
-            float* p = lds + (cw * 128 + 4 * row + q) * Ep + 32 * c + i;
-            *p = turn ? *p + acc[q][c][r] : acc[q][c][r];
-          }
+        for (int r = 0; r < 16; ++r) {
+          f32x4* p = chunk(32 * c + i, cw * 32 + 8 * (r >> 2) + 4 * h + (r & 3));
+          const f32x4 v = {acc[0][c][r], acc[1][c][r], acc[2][c][r], acc[3][c][r]};
+          *p = turn ? *p + v : v;
+        }
     __syncthreads();
   }
-  const uint32_t c0 = cg * kDwCols;
-  if (a.splits == 1) {
-    for (uint32_t o = threadIdx.x; o < kDwCols * Ep; o += kDwThreads)
-      if (o % Ep < a.E) a.dw[(uint64_t)(c0 + o / Ep) * a.E + o % Ep] = lds[o];
-  } else {
-    float* part = a.part + ((uint64_t)split * a.d + c0) * Ep;
-    for (uint32_t o = threadIdx.x; o < kDwCols * Ep; o += kDwThreads) part[o] = lds[o];
+  if (a.splits == 1) {  // dw itself, an expert per lane
+    for (uint32_t o = threadIdx.x; o < Ep * kDwCols; o += kDwThreads) {
+      const uint32_t e = o % Ep, c = o / Ep;
+      if (e < a.E) a.dw[(uint64_t)(cg * kDwCols + c) * a.E + e] = reinterpret_cast<const float*>(chunk(e, c / 4))[c % 4];
+    }
+    return;
   }
+  float* part = a.part + ((uint64_t)split * groups + cg) * Ep * kDwCols;
+  for (uint32_t o = threadIdx.x; o < Ep * kDwCols / 4; o += kDwThreads)
+    *reinterpret_cast<f32x4*>(part + 4 * o) = *chunk(o / (kDwCols / 4), o % (kDwCols / 4));
 }
 
-// Adds the partial sums of the token ranges, in order.
+// Adds the partial sums of the token ranges: 64 columns of one expert per
+// workgroup, 4 slices of the ranges, in a fixed order.
 template <int NC>
 __global__ __launch_bounds__(256) void k_router_dw_join(DispatchGradArgs a) {
+  __shared__ float s[4][64];
   constexpr uint32_t Ep = 32 * NC;
-  const uint32_t o = blockIdx.x * 256 + threadIdx.x;  // d is a multiple of 256: no rest
+  const uint32_t lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const uint32_t o = blockIdx.x * 64 + lane, e = o / kDwCols % Ep, col = o / (kDwCols * Ep) * kDwCols + o % kDwCols;
+  if (e >= a.E) return;  // whole workgroups
   const uint64_t n = (uint64_t)a.d * Ep;
-  float s = 0.f;
-#pragma unroll 8
-  for (uint32_t i = 0; i < a.splits; ++i) s += a.part[i * n + o];
-  if (o % Ep < a.E) a.dw[(uint64_t)(o / Ep) * a.E + o % Ep] = s;
+  float v = 0.f;
+#pragma unroll 16
+  for (uint32_t i = slice; i < a.splits; i += 4) v += a.part[i * n + o];
+  s[slice][lane] = v;
+  __syncthreads();
+  if (slice == 0) a.dw[(uint64_t)col * a.E + e] = s[0][lane] + s[1][lane] + s[2][lane] + s[3][lane];
 }
 
 // Zeroes dw (a call without tokens).
@@ -458,21 +484,21 @@ __global__ __launch_bounds__(256) void k_router_dw_zero(DispatchGradArgs a) {
 
 constexpr size_t kDefaultLds = 64 << 10;  // what a kernel may use without asking
 
-template <int KS, bool kVec, bool kStream>
+template <int KS, bool kFour, bool kStream>
 hipError_t launch_dx_steps(const DispatchGradArgs& a, uint32_t grid, hipStream_t s) {
   const size_t lds = (size_t)a.d / a.col_groups * KS * 64;
   if (lds > kDefaultLds) {
-    const hipError_t e = hipFuncSetAttribute((const void*)k_dispatch_grad<KS, kVec, kStream>,
+    const hipError_t e = hipFuncSetAttribute((const void*)k_dispatch_grad<KS, kFour, kStream>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_dispatch_grad<KS, kVec, kStream>), dim3(grid), dim3(kDxThreads), lds, s, a);
+  hipLaunchKernelGGL((k_dispatch_grad<KS, kFour, kStream>), dim3(grid), dim3(kDxThreads), lds, s, a);
   return hipGetLastError();
 }
 
-template <int KS, bool kVec>
+template <int KS, bool kFour>
 hipError_t launch_dx_loads(const DispatchGradArgs& a, uint32_t grid, bool stream, hipStream_t s) {
-  return stream ? launch_dx_steps<KS, kVec, true>(a, grid, s) : launch_dx_steps<KS, kVec, false>(a, grid, s);
+  return stream ? launch_dx_steps<KS, kFour, true>(a, grid, s) : launch_dx_steps<KS, kFour, false>(a, grid, s);
 }
 
 hipError_t launch_dx(DispatchGradArgs& a, bool stream, hipStream_t s) {
@@ -480,11 +506,11 @@ hipError_t launch_dx(DispatchGradArgs& a, bool stream, hipStream_t s) {
   // With a tile for every wave of the GPU a workgroup keeps all of W and a wave
   // takes whole rows; below that the column blocks go to different workgroups.
   a.col_groups = tiles >= kDxGrid * kDxWaves ? 1 : blocks;
-  const uint32_t grid = std::min(kDxGrid * (a.col_groups > 1 ? 2 : 1) / a.col_groups, (tiles + kDxWaves - 1) / kDxWaves) * a.col_groups;
-  a.whole_w = a.E % 8 == 0 && (uintptr_t)a.w % 16 == 0;
-  const bool vec = a.E % 4 == 0 && (uintptr_t)a.dlogits % 16 == 0;
-  if (a.E <= 32) return vec ? launch_dx_loads<1, true>(a, grid, stream, s) : launch_dx_loads<1, false>(a, grid, stream, s);
-  return vec ? launch_dx_loads<2, true>(a, grid, stream, s) : launch_dx_loads<2, false>(a, grid, stream, s);
+  const uint32_t most = kDxGrid * (a.col_groups > 1 ? 2 : 1) / a.col_groups;
+  const uint32_t grid = std::min(most, (tiles + kDxWaves - 1) / kDxWaves) * a.col_groups;
+  a.whole_w = a.E % 8 == 0 && !misaligned({a.w}, 16);
+  if (a.E < 4) return launch_dx_loads<1, false>(a, grid, stream, s);
+  return a.E <= 32 ? launch_dx_loads<1, true>(a, grid, stream, s) : launch_dx_loads<2, true>(a, grid, stream, s);
 }
 
 struct DwLayout {
@@ -634,7 +660,7 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
   else hipLaunchKernelGGL((k_router_dw<1, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
   if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw");
   if (a.splits > 1) {
-    const uint32_t jb = a.d * (two ? 64 : 32) / 256;
+    const uint32_t jb = a.d * (two ? 64 : 32) / 64;
     if (two) hipLaunchKernelGGL(k_router_dw_join<2>, dim3(jb), dim3(256), 0, s, a);
     else hipLaunchKernelGGL(k_router_dw_join<1>, dim3(jb), dim3(256), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw_join");

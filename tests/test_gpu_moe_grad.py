@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 U, HALF = 2.0 ** -24, 2.0 ** -8
 bf = torch.bfloat16
 
-CASES = [(1, 256, 2, 0), (1, 256, 64, 1), (7, 512, 5, 0), (33, 256, 33, 1), (300, 1280, 8, 0), (300, 512, 64, 6),
+CASES = [(1, 256, 2, 0), (50, 256, 3, 0), (50, 512, 4, 0), (70, 256, 6, 0), (70, 256, 31, 0), (90, 256, 34, 0), (1, 256, 64, 1), (7, 512, 5, 0), (33, 256, 33, 1), (300, 1280, 8, 0), (300, 512, 64, 6),
          (1000, 256, 5, 350), (1003, 768, 12, 0), (4097, 1024, 64, 100), (5000, 256, 64, 0),
          (65600, 256, 5, 0), (66001, 512, 64, 2000)]   # more tiles than waves
 
