@@ -518,13 +518,17 @@ struct DwLayout {
   size_t total = 0;
 };
 
-constexpr uint32_t kDwGrid = 256;  // workgroups wanted: one per CU
+// Token ranges of dw: one workgroup per CU for long batches; short ones are cut
+// into 16 ranges of up to 256 tokens, as a range costs a partial sum of 64 KiB
+// (3000 x 1024: 22.2 us the whole call against 25.2 with ranges of 64 tokens).
+constexpr uint32_t kDwGrid = 256;
+constexpr uint64_t kDwShort = 256;
 
 DwLayout dw_layout(const pw_moe_grad_desc& d) {
   DwLayout l;
   const uint32_t groups = d.d / kDwCols;
   const uint64_t want = std::max<uint64_t>(1, kDwGrid / groups);
-  const uint64_t per = (d.tokens + want - 1) / want;
+  const uint64_t per = std::max((d.tokens + want - 1) / want, std::min(kDwShort, (d.tokens + 15) / 16));
   l.split_tokens = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(64, (per + 63) / 64 * 64), kDwMaxTokens);
   l.splits = (uint32_t)std::max<uint64_t>(1, (d.tokens + l.split_tokens - 1) / l.split_tokens);
   if (l.splits > 1) l.total = up256((size_t)l.splits * d.d * (d.num_experts > 32 ? 64 : 32) * 4);

@@ -63,6 +63,11 @@ def check_combine(got, s, kept, before):
     assert np.all(np.abs(f64(dg) - dgw) <= 64 * U * size)
 
 
+def token_range(T, d):
+    """Tokens of one partial sum of dw_router."""
+    return -(-max(64, -(-T // (256 // (d // 256))), min(256, -(-T // 16))) // 64) * 64
+
+
 def check_dispatch(got, s, kept):
     slot_of = ob.slots(s["src_index"].numpy(), kept, s["x"].shape[0])
     valid = None if s["valid"] is None else s["valid"].numpy()
@@ -71,7 +76,7 @@ def check_dispatch(got, s, kept):
     assert np.all(np.abs(f64(got[0].cpu()) - dx) <= bound + HALF * (np.abs(dx) + bound) + 1e-38)
     if got[1] is not None:
         T, d = s["x"].shape
-        span = -(-max(64, -(-T // (256 // (d // 256)))) // 64) * 64
+        span = token_range(T, d)
         assert np.all(np.abs(f64(got[1].cpu()) - dw) <= (48 * span // 64 + -(-T // span) + 8) * U * dws + 1e-38)
 
 
@@ -206,7 +211,7 @@ def test_rows_beyond_the_caches(gpu, T, d, E):
         assert bool(((dx[lo:hi].double() - part).abs() <= bound + HALF * (part.abs() + bound) + 1e-38).all())
         want_dw += x64.t().contiguous() @ dl64
         terms += x64.abs().t().contiguous() @ dl64.abs()
-    span = -(-max(64, -(-T // (256 // (d // 256)))) // 64) * 64
+    span = token_range(T, d)
     assert bool(((dw.double() - want_dw).abs() <= (48 * span // 64 + -(-T // span) + 8) * U * terms).all())
 
 
