@@ -350,7 +350,7 @@ constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, 
 
 template <int NC, bool kStream>  // expert blocks of 32
 __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];  // [32 NC][kDwCols]
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // [2][32 NC][kDwCols]
   constexpr uint32_t Ep = 32 * NC;
   const uint32_t lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
   const uint32_t groups = a.d / kDwCols;
@@ -430,17 +430,20 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
         for (int q = 0; q < 4; ++q)
           acc[q][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[q], dt[c][m], acc[q][c], 0, 0, 0);
   }
-  // The token waves add up in LDS, [expert][256 columns], one after the other. A
-  // lane's four operands of one register are 4 consecutive columns: 16-byte
-  // accesses, their chunks permuted by expert so that 16 lanes meet 64 banks.
-  auto chunk = [&](uint32_t e, uint32_t c) { return reinterpret_cast<f32x4*>(lds + e * kDwCols + 4 * (c ^ (e & 15))); };
-  for (uint32_t turn = 0; turn < 4; ++turn) {
-    if (tw == turn)
+  // The token waves add up in two tables in LDS, [expert][256 columns]: 0 and 2
+  // in one, 1 and 3 in the other. A lane's four operands of one register are 4
+  // consecutive columns: 16-byte accesses, their chunks permuted by expert so
+  // that 16 lanes meet 64 banks.
+  auto chunk = [&](uint32_t table, uint32_t e, uint32_t c) {
+    return reinterpret_cast<f32x4*>(lds + (table * Ep + e) * kDwCols + 4 * (c ^ (e & 15)));
+  };
+  for (uint32_t turn = 0; turn < 2; ++turn) {
+    if (tw >> 1 == turn)
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          f32x4* p = chunk(32 * c + i, cw * 32 + 8 * (r >> 2) + 4 * h + (r & 3));
+          f32x4* p = chunk(tw & 1, 32 * c + i, cw * 32 + 8 * (r >> 2) + 4 * h + (r & 3));
           const f32x4 v = {acc[0][c][r], acc[1][c][r], acc[2][c][r], acc[3][c][r]};
           *p = turn ? *p + v : v;
         }
@@ -449,13 +452,17 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   if (a.splits == 1) {  // dw itself, an expert per lane
     for (uint32_t o = threadIdx.x; o < Ep * kDwCols; o += kDwThreads) {
       const uint32_t e = o % Ep, c = o / Ep;
-      if (e < a.E) a.dw[(uint64_t)(cg * kDwCols + c) * a.E + e] = reinterpret_cast<const float*>(chunk(e, c / 4))[c % 4];
+      if (e >= a.E) continue;
+      const float* p0 = reinterpret_cast<const float*>(chunk(0, e, c / 4)) + c % 4;
+      const float* p1 = reinterpret_cast<const float*>(chunk(1, e, c / 4)) + c % 4;
+      a.dw[(uint64_t)(cg * kDwCols + c) * a.E + e] = *p0 + *p1;
     }
     return;
   }
   float* part = a.part + ((uint64_t)split * groups + cg) * Ep * kDwCols;
   for (uint32_t o = threadIdx.x; o < Ep * kDwCols / 4; o += kDwThreads)
-    *reinterpret_cast<f32x4*>(part + 4 * o) = *chunk(o / (kDwCols / 4), o % (kDwCols / 4));
+    *reinterpret_cast<f32x4*>(part + 4 * o) = *chunk(0, o / (kDwCols / 4), o % (kDwCols / 4)) +
+                                              *chunk(1, o / (kDwCols / 4), o % (kDwCols / 4));
 }
 
 // Adds the partial sums of the token ranges: 64 columns of one expert per
@@ -656,8 +663,12 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
   if (!a.dw) return PW_OK;
   const bool two = a.E > 32;
   const uint32_t grid = 8 * (a.d / kDwCols) * ((a.splits + 7) / 8);
-  const size_t lds = (size_t)kDwCols * (two ? 64 : 32) * 4;
-  static_assert(kDwCols * 64 * 4 <= kDefaultLds, "no larger dynamic LDS to ask for");
+  const size_t lds = (size_t)2 * kDwCols * (two ? 64 : 32) * 4;
+  if (lds > kDefaultLds) {
+    const void* fn = stream_rows ? (const void*)k_router_dw<2, true> : (const void*)k_router_dw<2, false>;
+    if ((e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)
+      return hip_fail(e, "router_dw: dynamic LDS");
+  }
   if (two && stream_rows) hipLaunchKernelGGL((k_router_dw<2, true>), dim3(grid), dim3(kDwThreads), lds, s, a);
   else if (two) hipLaunchKernelGGL((k_router_dw<2, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
   else if (stream_rows) hipLaunchKernelGGL((k_router_dw<1, true>), dim3(grid), dim3(kDwThreads), lds, s, a);

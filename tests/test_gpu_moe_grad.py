@@ -153,8 +153,9 @@ def test_router_weights_that_are_not_16_byte_aligned(gpu):
     check_dispatch(f.dispatch(c["dxd"], c["dlogits"], w, c["x"]), s, kept)
 
 
-def test_a_replayed_graph_and_another_stream(gpu):
-    T, d, E, cap = 6000, 512, 16, 700
+@pytest.mark.parametrize("E,cap", [(16, 700), (64, 150)])
+def test_a_replayed_graph_and_another_stream(gpu, E, cap):
+    T, d = 6000, 512
     data = [make(T, d, E, cap, seed) for seed in range(4)]
     a, b, before, c, f = run(gpu, data[0][0])
     dy = a[0]
