@@ -430,13 +430,13 @@ __global__ __launch_bounds__(kThreads) void k_norm_zero(NormArgs a) {
 
 // The kernel variant of a row: elements per chunk, chunks per thread, threads
 // per row. At most 8 elements a thread, so that the gradient's registers (rows,
-// sums, weights) leave room for 4 waves per SIMD (131072 x 1024 bf16 with 16
-// elements and one wave a row: the same 340 us, with 192 registers; 2047 x 1001
-// fp32 with 256 threads: 42 us against 16). From 4096 on rows of 4-byte chunks
-// take 16 elements by 512 threads (8192 x 8192 fp32 back: 405 us against 570 by
-// 1024 threads of 8, 4000 x 8191 bf16: 221 against 507; 16384 x 8192 bf16 in
-// whole chunks: 505 against 477). Rows that are not whole aligned 16-byte
-// chunks go by single elements.
+// sums, weights) leave room for 4 waves per SIMD (2047 x 1001 fp32 by 256
+// threads with room for 8 elements each, half of it unused: 42 us against 16).
+// Above 4096 elements rows of 4-byte chunks take 16 elements by 512 threads: 1024
+// threads of 8 spill (backward, 8192 x 8192 fp32: 570 us against 405, 4000 x
+// 8191 bf16 507 against 221; 8192 bf16 in whole chunks is the other way round,
+// 477 against 505; all before the rows were dealt in turn). Rows that are not
+// whole aligned 16-byte chunks go by single elements.
 struct Shape {
   int V, C, team;
 };
