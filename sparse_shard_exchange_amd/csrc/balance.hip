@@ -9,8 +9,8 @@
 // Both kernels read each logit once: a token's row is spread over a group of
 // L lanes of 4 experts each (L = 4, 16, 64 for E <= 16, 64, 256), so a wave's
 // load covers 64 / L whole rows, and the row's maximum, sum and dot product
-// are lane exchanges inside the group. 131072 x 64: loss 12.1 + 4.5 us (35 MB, 2.9
-// TB/s), gradient 18.1 us (70 MB, 3.9 TB/s): reading, with the first loads', the
+// are lane exchanges inside the group. 131072 x 64: loss 12.2 + 4.4 us (35 MB, 2.8
+// TB/s), gradient 18.4 us (70 MB, 3.8 TB/s): reading, with the first loads', the
 // arithmetic's (a quarter) and the launches' latency on top. 48 x 8: 4.2 us, a few
 // memory latencies.
 #include "ops.h"

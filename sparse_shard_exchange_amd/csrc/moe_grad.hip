@@ -55,7 +55,7 @@ struct DispatchGradArgs {
 // Row loads bypass the caches (kStream) where the call's rows are twice the
 // last-level cache (256 MiB) or more, so that none can still be there: combine,
 // 131072 tokens x 1024, 271 us against 276 with plain loads, dispatch 233
-// against 239; below, rows that the caches hold are read from them (16384
+// against 239 (both before later steps); below, rows that the caches hold are read from them (16384
 // tokens: combine 31 us against 37, dispatch 45 against 55). Rows are always
 // stored nontemporally: written plainly, they are written back during the reads
 // of the next kernel (dW after dx: 72 us against 81).
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256) void k_combine_grad(CombineGradArgs a) {
 // contiguous bytes a row. dl is split into two bf16 terms (hi + lo, at most
 // 2^-16 of the value is lost, below the rounding of dx to bf16 at 2^-8), so
 // the products are as exact as dx can show. 131072 tokens x 1024, 64 experts:
-// 154 us, 5.5 TB/s, the rate of a large copy; bound by HBM. (W in registers,
+// 155 us, 5.4 TB/s, the rate of a large copy; bound by HBM. (W in registers,
 // 128 columns a wave, 8 waves per CU: 223 us; one token a lane, 64 bytes of
 // its row: 306 us.)
 constexpr uint32_t kDxThreads = 1024;
@@ -339,8 +339,8 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 // terms, which hold all 24 bits of it: every product is exact and the sums
 // are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
 // of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
-// 131072 tokens x 1024, 64 experts: 70 us, 4.3 TB/s; bound by reading x and dl
-// once from HBM. (Sharing the split terms between the waves through LDS, and
+// 131072 tokens x 1024, 64 experts: 55-58 us, 5.2-5.5 TB/s; bound by reading x
+// and dl once from HBM. (Sharing the split terms between the waves through LDS, and
 // requesting x two steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;

@@ -15,7 +15,7 @@
 // A row lives in the registers of its team (one wave up to 512 elements, up to
 // 16 waves for the widest) from its only read to its only write, so the passes
 // move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
-// bf16, all parts: forward 176 us (6.1 TB/s), backward 310 + 11 us (5.0 TB/s); a
+// bf16, all parts: forward 176 us (6.1 TB/s), backward 308 + 11 us (5.0 TB/s); a
 // large copy reaches 5.2. Rows are stored nontemporally: written plainly, they
 // are written back during the next operator's reads (forward and backward in
 // turn, 131072 rows 527 us against 542, 32768 rows 126 against 135, 16384 rows,
