@@ -534,33 +534,37 @@ def _address(t):
 
 
 class _Operator:
-    """What the plan-less operators share: the device, the workspace, checked
-    arguments, and output buffers, made by the first call that needs them and
-    kept (so every call returns the same tensors; a call that would make them
-    under HIP graph capture is refused: make one call before). Calls of one
-    object share its buffers: order them."""
+    """What the plan-less operators share: the device, checked arguments, and
+    the workspace and output buffers, made by the first call that needs them,
+    on its stream, and kept (so every call returns the same tensors; a call
+    that would make them under HIP graph capture is refused: make one call
+    before). Calls of one object share its buffers: order them, and keep the
+    object until work queued with it on another stream than the first call's,
+    or in a graph, is done."""
 
     def __init__(self, device):
         dev = torch.device(device)
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self._index = self.device.index
         self._buffers = {}
-        self._ws_args = (None, 0)  # address and bytes of the workspace
+        self._ws_args = (None, 0)  # address and bytes of the workspace; None: not made yet
 
-    def _buf(self, name, shape, dtype):
+    def _buf(self, name, shape, dtype, stream):
         b = self._buffers.get(name)
         if b is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise PwError(PW_ERR_STATE, f"the buffer for {name} is made by the first call: make it before capturing")
-            b = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.device)
+            capturing = torch.cuda.is_current_stream_capturing()
+            # a block that other work of the current stream still uses is no buffer for `stream`
+            with torch.cuda.stream(stream):
+                if capturing or torch.cuda.is_current_stream_capturing():
+                    raise PwError(PW_ERR_STATE, f"the buffer for {name} is made by the first call: make it before capturing")
+                b = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.device)
         return b
 
     def _workspace(self, sizer, d):
         need = C.c_size_t(0)
         check(sizer(C.byref(d), C.byref(need)))
         if need.value:
-            self._ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
-            self._ws_args = (self._ws.data_ptr(), need.value)
+            self._ws_bytes, self._ws_args = need.value, None
 
     def _arg(self, name, t, shape, dtype, or_dtype=None):
         """The address of a tensor that must be contiguous, on this device, of
@@ -574,6 +578,9 @@ class _Operator:
                                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _run(self, fn, d, io, stream, ws=False):
+        if ws and self._ws_args is None:
+            b = self._buf("workspace", (self._ws_bytes,), torch.uint8, stream)
+            self._ws_args = (b.data_ptr(), self._ws_bytes)
         args = self._ws_args if ws else ()
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
         if torch.cuda.current_device() == self._index:
@@ -607,9 +614,9 @@ class RouterBalance(_Operator):
         """(counts [E + 1] int32: tuples per expert, then tokens counted;
         prob_mean [E]; loss [2]: balance, z)."""
         io = self._io(logits, experts, valid)
-        counts = self._buf("counts", (self.E + 1,), torch.int32)
-        mean = self._buf("prob_mean", (self.E,), torch.float32)
-        loss = self._buf("loss", (2,), torch.float32)
+        counts = self._buf("counts", (self.E + 1,), torch.int32, stream)
+        mean = self._buf("prob_mean", (self.E,), torch.float32, stream)
+        loss = self._buf("loss", (2,), torch.float32, stream)
         io.counts, io.prob_mean, io.loss = _address(counts), _address(mean), _address(loss)
         self._run(lib.pw_router_balance, self.desc, io, stream, ws=True)
         self._counts = counts
@@ -625,7 +632,7 @@ class RouterBalance(_Operator):
         io.gates = self._arg("gates", gates, (self.T, self.k), torch.float32)
         io.dgates = self._arg("dgates", dgates, (self.T, self.k), torch.float32)
         io.grad_loss = self._arg("grad_loss", grad_loss, (2,), torch.float32)
-        out = self._buf("dlogits", (self.T, self.E), torch.float32)
+        out = self._buf("dlogits", (self.T, self.E), torch.float32, stream)
         io.dlogits = _address(out)
         self._run(lib.pw_router_grad, self.desc, io, stream)
         return out
@@ -660,9 +667,9 @@ class MoEGrad(_Operator):
         n = self._rows(y)
         bf = torch.bfloat16
         if dy is None:
-            dy = self._buf("dy", (self.rows, self.d), bf)[:n]
-        dgates = self._buf("dgates", (self.T, 2), torch.float32)
-        slot_of = self._buf("slot_of", (self.T, 2), torch.int32)
+            dy = self._buf("dy", (self.rows, self.d), bf, stream)[:n]
+        dgates = self._buf("dgates", (self.T, 2), torch.float32, stream)
+        slot_of = self._buf("slot_of", (self.T, 2), torch.int32, stream)
         if src_index.dim() == 1 and src_index.shape[0] > n:
             src_index = src_index[:n]
         io = pw_combine_grad_io()
@@ -685,8 +692,8 @@ class MoEGrad(_Operator):
         bf = torch.bfloat16
         if slot_of is None:
             slot_of = self._slot_of
-        dx = self._buf("dx", (self.T, self.d), bf)
-        dw = self._buf("dw_router", (self.d, self.E), torch.float32) if x is not None else None
+        dx = self._buf("dx", (self.T, self.d), bf, stream)
+        dw = self._buf("dw_router", (self.d, self.E), torch.float32, stream) if x is not None else None
         io = pw_dispatch_grad_io()
         io.dxd = self._arg("dxd", dxd, (n, self.d), bf)
         io.dlogits = self._arg("dlogits", dlogits, (self.T, self.E), torch.float32)
@@ -730,8 +737,8 @@ class BlockNorm(_Operator):
         if y is None and r is not None:
             raise PwError(PW_ERR_INVALID, "r is written with y only")
         if y is not None and r is None:
-            r = self._buf("r", (self.T, self.d), self.dtype)
-        h = self._buf("h", (self.T, self.d), self.dtype) if w_r is not None else None
+            r = self._buf("r", (self.T, self.d), self.dtype, stream)
+        h = self._buf("h", (self.T, self.d), self.dtype, stream) if w_r is not None else None
         io.r = self._arg("r", r, (self.T, self.d), self.dtype)
         io.h = _address(h)
         self._run(lib.pw_block_norm, self.desc, io, stream)
@@ -749,12 +756,12 @@ class BlockNorm(_Operator):
         io.dh = self._arg("dh", dh, rows, self.dtype)
         io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
         if dx is None:
-            dx = self._buf("dx", rows, self.dtype)
+            dx = self._buf("dx", rows, self.dtype, stream)
         io.dx = self._arg("dx", dx, rows, self.dtype)
-        dy = self._buf("dy", rows, self.dtype) if y is not None else None
-        dw_y = self._buf("dw_y", (self.d,), f32) if w_y is not None else None
-        dgate = self._buf("dgate", (self.G, self.d), f32) if gate is not None else None
-        dw_r = self._buf("dw_r", (self.d,), f32) if w_r is not None else None
+        dy = self._buf("dy", rows, self.dtype, stream) if y is not None else None
+        dw_y = self._buf("dw_y", (self.d,), f32, stream) if w_y is not None else None
+        dgate = self._buf("dgate", (self.G, self.d), f32, stream) if gate is not None else None
+        dw_r = self._buf("dw_r", (self.d,), f32, stream) if w_r is not None else None
         io.dy, io.dw_y, io.dgate, io.dw_r = _address(dy), _address(dw_y), _address(dgate), _address(dw_r)
         self._run(lib.pw_block_norm_grad, self.desc, io, stream, ws=True)
         return dx, dy, dw_y, dgate, dw_r
@@ -783,10 +790,14 @@ class MoEBlock:
         self.balance = RouterBalance(moe.T, moe.E, 2, balance_coef, z_coef, device)
         self.grads = MoEGrad(moe.T, moe.d, moe.E, moe.static_rows, device)
 
+        self.h = self._dgates = None  # of forward, of grad_begin
+
     def forward(self, x, valid=None, stream=None):
         """(r, loss [2], counts [E + 1], future of the MoE step); x is kept for the
         backward pass."""
         m = self.moe
+        if m.y.shape[0] < m.static_rows:
+            raise PwError(PW_ERR_STATE, "the block's step needs an MoE with static buffers")
         self.x, self.valid = x, valid
         _, self.h = self.norm_in.forward(x, w_r=self.w_in, stream=stream)
         f = m.step(self.h, stream)
@@ -797,6 +808,8 @@ class MoEBlock:
     def grad_begin(self, dr, stream=None):
         """dy [rows][d], the gradient of the expert outputs moe.y, from dr, that of r."""
         m = self.moe
+        if self.h is None:
+            raise PwError(PW_ERR_STATE, "grad_begin follows a forward")
         self._dx, dout, self._dw_out, self._dgate, _ = self.norm_out.grad(dr, y=m.out, w_y=self.w_out, gate=self.gate,
                                                                           valid=self.valid, stream=stream)
         dy, self._dgates, _ = self.grads.combine(dout, m.y, m.gates, m.src_index, m.offsets, self.valid, stream=stream)
@@ -806,6 +819,8 @@ class MoEBlock:
         """{"x", "w_in", "w_out", "gate", "w_router"} gradients from dxd, that of the
         dispatched rows moe.xd, and grad_loss [2], that of the losses (None: ones)."""
         m = self.moe
+        if self._dgates is None:
+            raise PwError(PW_ERR_STATE, "grad_end follows a grad_begin")
         dl = self.balance.grad(m.logits, m.experts, gates=m.gates, dgates=self._dgates, valid=self.valid,
                                grad_loss=grad_loss, stream=stream)
         dh, dw_router = self.grads.dispatch(dxd, dl, m.w[0], self.h, valid=self.valid, stream=stream)

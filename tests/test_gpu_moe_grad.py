@@ -360,3 +360,20 @@ def test_block_forward_and_backward(gpu, T, E, cap, masked):
     assert off(r[v.cuda()], R.detach()[v]) <= 6 * HALF
     for name, b, k in zip(("x", "w_in", "w_out", "gate", "w_router"), want, (10, 11, 11, 11, 12)):
         assert off(g[name], b.view_as(g[name].cpu())) <= k * HALF, (name, off(g[name], b))
+
+
+def test_block_calls_out_of_order(gpu):
+    T, d, E, H = 64, 256, 4, 256
+    inp = pw_inputs.moe(T, d, E, H)
+    w = inp.w_router.cuda(), inp.w1.cuda(), inp.w2.cuda()
+    x, one = torch.ones(T, d, dtype=bf, device="cuda"), torch.ones(d, dtype=bf, device="cuda")
+    block = gpu.MoEBlock(gpu.MoE(*w, T, num_src_shards=1), one)
+    split = gpu.MoEBlock(gpu.MoE(*w, T, num_src_shards=1, static_buffers=False), one)
+    for call in (lambda: block.grad_begin(x), lambda: block.grad_end(x), lambda: split.forward(x)):
+        with pytest.raises(gpu.PwError) as e:
+            call()
+        assert e.value.code == gpu.PW_ERR_STATE
+    *_, f = block.forward(x)
+    with pytest.raises(gpu.PwError):
+        block.grad_end(x)             # no grad_begin yet
+    gpu.future_wait(f, 60_000_000_000)

@@ -202,6 +202,26 @@ def test_a_first_call_under_capture_is_refused(gpu):
     assert bool((y == 1).all())
 
 
+def test_buffers_belong_to_the_stream_of_the_first_call(gpu):
+    """Memory that was just freed on the current stream may still be in use
+    there: a call on another stream gets none of it."""
+    T, E = 50000, 64
+    f = gpu.RouterBalance(T, E, 2)
+    l, x = torch.zeros(T, E, device="cuda"), torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    freed = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (4 * T * E, 256 * (E + 1) * 8, 4 * E, 8, 4 * (E + 1))]
+    spans = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in freed]
+    torch.cuda.synchronize()
+    del freed
+    side = torch.cuda.Stream()
+    f.loss(l, x, stream=side)
+    f.grad(l, x, stream=side)
+    side.synchronize()
+    assert set(f._buffers) == {"counts", "prob_mean", "loss", "dlogits", "workspace"}
+    for name, b in f._buffers.items():
+        lo, hi = b.data_ptr(), b.data_ptr() + b.numel() * b.element_size()
+        assert all(hi <= s or e <= lo for s, e in spans), name
+
+
 def test_refusals(gpu):
     f = gpu.RouterBalance(16, 8, 2)
     l, x = torch.zeros(16, 8, device="cuda"), torch.zeros(16, 2, dtype=torch.int32, device="cuda")
