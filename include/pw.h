@@ -482,7 +482,8 @@ typedef struct {
 
 typedef struct {
   const void* dxd;          /* [rows][d] gradient of the dispatched rows        */
-  const float* dlogits;     /* [tokens][E] (pw_router_grad)                     */
+  const float* dlogits;     /* [tokens][E] (pw_router_grad); an infinite value makes
+                               its row of dx and its column of dw_router NaN    */
   const void* w_router;     /* [d][E] bf16, as the plan was given it            */
   const void* x;            /* [tokens][d] the step's tokens (with dw_router)   */
   const int32_t* slot_of;   /* [tokens][2] (pw_moe_combine_grad)                */
@@ -508,7 +509,8 @@ int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch_grad_io* i
  * Parts that are NULL drop out: y (r = x_scale x), w_y (y as it is), gate
  * (ones), w_r with h (no next norm). Intermediate values stay fp32; r and h
  * are each rounded once (h is the norm of r before its rounding). The gradient
- * takes r as it was stored. */
+ * takes r as it was stored. A row whose sum of squares passes the range of fp32
+ * counts as one of infinite length. */
 typedef struct {
   uint64_t rows;     /* at most 2^31 - 1; a multiple of gates                   */
   uint32_t d;        /* 1..8192                                                 */
