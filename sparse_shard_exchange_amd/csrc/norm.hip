@@ -12,7 +12,7 @@
 //   Q_g = sum over g's rows of D y t     dgate_g = ay wy Q_g
 //   dwy = ay sum_g gate_g Q_g            dwr = sum dh r s
 //
-// A row lives in the registers of its team (one wave up to 512 elements, up to
+// A row lives in the registers of its team (16 lanes up to 128 elements, up to
 // 16 waves for the widest) from its only read to its only write, so the passes
 // move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
 // bf16, all parts: forward 176 us (6.1 TB/s), backward 308 + 11 us (5.0 TB/s); a
@@ -64,20 +64,31 @@ struct NormArgs {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
-// One chunk of a row: 16 bytes, or one element where rows are not 16-byte
-// aligned. Kept as loaded until it is used.
+// One chunk of a row: 16 bytes, or one element where a row is shorter. Kept as
+// loaded until it is used. At: the chunk in memory, aligned to its elements.
 template <typename T, int V>
 struct Chunk;
 template <>
-struct Chunk<__bf16, 8> { bf16x8 q; };
+struct Chunk<__bf16, 8> {
+  typedef __attribute__((ext_vector_type(8), aligned(2))) __bf16 At;
+  bf16x8 q;
+};
 template <>
-struct Chunk<float, 4> { f32x4 q; };
+struct Chunk<float, 4> {
+  typedef __attribute__((ext_vector_type(4), aligned(4))) float At;
+  f32x4 q;
+};
 template <typename T>
-struct Chunk<T, 1> { T q; };
+struct Chunk<T, 1> {
+  typedef T At;
+  T q;
+};
 
-template <typename T, int V>
+template <typename T, int V, bool kWhole>
 __device__ __forceinline__ Chunk<T, V> load(const void* base, uint64_t off) {
-  return *reinterpret_cast<const Chunk<T, V>*>(static_cast<const T*>(base) + off);
+  const T* p = static_cast<const T*>(base) + off;
+  if constexpr (kWhole) return *reinterpret_cast<const Chunk<T, V>*>(p);
+  return {*reinterpret_cast<const typename Chunk<T, V>::At*>(p)};
 }
 template <typename T, int V>
 __device__ __forceinline__ float at(const Chunk<T, V>& c, int v) {
@@ -89,21 +100,67 @@ __device__ __forceinline__ void put(Chunk<T, V>& c, int v, float f) {
   if constexpr (V == 1) c.q = (T)f;
   else c.q[v] = (T)f;
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(void* base, uint64_t off, const Chunk<T, V>& c) {
-  T* p = static_cast<T*>(base) + off;
-  if constexpr (V > 1) __builtin_nontemporal_store(c.q, reinterpret_cast<decltype(Chunk<T, V>::q)*>(p));
-  else *p = c.q;
-}
+
+// A row's chunks. Rows that are whole aligned chunks (kWhole) have no rest; in
+// others the last chunk is moved back to end with the row, and its first `over`
+// elements are those of the chunk before it (131072 x 1023 bf16 in 16-byte
+// accesses at any alignment: forward 177 us, backward 341, by single elements 280
+// and 474). No sum sees them twice. Chunks of 8 write them twice (kTwice), with
+// the same bits; chunks of 4, two or four of them a thread and fewer registers
+// left, zero them after the load and store their own elements one by one
+// (backward, this way against the other: 131072 x 1023 bf16 341 us against 370,
+// 4000 x 3001 fp32 65 against 100).
+template <typename T, int V, bool kWhole>
+struct Row {
+  static constexpr bool kTwice = !kWhole && V == 8;
+  uint32_t d, nch, over;
+  __device__ __forceinline__ explicit Row(uint32_t d) : d(d), nch(kWhole ? d / V : (d + V - 1) / V), over(nch * V - d) {}
+  __device__ __forceinline__ uint32_t start(uint32_t ch) const { return kWhole ? ch * V : min(ch * V, d - V); }
+  __device__ __forceinline__ Chunk<T, V> load_chunk(const void* base, uint64_t row, uint32_t ch) const {
+    return load<T, V, kWhole>(base, row + start(min(ch, nch - 1)));
+  }
+  // Element v of chunk ch, d where it is none.
+  __device__ __forceinline__ uint32_t column(uint32_t ch, uint32_t v) const {
+    const uint32_t c = start(ch) + v;
+    return kWhole || c >= ch * V ? c : d;
+  }
+  __device__ __forceinline__ bool again(uint32_t ch, uint32_t v) const { return !kWhole && ch + 1 == nch && v < over; }
+  // After the load of a chunk whose values are summed.
+  __device__ __forceinline__ void clip(Chunk<T, V>& c, uint32_t ch) const {
+    if constexpr (!kWhole && !kTwice) {
+      if (ch + 1 != nch) return;
+#pragma unroll
+      for (uint32_t v = 0; v < V; ++v)
+        if (v < over) put<T, V>(c, v, 0.f);
+    }
+  }
+  // Element v of chunk ch as sums take it.
+  __device__ __forceinline__ float own(float f, uint32_t ch, uint32_t v) const { return kTwice && again(ch, v) ? 0.f : f; }
+  __device__ __forceinline__ void store_chunk(void* base, uint64_t row, uint32_t ch, const Chunk<T, V>& c) const {
+    T* p = static_cast<T*>(base) + row + start(ch);
+    if constexpr (V == 1) {
+      *p = c.q;
+    } else if constexpr (kWhole) {
+      __builtin_nontemporal_store(c.q, reinterpret_cast<decltype(Chunk<T, V>::q)*>(p));
+    } else if (kTwice || ch + 1 != nch || over == 0) {
+      const typename Chunk<T, V>::At q = c.q;
+      __builtin_nontemporal_store(q, reinterpret_cast<typename Chunk<T, V>::At*>(p));
+    } else {
+#pragma unroll
+      for (uint32_t v = 0; v < V; ++v)
+        if (!again(ch, v)) p[v] = c.q[v];
+    }
+  }
+};
 
 // A chunk of a row vector that every row uses (a weight or a gate). Chunks of
 // bf16 the compiler may keep in registers for all rows; wider elements are
 // loaded again for each row, from the caches (the empty asm statement hides
 // that the address is the same): as many more registers would halve the waves.
-template <typename T, int V>
-__device__ __forceinline__ Chunk<T, V> load_shared(const void* p, uint64_t off) {
+template <typename T, int V, bool kWhole>
+__device__ __forceinline__ Chunk<T, V> load_shared(const Row<T, V, kWhole>& R, const void* p, uint64_t row, uint32_t ch) {
   if constexpr (V < 8) asm volatile("" : "+s"(p));
-  return load<T, V>(p, off);
+  return R.load_chunk(p, row, ch);
 }
 
 // The waves' sums of one exchange, by wave. A workgroup alternates between two
@@ -119,7 +176,7 @@ struct Exchange {
 template <int TEAM, int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint32_t& turn) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lanes_sum<64>(v[i]);
+  for (int i = 0; i < N; ++i) v[i] = lanes_sum<(TEAM < 64 ? TEAM : 64)>(v[i]);
   if constexpr (TEAM > 64) {
     constexpr int W = TEAM / 64;
     auto& sums = x.sums[turn];
@@ -138,11 +195,12 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Exchange<TEAM>& x, uint3
 // one row per team and ends (131072 x 1024 bf16: 178 us; walking the rows with
 // 4096 workgroups 200, with 1024 224: rows that run at the same time are
 // neighbours, and the next workgroup's loads overlap this one's stores).
-template <typename T, int V, int C, int TEAM, bool kY, bool kH>
+template <typename T, int V, bool kWhole, int C, int TEAM, bool kY, bool kH>
 __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
   __shared__ Exchange<TEAM> ex;
   uint32_t turn = 0;
-  const uint32_t lane = threadIdx.x % TEAM, nch = a.d / V;
+  const Row<T, V, kWhole> R(a.d);
+  const uint32_t lane = threadIdx.x % TEAM, nch = R.nch;
   constexpr uint32_t kTeams = threads_of(TEAM) / TEAM;
   const bool norm_y = kY && a.w_y, gated = kY && a.gate;
   for (uint32_t row0 = blockIdx.x * kTeams; row0 < a.rows; row0 += gridDim.x * kTeams) {  // (one turn: see kMaxGrid)
@@ -153,12 +211,17 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
     Chunk<T, V> x[C], y[C], wy[C], g[C], wr[C];  // all requested before any is used
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint64_t ch = (uint64_t)min(lane + c * TEAM, nch - 1) * V;
-      x[c] = load<T, V>(a.x, base + ch);
-      if (kY) y[c] = load<T, V>(a.y, base + ch);
-      if (norm_y) wy[c] = load<T, V>(a.w_y, ch);
-      if (gated) g[c] = load<T, V>(a.gate, gbase + ch);
-      if (kH) wr[c] = load<T, V>(a.w_r, ch);
+      const uint32_t ch = lane + c * TEAM;
+      x[c] = R.load_chunk(a.x, base, ch);
+      if (kY) y[c] = R.load_chunk(a.y, base, ch);
+      if (norm_y) wy[c] = R.load_chunk(a.w_y, 0, ch);
+      if (gated) g[c] = R.load_chunk(a.gate, gbase, ch);
+      if (kH) wr[c] = R.load_chunk(a.w_r, 0, ch);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      R.clip(x[c], lane + c * TEAM);
+      if (kY) R.clip(y[c], lane + c * TEAM);
     }
     float ty = a.y_scale;
     if (norm_y) {
@@ -167,7 +230,10 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
       for (int c = 0; c < C; ++c)
         if (lane + c * TEAM < nch)
 #pragma unroll
-          for (int v = 0; v < V; ++v) ss[0] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), ss[0]);
+          for (int v = 0; v < V; ++v) {
+            const float yv = R.own(at<T, V>(y[c], v), lane + c * TEAM, v);
+            ss[0] = fmaf(yv, yv, ss[0]);
+          }
       team_sum(ss, ex, turn);
       ty = a.y_scale * rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
     }
@@ -183,7 +249,10 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
           f = gated ? fmaf(n, at<T, V>(g[c], v), f) : f + n;
         }
         r[c][v] = f;
-        if (kH && lane + c * TEAM < nch) ss[0] = fmaf(f, f, ss[0]);
+        if (kH && lane + c * TEAM < nch) {
+          const float rv = R.own(f, lane + c * TEAM, v);
+          ss[0] = fmaf(rv, rv, ss[0]);
+        }
       }
     }
     float s = 0.f;
@@ -191,6 +260,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
       team_sum(ss, ex, turn);
       s = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
     }
+    if (R.kTwice && TEAM > 64 && !kH && !norm_y) __syncthreads();  // uniform; see k_norm_grad
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t ch = lane + c * TEAM;
@@ -199,12 +269,12 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
       if (a.r) {
 #pragma unroll
         for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v]);
-        store<T, V>(a.r, base + (uint64_t)ch * V, o);
+        R.store_chunk(a.r, base, ch, o);
       }
       if (kH) {
 #pragma unroll
         for (int v = 0; v < V; ++v) put<T, V>(o, v, r[c][v] * s * at<T, V>(wr[c], v));
-        store<T, V>(a.h, base + (uint64_t)ch * V, o);
+        R.store_chunk(a.h, base, ch, o);
       }
     }
   }
@@ -218,15 +288,16 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_norm(NormArgs a) {
 // summed over the teams, to dgate where the segment is the whole group, else to
 // part_q; and gate Q to the running sum P of dw_y. W and P end in one partial
 // row per workgroup; k_norm_join adds the rows.
-template <typename T, int V, int C, int TEAM, bool kY, bool kH>
-__global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) void k_norm_grad(NormArgs a) {
+template <typename T, int V, bool kWhole, int C, int TEAM, bool kY, bool kH>
+__global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : 4) void k_norm_grad(NormArgs a) {
   constexpr int NT = threads_of(TEAM);
   extern __shared__ float lds[];  // several teams: [teams][d] their sums
   __shared__ Exchange<TEAM> ex;
   uint32_t turn = 0;
-  const uint32_t lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, nch = a.d / V;
+  const Row<T, V, kWhole> R(a.d);
+  const uint32_t lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, nch = R.nch;
   constexpr uint32_t kTeams = NT / TEAM;
-  constexpr int kOwn = C * V / (int)kTeams;  // columns of a thread at the end of a segment
+  constexpr int kOwn = C * V < (int)kTeams ? 1 : C * V / (int)kTeams;  // columns of a thread at the end of a segment
   const bool norm_y = kY && a.w_y, gated = kY && a.gate, sums_y = norm_y || gated;
   float Q[C][V], W[C][V], P[kOwn];
 #pragma unroll
@@ -238,7 +309,7 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
 
   // Column i of this thread at a segment's end, and its sum over the teams.
   auto column = [&](int i) -> uint32_t {
-    if constexpr (kTeams == 1) return (lane + (i / V) * TEAM) * V + i % V;
+    if constexpr (kTeams == 1) return R.column(lane + (i / V) * TEAM, i % V);
     return threadIdx.x + i * NT;
   };
   auto gather = [&](const float (&s)[C][V], float (&out)[kOwn]) {
@@ -251,7 +322,10 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
       for (int c = 0; c < C; ++c)
         if (lane + c * TEAM < nch)
 #pragma unroll
-          for (int v = 0; v < V; ++v) lds[team * a.d + (lane + c * TEAM) * V + v] = s[c][v];
+          for (int v = 0; v < V; ++v) {
+            const uint32_t col = R.column(lane + c * TEAM, v);
+            if (kWhole || col < a.d) lds[team * a.d + col] = s[c][v];
+          }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
@@ -276,13 +350,18 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
       Chunk<T, V> dr[C], dh[C], r[C], y[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint64_t o = base + (uint64_t)min(lane + c * TEAM, nch - 1) * V;
-        if (a.dr) dr[c] = load<T, V>(a.dr, o);
+        const uint32_t ch = lane + c * TEAM;
+        if (a.dr) dr[c] = R.load_chunk(a.dr, base, ch);
         if (kH) {
-          dh[c] = load<T, V>(a.dh, o);
-          r[c] = load<T, V>(a.r_in, o);
+          dh[c] = R.load_chunk(a.dh, base, ch);
+          r[c] = R.load_chunk(a.r_in, base, ch);
         }
-        if (kY) y[c] = load<T, V>(a.y, o);
+        if (kY) y[c] = R.load_chunk(a.y, base, ch);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (kH) R.clip(r[c], lane + c * TEAM);
+        if (kY) R.clip(y[c], lane + c * TEAM);
       }
       float D[C][V];
       float sum[3] = {0.f, 0.f, 0.f};  // r^2, G r, y^2
@@ -290,21 +369,28 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
       for (int c = 0; c < C; ++c) {
         const bool in = lane + c * TEAM < nch;
         Chunk<T, V> w;
-        if (kH) w = load_shared<T, V>(a.w_r, (uint64_t)min(lane + c * TEAM, nch - 1) * V);
+        if (kH) w = load_shared(R, a.w_r, 0, lane + c * TEAM);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if (kH) {
             D[c][v] = at<T, V>(dh[c], v) * at<T, V>(w, v);
             if (in) {
-              sum[0] = fmaf(at<T, V>(r[c], v), at<T, V>(r[c], v), sum[0]);
-              sum[1] = fmaf(D[c][v], at<T, V>(r[c], v), sum[1]);
+              const float rv = R.own(at<T, V>(r[c], v), lane + c * TEAM, v);
+              sum[0] = fmaf(rv, rv, sum[0]);
+              sum[1] = fmaf(D[c][v], rv, sum[1]);
             }
           }
-          if (norm_y && in) sum[2] = fmaf(at<T, V>(y[c], v), at<T, V>(y[c], v), sum[2]);
+          if (norm_y && in) {
+            const float yv = R.own(at<T, V>(y[c], v), lane + c * TEAM, v);
+            sum[2] = fmaf(yv, yv, sum[2]);
+          }
         }
       }
       float s = 0.f, m = 0.f, t = 1.f;
+      // An element that two waves hold (kTwice) is written in place when both
+      // have read it: the sums' barrier, or this one.
       if (kH || norm_y) team_sum(sum, ex, turn);  // uniform
+      else if (R.kTwice && TEAM > 64) __syncthreads();
       if (kH) {
         s = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
         m = s * s * sum[1] * a.inv_d;
@@ -316,8 +402,8 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
         const uint32_t ch = lane + c * TEAM;
         const bool in = ok && ch < nch;
         Chunk<T, V> o, wy, gt;
-        if (norm_y) wy = load_shared<T, V>(a.w_y, (uint64_t)min(ch, nch - 1) * V);
-        if (gated) gt = load_shared<T, V>(a.gate, gbase + (uint64_t)min(ch, nch - 1) * V);
+        if (norm_y) wy = load_shared(R, a.w_y, 0, ch);
+        if (gated) gt = load_shared(R, a.gate, gbase, ch);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float f = a.dr ? at<T, V>(dr[c], v) : 0.f;
@@ -334,12 +420,12 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
             if (gated) f *= at<T, V>(gt, v);
             if (norm_y) {
               f *= at<T, V>(wy, v);
-              if (ch < nch) qy[0] = fmaf(f, yv, qy[0]);
+              if (ch < nch) qy[0] = fmaf(f, R.own(yv, ch, v), qy[0]);
             }
           }
           D[c][v] = f;
         }
-        if (live && ch < nch) store<T, V>(a.dx, base + (uint64_t)ch * V, o);
+        if (live && ch < nch) R.store_chunk(a.dx, base, ch, o);
       }
       if (kY) {
         float m2 = 0.f;
@@ -355,7 +441,7 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : V == 1 ? 3 : 4) v
 #pragma unroll
           for (int v = 0; v < V; ++v)
             put<T, V>(o, v, !ok ? 0.f : norm_y ? t * (D[c][v] - at<T, V>(y[c], v) * m2) : D[c][v]);
-          store<T, V>(a.dy, base + (uint64_t)ch * V, o);
+          R.store_chunk(a.dy, base, ch, o);
         }
       }
     }
@@ -432,28 +518,32 @@ __global__ __launch_bounds__(kThreads) void k_norm_zero(NormArgs a) {
 // per row. At most 8 elements a thread, so that the gradient's registers (rows,
 // sums, weights) leave room for 4 waves per SIMD (2047 x 1001 fp32 by 256
 // threads with room for 8 elements each, half of it unused: 42 us against 16).
-// Above 4096 elements rows of 4-byte chunks take 16 elements by 512 threads: 1024
-// threads of 8 spill (backward, 8192 x 8192 fp32: 570 us against 405, 4000 x
-// 8191 bf16 507 against 221; 8192 bf16 in whole chunks is the other way round,
-// 477 against 505; all before the rows were dealt in turn). Rows that are not
-// whole aligned 16-byte chunks go by single elements.
+// Narrow rows share a wave, 4 or 2 at a time (300000 x 128 bf16: forward 44 us,
+// backward 88; with a wave for each row 94 and 207; 4096 x 127 9.5 against 9.7).
+// Above 4096 elements fp32 rows take 16 elements by 512 threads: 1024 threads of
+// 8 spill (backward, 8192 x 8192: 570 us against 405; for bf16, whose chunks are
+// half as wide in registers, it is the other way round, 477 against 505; both
+// before the rows were dealt in turn). Rows shorter than a chunk go by single
+// elements.
 struct Shape {
   int V, C, team;
 };
 
-Shape shape_of(uint32_t d, bool f32, bool aligned) {
-  const int V = aligned ? (f32 ? 4 : 8) : 1;
+Shape shape_of(uint32_t d, bool f32) {
+  const int V = f32 ? 4 : 8;
+  if (d < (uint32_t)V) return {1, 1, 16};
   if (d > 4096) return V == 8 ? Shape{8, 1, 1024} : Shape{V, 16 / V, 512};
   if (d > 2048) return {V, 8 / V, 512};
   if (d > 1024) return {V, 8 / V, 256};
   if (d > 512) return {V, 8 / V, 128};
-  if (d > 256 || V == 8) return {V, 8 / V, 64};
-  return {V, 4 / V, 64};
+  if (d > 256) return {V, 8 / V, 64};
+  if (d > 128) return {V, 8 / V, 32};
+  return {V, 8 / V, 16};
 }
 
 // Rows a workgroup takes at a time.
 uint32_t teams_of(uint32_t d) {
-  const uint32_t team = shape_of(d, false, true).team;  // the same for every type and alignment
+  const uint32_t team = shape_of(d, false).team;  // (fp32: as many teams)
   return threads_of(team) / team;
 }
 
@@ -559,46 +649,54 @@ NormArgs args(const pw_norm_desc& d, const pw_norm_io& io) {
   return a;
 }
 
-template <typename T, int V, int C, int TEAM, bool kY, bool kH>
+template <typename T, int V, bool kWhole, int C, int TEAM, bool kY, bool kH>
 void launch(const NormArgs& a, bool grad, hipStream_t s) {
   constexpr uint32_t NT = threads_of(TEAM), teams = NT / TEAM;
   if (grad) {
     const size_t lds = teams > 1 ? (size_t)teams * a.d * 4 : 0;
-    hipLaunchKernelGGL((k_norm_grad<T, V, C, TEAM, kY, kH>), dim3(a.grid), dim3(NT), lds, s, a);
+    hipLaunchKernelGGL((k_norm_grad<T, V, kWhole, C, TEAM, kY, kH>), dim3(a.grid), dim3(NT), lds, s, a);
   } else {
     const uint32_t blocks = std::min((a.rows + teams - 1) / teams, kMaxGrid);
-    hipLaunchKernelGGL((k_norm<T, V, C, TEAM, kY, kH>), dim3(blocks), dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((k_norm<T, V, kWhole, C, TEAM, kY, kH>), dim3(blocks), dim3(NT), 0, s, a);
   }
 }
 
-template <typename T, int V, int C, int TEAM>
+template <typename T, int V, bool kWhole, int C, int TEAM>
 void launch_parts(const NormArgs& a, bool grad, hipStream_t s) {
-  if (!a.y) launch<T, V, C, TEAM, false, true>(a, grad, s);
-  else if (!a.w_r) launch<T, V, C, TEAM, true, false>(a, grad, s);
-  else launch<T, V, C, TEAM, true, true>(a, grad, s);
+  if (!a.y) launch<T, V, kWhole, C, TEAM, false, true>(a, grad, s);
+  else if (!a.w_r) launch<T, V, kWhole, C, TEAM, true, false>(a, grad, s);
+  else launch<T, V, kWhole, C, TEAM, true, true>(a, grad, s);
 }
 
-template <typename T, int V>
+template <typename T, int V, bool kWhole>
 void launch_shape(const NormArgs& a, const Shape& sh, bool grad, hipStream_t s) {
   switch (sh.team) {
     case 1024:
-      if constexpr (V == 8) return launch_parts<T, 8, 1, 1024>(a, grad, s);
+      if constexpr (V == 8) return launch_parts<T, 8, kWhole, 1, 1024>(a, grad, s);
     case 512:
       if constexpr (V < 8)
-        if (sh.C * V == 16) return launch_parts<T, V, 16 / V, 512>(a, grad, s);
-      return launch_parts<T, V, 8 / V, 512>(a, grad, s);
-    case 256: return launch_parts<T, V, 8 / V, 256>(a, grad, s);
-    case 128: return launch_parts<T, V, 8 / V, 128>(a, grad, s);
+        if (sh.C * V == 16) return launch_parts<T, V, kWhole, 16 / V, 512>(a, grad, s);
+      return launch_parts<T, V, kWhole, 8 / V, 512>(a, grad, s);
+    case 256: return launch_parts<T, V, kWhole, 8 / V, 256>(a, grad, s);
+    case 128: return launch_parts<T, V, kWhole, 8 / V, 128>(a, grad, s);
+    case 64: return launch_parts<T, V, kWhole, 8 / V, 64>(a, grad, s);
+    case 32: return launch_parts<T, V, kWhole, 8 / V, 32>(a, grad, s);
   }
-  if (sh.C * V == 8) return launch_parts<T, V, 8 / V, 64>(a, grad, s);
-  if constexpr (V < 8) launch_parts<T, V, 4 / V, 64>(a, grad, s);
+  launch_parts<T, V, kWhole, 8 / V, 16>(a, grad, s);
+}
+
+template <typename T, int V>
+void launch_type(const NormArgs& a, const Shape& sh, bool aligned, bool grad, hipStream_t s) {
+  if (sh.V == 1) launch_parts<T, 1, true, 1, 16>(a, grad, s);
+  else if (aligned && a.d % V == 0) launch_shape<T, V, true>(a, sh, grad, s);
+  else launch_shape<T, V, false>(a, sh, grad, s);
 }
 
 hipError_t launch_any(const NormArgs& a, const pw_norm_desc& d, bool aligned, bool grad, hipStream_t s) {
   const bool f32 = d.dtype == PW_F32;
-  const Shape sh = shape_of(d.d, f32, aligned && (uint64_t)d.d * (f32 ? 4 : 2) % 16 == 0);
-  if (f32) sh.V > 1 ? launch_shape<float, 4>(a, sh, grad, s) : launch_shape<float, 1>(a, sh, grad, s);
-  else sh.V > 1 ? launch_shape<__bf16, 8>(a, sh, grad, s) : launch_shape<__bf16, 1>(a, sh, grad, s);
+  const Shape sh = shape_of(d.d, f32);
+  if (f32) launch_type<float, 4>(a, sh, aligned, grad, s);
+  else launch_type<__bf16, 8>(a, sh, aligned, grad, s);
   return hipGetLastError();
 }
 

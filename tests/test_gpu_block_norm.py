@@ -119,6 +119,60 @@ def test_in_place(gpu):
         assert torch.equal(dx, f.grad(dr, c["dh"], r, dx=dr, **kw)[0])
 
 
+EDGES = [(50, 127, "bf16", 0, "ywh"), (33, 129, "bf16", 3, "ywh"), (70, 9, "bf16", 0, "ywh"), (70, 8, "bf16", 7, "ywh"),
+         (40, 7, "bf16", 0, "yw"), (3, 5, "f32", 0, "ywh"), (40, 3, "f32", 2, "ywh"), (1000, 15, "bf16", 8, "yh"),
+         (5000, 65, "f32", 1, "ywh"), (40, 128, "f32", 4, "ywh"), (70, 256, "f32", 0, "h"), (31, 257, "bf16", 0, "ywh"),
+         (31, 511, "f32", 31, "ywh"), (12, 513, "f32", 0, "yw"), (8, 1025, "bf16", 2, "y"), (6, 2047, "f32", 1, "ywh"),
+         (6, 4095, "bf16", 3, "ywh"), (4, 4097, "bf16", 1, "yw"), (4, 4097, "f32", 2, "ywh"), (3, 8190, "f32", 0, "h")]
+
+
+@pytest.mark.parametrize("rows,d,dtype,gates,parts", EDGES)
+def test_widths_around_the_variants(gpu, rows, d, dtype, gates, parts):
+    """Widths next to those where the number of threads changes, and rows whose
+    last chunk is not whole."""
+    test_norm_and_gradients(gpu, rows, d, dtype, gates, parts)
+
+
+@pytest.mark.parametrize("parts", ["y", "yw", "yh"])
+@pytest.mark.parametrize("d", [61, 509, 1001, 2001, 4095, 8191])
+def test_in_place_with_a_part_of_a_chunk_left(gpu, d, parts):
+    rows = 700
+    s = make(rows, d, "bf16", 7, parts)
+    c = {n: cuda(t) for n, t in s.items()}
+    f = gpu.BlockNorm(rows, d, gpu.PW_BF16, 7, 0.9, 0.7, EPS)
+    kw = dict(y=c["y"], w_y=c["w_y"], gate=c["gate"], w_r=c["w_r"])
+    r = f.forward(c["x"], **kw)[0].clone()
+    dx = f.grad(c["dr"], c["dh"], r, **kw)[0].clone()
+    x, dr = c["x"].clone(), c["dr"].clone()
+    assert torch.equal(r, f.forward(x, r=x, **kw)[0])
+    assert torch.equal(dx, f.grad(dr, c["dh"], r, dx=dr, **kw)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [128, 1003, 1024])
+def test_gradient_of_rows_at_any_element(gpu, d, dtype):
+    """Every row buffer begins one element after a 16-byte boundary, with a guard
+    element before and after that stays as it was."""
+    rows, ax, ay = 37, 0.9, 0.7
+    s = make(rows, d, dtype, 0, "ywh")
+    dt = s["x"].dtype
+
+    def odd(t):
+        flat = torch.full((t.numel() + 2,), 7.0, dtype=dt, device="cuda")
+        v = flat[1:-1].view(t.shape)
+        v.copy_(t)
+        return v, flat
+    c = {n: odd(t)[0] for n, t in s.items() if t is not None}
+    f = gpu.BlockNorm(rows, d, gpu.PW_BF16 if dtype == "bf16" else gpu.PW_F32, 0, ax, ay, EPS)
+    r, r_flat = odd(torch.zeros(rows, d))
+    got = f.forward(c["x"], y=c["y"], w_y=c["w_y"], w_r=c["w_r"], r=r)
+    check_forward(got, s, ax, ay)
+    dx, dx_flat = odd(torch.zeros(rows, d))
+    check_grad(f.grad(c["dr"], c["dh"], r, y=c["y"], w_y=c["w_y"], w_r=c["w_r"], dx=dx), s, r.cpu(), ax, ay)
+    for flat in (r_flat, dx_flat):
+        assert flat[0] == 7 and flat[-1] == 7
+
+
 def test_rows_that_are_not_16_byte_aligned(gpu):
     rows, d = 30, 512
     s = make(rows, d, "bf16", 0, "ywh")
