@@ -76,6 +76,18 @@ __device__ __forceinline__ void load4(const float* row, uint32_t e0, uint32_t la
   }
 }
 
+// Whether a token counts, as a byte loaded without a branch (under one, the
+// compiler waits for it before the next row's load: the loss of 131072 x 64 took
+// 15.4 us). With no mask it reads a byte of the logits, which counts as nothing.
+struct Mask {
+  const uint8_t* p;
+  uint32_t every, index;  // no mask: 1, 0; else 0, all ones
+  __device__ __forceinline__ explicit Mask(const BalanceArgs& a)
+      : p(a.valid ? a.valid : reinterpret_cast<const uint8_t*>(a.logits)), every(a.valid ? 0 : 1), index(every - 1) {}
+  __device__ __forceinline__ uint32_t load(uint32_t t) const { return p[t & index]; }
+  __device__ __forceinline__ bool has(uint32_t v) const { return v | every; }
+};
+
 // e^x for x <= 0 (and NaN): the hardware's 2^t with t = x log2(e), and what the
 // product's rounding and log2(e)'s own left out put back to first order, so the
 // result is off by the rounding of x and two units in the last place. 8
@@ -152,29 +164,28 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   const uint32_t tid = threadIdx.x, lane = tid % L, grp = tid / L, e0 = first_of<kFour>(lane, a.E);
   for (uint32_t i = tid; i <= a.E; i += kThreads) s_cnt[i] = 0;
   __syncthreads();
+  const Mask mask(a);
   float p[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
   int n = 0;
   const uint32_t step = G * kRows;
   for (uint32_t t0 = blockIdx.x * step; t0 < a.tokens; t0 += gridDim.x * step) {
     const uint32_t here = min(step, a.tokens - t0);
     float v[kRows][4];
-    bool ok[kRows];
+    uint32_t ok[kRows];
 #pragma unroll
     for (uint32_t u = 0; u < kRows; ++u) {
-      const uint32_t t = t0 + u * G + grp;
-      const uint32_t tc = min(t, a.tokens - 1);
-      load4<kFour>(a.logits + (uint64_t)tc * a.E, e0, lane, a.E, v[u]);
-      ok[u] = t < a.tokens && (!a.valid || a.valid[tc]);
+      const uint32_t t = min(t0 + u * G + grp, a.tokens - 1);
+      load4<kFour>(a.logits + (uint64_t)t * a.E, e0, lane, a.E, v[u]);
+      ok[u] = mask.load(t);
     }
     for (uint32_t i = tid; i < here * a.k; i += kThreads) {
-      const uint32_t t = t0 + i / a.k;
-      const uint32_t e = (uint32_t)a.experts[(uint64_t)t0 * a.k + i];
-      if (e < a.E && (!a.valid || a.valid[t])) atomicAdd(&s_cnt[e], 1);
+      const uint32_t e = (uint32_t)a.experts[(uint64_t)t0 * a.k + i], in = mask.load(t0 + i / a.k);
+      if ((e < a.E) & mask.has(in)) atomicAdd(&s_cnt[e], 1);
     }
 #pragma unroll
     for (uint32_t u = 0; u < kRows; ++u) {
       const float lse = softmax_row<L>(v[u]);
-      if (ok[u]) {
+      if (mask.has(ok[u]) && t0 + u * G + grp < a.tokens) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[j] += v[u][j];
         if (lane == 0) {
@@ -269,15 +280,15 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
   constexpr uint32_t G = kGradThreads / L, S = L < 8 ? L : 8;  // lanes that hold gates
   constexpr uint32_t kOf = 8 / S;                              // gates of such a lane
   const uint32_t tid = threadIdx.x, lane = tid % L, grp = tid / L, e0 = first_of<kFour>(lane, a.E);
+  const Mask mask(a);
   for (uint32_t t0 = blockIdx.x * G * kRows + grp; t0 - grp < a.tokens; t0 += gridDim.x * G * kRows) {
     float v[kRows][4], g[kRows][kOf], dg[kRows][kOf];
-    uint32_t ex[kRows][kOf];
-    bool ok[kRows];
+    uint32_t ex[kRows][kOf], ok[kRows];
 #pragma unroll
     for (uint32_t u = 0; u < kRows; ++u) {
       const uint32_t t = min(t0 + u * G, a.tokens - 1);
       load4<kFour>(a.logits + (uint64_t)t * a.E, e0, lane, a.E, v[u]);
-      ok[u] = true;
+      ok[u] = mask.load(t);
     }
     if (a.gates)  // uniform
 #pragma unroll
@@ -289,18 +300,21 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
           dg[u][q] = a.dgates[o];
           ex[u][q] = (uint32_t)a.experts[o];
         }
-    if (a.valid)  // uniform
-#pragma unroll
-      for (uint32_t u = 0; u < kRows; ++u) ok[u] = a.valid[min(t0 + u * G, a.tokens - 1)];
+    // all without branches, so that one wait covers these and the rows
     const int n = a.counts[a.E];
+    const float* up = a.grad_loss ? a.grad_loss : reinterpret_cast<const float*>(a.counts);  // (then not used)
+    const float up0 = up[0], up1 = up[1];
+    int count[4];
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) count[j] = a.counts[min(e0 + j, a.E)];
     const float inv = n > 0 ? 1.0f / (float)n : 0.f;
-    const float u0 = a.grad_loss ? a.grad_loss[0] : 1.f, u1 = a.grad_loss ? a.grad_loss[1] : 1.f;
+    const float u0 = a.grad_loss ? up0 : 1.f, u1 = a.grad_loss ? up1 : 1.f;
     const float cb = u0 * a.balance_coef * (float)a.E / (float)a.k * inv, cz = u1 * 2.f * a.z_coef * inv;
     float c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t e = e0 + j;
-      c[j] = e < a.E ? (float)((int64_t)a.counts[e] * a.E - (int64_t)a.k * n) * (inv / (float)a.E) : 0.f;
+      c[j] = e < a.E ? (float)((int64_t)count[j] * a.E - (int64_t)a.k * n) * (inv / (float)a.E) : 0.f;
     }
 #pragma unroll
     for (uint32_t u = 0; u < kRows; ++u) {
@@ -320,12 +334,9 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
         for (uint32_t q = 0; q < kOf; ++q) part[q] = g[u][q] * (dg[u][q] - dot);
         for (uint32_t s = 0; s < a.k; ++s) {
           const int from = (int)(tid % 64 - lane + s / kOf);
-          float p = part[0];
-          uint32_t e = ex[u][0];
-          if (kOf > 1 && s % kOf) {
-            p = part[kOf - 1];
-            e = ex[u][kOf - 1];
-          }
+          const bool second = kOf > 1 && s % kOf;
+          float p = second ? part[kOf - 1] : part[0];
+          uint32_t e = second ? ex[u][kOf - 1] : ex[u][0];
           p = __shfl(p, from);
           e = (uint32_t)__shfl((int)e, from) - e0;
 #pragma unroll
@@ -336,7 +347,7 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
       if (t >= a.tokens) continue;
       float* out = a.dlogits + (uint64_t)t * a.E;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = ok[u] ? o[j] : 0.f;
+      for (int j = 0; j < 4; ++j) o[j] = mask.has(ok[u]) ? o[j] : 0.f;
       if (kFour && e0 == lane * 4) {
         *reinterpret_cast<f32x4_at4*>(out + e0) = f32x4{o[0], o[1], o[2], o[3]};
       } else {
