@@ -9,8 +9,8 @@
 // Both kernels read each logit once: a token's row is spread over a group of
 // L lanes of 4 experts each (L = 4, 16, 64 for E <= 16, 64, 256), so a wave's
 // load covers 64 / L whole rows, and the row's maximum, sum and dot product
-// are lane exchanges inside the group. 131072 x 64: loss 12.2 + 4.4 us (35 MB, 2.8
-// TB/s), gradient 18.4 us (70 MB, 3.8 TB/s): reading, with the first loads', the
+// are lane exchanges inside the group. 131072 x 64: loss 11 + 4.4 us (35 MB, 3.1
+// TB/s), gradient 15.5 us (70 MB, 4.5 TB/s): reading, with the first loads', the
 // arithmetic's (a quarter) and the launches' latency on top. 48 x 8: 4.2 us, a few
 // memory latencies.
 #include "ops.h"
@@ -31,9 +31,9 @@ constexpr uint32_t kParts = 256;        // partial sums at most: a workgroup of 
 // E = 8 and 256 cross over at the same count of 8 rows).
 constexpr uint32_t kAlone = 8;
 constexpr uint32_t rows_of(bool last) { return last ? 2 : 4; }  // rows of a group of k_balance in flight
-// Workgroups up to which k_router_grad takes one row a group (999 x 5: 5.8 us
-// against 8.6 with 4; 131072 x 64, 8192 workgroups: 24.7 us against 20).
-constexpr uint32_t kGradWide = 2048;
+// Workgroups up to which k_router_grad takes one row a group (16000 x 64, 1000
+// workgroups: 4.8 us against 5.1 with 4 rows; 32000 x 64: 6.9 against 6.6).
+constexpr uint32_t kGradWide = 1024;
 
 struct BalanceArgs {
   const float* logits;
@@ -273,8 +273,9 @@ __global__ __launch_bounds__(kThreads) void k_balance_join(BalanceArgs a) {
 // The gradient of the logits, kRows rows per group in flight. The counts enter centred on
 // their mean k n / E, a difference of whole numbers (the probabilities sum to
 // one, so a common part has no gradient): nearly even loads lose nothing in
-// c_e - sum_j c_j p_j. A row's gates are loaded by its group's first k lanes and
-// handed round.
+// c_e - sum_j c_j p_j. A row's gates are loaded by its group's first k lanes (two
+// each where there are 4 lanes) and handed round, picked by constant indices: an
+// array that is indexed at run time goes to LDS (131072 x 8: 20 us against 6).
 template <int L, bool kFour, uint32_t kRows>
 __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
   constexpr uint32_t G = kGradThreads / L, S = L < 8 ? L : 8;  // lanes that hold gates
@@ -332,16 +333,16 @@ __global__ __launch_bounds__(kGradThreads) void k_router_grad(BalanceArgs a) {
         dot = lanes_sum<S>(dot);
 #pragma unroll
         for (uint32_t q = 0; q < kOf; ++q) part[q] = g[u][q] * (dg[u][q] - dot);
-        for (uint32_t s = 0; s < a.k; ++s) {
+        for (uint32_t s = 0; s < a.k; s += kOf) {
           const int from = (int)(tid % 64 - lane + s / kOf);
-          const bool second = kOf > 1 && s % kOf;
-          float p = second ? part[kOf - 1] : part[0];
-          uint32_t e = second ? ex[u][kOf - 1] : ex[u][0];
-          p = __shfl(p, from);
-          e = (uint32_t)__shfl((int)e, from) - e0;
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j)
-            if (e == j) o[j] += p;
+          for (uint32_t q = 0; q < kOf; ++q) {
+            const float p = __shfl(s + q < a.k ? part[q] : 0.f, from);
+            const uint32_t e = (uint32_t)__shfl((int)ex[u][q], from) - e0;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              if (e == j) o[j] += p;
+          }
         }
       }
       if (t >= a.tokens) continue;
