@@ -55,10 +55,10 @@ struct DispatchGradArgs {
 // Row loads bypass the caches (kStream) where the call's rows are twice the
 // last-level cache (256 MiB) or more, so that none can still be there: combine,
 // 131072 tokens x 1024, 271 us against 276 with plain loads, dispatch 233
-// against 239 (both before later steps); below, rows that the caches hold are read from them (16384
-// tokens: combine 31 us against 37, dispatch 45 against 55). Rows are always
-// stored nontemporally: written plainly, they are written back during the reads
-// of the next kernel (dW after dx: 72 us against 81).
+// against 239 (both before later steps); below, rows that the caches hold are
+// read from them (16384 tokens: combine 31 us against 37, dispatch 45 against
+// 55). Rows are always stored nontemporally: written plainly, they are written
+// back during the reads of the next kernel (dW after dx: 72 us against 81).
 constexpr uint64_t kStreamBytes = 512ull << 20;
 
 template <bool kStream, typename V>
@@ -348,7 +348,7 @@ constexpr int kNontemporal = 2;  // nt in the cache-policy operand of buffer ins
 constexpr uint32_t kDwMaxTokens = 1u << 19;  // of a range: its rows of x (at most 2560 bytes) are one buffer
 constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, and below 2^32 with all that is added
 
-template <int NC, bool kStream>  // expert blocks of 32
+template <int NC, bool kStream, bool kMasked>  // expert blocks of 32; kMasked: there is a mask
 __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   extern __shared__ __attribute__((aligned(16))) float lds[];  // [2][32 NC][kDwCols]
   constexpr uint32_t Ep = 32 * NC;
@@ -368,6 +368,7 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   struct Step {
     u32x2 v[8];        // 4 columns of 8 tokens
     float dl[NC][8];
+    uint32_t valid[8];
   };
   // The range's rows of x and dl as buffers: past its end, and for experts
   // that are none (a distant offset), a load returns zero.
@@ -378,6 +379,7 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
   uint32_t doff[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) doff[c] = (16 * tw + 8 * h) * drow + (32 * c + i < a.E ? (32 * c + i) * 4 : kDistant);
+  const auto vb = raw_buffer(kMasked ? a.valid + first : nullptr, kMasked ? n : 0);
   auto fetch = [&](Step& s, uint32_t t) {  // tokens t + 16 tw + 8 h + j of the range
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -386,16 +388,19 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
       for (int c = 0; c < NC; ++c)
         s.dl[c][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(db, doff[c] + (t + j) * drow, 0, 0));
     }
+    if (kMasked)  // a step ahead too (131072 tokens x 1024, the call: 221-224 us, looked up when needed 232-235)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s.valid[j] = __builtin_amdgcn_raw_buffer_load_b8(vb, t + 16 * tw + 8 * h + j, 0, 0);
   };
   // A step's operands are made from its loads, the next step's loads requested
   // into the same registers, and then its products run.
   Step s;
   fetch(s, 0);
   for (uint32_t t = 0; t < n; t += 64) {
-    if (a.valid)  // uniform
+    if (kMasked)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (!a.valid[first + min(t + 16 * tw + 8 * h + j, n - 1)]) {
+        if (!s.valid[j]) {
           s.v[j] = u32x2{0, 0};
 #pragma unroll
           for (int c = 0; c < NC; ++c) s.dl[c][j] = 0.f;
@@ -518,6 +523,23 @@ hipError_t launch_dx(DispatchGradArgs& a, bool stream, hipStream_t s) {
   a.whole_w = a.E % 8 == 0 && !misaligned({a.w}, 16);
   if (a.E < 4) return launch_dx_loads<1, false>(a, grid, stream, s);
   return a.E <= 32 ? launch_dx_loads<1, true>(a, grid, stream, s) : launch_dx_loads<2, true>(a, grid, stream, s);
+}
+
+template <int NC, bool kStream, bool kMasked>
+hipError_t launch_dw_loads(const DispatchGradArgs& a, uint32_t grid, hipStream_t s) {
+  constexpr size_t lds = (size_t)2 * kDwCols * 32 * NC * 4;
+  if (lds > kDefaultLds) {
+    const hipError_t e = hipFuncSetAttribute((const void*)k_router_dw<NC, kStream, kMasked>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((k_router_dw<NC, kStream, kMasked>), dim3(grid), dim3(kDwThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int NC, bool kMasked>
+hipError_t launch_dw(const DispatchGradArgs& a, uint32_t grid, bool stream, hipStream_t s) {
+  return stream ? launch_dw_loads<NC, true, kMasked>(a, grid, s) : launch_dw_loads<NC, false, kMasked>(a, grid, s);
 }
 
 struct DwLayout {
@@ -663,17 +685,9 @@ extern "C" int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch
   if (!a.dw) return PW_OK;
   const bool two = a.E > 32;
   const uint32_t grid = 8 * (a.d / kDwCols) * ((a.splits + 7) / 8);
-  const size_t lds = (size_t)2 * kDwCols * (two ? 64 : 32) * 4;
-  if (lds > kDefaultLds) {
-    const void* fn = stream_rows ? (const void*)k_router_dw<2, true> : (const void*)k_router_dw<2, false>;
-    if ((e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)) != hipSuccess)
-      return hip_fail(e, "router_dw: dynamic LDS");
-  }
-  if (two && stream_rows) hipLaunchKernelGGL((k_router_dw<2, true>), dim3(grid), dim3(kDwThreads), lds, s, a);
-  else if (two) hipLaunchKernelGGL((k_router_dw<2, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
-  else if (stream_rows) hipLaunchKernelGGL((k_router_dw<1, true>), dim3(grid), dim3(kDwThreads), lds, s, a);
-  else hipLaunchKernelGGL((k_router_dw<1, false>), dim3(grid), dim3(kDwThreads), lds, s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch router_dw");
+  if (two) e = a.valid ? launch_dw<2, true>(a, grid, stream_rows, s) : launch_dw<2, false>(a, grid, stream_rows, s);
+  else e = a.valid ? launch_dw<1, true>(a, grid, stream_rows, s) : launch_dw<1, false>(a, grid, stream_rows, s);
+  if (e != hipSuccess) return hip_fail(e, "launch router_dw");
   if (a.splits > 1) {
     const uint32_t jb = a.d * (two ? 64 : 32) / 64;
     if (two) hipLaunchKernelGGL(k_router_dw_join<2>, dim3(jb), dim3(256), 0, s, a);
