@@ -339,8 +339,9 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 // terms, which hold all 24 bits of it: every product is exact and the sums
 // are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
 // of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
-// 131072 tokens x 1024, 64 experts: 55-58 us, 5.2-5.5 TB/s; bound by reading x
-// and dl once from HBM. (Sharing the split terms between the waves through LDS, and
+// 131072 tokens x 1024, 64 experts: 55 to 72 us (4.2-5.5 TB/s), reading x and dl
+// once from HBM; the split and the matrix instructions take nearly as long as the
+// reads, so it probably follows the core clock. (Sharing the split terms between the waves through LDS, and
 // requesting x two steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
