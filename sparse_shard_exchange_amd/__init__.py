@@ -775,7 +775,9 @@ class MoEBlock:
     plus the router's balance loss. moe: an MoE with want_logits. w_out and
     gate may be None. The experts' weights are packed when the MoE is built,
     and the gradient of their products is the caller's, between grad_begin
-    and grad_end. One forward, then its backward: the buffers are the object's."""
+    and grad_end. One forward, then its grad_begin, then grad_end: the buffers
+    are the object's, and a call out of this order is refused (grad_begin and
+    grad_end may be made again on the same forward)."""
 
     def __init__(self, moe, w_in, w_out=None, gate=None, x_scale=1.0, y_scale=1.0, eps=1e-6, balance_coef=1e-2,
                  z_coef=0.0):
@@ -790,7 +792,7 @@ class MoEBlock:
         self.balance = RouterBalance(moe.T, moe.E, 2, balance_coef, z_coef, device)
         self.grads = MoEGrad(moe.T, moe.d, moe.E, moe.static_rows, device)
 
-        self.h = self._dgates = None  # of forward, of grad_begin
+        self.h = self._back = None  # of forward; what grad_end takes from grad_begin
 
     def forward(self, x, valid=None, stream=None):
         """(r, loss [2], counts [E + 1], future of the MoE step); x is kept for the
@@ -798,11 +800,12 @@ class MoEBlock:
         m = self.moe
         if m.y.shape[0] < m.static_rows:
             raise PwError(PW_ERR_STATE, "the block's step needs an MoE with static buffers")
-        self.x, self.valid = x, valid
-        _, self.h = self.norm_in.forward(x, w_r=self.w_in, stream=stream)
-        f = m.step(self.h, stream)
+        self.h = self._back = None  # the step before is over, also if this one fails
+        _, h = self.norm_in.forward(x, w_r=self.w_in, stream=stream)
+        f = m.step(h, stream)
         counts, _, loss = self.balance.loss(m.logits, m.experts, valid, stream)
         r, _ = self.norm_out.forward(x, y=m.out, w_y=self.w_out, gate=self.gate, stream=stream)
+        self.x, self.valid, self.h, self._counts = x, valid, h, counts
         return r, loss, counts, f
 
     def grad_begin(self, dr, stream=None):
@@ -810,22 +813,24 @@ class MoEBlock:
         m = self.moe
         if self.h is None:
             raise PwError(PW_ERR_STATE, "grad_begin follows a forward")
-        self._dx, dout, self._dw_out, self._dgate, _ = self.norm_out.grad(dr, y=m.out, w_y=self.w_out, gate=self.gate,
-                                                                          valid=self.valid, stream=stream)
-        dy, self._dgates, _ = self.grads.combine(dout, m.y, m.gates, m.src_index, m.offsets, self.valid, stream=stream)
+        self._back = None
+        dx, dout, dw_out, dgate, _ = self.norm_out.grad(dr, y=m.out, w_y=self.w_out, gate=self.gate, valid=self.valid,
+                                                        stream=stream)
+        dy, dgates, slot_of = self.grads.combine(dout, m.y, m.gates, m.src_index, m.offsets, self.valid, stream=stream)
+        self._back = dx, dw_out, dgate, dgates, slot_of
         return dy
 
     def grad_end(self, dxd, grad_loss=None, stream=None):
         """{"x", "w_in", "w_out", "gate", "w_router"} gradients from dxd, that of the
         dispatched rows moe.xd, and grad_loss [2], that of the losses (None: ones)."""
         m = self.moe
-        if self._dgates is None:
-            raise PwError(PW_ERR_STATE, "grad_end follows a grad_begin")
-        dl = self.balance.grad(m.logits, m.experts, gates=m.gates, dgates=self._dgates, valid=self.valid,
-                               grad_loss=grad_loss, stream=stream)
-        dh, dw_router = self.grads.dispatch(dxd, dl, m.w[0], self.h, valid=self.valid, stream=stream)
-        dx, _, _, _, dw_in = self.norm_in.grad(self._dx, dh, self.x, w_r=self.w_in, valid=self.valid, stream=stream)
-        return {"x": dx, "w_in": dw_in, "w_out": self._dw_out, "gate": self._dgate, "w_router": dw_router}
+        if self._back is None:
+            raise PwError(PW_ERR_STATE, "grad_end follows the grad_begin of the last forward")
+        dr, dw_out, dgate, dgates, slot_of = self._back
+        dl = self.balance.grad(m.logits, m.experts, self._counts, m.gates, dgates, self.valid, grad_loss, stream)
+        dh, dw_router = self.grads.dispatch(dxd, dl, m.w[0], self.h, slot_of, self.valid, stream)
+        dx, _, _, _, dw_in = self.norm_in.grad(dr, dh, self.x, w_r=self.w_in, valid=self.valid, stream=stream)
+        return {"x": dx, "w_in": dw_in, "w_out": dw_out, "gate": dgate, "w_router": dw_router}
 
 
 class Sched:
