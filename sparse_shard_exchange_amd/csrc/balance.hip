@@ -31,6 +31,11 @@ constexpr uint32_t kParts = 256;        // partial sums at most: a workgroup of 
 // E = 8 and 256 cross over at the same count of 8 rows).
 constexpr uint32_t kAlone = 8;
 constexpr uint32_t rows_of(bool last) { return last ? 2 : 4; }  // rows of a group of k_balance in flight
+// Passes of a run of k_balance: a lane adds 256 rows, then that sum to its sum of
+// the runs (256 at most, for 2^28 tokens), so that no chain has more than 512
+// additions (2^25 equal tokens, 8192 rows a lane in one chain: probabilities off by
+// 1.1e-4). 2^20 tokens take one run up to 256 experts, 2^22 up to 64.
+constexpr uint32_t kRun = 64;
 // Workgroups up to which k_router_grad takes one row a group (16000 x 64, 1000
 // workgroups: 4.8 us against 5.1 with 4 rows; 32000 x 64: 6.9 against 6.6).
 constexpr uint32_t kGradWide = 1024;
@@ -151,7 +156,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, double p, int c, do
 }
 
 // Sums over the workgroup's tokens: probabilities per expert (fp32 per lane
-// over its rows, then across lanes and waves in a fixed order), squared
+// over its rows, in runs, then across lanes and waves in a fixed order), squared
 // logarithms, tuples per expert (whole numbers, in LDS), valid tokens. With
 // kLast the one workgroup writes the results, else its partial sums.
 template <int L, bool kFour, bool kLast>
@@ -166,8 +171,10 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   __syncthreads();
   const Mask mask(a);
   float p[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
+  float runs_p[4] = {0.f, 0.f, 0.f, 0.f}, runs_z = 0.f;
   int n = 0;
   const uint32_t step = G * kRows;
+  uint32_t pass = 0;
   for (uint32_t t0 = blockIdx.x * step; t0 < a.tokens; t0 += gridDim.x * step) {
     const uint32_t here = min(step, a.tokens - t0);
     float v[kRows][4];
@@ -194,6 +201,21 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
         }
       }
     }
+    if (!kLast && ++pass == kRun) {  // uniform; (kLast has kAlone rows a group at most)
+      pass = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        runs_p[j] += p[j];
+        p[j] = 0.f;
+      }
+      runs_z += z;
+      z = 0.f;
+    }
+  }
+  if (!kLast) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] += runs_p[j];
+    z += runs_z;
   }
   if (n) atomicAdd(&s_cnt[a.E], n);
   // across the groups of a wave, then across waves

@@ -234,3 +234,22 @@ def test_refusals(gpu):
         f.grad(l, x)                      # no counts yet
     with pytest.raises(gpu.PwError):
         gpu.RouterBalance(16, 1)
+
+
+@pytest.mark.parametrize("T,E", [(1 << 25, 65), (1 << 28, 2)])
+def test_long_batches_of_equal_tokens(gpu, T, E):
+    """Thousands of equal rows a lane, where fp32 additions err to the same side:
+    a lane adds them in runs of 256, and then the runs, here at most 32. Bar: p by
+    (2 D + 32) u, these additions, 40 more across lanes, waves and partial sums; lse
+    as above."""
+    row = np.linspace(0.5, -0.5, E).astype(np.float32)[None]
+    l = dev(row).expand(T, E).contiguous()
+    ex = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    counts, mean, loss = (t.cpu().numpy() for t in gpu.RouterBalance(T, E, 1, BAL, Z).loss(l, ex))
+    assert counts[0] == counts[E] == T and not counts[1:E].any()
+    p, lse = (a[0] for a in ob.softmax_lse(row))
+    rel = (2 * width(row) + 32 + 256 + 32 + 40) * U
+    assert np.all(np.abs(mean - p) <= rel * p)
+    assert abs(loss[0] - BAL * E * p[0]) <= (rel + 8 * U) * BAL * E * p[0]
+    e = U * (abs(lse) + 2 * width(row) + 32)
+    assert abs(loss[1] - Z * lse ** 2) <= Z * (2 * abs(lse) * e + e * e + 330 * U * lse ** 2)
