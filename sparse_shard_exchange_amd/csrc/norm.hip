@@ -58,6 +58,7 @@ struct NormArgs {
   uint32_t segs;       // segments of a group: every segs-th turn of its rows
   uint32_t num_segs;   // groups x segs
   uint32_t grid;       // workgroups of k_norm_grad
+  uint32_t joins;      // results k_norm_join looks at: dw_r, dw_y, then gates
   float x_scale, y_scale, eps, inv_d;
 };
 
@@ -475,26 +476,33 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : 4) void k_norm_gr
   }
 }
 
-// Adds the partial rows: blockIdx.y 0: dw_r, 1: dw_y, 2 + g: dgate of group
-// g. 32 columns per workgroup, 32 slices of rows, added in a fixed order.
-constexpr uint32_t kJoinCols = 32, kJoinSlices = 1024 / kJoinCols;
+// Adds the partial rows: 0: dw_r, 1: dw_y, 2 + g: dgate of group g. 32 columns
+// per workgroup, 32 slices of rows, added in a fixed order: up to 64 rows of a
+// slice in fp32, and these sums, whose number is not bounded, in double.
+constexpr uint32_t kJoinCols = 32, kJoinSlices = 1024 / kJoinCols, kJoinRun = 64 * kJoinSlices;
+constexpr uint32_t kMaxGridY = 65535;
 
 template <typename T>
 __global__ __launch_bounds__(1024) void k_norm_join(NormArgs a) {
   __shared__ float s[kJoinSlices][kJoinCols];
   const uint32_t c = threadIdx.x % kJoinCols, slice = threadIdx.x / kJoinCols, col = blockIdx.x * kJoinCols + c;
-  const uint32_t what = blockIdx.y;
-  if ((what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;  // whole workgroups
+  const uint32_t what = blockIdx.z * gridDim.y + blockIdx.y;
+  if (what >= a.joins || (what == 0 && !a.dw_r) || (what == 1 && !a.dw_y)) return;  // whole workgroups
   const float* part = what == 0 ? a.part_w : what == 1 ? a.part_p : a.part_q + (uint64_t)(what - 2) * a.segs * a.d;
   const uint32_t n = what < 2 ? a.grid : a.segs;
-  float v = 0.f;
+  double runs = 0.0;
   if (col < a.d)
+    for (uint32_t i0 = 0; i0 < n; i0 += kJoinRun) {
+      const uint32_t end = min(i0 + kJoinRun, n);
+      float v = 0.f;
 #pragma unroll 16
-    for (uint32_t i = slice; i < n; i += kJoinSlices) v += part[(uint64_t)i * a.d + col];
-  s[slice][c] = v;
+      for (uint32_t i = i0 + slice; i < end; i += kJoinSlices) v += part[(uint64_t)i * a.d + col];
+      runs += (double)v;
+    }
+  s[slice][c] = (float)runs;
   __syncthreads();
   if (slice != 0 || col >= a.d) return;
-  v = 0.f;
+  float v = 0.f;
 #pragma unroll
   for (uint32_t i = 0; i < kJoinSlices; ++i) v += s[i][c];
   if (what == 0) a.dw_r[col] = v;
@@ -560,7 +568,12 @@ struct Segments {
 // memory latencies (backward, bf16: 64 x 1024 8.2 us with 4 rows a segment, 7.1
 // with 2; 4096 x 1024 20.2 with 4, 18.3 with 8; 64 x 8192 25.8 and 20.0 with 4
 // and 2).
+// However many rows there are, a workgroup takes kTurns turns of its teams or little
+// more (twice as many where the groups divide badly), so that no fp32 chain of the
+// weights' sums gets longer: 2^29 equal rows of 8 elements, 16384 turns, left dw_y
+// off by 9e-5.
 constexpr uint32_t kSegments = 2048;
+constexpr uint32_t kTurns = 512;
 constexpr uint32_t kShortSegments = 512;
 constexpr uint32_t kShortRows = 8;
 
@@ -568,9 +581,12 @@ Segments segments(uint32_t rows, uint32_t gates, uint32_t d) {
   Segments s;
   const uint32_t groups = std::max(1u, gates);
   s.group = rows / groups;
-  const uint32_t most = teams_of(d) > 1 ? kSegments : kSegments / 2;
+  const uint32_t teams = teams_of(d);
+  const uint64_t turns = (uint64_t)groups * ((s.group + teams - 1) / teams);
+  const uint32_t most = std::max(teams > 1 ? kSegments : kSegments / 2,
+                                 (uint32_t)std::min<uint64_t>((turns + kTurns - 1) / kTurns, kMaxGrid));
   const uint32_t want = std::max(1u, most / groups);
-  uint32_t short_rows = teams_of(d);  // a power of two: whole turns of the teams
+  uint32_t short_rows = teams;  // a power of two: whole turns of the teams
   while (short_rows < kShortRows && (uint64_t)short_rows * kShortSegments < rows) short_rows *= 2;
   const uint32_t seg_rows = std::max((s.group + want - 1) / want, std::min(s.group, short_rows));
   s.segs = (s.group + seg_rows - 1) / seg_rows;
@@ -773,7 +789,8 @@ extern "C" int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, v
   if (e != hipSuccess) return hip_fail(e, "launch norm_grad");
   const bool gates = a.gate && a.segs > 1;
   if ((a.grid > 1 && (a.dw_r || a.dw_y)) || gates) {
-    const dim3 grid((a.d + kJoinCols - 1) / kJoinCols, 2 + (gates ? a.gates : 0));
+    a.joins = 2 + (gates ? a.gates : 0);
+    const dim3 grid((a.d + kJoinCols - 1) / kJoinCols, std::min(a.joins, kMaxGridY), (a.joins + kMaxGridY - 1) / kMaxGridY);
     if (d->dtype == PW_F32) hipLaunchKernelGGL(k_norm_join<float>, grid, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL(k_norm_join<__bf16>, grid, dim3(1024), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e, "launch norm_join");

@@ -17,6 +17,7 @@ from oracle import block as ob
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 EPS = 1e-5
+HALF = 2.0 ** -8
 
 # rows, d, dtype, gates, parts (y: block output, w: its norm, h: next norm)
 CASES = [
@@ -297,3 +298,47 @@ def test_refusals(gpu):
         f.grad(x, y=x, gate=g, w_r=w)                 # no dh, no r
     with pytest.raises(gpu.PwError):
         gpu.BlockNorm(8, 64, gates=3)
+
+
+@pytest.mark.parametrize("rows,d,parts", [(1 << 29, 8, "ywh"), (1 << 22, 1025, "yw")])
+def test_gradients_of_many_equal_rows(gpu, rows, d, parts):
+    """Thousands of equal rows for each workgroup, where fp32 additions err to the
+    same side: the weights' sums stay within 512 additions in a chain. Bar: a term
+    by 128 u, those additions, 112 more across teams and partial rows."""
+    s = make(1, d, "bf16", 0, parts)
+    s["x"] = None
+    if "h" in parts:
+        s["dr"], s["r"] = None, make(1, d, "bf16", 0, parts, 1)["x"]
+    long = {n: t if t is None or t.dim() == 1 else cuda(t).expand(rows, d).contiguous() for n, t in s.items()}
+    f = gpu.BlockNorm(rows, d, eps=EPS)
+    got = f.grad(long["dr"], long["dh"], long.get("r"), y=long["y"], w_y=cuda(s["w_y"]), w_r=cuda(s["w_r"]))
+    a = {n: f64(s[n]) for n in ("dr", "dh", "y", "w_y", "w_r")}
+    one = dict(r=f64(s.get("r")), x_scale=1.0, y_scale=1.0, eps=EPS, gate=None)
+    want, err = ob.block_norm_grad(u=128 * U, **a, **one)
+    _, more = ob.block_norm_grad(u=(128 + 512 + 112) * U, **a, **one)
+    for name, t in zip(("dx", "dy"), got):
+        assert bool((t == t[0]).all())
+        bound = err[name] + HALF * (np.abs(want[name]) + err[name]) + 1e-38
+        assert np.all(np.abs(f64(t[:1].cpu()) - want[name]) <= bound)
+    for name, t in (("dw_y", got[2]), ("dw_r", got[4])):
+        assert (t is None) == (name not in want)
+        if t is not None:
+            off = np.abs(f64(t.cpu()) / rows - want[name])
+            print(name, float((off / (more[name] + U * np.abs(want[name]))).max()), flush=True)
+            assert np.all(off <= more[name] + U * np.abs(want[name]))
+
+
+def test_more_gates_in_segments_than_a_grid_is_high(gpu):
+    """66000 gates of 16384 rows, each in two segments: the join is two grids deep. Whole
+    numbers, so that the sums are exact."""
+    gates, group = 66000, 16384
+    rows = gates * group
+    y = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    dr = torch.ones_like(y)
+    k = torch.arange(gates, device="cuda") % 5
+    dr.view(gates, group)[:, -3:] = k[:, None].to(torch.bfloat16)
+    gate = (1 + torch.arange(gates, device="cuda") % 3).to(torch.bfloat16)[:, None]
+    f = gpu.BlockNorm(rows, 1, gates=gates, eps=EPS)
+    dx, dy, _, dgate, _ = f.grad(dr, y=y, gate=gate)
+    assert torch.equal(dgate[:, 0], (group - 3 + 3 * k).float())
+    assert torch.equal(dx, dr) and torch.equal(dy.view(gates, group), dr.view(gates, group) * gate)
