@@ -346,7 +346,10 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
 constexpr int kNontemporal = 2;  // nt in the cache-policy operand of buffer instructions
-constexpr uint32_t kDwMaxTokens = 1u << 19;  // of a range: its rows of x (at most 2560 bytes) are one buffer
+// Tokens of a range at most: 768 additions to an accumulator, three for each 64
+// tokens, so that the sums are as good for any batch (2^26 equal tokens x 256 in
+// ranges of 2^18: off by 2.0e-4). A range's rows of x and dl are buffers below 2^31 bytes.
+constexpr uint32_t kDwMaxTokens = 1u << 14;
 constexpr uint32_t kDistant = 1u << 30;      // past the end of any range's dl, and below 2^32 with all that is added
 
 template <int NC, bool kStream, bool kMasked>  // expert blocks of 32; kMasked: there is a mask
@@ -472,7 +475,10 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
 }
 
 // Adds the partial sums of the token ranges: 64 columns of one expert per
-// workgroup, 4 slices of the ranges, in a fixed order.
+// workgroup, 4 slices of the ranges, in a fixed order: up to 64 ranges of a slice
+// in fp32, and these sums, whose number is not bounded, in double.
+constexpr uint32_t kDwJoinRun = 64 * 4;
+
 template <int NC>
 __global__ __launch_bounds__(256) void k_router_dw_join(DispatchGradArgs a) {
   __shared__ float s[4][64];
@@ -481,10 +487,15 @@ __global__ __launch_bounds__(256) void k_router_dw_join(DispatchGradArgs a) {
   const uint32_t o = blockIdx.x * 64 + lane, e = o / kDwCols % Ep, col = o / (kDwCols * Ep) * kDwCols + o % kDwCols;
   if (e >= a.E) return;  // whole workgroups
   const uint64_t n = (uint64_t)a.d * Ep;
-  float v = 0.f;
+  double runs = 0.0;
+  for (uint32_t i0 = 0; i0 < a.splits; i0 += kDwJoinRun) {
+    const uint32_t end = min(i0 + kDwJoinRun, a.splits);
+    float v = 0.f;
 #pragma unroll 16
-  for (uint32_t i = slice; i < a.splits; i += 4) v += a.part[i * n + o];
-  s[slice][lane] = v;
+    for (uint32_t i = i0 + slice; i < end; i += 4) v += a.part[i * n + o];
+    runs += (double)v;
+  }
+  s[slice][lane] = (float)runs;
   __syncthreads();
   if (slice == 0) a.dw[(uint64_t)col * a.E + e] = s[0][lane] + s[1][lane] + s[2][lane] + s[3][lane];
 }
@@ -548,18 +559,20 @@ struct DwLayout {
   size_t total = 0;
 };
 
-// Token ranges of dw: one workgroup per CU for long batches; short ones are cut
-// into 16 ranges of up to 256 tokens, as a range costs a partial sum of 64 KiB
-// (3000 x 1024: 22.2 us the whole call against 25.2 with ranges of 64 tokens).
+// Token ranges of dw: one workgroup per CU for long batches, two, three and so on
+// for those whose ranges would pass kDwMaxTokens; short ones are cut into 16
+// ranges of up to 256 tokens, as a range costs a partial sum of 64 KiB (3000 x
+// 1024: 22.2 us the whole call against 25.2 with ranges of 64 tokens).
 constexpr uint32_t kDwGrid = 256;
 constexpr uint64_t kDwShort = 256;
 
 DwLayout dw_layout(const pw_moe_grad_desc& d) {
   DwLayout l;
   const uint32_t groups = d.d / kDwCols;
-  const uint64_t want = std::max<uint64_t>(1, kDwGrid / groups);
+  uint64_t want = std::max<uint64_t>(1, kDwGrid / groups);
+  want *= std::max<uint64_t>(1, (d.tokens + want * kDwMaxTokens - 1) / (want * kDwMaxTokens));
   const uint64_t per = std::max((d.tokens + want - 1) / want, std::min(kDwShort, (d.tokens + 15) / 16));
-  l.split_tokens = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(64, (per + 63) / 64 * 64), kDwMaxTokens);
+  l.split_tokens = (uint32_t)std::max<uint64_t>(64, (per + 63) / 64 * 64);  // at most kDwMaxTokens
   l.splits = (uint32_t)std::max<uint64_t>(1, (d.tokens + l.split_tokens - 1) / l.split_tokens);
   if (l.splits > 1) l.total = up256((size_t)l.splits * d.d * (d.num_experts > 32 ? 64 : 32) * 4);
   return l;

@@ -377,3 +377,20 @@ def test_block_calls_out_of_order(gpu):
     with pytest.raises(gpu.PwError):
         block.grad_end(x)             # no grad_begin yet
     gpu.future_wait(f, 60_000_000_000)
+
+
+def test_router_gradient_of_many_equal_tokens(gpu):
+    """2^26 equal tokens, where fp32 additions err to the same side. The products
+    are exact, and so is the sum of a matrix instruction's 16 equal ones; it is
+    added to the accumulator in one rounding: 3 for each 64 tokens of a range of at
+    most 2^14, then 3 across waves, 64 ranges, and 4 slices."""
+    T, d, E = 1 << 26, 256, 2
+    g = torch.Generator().manual_seed(1)
+    x, dl, w = torch.randn(1, d, generator=g).to(bf), torch.randn(1, E, generator=g), torch.randn(d, E, generator=g).to(bf)
+    long = lambda t: t.cuda().expand(T, t.shape[1]).contiguous()  # noqa: E731
+    slot_of = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, d, dtype=bf, device="cuda")
+    _, dw = gpu.MoEGrad(T, d, E, rows=0).dispatch(none, long(dl), w.cuda(), long(x), slot_of=slot_of)
+    want = x.double().t().contiguous() @ dl.double()
+    off = (dw.double().cpu() / T - want).abs()
+    assert bool((off <= (3 * 256 + 3 + 64 + 4 + 2) * U * want.abs()).all())
