@@ -394,3 +394,26 @@ def test_router_gradient_of_many_equal_tokens(gpu):
     want = x.double().t().contiguous() @ dl.double()
     off = (dw.double().cpu() / T - want).abs()
     assert bool((off <= (3 * 256 + 3 + 64 + 4 + 2) * U * want.abs()).all())
+
+
+@pytest.mark.parametrize("T,d,E", [(50, 256, 3), (300, 512, 8), (200, 256, 33), (66000, 256, 64)])
+def test_router_terms_that_cancel(gpu, T, d, E):
+    """Pairs of experts with the same weights and opposite logit gradients but for
+    the last bits: dx is what the lowest bits of dlogits leave. Bar: all 24 bits of
+    them, fp32 sums of 3 E terms, and dx's own rounding."""
+    rng = np.random.default_rng([T, d, E])
+    dl = np.zeros((T, E), np.float32)
+    w = torch.from_numpy(rng.standard_normal((d, E)).astype(np.float32)).to(bf)
+    for e in range(0, E - 1, 2):
+        a = (1 + rng.random(T)).astype(np.float32)
+        dl[:, e], dl[:, e + 1] = a, -(a + 2.0 ** -20 * rng.integers(1, 9, T)).astype(np.float32)
+        w[:, e + 1] = w[:, e]
+    if E % 2:
+        dl[:, -1] = 0
+    slot_of = torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    dx, _ = gpu.MoEGrad(T, d, E, rows=0).dispatch(torch.empty(0, d, dtype=bf, device="cuda"), torch.from_numpy(dl).cuda(),
+                                                  w.cuda(), slot_of=slot_of)
+    want = dl.astype(np.float64) @ f64(w).T
+    size = np.abs(dl).astype(np.float64) @ np.abs(f64(w)).T
+    bound = 3 * E * U * size
+    assert np.all(np.abs(f64(dx.cpu()) - want) <= bound + HALF * (np.abs(want) + bound))
