@@ -67,6 +67,27 @@ __device__ __forceinline__ V load_row(const V* p) {
   return *p;
 }
 
+// Eight logit gradients as three bf16 terms each, of 8 of their 24 bits in turn:
+// cut off, not rounded, so that the largest finite value does not become infinite
+// and the last term holds what is left exactly. (The third term of a value below
+// 2^-110 may fall under bf16's range; an infinite value leaves a NaN behind.)
+__device__ __forceinline__ void split_terms(const float (&v)[8], bf16x8 (&terms)[3]) {
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = v[j];
+#pragma unroll
+  for (int m = 0; m < 3; ++m) {
+    u32x4 p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // the upper halves of two values
+      p[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, r[2 * j + 1]), __builtin_bit_cast(uint32_t, r[2 * j]), 0x07060302u);
+    terms[m] = __builtin_bit_cast(bf16x8, p);
+    if (m == 2) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r[j]) & 0xffff0000u);
+  }
+}
+
 // ---- slot_of: the inverse of src_index ---------------------------------------
 
 // Up to kSlotsInside tuples the combine's kernel inverts the index itself: each
@@ -273,13 +294,7 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = row[min(e0 + j, a.E - 1)];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dt[s][0][j] = (__bf16)v[j];
-        const float r1 = v[j] - (float)dt[s][0][j];
-        dt[s][1][j] = (__bf16)r1;
-        dt[s][2][j] = (__bf16)(r1 - (float)dt[s][1][j]);
-      }
+      split_terms(v, dt[s]);
     }
     const bool pad = a.valid && !a.valid[ti];
     // of the lane's own 4 tokens (4 h + r): row, whether there is one, padding
@@ -425,15 +440,7 @@ __global__ __launch_bounds__(kDwThreads) void k_router_dw(DispatchGradArgs a) {
       xa[q] = __builtin_bit_cast(bf16x8, p);
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = s.dl[c][j];
-        dt[c][0][j] = (__bf16)f;
-        const float r1 = f - (float)dt[c][0][j];
-        dt[c][1][j] = (__bf16)r1;
-        dt[c][2][j] = (__bf16)(r1 - (float)dt[c][1][j]);
-      }
+    for (int c = 0; c < NC; ++c) split_terms(s.dl[c], dt[c]);
     __builtin_amdgcn_sched_barrier(0);
     fetch(s, t + 64);
     __builtin_amdgcn_sched_barrier(0);

@@ -417,3 +417,25 @@ def test_router_terms_that_cancel(gpu, T, d, E):
     size = np.abs(dl).astype(np.float64) @ np.abs(f64(w)).T
     bound = 3 * E * U * size
     assert np.all(np.abs(f64(dx.cpu()) - want) <= bound + HALF * (np.abs(want) + bound))
+
+
+@pytest.mark.parametrize("T,E", [(70, 3), (70, 8), (3000, 64)])
+def test_the_largest_finite_logit_gradients(gpu, T, E):
+    """The largest fp32 value, which rounds to no finite bf16, gives what the formula
+    gives: finite results next to small weights and tokens."""
+    d = 256
+    rng = np.random.default_rng([T, E])
+    dl = rng.standard_normal((T, E)).astype(np.float32)
+    top = np.finfo(np.float32).max
+    dl[5, 1], dl[7, 0], dl[9, 2] = top, -top, top * np.float32(0.9999)
+    t = lambda *s, k: torch.from_numpy((rng.standard_normal(s) * k).astype(np.float32)).to(bf)  # noqa: E731
+    w, x = t(d, E, k=2.0 ** -12), t(T, d, k=2.0 ** -12)
+    none, slot_of = torch.empty(0, d, dtype=bf, device="cuda"), torch.full((T, 2), -1, dtype=torch.int32, device="cuda")
+    dx, dw = gpu.MoEGrad(T, d, E, rows=0).dispatch(none, torch.from_numpy(dl).cuda(), w.cuda(), x.cuda(), slot_of=slot_of)
+    dl64, w64, x64 = dl.astype(np.float64), f64(w), f64(x)
+    want, size = dl64 @ w64.T, np.abs(dl64) @ np.abs(w64).T
+    bound = 3 * E * U * size
+    assert np.all(np.abs(f64(dx.cpu()) - want) <= bound + HALF * (np.abs(want) + bound) + 1e-38)
+    span = token_range(T, d)
+    want, size = x64.T @ dl64, np.abs(x64).T @ np.abs(dl64)
+    assert np.all(np.abs(f64(dw.cpu()) - want) <= (48 * span // 64 + -(-T // span) + 8) * U * size + 1e-38)
