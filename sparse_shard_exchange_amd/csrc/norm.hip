@@ -394,7 +394,7 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : 4) void k_norm_gr
       else if (R.kTwice && TEAM > 64) __syncthreads();
       if (kH) {
         s = rsqrtf(fmaf(sum[0], a.inv_d, a.eps));
-        m = s * s * sum[1] * a.inv_d;
+        m = s * sum[1] * (s * a.inv_d);  // (s may be too large for its square)
       }
       if (norm_y) t = rsqrtf(fmaf(sum[2], a.inv_d, a.eps));
       float qy[1] = {0.f};
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(threads_of(TEAM), C * V > 8 ? 2 : 4) void k_norm_gr
         float m2 = 0.f;
         if (norm_y) {
           team_sum(qy, ex, turn);
-          m2 = t * t * qy[0] * a.inv_d;
+          m2 = t * qy[0] * (t * a.inv_d);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {

@@ -342,3 +342,29 @@ def test_more_gates_in_segments_than_a_grid_is_high(gpu):
     dx, dy, _, dgate, _ = f.grad(dr, y=y, gate=gate)
     assert torch.equal(dgate[:, 0], (group - 3 + 3 * k).float())
     assert torch.equal(dx, dr) and torch.equal(dy.view(gates, group), dr.view(gates, group) * gate)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 5), ("f32", 1001), ("bf16", 64), ("bf16", 1024)])
+def test_the_smallest_eps(gpu, dtype, d):
+    """eps below the normal numbers, next to rows of zeros: 1 / sqrt(eps) is finite,
+    its square is not. Bar: as elsewhere."""
+    rows, eps = 40, float(np.float32(1e-40))
+    s = make(rows, d, dtype, 0, "ywh")
+    zero = torch.arange(rows) % 3 == 0
+    c = {n: cuda(t) for n, t in s.items()}
+    x, y = c["x"].clone(), c["y"].clone()
+    x[zero.cuda()], y[zero.cuda()] = 0, 0
+    f = gpu.BlockNorm(rows, d, gpu.PW_BF16 if dtype == "bf16" else gpu.PW_F32, 0, 1.0, 1.0, eps)
+    e = half_step(s["x"].dtype)
+    v = dict(valid=None, x_scale=1.0, y_scale=1.0, eps=eps, gate=None, u=128 * U)
+    dx, dy, dw_y = (t.clone() for t in f.grad(c["dr"], y=y, w_y=c["w_y"])[:3])
+    want, err = ob.block_norm_grad(f64(s["dr"]), None, None, f64(y.cpu()), f64(s["w_y"]), w_r=None, **v)
+    hx, _, _, _, dw_r = f.grad(None, c["dh"], x, w_r=c["w_r"])
+    want2, err2 = ob.block_norm_grad(None, f64(s["dh"]), f64(x.cpu()), None, None, w_r=f64(s["w_r"]), **v)
+    assert float(np.abs(want["dy"][zero.numpy()]).max()) > 1e19
+    for got, w, b in ((dx, want["dx"], err["dx"]), (dy, want["dy"], err["dy"]), (hx, want2["dx"], err2["dx"])):
+        assert np.all(np.abs(f64(got.cpu()) - w) <= b + e * (np.abs(w) + b) + 1e-38)
+    for got, w, b in ((dw_y, want["dw_y"], err["dw_y"]), (dw_r, want2["dw_r"], err2["dw_r"])):
+        assert np.all(np.abs(f64(got.cpu()) - w) <= 3 * b + U * np.abs(w) + 1e-38)
+    r, h = f.forward(x, y=y, w_y=c["w_y"], w_r=c["w_r"])
+    assert not r[zero.cuda()].any() and not h[zero.cuda()].any() and bool(torch.isfinite(h).all())
