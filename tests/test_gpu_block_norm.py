@@ -368,3 +368,28 @@ def test_the_smallest_eps(gpu, dtype, d):
         assert np.all(np.abs(f64(got.cpu()) - w) <= 3 * b + U * np.abs(w) + 1e-38)
     r, h = f.forward(x, y=y, w_y=c["w_y"], w_r=c["w_r"])
     assert not r[zero.cuda()].any() and not h[zero.cuda()].any() and bool(torch.isfinite(h).all())
+
+
+@pytest.mark.parametrize("parts", ["y", "yw", "yh", "ywh"])
+@pytest.mark.parametrize("d", [513, 519, 1025, 1031, 1537, 2049, 4097])
+def test_in_place_where_two_waves_share_elements(gpu, d, parts):
+    """bf16 rows whose last chunk, moved back, begins in the last chunk of the wave
+    before: ceil(d / 8) = 64 n + 1. Both waves write those elements, and neither may
+    do so before the other has read them."""
+    assert -(-d // 8) % 64 == 1
+    rows = 6000
+    s = make(rows, d, "bf16", 6, parts)
+    c = {n: cuda(t) for n, t in s.items()}
+    f = gpu.BlockNorm(rows, d, gpu.PW_BF16, 6, 0.9, 0.7, EPS)
+    kw = dict(y=c["y"], w_y=c["w_y"], gate=c["gate"], w_r=c["w_r"])
+    r, h = (None if t is None else t.clone() for t in f.forward(c["x"], **kw))
+    back = [None if t is None else t.clone() for t in f.grad(c["dr"], c["dh"], r, **kw)]
+    few = slice(0, 1000 * 6, 1000)   # a row of each gate against the oracle
+    some = {n: t if t is None or n in ("w_y", "w_r", "gate") else t[few] for n, t in s.items()}
+    check_forward((r[few], None if h is None else h[few]), some, 0.9, 0.7)
+    same = lambda a, b: (a is None and b is None) or torch.equal(a, b)  # noqa: E731
+    for _ in range(3):
+        x, dr = c["x"].clone(), c["dr"].clone()
+        r2, h2 = f.forward(x, r=x, **kw)
+        assert r2 is x and same(r, r2) and same(h, h2)
+        assert all(same(a, b) for a, b in zip(back, f.grad(dr, c["dh"], r, dx=dr, **kw)))

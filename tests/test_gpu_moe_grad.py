@@ -439,3 +439,62 @@ def test_the_largest_finite_logit_gradients(gpu, T, E):
     span = token_range(T, d)
     want, size = x64.T @ dl64, np.abs(x64).T @ np.abs(dl64)
     assert np.all(np.abs(f64(dw.cpu()) - want) <= (48 * span // 64 + -(-T // span) + 8) * U * size + 1e-38)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,d,E", [(68000, 1280, 37), (68000, 1024, 64), (140000, 512, 20)])
+def test_all_of_the_router_weights_in_lds(gpu, T, d, E, masked):
+    """From 65521 tokens on a workgroup keeps all of W, 160 KiB of it at d = 1280 and
+    more than 32 experts, here with 512 MiB of rows and more, a capacity that drops
+    tuples, and padding that holds anything; 64-bit sums on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(T + masked)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    n = 2 * T - 5000                                    # kept tuples; 3000 rows behind them hold nothing
+    rows = n + 3000
+    src = torch.full((rows,), -5, dtype=torch.int32, device="cuda")
+    src[:n] = torch.randperm(2 * T, generator=g, device="cuda")[:n].int()
+    offsets = torch.full((E + 1,), n, dtype=torch.int64, device="cuda")
+    dout, y, gates = rnd(T, d).to(bf), rnd(rows, d).to(bf), torch.rand(T, 2, generator=g, device="cuda")
+    dxd, dl, w, x = rnd(rows, d).to(bf), rnd(T, E), (rnd(d, E) * d ** -0.5).to(bf), rnd(T, d).to(bf)
+    valid, live = None, torch.ones(T, dtype=torch.bool, device="cuda")
+    y[n:] = dxd[n:] = float("nan")
+    if masked:
+        valid = live = torch.rand(T, generator=g, device="cuda") < 0.8
+        for t in (dout, x, dl):
+            t[~valid] = float("nan")
+        gates[~valid] = float("inf")
+    assert (T + 2 * rows) * d * 2 >= 512 << 20 and (2 * T + rows) * d * 2 >= 512 << 20 or d == 512
+    f = gpu.MoEGrad(T, d, E, rows=rows)
+    dy = torch.full_like(y, 3.0)
+    dy, dg, slot_of = f.combine(dout, y, gates, src, offsets, valid, dy=dy)
+    assert bool((dy[n:] == 3).all())
+    want_slot = torch.full((2 * T,), -1, dtype=torch.int32, device="cuda")
+    want_slot[src[:n].long()] = torch.arange(n, device="cuda", dtype=torch.int32)
+    assert torch.equal(slot_of.view(-1), want_slot)
+    dx, dw = f.dispatch(dxd, dl, w, x, valid=valid)
+    assert not dx[~live].any() and not dg[~live].any()
+    want_dw, terms = (torch.zeros(d, E, dtype=torch.float64, device="cuda") for _ in range(2))
+    zero = lambda t, v: torch.where(v[:, None], t, torch.zeros_like(t)).double()  # noqa: E731
+    w64 = w.double().t().contiguous()
+    for lo in range(0, T, 16384):
+        hi = min(lo + 16384, T)
+        v, s = live[lo:hi], slot_of[lo:hi].long()
+        o, dl64, x64 = zero(dout[lo:hi], v), zero(dl[lo:hi], v), zero(x[lo:hi], v)
+        part, size = dl64 @ w64, dl64.abs() @ w64.abs()
+        add = torch.zeros_like(part)
+        for j in range(2):
+            have = s[:, j] >= 0
+            at = s[:, j].clamp(min=0)
+            yj, gj = zero(y[at], have & v), torch.where(v, gates[lo:hi, j], 0.0).double()[:, None]
+            assert bool(((dg[lo:hi, j].double() - (o * yj).sum(1)).abs() <= 64 * U * (o * yj).abs().sum(1)).all())
+            want = gj * o
+            assert bool((((dy[at].double() - want).abs() <= (HALF + 2 * U) * want.abs() + 1e-38) | ~have[:, None]).all())
+            r = zero(dxd[at], have & v)
+            part += r
+            add += r.abs()
+        bound = 200 * U * size + 4 * U * add
+        assert bool(((dx[lo:hi].double() - part).abs() <= bound + HALF * (part.abs() + bound) + 1e-38).all())
+        want_dw += x64.t().contiguous() @ dl64
+        terms += x64.abs().t().contiguous() @ dl64.abs()
+    span = token_range(T, d)
+    assert bool(((dw.double() - want_dw).abs() <= (48 * span // 64 + -(-T // span) + 8) * U * terms).all())

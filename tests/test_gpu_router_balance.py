@@ -253,3 +253,12 @@ def test_long_batches_of_equal_tokens(gpu, T, E):
     assert abs(loss[0] - BAL * E * p[0]) <= (rel + 8 * U) * BAL * E * p[0]
     e = U * (abs(lse) + 2 * width(row) + 32)
     assert abs(loss[1] - Z * lse ** 2) <= Z * (2 * abs(lse) * e + e * e + 330 * U * lse ** 2)
+
+
+@pytest.mark.parametrize("T,E,k,masked", [(300, 61, 2, None), (20000, 61, 2, "some"), (40000, 18, 3, "some"), (70001, 35, 8, None),
+                                          (3000, 3, 2, "some"), (70001, 2, 1, None), (140000, 3, 3, "some"), (9, 2, 2, None)])
+def test_expert_counts_that_fill_no_lane(gpu, T, E, k, masked):
+    """17 to 64 experts that are no multiple of 4 (a lane moved back to the row's
+    last four) and fewer than 4, in one launch and in two, and with one and with four
+    rows of the logit gradient in flight."""
+    test_loss_counts_and_gradient(gpu, T, E, k, masked)
