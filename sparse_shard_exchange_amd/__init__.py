@@ -533,6 +533,11 @@ def _address(t):
     return None if t is None else t.data_ptr() or 256
 
 
+def _storage(t):
+    """Where the memory that a tensor is a part of begins."""
+    return None if t is None else t.untyped_storage().data_ptr()
+
+
 class _Operator:
     """What the plan-less operators share: the device, checked arguments, and
     the workspace and output buffers, made by the first call that needs them,
@@ -796,8 +801,12 @@ class MoEBlock:
 
     def forward(self, x, valid=None, stream=None):
         """(r, loss [2], counts [E + 1], future of the MoE step); x is kept for the
-        backward pass."""
+        backward pass. x may be the r of an earlier call, which is then updated in
+        place and leaves no backward pass, but no other buffer that the step writes."""
         m = self.moe
+        at = _storage(x)
+        if at in [_storage(t) for t in (m.xd, m.y, m.out, self.norm_in._buffers.get("h"))]:
+            raise PwError(PW_ERR_INVALID, "x lies in a buffer that the step writes")
         if m.y.shape[0] < m.static_rows:
             raise PwError(PW_ERR_STATE, "the block's step needs an MoE with static buffers")
         self.h = self._back = None  # the step before is over, also if this one fails
@@ -805,14 +814,15 @@ class MoEBlock:
         f = m.step(h, stream)
         counts, _, loss = self.balance.loss(m.logits, m.experts, valid, stream)
         r, _ = self.norm_out.forward(x, y=m.out, w_y=self.w_out, gate=self.gate, stream=stream)
-        self.x, self.valid, self.h, self._counts = x, valid, h, counts
+        if at != _storage(r):
+            self.x, self.valid, self.h, self._counts = x, valid, h, counts
         return r, loss, counts, f
 
     def grad_begin(self, dr, stream=None):
         """dy [rows][d], the gradient of the expert outputs moe.y, from dr, that of r."""
         m = self.moe
         if self.h is None:
-            raise PwError(PW_ERR_STATE, "grad_begin follows a forward")
+            raise PwError(PW_ERR_STATE, "grad_begin follows a forward whose x is still there")
         self._back = None
         dx, dout, dw_out, dgate, _ = self.norm_out.grad(dr, y=m.out, w_y=self.w_out, gate=self.gate, valid=self.valid,
                                                         stream=stream)
