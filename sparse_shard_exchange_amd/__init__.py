@@ -657,8 +657,10 @@ class MoEGrad(_Operator):
         self.desc = pw_moe_grad_desc(tokens, self.rows, d, num_experts, 2, PW_BF16)
         self._workspace(lib.pw_moe_dispatch_grad_workspace, self.desc)
 
-    def _rows(self, t):
+    def _rows(self, name, t):
         """The descriptor of a call whose dispatched buffers are like t."""
+        if t is None or t.dim() != 2:
+            raise PwError(PW_ERR_INVALID, f"{name} must be a tensor of shape [rows][d]")
         n = t.shape[0]
         if n > self.rows:
             raise PwError(PW_ERR_INVALID, f"{n} dispatched rows, at most {self.rows}")
@@ -669,13 +671,13 @@ class MoEGrad(_Operator):
         """(dy like y, dgates [tokens][2] fp32, slot_of [tokens][2] int32) from
         the step's y, gates, src_index and offsets. Rows of dy behind
         offsets[E] are left as they are; dy=None: a kept buffer."""
-        n = self._rows(y)
+        n = self._rows("y", y)
         bf = torch.bfloat16
         if dy is None:
             dy = self._buf("dy", (self.rows, self.d), bf, stream)[:n]
         dgates = self._buf("dgates", (self.T, 2), torch.float32, stream)
         slot_of = self._buf("slot_of", (self.T, 2), torch.int32, stream)
-        if src_index.dim() == 1 and src_index.shape[0] > n:
+        if src_index is not None and src_index.dim() == 1 and src_index.shape[0] > n:
             src_index = src_index[:n]
         io = pw_combine_grad_io()
         io.dout = self._arg("dout", dout, (self.T, self.d), bf)
@@ -693,7 +695,7 @@ class MoEGrad(_Operator):
     def dispatch(self, dxd, dlogits, w_router, x=None, slot_of=None, valid=None, stream=None):
         """(dx [tokens][d] bf16, dw_router [d][E] fp32); slot_of None: that of
         the last combine() call; x None: dx alone (dw_router None)."""
-        n = self._rows(dxd)
+        n = self._rows("dxd", dxd)
         bf = torch.bfloat16
         if slot_of is None:
             slot_of = self._slot_of

@@ -498,3 +498,18 @@ def test_all_of_the_router_weights_in_lds(gpu, T, d, E, masked):
         terms += x64.abs().t().contiguous() @ dl64.abs()
     span = token_range(T, d)
     assert bool(((dw.double() - want_dw).abs() <= (48 * span // 64 + -(-T // span) + 8) * U * terms).all())
+
+
+def test_missing_arguments_are_refused(gpu):
+    s, _ = make(16, 256, 4, 0)
+    f = gpu.MoEGrad(16, 256, 4)
+    c = {n: None if t is None else t.cuda() for n, t in s.items()}
+    args = ("dout", "y", "gates", "src_index", "offsets")
+    for n in args:
+        with pytest.raises(gpu.PwError):
+            f.combine(*[None if m == n else c[m] for m in args])
+    f.combine(*[c[m] for m in args])
+    args = ("dxd", "dlogits", "w_router")
+    for n in args:
+        with pytest.raises(gpu.PwError):
+            f.dispatch(*[None if m == n else c[m] for m in args])

@@ -252,3 +252,14 @@ def test_norm_grad_workspace_errors():
         assert pw.lib.pw_block_norm_grad(C.byref(d), C.byref(io), ws, b, None) == code
     io.w_r = io.dr = None                                # neither part
     assert pw.lib.pw_block_norm_grad(C.byref(d), C.byref(io), P, n.value, None) == INV
+
+
+def test_missing_dispatched_rows_are_refused():
+    """The number of rows comes from y and dxd: without them, or from scalars, there is none."""
+    import torch
+    f = pw.MoEGrad(4, 256, 2, device="cuda:0")
+    for call in (lambda t: f.combine(None, t, None, None, None), lambda t: f.dispatch(t, None, None)):
+        for t in (None, torch.zeros(()), torch.zeros(8)):
+            with pytest.raises(pw.PwError) as e:
+                call(t)
+            assert e.value.code == INV
