@@ -408,8 +408,9 @@ int pw_plan_reset_times(pw_plan_t plan);
  * HIP graphs and replayed. All buffers and the stream must belong to the
  * current device. Buffers are contiguous and aligned to their elements (those
  * of the MOE gradients' rows to 16 bytes, their gates, slots and offsets to
- * 8); outputs must not overlap inputs or each other except where said. Sums are fp32 or wider and in a fixed order:
- * equal inputs give equal bits.
+ * 8); outputs must not overlap inputs or each other except where said. Sums are
+ * fp32 or wider and in a fixed order: equal inputs give equal bits. Sums over
+ * tokens or rows are split so that no fp32 chain grows with the batch.
  * ======================================================================== */
 
 /* ---- router balance: loss, per-expert counts, gradient of the logits ------
@@ -418,8 +419,8 @@ int pw_plan_reset_times(pw_plan_t plan);
  *   prob_mean[e] = 1/n sum_t p[t][e]
  *   loss[0]      = balance_coef E sum_e counts[e] / (k n) prob_mean[e]
  *   loss[1]      = z_coef / n sum_t (log sum_e exp logits[t][e])^2
- * and zeros if n == 0 (loss[1] also if z_coef is). Tokens with valid[t] == 0 are not looked at. An expert
- * id outside [0, E) is no tuple. A token whose logits are all -infinity has
+ * and zeros if n == 0 (loss[1] also if z_coef is). Tokens with valid[t] == 0 are
+ * not looked at. An expert id outside [0, E) is no tuple. A token whose logits are all -infinity has
  * zero probabilities and a zero logarithm. */
 typedef struct {
   uint64_t tokens;       /* at most 2^28; tokens x top_k below 2^31             */
@@ -470,7 +471,8 @@ typedef struct {
   const void* dout;         /* [tokens][d] gradient of the combined output      */
   const void* y;            /* [rows][d] expert outputs                         */
   const float* gates;       /* [tokens][2]                                      */
-  const int32_t* src_index; /* [rows] tuple held by each dispatched row         */
+  const int32_t* src_index; /* [rows] tuple held by each dispatched row, no tuple
+                               twice; values outside [0, 2 tokens) are no tuple */
   const int64_t* offsets;   /* [E + 1] segment offsets; rows from offsets[E] on
                                hold nothing and are left as they are            */
   const uint8_t* valid;     /* [tokens], nullable: where 0 (padding), dy and
@@ -484,8 +486,11 @@ typedef struct {
   const void* dxd;          /* [rows][d] gradient of the dispatched rows        */
   const float* dlogits;     /* [tokens][E] (pw_router_grad); an infinite value makes
                                its row of dx and its column of dw_router NaN    */
-  const void* w_router;     /* [d][E] bf16, as the plan was given it            */
-  const void* x;            /* [tokens][d] the step's tokens (with dw_router)   */
+  const void* w_router;     /* [d][E] bf16, as the plan was given it; an infinite
+                               value makes its column of dx infinite or NaN     */
+  const void* x;            /* [tokens][d] the step's tokens (with dw_router); an
+                               infinite value makes its row of dw_router infinite
+                               or NaN                                           */
   const int32_t* slot_of;   /* [tokens][2] (pw_moe_combine_grad)                */
   const uint8_t* valid;     /* [tokens], nullable: where 0 (padding), dx is zero
                                and the token adds nothing to dw_router, whatever
@@ -510,7 +515,8 @@ int pw_moe_dispatch_grad(const pw_moe_grad_desc* d, const pw_dispatch_grad_io* i
  * (ones), w_r with h (no next norm). Intermediate values stay fp32; r and h
  * are each rounded once (h is the norm of r before its rounding). The gradient
  * takes r as it was stored. A row whose sum of squares passes the range of fp32
- * counts as one of infinite length. */
+ * counts as one of infinite length; in the gradient a row's sums of products, of
+ * rows and their gradients, have to stay in that range too. */
 typedef struct {
   uint64_t rows;     /* at most 2^31 - 1; a multiple of gates                   */
   uint32_t d;        /* 1..8192                                                 */

@@ -9,10 +9,10 @@
 // Both kernels read each logit once: a token's row is spread over a group of
 // L lanes of 4 experts each (L = 4, 16, 64 for E <= 16, 64, 256), so a wave's
 // load covers 64 / L whole rows, and the row's maximum, sum and dot product
-// are lane exchanges inside the group. 131072 x 64: loss 11 + 4.4 us (35 MB, 3.1
-// TB/s), gradient 15.5 us (70 MB, 4.5 TB/s): reading, with the first loads', the
-// arithmetic's (a quarter) and the launches' latency on top. 48 x 8: 4.2 us, a few
-// memory latencies.
+// are lane exchanges inside the group. 131072 x 64: loss 11.0 + 4.5 us (35 MB,
+// 3.2 TB/s), gradient 15.6 us (70 MB, 4.5 TB/s). At this size a workgroup of the loss
+// makes two passes, the second's loads behind the first's arithmetic, and the join
+// is a launch's latency. 48 x 8: 4.1 us, a few memory latencies.
 #include "ops.h"
 
 #include <algorithm>

@@ -54,11 +54,12 @@ struct DispatchGradArgs {
 
 // Row loads bypass the caches (kStream) where the call's rows are twice the
 // last-level cache (256 MiB) or more, so that none can still be there: combine,
-// 131072 tokens x 1024, 271 us against 276 with plain loads, dispatch 233
-// against 239 (both before later steps); below, rows that the caches hold are
-// read from them (16384 tokens: combine 31 us against 37, dispatch 45 against
-// 55). Rows are always stored nontemporally: written plainly, they are written
-// back during the reads of the next kernel (dW after dx: 72 us against 81).
+// 131072 tokens x 1024, 260 us against 267 with plain loads, dispatch 228
+// against 237; below, rows that the caches hold are read from them (16384 tokens:
+// combine 36.3 us against 37.7, dispatch 51.3 against 54.2). Rows are always stored
+// nontemporally: written plainly, they are written back during later reads
+// (131072 tokens: combine 273 us, dispatch 239; 16384: 41.5 and 52.0). All are
+// times of the whole call.
 constexpr uint64_t kStreamBytes = 512ull << 20;
 
 template <bool kStream, typename V>
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(256) void k_slots_put(CombineGradArgs a) {
 // One wave handles kTokens tokens: their slots and gates in one round of loads,
 // then every chunk of dout and of both y rows in flight before any is used (a
 // dropped tuple reads row 0 and is masked). A workgroup takes its 8 tokens and
-// ends: 131072 tokens x 1024, 253 us, 5.3 TB/s on random rows of 2 KiB, against
+// ends: 131072 tokens x 1024, 254 us, 5.3 TB/s on random rows of 2 KiB, against
 // 264 us with 2048 workgroups that walk the tokens. Bound by HBM.
 constexpr int kTokens = 2;
 
@@ -360,10 +361,10 @@ __global__ __launch_bounds__(kDxThreads) void k_dispatch_grad(DispatchGradArgs a
 // terms, which hold all 24 bits of it: every product is exact and the sums
 // are fp32 (an infinite dl gives NaN). A workgroup covers 256 columns (2 waves
 // of 128) with 4 waves of tokens each, joined through LDS in a fixed order.
-// 131072 tokens x 1024, 64 experts: 55 to 72 us (4.2-5.5 TB/s), reading x and dl
-// once from HBM; the split and the matrix instructions take nearly as long as the
-// reads, so it probably follows the core clock. (Sharing the split terms between the waves through LDS, and
-// requesting x two steps ahead, measured no faster.)
+// 131072 tokens x 1024, 64 experts: 57 to 72 us from one run to another (4.2-5.3
+// TB/s), reading x and dl once from HBM; what makes the difference is not known.
+// (Sharing the split terms between the waves through LDS, and requesting x two
+// steps ahead, measured no faster.)
 constexpr uint32_t kDwThreads = 512;
 constexpr uint32_t kDwCols = 256;
 constexpr int kNontemporal = 2;  // nt in the cache-policy operand of buffer instructions
@@ -520,10 +521,12 @@ __global__ __launch_bounds__(256) void k_router_dw_zero(DispatchGradArgs a) {
 }
 
 constexpr size_t kDefaultLds = 64 << 10;  // what a kernel may use without asking
+constexpr uint32_t kMaxD = 1280;          // width of a row at most
 
 template <int KS, bool kFour, bool kStream>
 hipError_t launch_dx_steps(const DispatchGradArgs& a, uint32_t grid, hipStream_t s) {
   const size_t lds = (size_t)a.d / a.col_groups * KS * 64;
+  static_assert(kMaxD * 2 * 64 <= 160 << 10, "all of W in the LDS of a CU");
   if (lds > kDefaultLds) {
     const hipError_t e = hipFuncSetAttribute((const void*)k_dispatch_grad<KS, kFour, kStream>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -595,7 +598,8 @@ int validate(const pw_moe_grad_desc* d) {
   if (!d) return fail(PW_ERR_INVALID, "descriptor is NULL");
   if (d->tokens > (1ull << 28)) return fail(PW_ERR_INVALID, "tokens must be at most 2^28");
   if (d->rows > 2 * d->tokens) return fail(PW_ERR_INVALID, "rows must be at most 2 tokens");
-  if (d->d == 0 || d->d % 256 || d->d > 1280) return fail(PW_ERR_INVALID, "d must be a positive multiple of 256, <= 1280");
+  if (d->d == 0 || d->d % 256 || d->d > kMaxD)
+    return fail(PW_ERR_INVALID, "d must be a positive multiple of 256, <= %u", kMaxD);
   if (d->num_experts < 2 || d->num_experts > 64) return fail(PW_ERR_INVALID, "num_experts must be in [2, 64]");
   if (d->top_k != 2) return fail(PW_ERR_UNSUPPORTED, "only top-2 routing is built");
   if (d->dtype != PW_BF16) return fail(PW_ERR_INVALID, "rows and weights are bf16");

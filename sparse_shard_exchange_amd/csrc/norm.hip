@@ -15,12 +15,14 @@
 // A row lives in the registers of its team (16 lanes up to 128 elements, up to
 // 16 waves for the widest) from its only read to its only write, so the passes
 // move 4 and 6 row tensors and nothing else; the bound is HBM. 131072 x 1024
-// bf16, all parts: forward 176 us (6.1 TB/s), backward 308 + 11 us (5.0 TB/s); a
-// large copy reaches 5.2. Rows are stored nontemporally: written plainly, they
-// are written back during the next operator's reads (forward and backward in
-// turn, 131072 rows 527 us against 542, 32768 rows 126 against 135, 16384 rows,
-// where the last-level cache would hold them, 70 against 67). They are loaded
-// plainly: nontemporal loads take 3% less at 131072 rows, 10% more below 65536.
+// bf16, all parts: forward 178 us (6.0 TB/s), backward 307 + 11.6 us (5.2 TB/s in
+// the first); a large copy reaches 5.2. Rows are stored nontemporally: written
+// plainly, they are written back during the next operator's reads (forward and
+// backward in turn, 131072 rows 493 us against 508, 32768 rows 142 against 146,
+// 16384 rows 86.8 against 87.7). They are loaded plainly: nontemporal loads take
+// 4% less in the gradient from 65536 rows on (131072: 306 us against 318), as long
+// or up to 17% more below (forward 16384 rows 25.4 against 21.7, gradient 4096 rows
+// 21.6 against 19.4).
 #include "ops.h"
 
 #include <algorithm>
@@ -104,9 +106,9 @@ __device__ __forceinline__ void put(Chunk<T, V>& c, int v, float f) {
 
 // A row's chunks. Rows that are whole aligned chunks (kWhole) have no rest; in
 // others the last chunk is moved back to end with the row, and its first `over`
-// elements are those of the chunk before it (131072 x 1023 bf16 in 16-byte
-// accesses at any alignment: forward 177 us, backward 341, by single elements 280
-// and 474). No sum sees them twice. Chunks of 8 write them twice (kTwice), with
+// elements are those of the chunk before it (131072 x 1023 bf16, all parts, in
+// 16-byte accesses at any alignment: forward 182 us, backward 338, by single
+// elements 270 and 471). No sum sees them twice. Chunks of 8 write them twice (kTwice), with
 // the same bits; chunks of 4, two or four of them a thread and fewer registers
 // left, zero them after the load and store their own elements one by one
 // (backward, this way against the other: 131072 x 1023 bf16 341 us against 370,
@@ -526,8 +528,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_zero(NormArgs a) {
 // per row. At most 8 elements a thread, so that the gradient's registers (rows,
 // sums, weights) leave room for 4 waves per SIMD (2047 x 1001 fp32 by 256
 // threads with room for 8 elements each, half of it unused: 42 us against 16).
-// Narrow rows share a wave, 4 or 2 at a time (300000 x 128 bf16: forward 44 us,
-// backward 88; with a wave for each row 94 and 207; 4096 x 127 9.5 against 9.7).
+// Narrow rows share a wave, 4 or 2 at a time (300000 x 128 bf16, all parts: forward
+// 53.5 us, backward 95; with a wave for each row 109 and 202).
 // Above 4096 elements fp32 rows take 16 elements by 512 threads: 1024 threads of
 // 8 spill (backward, 8192 x 8192: 570 us against 405; for bf16, whose chunks are
 // half as wide in registers, it is the other way round, 477 against 505; both

@@ -1,5 +1,5 @@
-// Host checks shared by the plan-less operators (balance.hip, moe_grad.hip,
-// norm.hip): they take a descriptor, buffers, a workspace and a stream.
+// What the plan-less operators share (balance.hip, moe_grad.hip, norm.hip): sums
+// and maxima over lanes, and the host checks of buffers, workspace and stream.
 #pragma once
 
 #include <math.h>
