@@ -842,6 +842,8 @@ class MoEBlock:
         dl = self.balance.grad(m.logits, m.experts, self._counts, m.gates, dgates, self.valid, grad_loss, stream)
         dh, dw_router = self.grads.dispatch(dxd, dl, m.w[0], self.h, slot_of, self.valid, stream)
         dx, _, _, _, dw_in = self.norm_in.grad(dr, dh, self.x, w_r=self.w_in, valid=self.valid, stream=stream)
+        if _storage(dx) == _storage(self.x):  # x was an earlier call's "x" gradient, whose buffer this one is
+            self.h = self._back = None
         return {"x": dx, "w_in": dw_in, "w_out": dw_out, "gate": dgate, "w_router": dw_router}
 
 

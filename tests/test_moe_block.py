@@ -116,6 +116,20 @@ def test_an_x_that_is_updated_in_place_has_no_backward_pass(block):
     assert refused(block.grad_end, "dxd") == pw.PW_ERR_STATE
 
 
+def test_an_x_that_grad_end_overwrites_is_gone_after_it(block):
+    g = Memory("the gradient's buffer")
+    block.norm_in = Ops()
+    block.norm_in.grad = lambda *a, **kw: (g, None, None, None, None)
+    block.forward(Memory("x"))
+    block.grad_begin("dr")
+    assert block.grad_end("dxd")["x"] is g
+    block.forward(g)
+    block.grad_begin("dr")
+    block.grad_end("dxd")
+    assert refused(block.grad_end, "dxd") == pw.PW_ERR_STATE
+    assert refused(block.grad_begin, "dr") == pw.PW_ERR_STATE
+
+
 @pytest.mark.gpu
 def test_steps_after_the_first(gpu):
     """A second step's grad_end without a grad_begin is refused, and its
