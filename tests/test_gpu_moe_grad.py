@@ -3,8 +3,8 @@ against the oracle in 64 bits, and a run of the whole block.
 
 Bars, u = 2^-24, bf16's half step 2^-8: dy is one fp32 product rounded once; a
 gate's gradient is an fp32 sum of d <= 1280 products, 24 in a lane and 6
-exchanges (64 u of its terms); dx adds a product whose dlogits keep 2^-16 of
-their value (two bf16 terms) and sum in fp32, and two rows; dw_router's
+exchanges (64 u of its terms); dx adds a product in fp32, for which the bar
+lets dlogits lose 2^-16 (they lose nothing), and two rows; dw_router's
 products are exact and its sums fp32: over a token range 48 roundings (3 terms
 of 16 tokens) for each 64 tokens, then 4 waves and the ranges, 65536 / d of them
 at most and whole multiples of 64 tokens.
