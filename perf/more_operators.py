@@ -100,7 +100,8 @@ def _codes(x):
 
 
 def _padded(d):
-    return (d + 15) // 16 * 16
+    """Bytes of a row of codes: whole steps of the matrix instructions, zeros behind its d."""
+    return (d + 63) // 64 * 64
 
 
 def prepare(case, seed):
