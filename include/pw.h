@@ -551,6 +551,147 @@ int pw_block_norm_grad_workspace(const pw_norm_desc* d, size_t* bytes);
 int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, void* ws, size_t ws_bytes, void* stream);
 
 /* ======================================================================== *
+ * Operators that serve a mixture of experts with any top-k (PATHWAYS page,
+ * section 6.3: data is routed to the accelerators that hold different
+ * experts' weights): the routing, the experts' products in 8-bit integers and
+ * the combine. The tuples are ordered by expert between routing and products
+ * with the exchange itself (pw_exchange or pw_exchange_scratch, destination =
+ * expert, E + 1 destinations: padding goes to the last). Conventions as of the
+ * operators above: no plan, kernel launches only, capturable, contiguous
+ * buffers, outputs that overlap nothing else, sums of 32 bits or more in a fixed
+ * order. Buffers are aligned to their elements, codes (w, q) to 16 bytes.
+ * ======================================================================== */
+
+/* ---- routing ---------------------------------------------------------------
+ * Of a token's logits l over E experts, with a bias b that balances the choice:
+ *   s_e = softmax(l)_e  or  1 / (1 + exp(-l_e))
+ *   c_e = s_e + b_e, compared in 64 bits
+ *   mark of a group of E / groups neighbouring experts: the sum of its group_best
+ *   highest c; the experts of the top_groups groups of highest mark may be chosen
+ *   experts[j]: the k highest c among them, best first
+ *   weights[j] = scale s_ej, divided by the sum of the k chosen s if renorm
+ * Equal values: the lowest index comes first. An expert whose logit or bias is NaN or
+ * -infinity is never chosen (and a NaN logit adds nothing to the softmax; +infinity
+ * counts as the largest finite value); a group of such experts alone is never kept, and
+ * one with a single other has that one's c as its mark. Where fewer than k experts can be
+ * chosen, and where valid[t] == 0, the expert is E (no expert) and the weight 0. Weights
+ * that renorm divides keep their ratio also where the scores underflow. */
+typedef enum { PW_SCORE_SOFTMAX = 0, PW_SCORE_SIGMOID = 1 } pw_score;
+
+typedef struct {
+  uint64_t tokens;       /* at most 2^28; tokens x top_k below 2^31             */
+  uint32_t num_experts;  /* 2..256                                              */
+  uint32_t top_k;        /* 1..8, at most num_experts                           */
+  uint32_t score;        /* pw_score                                            */
+  uint32_t groups;       /* 1..16, divides num_experts                          */
+  uint32_t top_groups;   /* 1..groups                                           */
+  uint32_t group_best;   /* 1 or 2                                              */
+  uint32_t renorm;       /* 0 or 1                                              */
+  float scale;           /* finite                                              */
+} pw_route_desc;
+
+typedef struct {
+  const float* logits;   /* [tokens][E]                                         */
+  const float* bias;     /* [E], nullable (pw_route; the gradient has no part of it) */
+  const uint8_t* valid;  /* [tokens], nullable: where 0 (padding) the token is not looked at */
+  int32_t* experts;      /* [tokens][k]: written by pw_route, read by pw_route_grad
+                            (there an id outside [0, E) is no expert)           */
+  float* weights;        /* [tokens][k] (pw_route)                              */
+  /* pw_route_grad only */
+  const float* dweights; /* [tokens][k] gradient of the weights                 */
+  const float* add;      /* [tokens][E] added to the result, e.g. the dlogits of
+                            pw_router_grad; nullable                            */
+  float* dlogits;        /* [tokens][E], written whole: zero where valid == 0; may be add */
+} pw_route_io;
+
+int pw_route(const pw_route_desc* d, const pw_route_io* io, void* stream);
+/* The gradient of the weights with the choice as a constant (groups, top_groups and
+ * group_best are not looked at). */
+int pw_route_grad(const pw_route_desc* d, const pw_route_io* io, void* stream);
+
+/* ---- rows as 8-bit codes ----------------------------------------------------
+ *   scale = max |x| / 127,  q = the whole number nearest to x / scale (both
+ * quotients rounded to fp32, ties to even), x ~ scale q. A row of zeros, or whose scale
+ * underflows to zero, has zeros; one that holds an infinity or a NaN has zeros and the
+ * scale NaN, so that what is computed from it is NaN. A row of codes takes
+ * PW_Q8_ROW(d) bytes, zeros behind the d-th. Weights are rows too: one for each
+ * output channel. */
+#define PW_Q8_ROW(d) (((uint64_t)(d) + 63) / 64 * 64)
+
+typedef struct {
+  uint64_t rows;         /* at most 2^31 - 1                                    */
+  uint32_t d;            /* 1..65536                                            */
+  uint32_t dtype;        /* pw_dtype of x                                       */
+} pw_quant_desc;
+
+typedef struct {
+  const void* x;         /* [rows][d]                                           */
+  const int64_t* limit;  /* device [1], nullable: rows from *limit on are not read
+                            and their outputs left as they are                  */
+  int8_t* q;             /* [rows][PW_Q8_ROW(d)]                                */
+  float* scale;          /* [rows]                                              */
+} pw_quant_io;
+
+int pw_quant_rows(const pw_quant_desc* d, const pw_quant_io* io, void* stream);
+
+/* ---- products in 8-bit integers --------------------------------------------
+ * For each dispatched row i of expert e (offsets[e] <= i < offsets[e + 1]):
+ *   out[o][j] = act(q_scale[a] w_scale[e][j] sum_k q[a][k] w[e][j][k])
+ * with q and q_scale the codes of x as pw_quant_rows makes them, the sum exact,
+ * act GELU (z Phi(z)) or nothing, the result rounded once. Row a of x is i, or
+ * src_index[i] / gather where gather > 0 (x holds tokens, of gather tuples each);
+ * row o of out is i, or src_index[i] where scatter is set (out is in tuple
+ * order). Rows of out that no i names are left as they are: those behind
+ * offsets[E], and those whose src_index is no row. src_index holds no tuple twice.
+ * Without offsets (num_experts 1) every row is the one matrix's. */
+typedef struct {
+  uint64_t rows;         /* dispatched rows at most, the rows of out: at most 2^31 - 1 */
+  uint64_t x_rows;       /* rows of x: at least rows if gather == 0             */
+  uint32_t d;            /* 1..65536                                            */
+  uint32_t n;            /* 1..65536                                            */
+  uint32_t num_experts;  /* 1..256                                              */
+  uint32_t dtype;        /* pw_dtype of x and out                               */
+  uint32_t gather;       /* tuples of each row of x, 0: x is in dispatched order; at most 256 */
+  uint32_t scatter;      /* 0 or 1                                              */
+  uint32_t gelu;         /* 0 or 1                                              */
+} pw_q8_desc;
+
+typedef struct {
+  const void* x;             /* [x_rows][d]; NULL: q and q_scale are given instead */
+  const int8_t* q;           /* [x_rows][PW_Q8_ROW(d)], in [-127, 127]          */
+  const float* q_scale;      /* [x_rows]                                        */
+  const int8_t* w;           /* [E][n][PW_Q8_ROW(d)], zeros behind the d-th     */
+  const float* w_scale;      /* [E][n]                                          */
+  const int64_t* offsets;    /* [E + 1] ascending (one below an earlier one counts as
+                                that); nullable if num_experts == 1             */
+  const int32_t* src_index;  /* [rows] (with gather or scatter)                 */
+  void* out;                 /* [rows][n]                                       */
+} pw_q8_io;
+
+int pw_q8_product_workspace(const pw_q8_desc* d, size_t* bytes);
+int pw_q8_product(const pw_q8_desc* d, const pw_q8_io* io, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- combine ----------------------------------------------------------------
+ *   out[t] = add[t] + sum_j weights[t][j] y[t][j]
+ * in fp32, rounded once. A tuple of weight 0 (no expert) adds nothing, whatever its
+ * row of y holds. */
+typedef struct {
+  uint64_t tokens;       /* at most 2^31 - 1                                    */
+  uint32_t d;            /* 1..65536                                            */
+  uint32_t top_k;        /* 1..8                                                */
+  uint32_t dtype;        /* pw_dtype of y, add and out                          */
+} pw_combine_desc;
+
+typedef struct {
+  const void* y;         /* [tokens][k][d]: tuple order                         */
+  const float* weights;  /* [tokens][k]                                         */
+  const void* add;       /* [tokens][d], nullable                               */
+  void* out;             /* [tokens][d] (may be add)                            */
+} pw_topk_combine_io;
+
+int pw_topk_combine(const pw_combine_desc* d, const pw_topk_combine_io* io, void* stream);
+
+/* ======================================================================== *
  * Multi-tenant scheduler (PATHWAYS page, section 5.2 "Multi-tenancy",
  * Figures 8 and 9; Appendix D, Figure 11): programs of several clients are
  * gang-scheduled onto the whole GPU one after another, interleaved at the

@@ -108,6 +108,44 @@ class pw_norm_io(C.Structure):
                                           "dgate", "dw_r")]
 
 
+PW_SCORE_SOFTMAX, PW_SCORE_SIGMOID = 0, 1
+
+
+class pw_route_desc(C.Structure):
+    _fields_ = [("tokens", C.c_uint64), ("num_experts", C.c_uint32), ("top_k", C.c_uint32), ("score", C.c_uint32),
+                ("groups", C.c_uint32), ("top_groups", C.c_uint32), ("group_best", C.c_uint32), ("renorm", C.c_uint32),
+                ("scale", C.c_float)]
+
+
+class pw_route_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("logits", "bias", "valid", "experts", "weights", "dweights", "add", "dlogits")]
+
+
+class pw_quant_desc(C.Structure):
+    _fields_ = [("rows", C.c_uint64), ("d", C.c_uint32), ("dtype", C.c_uint32)]
+
+
+class pw_quant_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x", "limit", "q", "scale")]
+
+
+class pw_q8_desc(C.Structure):
+    _fields_ = [("rows", C.c_uint64), ("x_rows", C.c_uint64), ("d", C.c_uint32), ("n", C.c_uint32), ("num_experts", C.c_uint32),
+                ("dtype", C.c_uint32), ("gather", C.c_uint32), ("scatter", C.c_uint32), ("gelu", C.c_uint32)]
+
+
+class pw_q8_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x", "q", "q_scale", "w", "w_scale", "offsets", "src_index", "out")]
+
+
+class pw_combine_desc(C.Structure):
+    _fields_ = [("tokens", C.c_uint64), ("d", C.c_uint32), ("top_k", C.c_uint32), ("dtype", C.c_uint32)]
+
+
+class pw_topk_combine_io(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("y", "weights", "add", "out")]
+
+
 PW_PROG_CHAIN, PW_PROG_EXCHANGE = 0, 1
 
 
@@ -165,6 +203,12 @@ _SIGNATURES = {
     "pw_block_norm_grad_workspace": (C.c_int, [C.POINTER(pw_norm_desc), C.POINTER(C.c_size_t)]),
     "pw_block_norm_grad": (C.c_int, [C.POINTER(pw_norm_desc), C.POINTER(pw_norm_io), C.c_void_p, C.c_size_t,
                                      C.c_void_p]),
+    "pw_route": (C.c_int, [C.POINTER(pw_route_desc), C.POINTER(pw_route_io), C.c_void_p]),
+    "pw_route_grad": (C.c_int, [C.POINTER(pw_route_desc), C.POINTER(pw_route_io), C.c_void_p]),
+    "pw_quant_rows": (C.c_int, [C.POINTER(pw_quant_desc), C.POINTER(pw_quant_io), C.c_void_p]),
+    "pw_q8_product_workspace": (C.c_int, [C.POINTER(pw_q8_desc), C.POINTER(C.c_size_t)]),
+    "pw_q8_product": (C.c_int, [C.POINTER(pw_q8_desc), C.POINTER(pw_q8_io), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "pw_topk_combine": (C.c_int, [C.POINTER(pw_combine_desc), C.POINTER(pw_topk_combine_io), C.c_void_p]),
     "pw_sched_create": (C.c_int, [C.c_uint32, C.POINTER(C.c_void_p)]),
     "pw_sched_add_client": (C.c_int, [C.c_void_p, C.c_uint32, C.POINTER(C.c_uint32)]),
     "pw_sched_submit": (C.c_int, [C.c_void_p, C.c_uint32, C.POINTER(pw_program), C.POINTER(C.c_uint64)]),
@@ -772,6 +816,150 @@ class BlockNorm(_Operator):
         io.dy, io.dw_y, io.dgate, io.dw_r = _address(dy), _address(dw_y), _address(dgate), _address(dw_r)
         self._run(lib.pw_block_norm_grad, self.desc, io, stream, ws=True)
         return dx, dy, dw_y, dgate, dw_r
+
+
+class Router(_Operator):
+    """Routing of tokens to experts (pw_route) and the gradient of its weights
+    (pw_route_grad): softmax or sigmoid scores, a bias that balances the choice,
+    groups, top-k, renormalised weights. Padding (valid 0) and places without an
+    expert get the id num_experts and the weight 0."""
+
+    def __init__(self, tokens, num_experts, top_k, score="softmax", groups=1, top_groups=1, group_best=2, renorm=True,
+                 scale=1.0, device="cuda"):
+        super().__init__(device)
+        kinds = {"softmax": PW_SCORE_SOFTMAX, "sigmoid": PW_SCORE_SIGMOID}
+        if score not in kinds:
+            raise PwError(PW_ERR_INVALID, f"score must be one of {sorted(kinds)}, got {score!r}")
+        self.T, self.E, self.k = tokens, num_experts, top_k
+        self.desc = pw_route_desc(tokens, num_experts, top_k, kinds[score], groups, top_groups, group_best, bool(renorm), scale)
+
+    def _io(self, logits, valid):
+        io = pw_route_io()
+        io.logits = self._arg("logits", logits, (self.T, self.E), torch.float32)
+        io.valid = self._arg("valid", valid, (self.T,), torch.bool, torch.uint8)
+        return io
+
+    def forward(self, logits, bias=None, valid=None, stream=None):
+        """(experts [tokens][k] int32, best first; weights [tokens][k] fp32)."""
+        io = self._io(logits, valid)
+        io.bias = self._arg("bias", bias, (self.E,), torch.float32)
+        experts = self._buf("experts", (self.T, self.k), torch.int32, stream)
+        weights = self._buf("weights", (self.T, self.k), torch.float32, stream)
+        io.experts, io.weights = _address(experts), _address(weights)
+        self._run(lib.pw_route, self.desc, io, stream)
+        return experts, weights
+
+    def grad(self, logits, experts, dweights, valid=None, add=None, stream=None):
+        """dlogits [tokens][E] of dweights, with the choice as a constant; add: a
+        gradient of the logits that is added (RouterBalance.grad's)."""
+        io = self._io(logits, valid)
+        io.experts = self._arg("experts", experts, (self.T, self.k), torch.int32)
+        io.dweights = self._arg("dweights", dweights, (self.T, self.k), torch.float32)
+        io.add = self._arg("add", add, (self.T, self.E), torch.float32)
+        out = self._buf("dlogits", (self.T, self.E), torch.float32, stream)
+        io.dlogits = _address(out)
+        self._run(lib.pw_route_grad, self.desc, io, stream)
+        return out
+
+
+def q8_row(d):
+    """Bytes of a row of d 8-bit codes (PW_Q8_ROW)."""
+    return (d + 63) // 64 * 64
+
+
+class RowQuant(_Operator):
+    """Rows as 8-bit codes with a scale each (pw_quant_rows): tokens, or
+    weights [experts * n][d] with a row for each output channel."""
+
+    def __init__(self, rows, d, dtype=PW_BF16, device="cuda"):
+        super().__init__(device)
+        self.T, self.d = rows, d
+        self.dtype = torch.float32 if dtype == PW_F32 else torch.bfloat16
+        self.desc = pw_quant_desc(rows, d, dtype)
+
+    def forward(self, x, limit=None, q=None, scale=None, stream=None):
+        """(q [rows][q8_row(d)] int8, scale [rows] fp32); q and scale may be given.
+        limit: an int64 tensor of one element on the device; rows from there on are
+        left as they are."""
+        if q is None:
+            q = self._buf("q", (self.T, q8_row(self.d)), torch.int8, stream)
+        if scale is None:
+            scale = self._buf("scale", (self.T,), torch.float32, stream)
+        io = pw_quant_io()
+        io.x = self._arg("x", x, (self.T, self.d), self.dtype)
+        io.limit = self._arg("limit", limit, (1,), torch.int64)
+        io.q = self._arg("q", q, (self.T, q8_row(self.d)), torch.int8)
+        io.scale = self._arg("scale", scale, (self.T,), torch.float32)
+        self._run(lib.pw_quant_rows, self.desc, io, stream)
+        return q, scale
+
+
+class Int8Product(_Operator):
+    """Products of dispatched rows with their experts' matrices in 8-bit integers
+    (pw_q8_product): out = act(x_scale w_scale (x codes . w codes)). w
+    [experts][n][q8_row(d)] int8 with w_scale [experts][n], as RowQuant makes
+    them (borrowed: keep them alive). rows: dispatched rows at most. gather k: x
+    holds tokens of k tuples each, and src_index[i] // k is the row of dispatched
+    row i; scatter: out is in tuple order, row i at src_index[i]."""
+
+    def __init__(self, w, w_scale, d, rows, x_rows=None, gather=0, scatter=False, gelu=False, dtype=PW_BF16, device="cuda"):
+        super().__init__(device)
+        if w is None or w.dim() != 3:
+            raise PwError(PW_ERR_INVALID, "w must be a tensor of shape [experts][n][q8_row(d)]")
+        self.E, self.n = w.shape[0], w.shape[1]
+        self.d, self.rows = d, rows
+        if x_rows is None:
+            x_rows = -(-rows // gather) if gather else rows
+        self.x_rows = x_rows
+        self.dtype = torch.float32 if dtype == PW_F32 else torch.bfloat16
+        self.w = (w, w_scale)
+        self._w = (self._arg("w", w, (self.E, self.n, q8_row(d)), torch.int8),
+                   self._arg("w_scale", w_scale, (self.E, self.n), torch.float32))
+        self.desc = pw_q8_desc(rows, x_rows, d, self.n, self.E, dtype, gather, bool(scatter), bool(gelu))
+        self._workspace(lib.pw_q8_product_workspace, self.desc)
+
+    def forward(self, x, x_scale=None, offsets=None, src_index=None, out=None, stream=None):
+        """out [rows][n]. x [x_rows][d], or its codes [x_rows][q8_row(d)] with
+        x_scale [x_rows]. Rows of out that no dispatched row gives are left as they
+        are; out=None: a kept buffer."""
+        if out is None:
+            out = self._buf("out", (self.rows, self.n), self.dtype, stream)
+        io = pw_q8_io()
+        if x_scale is None:
+            io.x = self._arg("x", x, (self.x_rows, self.d), self.dtype)
+        else:
+            io.q = self._arg("x", x, (self.x_rows, q8_row(self.d)), torch.int8)
+            io.q_scale = self._arg("x_scale", x_scale, (self.x_rows,), torch.float32)
+        io.w, io.w_scale = self._w
+        io.offsets = self._arg("offsets", offsets, (self.E + 1,), torch.int64)
+        io.src_index = self._arg("src_index", src_index, (self.rows,), torch.int32)
+        io.out = self._arg("out", out, (self.rows, self.n), self.dtype)
+        self._run(lib.pw_q8_product, self.desc, io, stream, ws=True)
+        return out
+
+
+class TopkCombine(_Operator):
+    """The expert rows of each token, in tuple order, joined by their weights
+    (pw_topk_combine): out = add + sum_j weights_j y_j."""
+
+    def __init__(self, tokens, d, top_k, dtype=PW_BF16, device="cuda"):
+        super().__init__(device)
+        self.T, self.d, self.k = tokens, d, top_k
+        self.dtype = torch.float32 if dtype == PW_F32 else torch.bfloat16
+        self.desc = pw_combine_desc(tokens, d, top_k, dtype)
+
+    def forward(self, y, weights, add=None, out=None, stream=None):
+        """out [tokens][d] from y [tokens * k][d]; a tuple of weight 0 adds nothing.
+        out may be given (add itself, to update it in place)."""
+        if out is None:
+            out = self._buf("out", (self.T, self.d), self.dtype, stream)
+        io = pw_topk_combine_io()
+        io.y = self._arg("y", y, (self.T * self.k, self.d), self.dtype)
+        io.weights = self._arg("weights", weights, (self.T, self.k), torch.float32)
+        io.add = self._arg("add", add, (self.T, self.d), self.dtype)
+        io.out = self._arg("out", out, (self.T, self.d), self.dtype)
+        self._run(lib.pw_topk_combine, self.desc, io, stream)
+        return out
 
 
 class MoEBlock:

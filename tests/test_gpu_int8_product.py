@@ -1,0 +1,380 @@
+"""GPU parity of the 8-bit rows, the experts' products and the combine against
+the oracle in 64 bits.
+
+Codes and scales are equal bit for bit. Bars, with u = 2^-24: a product's sum is
+exact, its conversion and the two scales round three times, 3 u of z; GELU
+carries a relative error of z on as at most z^2 + 2 times itself (its slope over
+its value), and its own is 5.1e-5 in bf16 (8 u of the error function in fp32, whose
+rounded argument counts z^2 times); the result is rounded once, by half a step
+of its type. The combine's sum of k + 1 terms is off by (k + 2) u of their
+absolute values.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import experts as ox
+
+pytestmark = pytest.mark.gpu
+U = ox.U
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def pwt(gpu, dtype):
+    return gpu.PW_BF16 if dtype == "bf16" else gpu.PW_F32
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def rows_of(rng, rows, d, dtype, scale=1.0):
+    """Random rows as the type holds them (fp32 array)."""
+    x = torch.from_numpy((rng.standard_normal((rows, d)) * scale).astype(np.float32))
+    return x.to(DT[dtype]).float().numpy()
+
+
+# ---- rows as codes ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(1, 1), (3, 7), (5, 64), (70, 65), (300, 128), (33, 200), (64, 1000), (257, 1024),
+                                    (9, 2048), (20, 2049), (5, 4096), (7, 8191), (3, 8192), (2, 12345), (2, 65536)])
+def test_codes_are_equal(gpu, rows, d, dtype):
+    print(f"quant {rows} x {d} {dtype}", flush=True)
+    rng = np.random.default_rng([rows, d])
+    x = rows_of(rng, rows, d, dtype, 3.0)
+    x[:, d // 2] = x[:, 0] / 2  # the middle of two codes, where the scale rounds evenly
+    x = torch.from_numpy(x).to(DT[dtype]).float().numpy()
+    q, s = gpu.RowQuant(rows, d, pwt(gpu, dtype)).forward(dev(x, DT[dtype]))
+    wq, ws = ox.quant(x)
+    assert np.array_equal(s.cpu().numpy(), ws)
+    assert np.array_equal(q.cpu().numpy(), wq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [40, 1024, 9000])
+def test_codes_of_ties_zeros_and_extremes(gpu, d, dtype):
+    rng = np.random.default_rng(d)
+    x = rows_of(rng, 16, d, dtype)
+    x[0] = 0
+    x[1] = 0
+    x[1, d - 1] = 1e-45 if dtype == "f32" else 2.0 ** -133
+    x[2] *= 1e-37
+    x[3, 5] = np.inf
+    x[4, d - 1] = -np.inf
+    x[5, 0] = np.nan
+    x[6] = -np.float32(3.0e38)
+    x[7] *= 1e37
+    m = rng.integers(-254, 255, d)
+    x[8], x[8, 0] = m * 0.5, 127               # every half
+    x[9], x[9, 0] = m * 0.25, 254 * 0.25       # amax / 2 and the like
+    x[10], x[10, 0] = m * 2.0 ** -130, 254 * 2.0 ** -130
+    x[11] = 2.0 ** -126 * np.sign(x[11])
+    x = torch.from_numpy(x).to(DT[dtype]).float().numpy()
+    q, s = gpu.RowQuant(16, d, pwt(gpu, dtype)).forward(dev(x, DT[dtype]))
+    wq, ws = ox.quant(x)
+    assert np.array_equal(s.cpu().numpy(), ws, equal_nan=True)
+    assert np.array_equal(q.cpu().numpy(), wq)
+
+
+def test_codes_up_to_a_limit_and_unaligned_rows(gpu):
+    rng = np.random.default_rng(1)
+    x = rows_of(rng, 50, 131, "bf16")
+    flat = torch.zeros(50 * 131 + 1, dtype=torch.bfloat16, device="cuda")
+    X = flat[1:].view(50, 131)
+    X.copy_(dev(x))
+    wq, ws = ox.quant(x)
+    for limit in (-3, 0, 1, 20, 50, 1 << 40):
+        q = torch.full((50, 192), 99, dtype=torch.int8, device="cuda")
+        s = torch.full((50,), -1.0, device="cuda")
+        gpu.RowQuant(50, 131).forward(X, limit=torch.tensor([limit], device="cuda"), q=q, scale=s)
+        n = min(max(limit, 0), 50)
+        assert np.array_equal(q.cpu().numpy()[:n], wq[:n]) and np.array_equal(s.cpu().numpy()[:n], ws[:n])
+        assert bool((q[n:] == 99).all()) and bool((s[n:] == -1).all())
+
+
+# ---- products -----------------------------------------------------------------
+
+def weights(gpu, rng, E, n, d):
+    w = (rng.standard_normal((E * n, d)) * d ** -0.5).astype(np.float32)
+    wq, ws = ox.quant(w)
+    return wq.reshape(E, n, -1), ws.reshape(E, n)
+
+
+def route(rng, T, k, E, kind):
+    """offsets, src_index of T k tuples: some experts popular, some without any; the last tuples are padding's."""
+    p = np.linspace(3, 0, E) ** 2 if kind == "skewed" else np.ones(E)
+    dest = rng.choice(E, T * k, p=p / p.sum())
+    if kind == "padded":
+        dest = np.where(rng.random(T * k) < 0.3, E, dest)
+    if kind == "one":
+        dest[:] = E - 1
+    off = np.concatenate([[0], np.cumsum(np.bincount(dest, minlength=E + 1)[:E])])
+    return off, np.argsort(dest, kind="stable").astype(np.int32)
+
+
+def check_product(got, want, pre, dtype, act):
+    e = 3 * U
+    if act:
+        e = e * (pre ** 2 + 2) + (5.2e-5 if dtype == "bf16" else (8 + 3 * pre ** 2) * U)
+    ok = np.abs(got.cpu().double().numpy() - want) <= np.abs(want) * (HALF[dtype] + 1.01 * e) + 1e-37
+    assert ok.all(), np.argwhere(~ok)[:5]
+
+
+# tokens, k, experts, d, n, kind, gather, scatter, act, dtype
+CASES = [(1, 1, 1, 1, 1, "even", True, False, False, "f32"), (1, 8, 16, 64, 64, "even", True, False, True, "bf16"),
+         (3, 2, 4, 100, 70, "one", True, True, False, "bf16"), (16, 2, 8, 128, 256, "even", False, True, False, "bf16"),
+         (17, 1, 1, 64, 16, "even", False, False, True, "f32"), (48, 8, 64, 256, 128, "skewed", True, False, True, "bf16"),
+         (65, 4, 5, 333, 131, "padded", False, True, True, "bf16"), (100, 3, 5, 200, 77, "skewed", True, True, True, "f32"),
+         (128, 1, 1, 512, 384, "even", False, False, False, "bf16"), (200, 2, 256, 64, 96, "even", True, False, False, "bf16"),
+         (300, 2, 7, 1000, 515, "padded", True, False, True, "f32"), (500, 2, 3, 192, 264, "skewed", False, True, True, "bf16"),
+         (700, 4, 2, 128, 128, "one", True, False, False, "bf16"), (1025, 1, 1, 640, 512, "even", False, False, True, "bf16"),
+         (1500, 2, 4, 320, 513, "skewed", True, False, False, "bf16"), (1111, 2, 6, 130, 520, "padded", False, True, False, "f32"),
+         (2048, 2, 3, 256, 768, "padded", True, True, True, "bf16"), (4000, 1, 1, 448, 250, "even", False, False, False, "bf16"),
+         (3000, 2, 8, 512, 512, "skewed", True, False, True, "bf16")]
+
+
+@pytest.mark.parametrize("T,k,E,d,n,kind,gather,scatter,act,dtype", CASES)
+def test_product(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
+    print(f"product T={T} k={k} E={E} d={d} n={n} {kind} gather={gather} scatter={scatter} {dtype}", flush=True)
+    rng = np.random.default_rng([T, k, E, d, n])
+    rows = T * k
+    w, ws = weights(gpu, rng, E, n, d)
+    off, src = route(rng, T, k, E, kind) if E > 1 else (None, None)
+    indexed = E > 1 and (gather or scatter)
+    gather = k if indexed and gather else 0
+    scatter = indexed and scatter
+    x = rows_of(rng, T if gather else rows, d, dtype)
+    W, WS = dev(w), dev(ws)
+    f = gpu.Int8Product(W, WS, d, rows, gather=gather, scatter=scatter, gelu=act, dtype=pwt(gpu, dtype))
+    out = torch.full((rows, n), 7.0, dtype=DT[dtype], device="cuda")
+    q, s = ox.quant(x)
+    want, pre = ox.product(q, s, w, ws, off, src if indexed else None, rows, gather, scatter, act, np.full((rows, n), 7.0))
+    kw = dict(offsets=None if off is None else dev(off), src_index=dev(src) if indexed else None)
+    check_product(f.forward(dev(x, DT[dtype]), out=out, **kw), want, pre, dtype, act)
+    first = out.clone()
+    # codes given: the same bits; a kept buffer
+    out.fill_(7.0)
+    got = f.forward(dev(q), x_scale=dev(s), out=out, **kw)
+    assert got is out and torch.equal(got, first)
+    assert f.forward(dev(x, DT[dtype]), **kw).shape == (rows, n)
+
+
+@pytest.mark.parametrize("n", [64, 130, 256])
+@pytest.mark.parametrize("E", [3, 70])
+def test_offsets_and_indexes_that_are_none(gpu, n, E):
+    """Descending, negative and far offsets, ids outside the tuples: nothing out of range is read or written, no row twice."""
+    rng = np.random.default_rng(n)
+    T, k, d = 60, 2, 96
+    rows = T * k
+    w, ws = weights(gpu, rng, E, n, d)
+    x = rows_of(rng, T, d, "bf16")
+    q, s = ox.quant(x)
+    src = rng.permutation(rows).astype(np.int32)
+    src[::7] = -1
+    src[3::11] = 1 << 30
+    src[4::13] = rows
+    for off in ([0, 50, 40, 200], [-5, 10, 100, 1 << 40], [60, 60, 60, 60]):
+        off = np.array(off + [off[-1]] * (E - 3), np.int64)
+        for gather, scatter in ((k, False), (k, True), (0, True)):
+            xs = x if gather else np.concatenate([x, x])
+            f = gpu.Int8Product(dev(w), dev(ws), d, rows, gather=gather, scatter=scatter)
+            out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            f.forward(dev(xs, torch.bfloat16), offsets=dev(off), src_index=dev(src), out=out)
+            qq, ss = ox.quant(xs)
+            want, pre = ox.product(qq, ss, w, ws, off, src, rows, gather, scatter, False, np.full((rows, n), 7.0))
+            check_product(out, want, pre, "bf16", False)
+
+
+def test_scales_that_are_not_numbers_and_zero_rows(gpu):
+    rng = np.random.default_rng(2)
+    x = rows_of(rng, 40, 80, "bf16")
+    x[3], x[5, 7], x[6, 0] = 0, np.inf, np.nan
+    w, ws = weights(gpu, rng, 1, 50, 80)
+    ws[0, 9] = np.inf
+    out = gpu.Int8Product(dev(w), dev(ws), 80, 40).forward(dev(x, torch.bfloat16)).float().cpu().numpy()
+    assert np.isnan(out[[5, 6]]).all() and np.isnan(out[3, 9]) and not out[3, :9].any()
+    clean = np.delete(np.delete(out, [3, 5, 6], 0), 9, 1)
+    assert np.isfinite(clean).all()
+
+
+def test_the_largest_sums(gpu):
+    """Every code at its limit over the widest row: the sum needs all 31 bits' worth of room that there is."""
+    d, n = 65536, 20
+    w = np.full((1, n, d), 127, np.int8)
+    w[0, 1] = -127
+    x = np.ones((3, d), np.float32)
+    x[1] = -1
+    out = gpu.Int8Product(dev(w), dev(np.ones((1, n), np.float32)), d, 3, dtype=gpu.PW_F32).forward(dev(x)).cpu().numpy()
+    top = np.float32(127 * 127 * 65536) * (np.float32(1) / np.float32(127))
+    assert np.all(np.abs(np.abs(out) - top) <= 2 * U * top) and out[0, 0] > 0 > out[0, 1] and out[1, 0] < 0 < out[1, 1]
+
+
+def test_offsets_past_32_bits(gpu):
+    """Outputs, codes and weights beyond 2^32 bytes; the last rows alone are computed."""
+    rng = np.random.default_rng(4)
+    T, d, n, E = 2400000, 1024, 1024, 3
+    w, ws = weights(gpu, rng, E, n, d)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    last = rows_of(rng, 50, d, "bf16")
+    x[-50:] = dev(last, torch.bfloat16)
+    off = torch.tensor([T - 50, T - 50, T - 20, T], device="cuda")
+    f = gpu.Int8Product(dev(w), dev(ws), d, T)
+    out = torch.zeros(T, n, dtype=torch.bfloat16, device="cuda")
+    f.forward(x, offsets=off, out=out)
+    q, s = ox.quant(last)
+    want, pre = ox.product(q, s, w, ws, np.array([0, 0, 30, 50]), None, 50)
+    check_product(out[-50:], want, pre, "bf16", False)
+    assert float(out[:-50].abs().max()) == 0
+
+
+def test_product_refusals(gpu):
+    w, ws = torch.zeros(4, 32, 128, dtype=torch.int8, device="cuda"), torch.zeros(4, 32, device="cuda")
+    with pytest.raises(gpu.PwError):
+        gpu.Int8Product(w, ws, 200, 8)           # rows of codes of another length
+    with pytest.raises(gpu.PwError):
+        gpu.Int8Product(w.float(), ws, 100, 8)
+    with pytest.raises(gpu.PwError):
+        gpu.Int8Product(w, ws[:3], 100, 8)
+    with pytest.raises(gpu.PwError):
+        gpu.Int8Product(w[0], ws, 100, 8)
+    f = gpu.Int8Product(w, ws, 100, 8)
+    x = torch.zeros(8, 100, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(), dict(offsets=torch.zeros(4, dtype=torch.int64, device="cuda")),
+               dict(offsets=torch.zeros(5, dtype=torch.int32, device="cuda")),
+               dict(offsets=torch.zeros(5, dtype=torch.int64, device="cuda"),
+                    src_index=torch.zeros(8, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(gpu.PwError):
+            f.forward(x, **kw)
+    with pytest.raises(gpu.PwError):
+        f.forward(x.float(), offsets=torch.zeros(5, dtype=torch.int64, device="cuda"))
+    none = gpu.Int8Product(w, ws, 100, 0).forward(x[:0], offsets=torch.zeros(5, dtype=torch.int64, device="cuda"))
+    assert none.shape == (0, 32)
+
+
+# ---- combine ------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,k", [(1, 1, 1), (1, 1024, 8), (3, 7, 2), (48, 1024, 8), (100, 130, 3), (257, 64, 6), (33, 4096, 5),
+                                   (500, 1001, 4), (2, 65536, 2), (1000, 24, 7), (4099, 256, 2)])
+def test_combine(gpu, T, d, k, dtype):
+    print(f"combine {T} x {k} x {d} {dtype}", flush=True)
+    rng = np.random.default_rng([T, d, k])
+    y, add = rows_of(rng, T * k, d, dtype), rows_of(rng, T, d, dtype)
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    w[rng.random((T, k)) < 0.2] = 0
+    if T > 1:
+        w[1] = 0
+    y[(w == 0).reshape(-1)] = np.nan            # what nothing wrote
+    f = gpu.TopkCombine(T, d, k, pwt(gpu, dtype))
+    for a in (None, add):
+        got = f.forward(dev(y, DT[dtype]), dev(w), add=None if a is None else dev(a, DT[dtype]))
+        want, size = ox.combine(y, w, a)
+        assert np.all(np.abs(got.cpu().double().numpy() - want) <= (k + 2) * U * size + HALF[dtype] * np.abs(want) * 1.01 + 1e-37)
+    out = dev(add, DT[dtype])
+    assert f.forward(dev(y, DT[dtype]), dev(w), add=out, out=out) is out and torch.equal(out, got)
+
+
+def test_combine_of_unaligned_rows_and_far_ones(gpu):
+    rng = np.random.default_rng(6)
+    T, d, k = 30, 72, 3
+    y = rows_of(rng, T * k, d, "bf16")
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    flat = torch.zeros(T * k * d + 1, dtype=torch.bfloat16, device="cuda")
+    flat[1:] = dev(y, torch.bfloat16).view(-1)
+    got = gpu.TopkCombine(T, d, k).forward(flat[1:].view(T * k, d), dev(w))
+    want, size = ox.combine(y, w, None)
+    assert np.all(np.abs(got.cpu().double().numpy() - want) <= (k + 2) * U * size + HALF["bf16"] * np.abs(want) * 1.01)
+    T, d, k = 1100000, 1024, 4                  # more than 2^32 elements
+    far = torch.zeros(T * k, d, dtype=torch.bfloat16, device="cuda")
+    far[-k:] = 1.0
+    out = gpu.TopkCombine(T, d, k).forward(far, torch.full((T, k), 0.25, device="cuda"))
+    assert float(out[-1].float().min()) == 1.0 and float(out[:-1].float().abs().max()) == 0
+
+
+# ---- together -------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,E,k,d,hidden,masked", [(1, 8, 8, 256, 512, False), (40, 16, 4, 192, 320, True), (600, 64, 6, 256, 384, True)])
+def test_route_order_products_and_combine(gpu, T, E, k, d, hidden, masked):
+    """A token's way: routing, the exchange that orders its tuples (padding behind the last expert), both products, the combine."""
+    rng = np.random.default_rng([T, E, k])
+    l = (rng.standard_normal((T, E)) * 1.5).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    valid = rng.random(T) < 0.8 if masked else None
+    x, shared = rows_of(rng, T, d, "bf16"), rows_of(rng, T, d, "bf16")
+    w1, s1 = weights(gpu, rng, E, hidden, d)
+    w2, s2 = weights(gpu, rng, E, d, hidden)
+    rows = T * k
+    router = gpu.Router(T, E, k, "sigmoid", groups=4, top_groups=4, scale=2.0)
+    order = gpu.Exchange(E + 1, rows, 1, num_src_shards=1)
+    first = gpu.Int8Product(dev(w1), dev(s1), d, rows, gather=k, gelu=True)
+    second = gpu.Int8Product(dev(w2), dev(s2), hidden, rows, scatter=True)
+    join = gpu.TopkCombine(T, d, k)
+    y = torch.full((rows, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    experts, wt = router.forward(dev(l), bias=dev(bias), valid=None if valid is None else dev(valid))
+    gpu.future_wait(order.step(wt.view(rows, 1), experts.view(rows)))
+    off = order.offsets[:E + 1]
+    h = first.forward(dev(x, torch.bfloat16), offsets=off, src_index=order.src_index)
+    second.forward(h, offsets=off, src_index=order.src_index, out=y)
+    out = join.forward(y, wt, add=dev(shared, torch.bfloat16)).float().cpu().numpy()
+    ids, w = ox.route(l, bias, valid, k, True, 4, 4, 2, True, 2.0)
+    assert np.array_equal(experts.cpu().numpy(), ids)
+    # the oracle's way, tuple by tuple, from the GPU's hidden rows as they are rounded
+    q, s = ox.quant(x)
+    src = np.argsort(ids.reshape(-1), kind="stable").astype(np.int32)
+    offs = np.concatenate([[0], np.cumsum(np.bincount(ids.reshape(-1), minlength=E + 1)[:E])])
+    assert np.array_equal(off.cpu().numpy(), offs) and np.array_equal(order.src_index.cpu().numpy(), src)
+    want_h, pre = ox.product(q, s, w1, s1, offs, src, rows, k, False, True)
+    n = offs[-1]
+    check_product(h[:n], want_h[:n], pre[:n], "bf16", True)
+    hq, hs = ox.quant(h.float().cpu().numpy()[:n])
+    yy, pre = ox.product(np.concatenate([hq, np.zeros((rows - n, hq.shape[1]), np.int8)]), np.concatenate([hs, np.zeros(rows - n, np.float32)]),
+                         w2, s2, offs, src, rows, 0, True)
+    live = ids.reshape(-1) < E
+    check_product(y[dev(live)], yy[live], pre[live], "bf16", False)
+    assert bool(torch.isnan(y[dev(~live)]).all())
+    want, size = ox.combine(np.where(live[:, None], y.float().cpu().numpy(), 0), wt.cpu().numpy(), shared)
+    assert np.all(np.abs(out - want) <= (k + 2) * U * size + HALF["bf16"] * np.abs(want) * 1.01)
+
+
+def test_captured_with_the_exchange_and_replayed(gpu):
+    """The whole way in a graph, with the exchange's form that can be captured; and two objects in one graph."""
+    rng = np.random.default_rng(9)
+    T, E, k, d, hidden = 24, 16, 4, 128, 192
+    rows = T * k
+    w1, s1 = (dev(t) for t in weights(gpu, rng, E, hidden, d))
+    w2, s2 = (dev(t) for t in weights(gpu, rng, E, d, hidden))
+    router = gpu.Router(T, E, k, "sigmoid")
+    ex = gpu.desc(gpu.PW_GRAPH_EXCHANGE, E + 1, rows, 1, num_src_shards=1)
+    sorted_w = torch.empty(rows, 1, device="cuda")
+    off = torch.empty(E + 2, dtype=torch.int64, device="cuda")
+    src = torch.empty(rows, dtype=torch.int32, device="cuda")
+    first = gpu.Int8Product(w1, s1, d, rows, gather=k, gelu=True)
+    second = gpu.Int8Product(w2, s2, hidden, rows, scatter=True)
+    join = gpu.TopkCombine(T, d, k)
+    l, x = torch.zeros(T, E, device="cuda"), torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+
+    def way():
+        experts, wt = router.forward(l)
+        gpu.exchange_scratch(ex, gpu.exchange_io(wt, experts, sorted_w, 1, E + 1, 1, src_index=src, offsets=off))
+        h = first.forward(x, offsets=off[:E + 1], src_index=src)
+        return join.forward(second.forward(h, offsets=off[:E + 1], src_index=src), wt)
+
+    with pytest.raises(gpu.PwError):  # buffers are not made under capture
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            gpu.TopkCombine(T, d, k).forward(torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, k, device="cuda"))
+    way()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = way()
+    for seed in range(4):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        l.copy_(torch.randn(T, E, generator=gen, device="cuda"))
+        x.copy_(torch.randn(T, d, generator=gen, device="cuda"))
+        g.replay()
+        got = out.clone()
+        assert torch.equal(got, way())
+        torch.cuda.synchronize()
