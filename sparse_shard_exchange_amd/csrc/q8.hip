@@ -77,7 +77,6 @@ struct Q8Args {
   const int64_t* offsets;    // or null: one expert, every row
   const int32_t* src_index;  // or null
   void* out;
-  uint64_t tiles;
   uint32_t tuples;           // ids of src_index are below this
   uint32_t rows, n, E, stride;
   uint32_t gather;           // tuples of a row of q; 0: dispatched order
@@ -85,49 +84,69 @@ struct Q8Args {
   uint32_t col_tiles;
 };
 
-// Where a workgroup works: `rows` rows from row0 on, of expert e.
-struct Segment {
-  uint32_t e, row0, rows;
+// Where a workgroup works: `rows` rows from row0 on, of expert e, and the
+// columns from col0 on; rows == 0: there is no such tile.
+struct Piece {
+  uint32_t e, row0, rows, col0;
 };
 
-// The rb-th block of at most M rows, blocks counted over the experts' segments
-// in turn; rows == 0: there is none. Every lane of the wave takes part.
-template <uint32_t M>
-__device__ __forceinline__ Segment segment_of(const Q8Args& a, uint32_t rb) {
+// The b-th tile of M rows and N columns. Row blocks are counted over the experts'
+// segments in turn, a block's column tiles one after the other, and each XCD takes
+// a contiguous range of them. Every lane of the wave takes part.
+template <uint32_t M, uint32_t N>
+__device__ __forceinline__ Piece piece_of(const Q8Args& a, uint64_t b) {
   if (!a.offsets) {
-    const uint32_t row0 = rb * M;
-    return {0, row0, row0 < a.rows ? min(M, a.rows - row0) : 0u};
+    const uint64_t total = (uint64_t)((a.rows + M - 1) / M) * a.col_tiles;
+    if (b >= total) return {0, 0, 0, 0};
+    if (total <= 0x7fffffffu) b = xcd_contiguous((uint32_t)b, (uint32_t)total);
+    const uint32_t row0 = (uint32_t)(b / a.col_tiles) * M;
+    return {0, row0, min(M, a.rows - row0), (uint32_t)(b % a.col_tiles) * N};
   }
+  constexpr uint32_t kChunks = kMaxQ8Experts / 64;
   const uint32_t lane = threadIdx.x & 63;
-  uint32_t done = 0, from = 0;  // blocks and rows of the experts before
-  for (uint32_t e0 = 0; e0 < a.E; e0 += 64) {
-    // where the lane's expert ends, and where the one before it did
-    const uint32_t e = e0 + lane;
-    if (e0 == 0) from = (uint32_t)min(max(a.offsets[0], (int64_t)0), (int64_t)a.rows);
-    uint32_t end = (uint32_t)min(max(a.offsets[min(e + 1, a.E)], (int64_t)0), (int64_t)a.rows);
-    end = max(end, from);
+  const int64_t most = a.rows;
+  // the rows where the lane's experts (64 c + lane) begin and end, and the blocks up to theirs
+  uint32_t begin[kChunks], end[kChunks], upto[kChunks];
+  uint32_t from = (uint32_t)min(max(a.offsets[0], (int64_t)0), most), done = 0;
 #pragma unroll
-    for (int m = 1; m < 64; m *= 2) end = max(end, (uint32_t)__shfl_up((int)end, m));  // a lane too low keeps its own
-    uint32_t begin = (uint32_t)__shfl_up((int)end, 1);
-    if (lane == 0) begin = from;
-    const uint32_t blocks = (end - begin + M - 1) / M;
-    uint32_t upto = blocks;  // blocks of this expert and those before it
+  for (uint32_t c = 0; c < kChunks; ++c)
+    if (64 * c < a.E) end[c] = (uint32_t)min(max(a.offsets[min(64 * c + lane + 1, a.E)], (int64_t)0), most);
+#pragma unroll
+  for (uint32_t c = 0; c < kChunks; ++c) {
+    if (64 * c >= a.E) break;
+    uint32_t v = max(end[c], from);
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v = max(v, (uint32_t)__shfl_up((int)v, m));  // a lane too low keeps its own
+    uint32_t o = (uint32_t)__shfl_up((int)v, 1);
+    begin[c] = lane == 0 ? from : o;
+    end[c] = v;
+    uint32_t n = (v - begin[c] + M - 1) / M;
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
-      const uint32_t o = (uint32_t)__shfl_up((int)upto, m);
-      if ((int)lane >= m) upto += o;
+      o = (uint32_t)__shfl_up((int)n, m);
+      if ((int)lane >= m) n += o;
     }
-    const uint64_t has = __ballot(rb < done + upto);
-    if (has) {
-      const int at = __builtin_ctzll(has);
-      const uint32_t first = done + (uint32_t)__builtin_amdgcn_readlane((int)(upto - blocks), at);
-      const uint32_t row0 = (uint32_t)__builtin_amdgcn_readlane((int)begin, at) + (rb - first) * M;
-      return {e0 + (uint32_t)at, row0, min(M, (uint32_t)__builtin_amdgcn_readlane((int)end, at) - row0)};
-    }
-    done += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    from = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    upto[c] = done + n;
+    done = (uint32_t)__builtin_amdgcn_readlane((int)upto[c], 63);
+    from = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
   }
-  return {0, 0, 0};
+  const uint64_t total = (uint64_t)done * a.col_tiles;
+  if (b >= total) return {0, 0, 0, 0};
+  if (total <= 0x7fffffffu) b = xcd_contiguous((uint32_t)b, (uint32_t)total);
+  const uint32_t rb = (uint32_t)(b / a.col_tiles), col0 = (uint32_t)(b % a.col_tiles) * N;
+#pragma unroll
+  for (uint32_t c = 0; c < kChunks; ++c) {
+    if (64 * c >= a.E) break;
+    const uint64_t has = __ballot(rb < upto[c]);
+    if (!has) continue;
+    const int at = __builtin_ctzll(has);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)begin[c], at);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)end[c], at);
+    const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)upto[c], at);
+    const uint32_t row0 = lo + (rb + (hi - lo + M - 1) / M - last) * M;
+    return {64 * c + (uint32_t)at, row0, min(M, hi - row0), col0};
+  }
+  return {0, 0, 0, 0};
 }
 
 // Row of q that dispatched row i multiplies, and row of out that it gives (-1: none).
@@ -152,66 +171,254 @@ __device__ __forceinline__ float finish(int sum, float s, float ws) {
   else return 0.5f * z * erfcf(z * -0.70710678f);
 }
 
-constexpr int kTile = 64, kStep = 64;
-
-// One 64 x 64 tile a workgroup: operands through LDS in steps of 64 bytes, wave
-// w the rows from 16 w on.
+// Scale, activation, one rounding and the store of 16 neighbouring results from
+// column c on, of a row of n (0: not stored). Rows may begin anywhere.
 template <typename T, bool kGelu>
-__global__ __launch_bounds__(kThreads) void k_q8_product(Q8Args a) {
-  __shared__ __attribute__((aligned(16))) int8_t s_a[kTile][kStep + 16], s_b[kTile][kStep + 16];
-  __shared__ float s_scale[kTile];
-  __shared__ int64_t s_out[kTile];
-  for (uint64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    const Segment g = segment_of<kTile>(a, (uint32_t)(tile / a.col_tiles));
-    if (g.rows == 0) return;  // nor is there a later one
-    const uint32_t col0 = (uint32_t)(tile % a.col_tiles) * kTile;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const uint32_t ra = tid / 4, chunk = tid % 4 * 16;
-    const RowOf row = row_of(a, g.row0 + min(ra, g.rows - 1));
-    __syncthreads();
-    if (tid % 4 == 0) {
-      s_scale[ra] = a.q_scale[row.in];
-      s_out[ra] = ra < g.rows ? row.out : -1;
+__device__ __forceinline__ void store_run(const i32x16& acc, float s, const float* ws, T* row, uint32_t c, uint32_t n) {
+  constexpr int V = 16 / sizeof(T);
+  typedef T Vec __attribute__((ext_vector_type(V)));
+  typedef T At __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+#pragma unroll
+  for (int p = 0; p < 16 / V; ++p) {
+    Vec v;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = (T)finish<T, kGelu>(acc[p * V + e], s, ws[p * V + e]);
+    const uint32_t at = c + p * V;
+    if (at + V <= n) {
+      *reinterpret_cast<At*>(row + at) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (at + e < n) row[at + e] = v[e];
     }
-    const int8_t* pa = a.q + (uint64_t)row.in * a.stride + chunk;
-    const int8_t* pb = a.w + ((uint64_t)g.e * a.n + min(col0 + ra, a.n - 1)) * a.stride + chunk;
-    i32x4 acc[4] = {};
-    for (uint32_t k = 0; k < a.stride; k += kStep) {
-      __syncthreads();
-      *reinterpret_cast<i32x4*>(&s_a[ra][chunk]) = *reinterpret_cast<const i32x4*>(pa + k);
-      *reinterpret_cast<i32x4*>(&s_b[ra][chunk]) = *reinterpret_cast<const i32x4*>(pb + k);
-      __syncthreads();
-      const i32x4 x = *reinterpret_cast<const i32x4*>(&s_a[16 * w + lane % 16][lane / 16 * 16]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const i32x4 y = *reinterpret_cast<const i32x4*>(&s_b[16 * j + lane % 16][lane / 16 * 16]);
-        acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(y, x, acc[j], 0, 0, 0);
-      }
-    }
-    // the lane holds 4 columns from 16 j + 4 (lane / 16) on of row 16 w + lane % 16
-    const int r = 16 * w + lane % 16;
-    const int64_t o = s_out[r];
-    if (o < 0) continue;
-    const float s = s_scale[r];
-    T* out = static_cast<T*>(a.out) + (uint64_t)o * a.n;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t c = col0 + 16 * j + 4 * (lane / 16) + v;
-        if (c < a.n) out[c] = (T)finish<T, kGelu>(acc[j][v], s, a.w_scale[(uint64_t)g.e * a.n + c]);
-      }
   }
 }
 
-template <typename T, bool kGelu>
-hipError_t launch_product(Q8Args a, hipStream_t s) {
-  a.col_tiles = (a.n + kTile - 1) / kTile;
-  const uint64_t full = (a.rows + kTile - 1) / kTile;
-  const uint64_t blocks = a.offsets ? std::min<uint64_t>(a.rows, a.rows / kTile + a.E) : full;
-  a.tiles = blocks * a.col_tiles;
-  hipLaunchKernelGGL((k_q8_product<T, kGelu>), dim3((uint32_t)std::min<uint64_t>(a.tiles, kMaxGrid)), dim3(kThreads), 0, s, a);
+// Shape of a tile: BM x BN results by WM x WN waves, each MI x NI blocks of
+// v_mfma_i32_32x32x32_i8; operands pass through a ring of S stages of 64 bytes
+// of each row in LDS.
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int NT = 64 * WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
+  static constexpr int LA = BM * 4 / NT, LB = BN * 4 / NT;  // 16-byte loads of a lane and stage
+  static constexpr int kB = BM * 64, kStage = (BM + BN) * 64;
+  static constexpr int kLds = S * kStage;
+};
+
+// Column of a tile that row r of B's LDS block holds: inside 32 columns the
+// order that leaves a lane with 16 neighbouring columns of its row in the
+// accumulators (register 4 q + e of lane l is MFMA row 8 q + 4 (l / 32) + e).
+__device__ __forceinline__ int column_of(int r) {
+  return (r & ~31) | (r >> 2 & 1) << 4 | (r >> 3 & 3) << 2 | (r & 3);
+}
+
+// What one lane loads: the chunk of its rows that its slot of each stage holds.
+template <typename P>
+struct Feed {
+  const int8_t* a[P::LA];
+  const int8_t* b[P::LB];
+};
+
+// 16 bytes a lane into 1 KiB of LDS, past the registers.
+__device__ __forceinline__ void load_direct(const int8_t* from, unsigned char* to) {
+  __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 16, 0, 0);
+}
+
+template <typename P>
+__device__ __forceinline__ void load_stage(const Feed<P>& f, uint32_t k, unsigned char* stage) {
+  const int w = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < P::LA; ++i)
+    load_direct(f.a[i] + k, stage + (w * P::LA + i) * 1024);
+#pragma unroll
+  for (int i = 0; i < P::LB; ++i)
+    load_direct(f.b[i] + k, stage + P::kB + (w * P::LB + i) * 1024);
+}
+
+template <typename P>
+struct Frags {
+  i32x4 a[P::MI], b[P::NI];
+};
+
+// Byte offsets in a stage of the lane's operands in each half of its 64 columns
+// (those of the wave's other blocks follow in steps of 32 rows).
+struct Places {
+  int a[2], b[2];
+};
+
+template <typename P>
+__device__ __forceinline__ Places places() {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int ra = w / P::WN * (P::BM / P::WM) + (lane & 31), rb = w % P::WN * (P::BN / P::WN) + (lane & 31);
+  Places p;
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const int c = 2 * kk + (lane >> 5);
+    p.a[kk] = ra * 64 + ((c ^ mm::swz(ra)) << 4);
+    p.b[kk] = P::kB + rb * 64 + ((c ^ mm::swz(rb)) << 4);
+  }
+  return p;
+}
+
+template <typename P>
+__device__ __forceinline__ void read_frags(const unsigned char* stage, const Places& p, int kk, Frags<P>& f) {
+#pragma unroll
+  for (int i = 0; i < P::MI; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(stage + p.a[kk] + i * 2048);
+#pragma unroll
+  for (int j = 0; j < P::NI; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(stage + p.b[kk] + j * 2048);
+}
+
+template <typename P>
+__device__ __forceinline__ void multiply(const Frags<P>& f, i32x16 (&acc)[P::MI][P::NI]) {
+#pragma unroll
+  for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+}
+
+// Instruction order of half a stage: the reads of the next half's operands
+// follow its first products, the loads of a stage the others (the compiler keeps
+// loads that write LDS behind earlier reads of it).
+template <typename P, bool kLoad>
+__device__ __forceinline__ void schedule() {
+  constexpr int M = P::MI * P::NI, R = P::MI + P::NI, L = kLoad ? P::LA + P::LB : 0;
+  constexpr int kReads = kLoad && M > 2 ? (M - 1) / 2 : M;  // products among which the reads are spread
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (m < kReads) {
+#pragma unroll
+      for (int r = (R * m + kReads - 1) / kReads; r < (R * (m + 1) + kReads - 1) / kReads; ++r)
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    } else {
+#pragma unroll
+      for (int l = L * (m - kReads) / (M - kReads); l < L * (m + 1 - kReads) / (M - kReads); ++l)
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);  // no product moves across: each has waited for its operands' reads
+}
+
+// The slots of the ring that a stage, the next one and the one that is loaded take.
+struct Ring {
+  uint32_t cur, next, load;
+};
+
+template <typename P>
+__device__ __forceinline__ uint32_t after(uint32_t slot) {
+  return slot + P::kStage == P::S * P::kStage ? 0u : slot + P::kStage;
+}
+
+// Stage ks: its second half's operands are read while the first half
+// multiplies, the next stage's first half's while the second does. The barrier
+// between them publishes stage ks + 1 and frees the slot of stage ks - 1, which
+// stage ks + S - 1 (kLoad) takes. kWait: loads that may still be in flight
+// then, -1: there is no stage ks + 1.
+template <typename P, bool kLoad, int kWait>
+__device__ __forceinline__ void stage_step(const Feed<P>& f, const Places& p, unsigned char* lds, uint32_t ks, Ring& slot,
+                                           Frags<P>& f0, Frags<P>& f1, i32x16 (&acc)[P::MI][P::NI]) {
+  read_frags<P>(lds + slot.cur, p, 1, f1);
+  multiply<P>(f0, acc);
+  schedule<P, false>();
+  if constexpr (kWait >= 0) {
+    mm::wait_vmem<kWait>();
+    mm::ring_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_frags<P>(lds + slot.next, p, 0, f0);
+    if constexpr (kLoad) load_stage<P>(f, (ks + P::S - 1) * 64, lds + slot.load);
+  }
+  multiply<P>(f1, acc);
+  schedule<P, kLoad>();
+  slot = {slot.next, after<P>(slot.next), slot.cur};
+}
+
+template <typename P, typename T, bool kGelu>
+__global__ __launch_bounds__(P::NT, 2) void k_q8_tile(Q8Args a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float s_scale[P::BM], s_ws[P::BN];
+  __shared__ int64_t s_out[P::BM];
+  constexpr int LD = P::LA + P::LB;
+  for (uint64_t b = blockIdx.x;; b += gridDim.x) {
+    const Piece g = piece_of<P::BM, P::BN>(a, b);
+    if (g.rows == 0) return;  // nor is there a later one
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    Feed<P> f;
+#pragma unroll
+    for (int i = 0; i < P::LA; ++i) {
+      const uint32_t r = (w * P::LA + i) * 16 + (lane >> 2);
+      const RowOf row = row_of(a, g.row0 + min(r, g.rows - 1));
+      f.a[i] = a.q + (uint64_t)row.in * a.stride + (((lane & 3) ^ mm::swz((int)r)) << 4);
+      if ((lane & 3) == 0) {
+        s_scale[r] = a.q_scale[row.in];
+        s_out[r] = r < g.rows ? row.out : -1;
+      }
+    }
+    const uint64_t wrow = (uint64_t)g.e * a.n;
+#pragma unroll
+    for (int i = 0; i < P::LB; ++i) {
+      const uint32_t r = (w * P::LB + i) * 16 + (lane >> 2);
+      const uint32_t c = min(g.col0 + column_of((int)r), a.n - 1);
+      f.b[i] = a.w + (wrow + c) * a.stride + (((lane & 3) ^ mm::swz((int)r)) << 4);
+    }
+    for (int c = tid; c < P::BN; c += P::NT) s_ws[c] = a.w_scale[wrow + min(g.col0 + c, a.n - 1)];
+    mm::wait_vmem<0>();  // from here on the counter counts stages
+    const uint32_t nk = a.stride / 64;
+#pragma unroll
+    for (uint32_t s = 0; s < P::S - 1; ++s)
+      if (s < nk) load_stage<P>(f, s * 64, lds + s * P::kStage);
+    i32x16 acc[P::MI][P::NI];
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) acc[i][j] = i32x16{};
+    if (nk >= P::S - 1) mm::wait_vmem<(P::S - 2) * LD>();
+    else mm::wait_vmem<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // s_scale, s_out, s_ws are written
+    mm::ring_barrier();
+    const Places p = places<P>();
+    Ring slot = {0, after<P>(0), (P::S - 1) * P::kStage};
+    Frags<P> f0, f1;
+    read_frags<P>(lds, p, 0, f0);
+    uint32_t ks = 0;
+    for (; ks + P::S - 1 < nk; ++ks) stage_step<P, true, (P::S - 3) * LD>(f, p, lds, ks, slot, f0, f1, acc);
+    for (; ks + 1 < nk; ++ks) stage_step<P, false, 0>(f, p, lds, ks, slot, f0, f1, acc);
+    stage_step<P, false, -1>(f, p, lds, ks, slot, f0, f1, acc);
+    // the lane holds 16 neighbouring columns of a row in each block
+    T* out = static_cast<T*>(a.out);
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i) {
+      const int r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
+      const int64_t o = s_out[r];
+      const float s = s_scale[r];
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) {
+        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
+        store_run<T, kGelu>(acc[i][j], s, s_ws + c, out + (uint64_t)o * a.n, g.col0 + c, o < 0 ? 0u : a.n);
+      }
+    }
+    __syncthreads();  // before the next tile's scales and stages
+  }
+}
+
+template <typename P, typename T, bool kGelu>
+hipError_t launch_tile(Q8Args a, hipStream_t s) {
+  a.col_tiles = (a.n + P::BN - 1) / P::BN;
+  const uint64_t blocks = a.offsets ? std::min<uint64_t>(a.rows, a.rows / P::BM + a.E) : ((uint64_t)a.rows + P::BM - 1) / P::BM;
+  const uint32_t grid = (uint32_t)std::min<uint64_t>(blocks * a.col_tiles, kMaxGrid);
+  const hipError_t e = hipFuncSetAttribute((const void*)k_q8_tile<P, T, kGelu>, hipFuncAttributeMaxDynamicSharedMemorySize, P::kLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_q8_tile<P, T, kGelu>), dim3(grid), dim3(P::NT), P::kLds, s, a);
   return hipGetLastError();
+}
+
+template <typename T, bool kGelu>
+hipError_t launch_product(const Q8Args& a, hipStream_t s) {
+  typedef Shape<128, 256, 2, 2, 3> Large;
+  typedef Shape<64, 64, 2, 2, 4> Small;
+  const uint64_t large = (uint64_t)(a.rows / Large::BM) * ((a.n + Large::BN - 1) / Large::BN);
+  return large >= 256 ? launch_tile<Large, T, kGelu>(a, s) : launch_tile<Small, T, kGelu>(a, s);
 }
 
 // ---- host --------------------------------------------------------------------
