@@ -31,40 +31,163 @@ struct QuantArgs {
   uint32_t rows, d, stride;
 };
 
-// The largest |x| as bits: NaN and infinity are the largest of all.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) float f32x8;
+typedef __attribute__((ext_vector_type(8))) uint16_t u16x8;
+typedef __attribute__((ext_vector_type(8))) uint32_t u32x8;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
+// Eight elements of a row, as loaded; At: in memory, aligned to its elements.
 template <typename T>
+struct Eight;
+template <>
+struct Eight<__bf16> {
+  typedef __attribute__((ext_vector_type(8), aligned(2))) __bf16 At;
+  typedef bf16x8 Vec;
+  // the largest magnitude as the bits of an fp32 number: NaN and infinity are the largest of all
+  static __device__ __forceinline__ uint32_t top(const Vec& v) {
+    const u16x8 m = __builtin_bit_cast(u16x8, v) & (uint16_t)0x7fff;
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2;
+    const u16x2 a = __builtin_elementwise_max(m.s01, m.s23), b = __builtin_elementwise_max(m.s45, m.s67);
+    const u16x2 c = __builtin_elementwise_max(a, b);
+    return (uint32_t)max(c.x, c.y) << 16;
+  }
+};
+template <>
+struct Eight<float> {
+  typedef __attribute__((ext_vector_type(8), aligned(4))) float At;
+  typedef f32x8 Vec;
+  static __device__ __forceinline__ uint32_t top(const Vec& v) {
+    const u32x8 m = __builtin_bit_cast(u32x8, v) & 0x7fffffffu;
+    return max(max(max(m.s0, m.s1), max(m.s2, m.s3)), max(max(m.s4, m.s5), max(m.s6, m.s7)));
+  }
+};
+
+// Eight codes. x / s as fp32 rounds it, without a division: with r = 1 / s
+// correctly rounded, q + r (x - q s) is within an ulp of x / s after one step
+// from q = x r, and the correctly rounded quotient after another (Markstein's
+// theorem on division by a correctly rounded reciprocal; the remainders are exact
+// where nothing leaves the normal numbers, so for s from 2^-100 to 2^100:
+// quotients below 1/4, whose remainders might, are 0 either way). 1.5 x 2^23 added
+// rounds to the nearest whole number, ties to even, and leaves it in the low byte.
+template <typename T>
+__device__ __forceinline__ u32x2 codes(const typename Eight<T>::Vec& v, float s, float r) {
+  uint32_t c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = (float)v[e];
+    float q = x * r;
+    q = fmaf(fmaf(-q, s, x), r, q);
+    q = fmaf(fmaf(-q, s, x), r, q);
+    c[e] = __builtin_bit_cast(uint32_t, q + 12582912.0f);
+  }
+  u32x2 out;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x04000c0cu);
+    out[h] = lo | hi;
+  }
+  return out;
+}
+
+// The same for any scale above zero.
+template <typename T>
+__device__ __forceinline__ u32x2 codes_any(const typename Eight<T>::Vec& v, float s) {
+  u32x2 out = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = fminf(fmaxf(rintf((float)v[e] / s), -127.0f), 127.0f);
+    out[e / 4] |= ((uint32_t)(int)q & 0xff) << e % 4 * 8;
+  }
+  return out;
+}
+
+// Elements 8 c to 8 c + 7 of a row of d, zeros behind the row.
+template <typename T>
+__device__ __forceinline__ typename Eight<T>::Vec eight_of(const T* row, uint32_t c, uint32_t d) {
+  typename Eight<T>::Vec v = {};
+  if (8 * c + 8 <= d) v = *reinterpret_cast<const typename Eight<T>::At*>(row + 8 * c);
+  else if (8 * c < d) {
+#pragma unroll
+    for (uint32_t e = 0; e < 7; ++e)
+      if (8 * c + e < d) v[e] = row[8 * c + e];
+  }
+  return v;
+}
+
+// A team of L lanes takes a row into registers, C times eight elements a lane
+// (C == 0: a wider row, read twice), finds its largest magnitude and writes its
+// codes.
+template <typename T, int L, int C>
 __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantArgs a) {
-  __shared__ uint32_t s_top[kThreads / 64];
+  constexpr int kTeams = kThreads / L, kHold = C ? C : 1;
+  __shared__ uint32_t s_top[2][kThreads / 64];
   const int64_t limit = a.limit ? *a.limit : (int64_t)a.rows;
   const uint32_t rows = limit < 0 ? 0u : limit < (int64_t)a.rows ? (uint32_t)limit : a.rows;
-  for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+  const uint32_t lane = threadIdx.x % L, team = threadIdx.x / L;
+  uint32_t turn = 0;
+  for (uint64_t r0 = (uint64_t)blockIdx.x * kTeams; r0 < rows; r0 += (uint64_t)gridDim.x * kTeams, turn ^= 1) {
+    const uint64_t r = min(r0 + team, (uint64_t)rows - 1);  // a team without a row repeats the last one
     const T* x = static_cast<const T*>(a.x) + r * a.d;
+    typename Eight<T>::Vec v[kHold];
     uint32_t top = 0;
-    for (uint32_t c = threadIdx.x; c < a.d; c += kThreads) top = max(top, magnitude((float)x[c]));
-    for (int m = 1; m < 64; m *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) s_top[threadIdx.x / 64] = top;
-    __syncthreads();
-    top = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
-    const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : NAN;
-    const bool some = scale > 0.0f;
-    for (uint32_t c = threadIdx.x; c < a.stride; c += kThreads) {
-      float q = 0.0f;
-      if (some && c < a.d) q = fminf(fmaxf(rintf((float)x[c] / scale), -127.0f), 127.0f);
-      a.q[r * a.stride + c] = (int8_t)q;
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] = eight_of<T>(x, c * L + lane, a.d);
+#pragma unroll
+      for (int c = 0; c < C; ++c) top = max(top, Eight<T>::top(v[c]));
+    } else {
+      for (uint32_t c = lane; 8 * c < a.d; c += L) top = max(top, Eight<T>::top(eight_of<T>(x, c, a.d)));
     }
-    if (threadIdx.x == 0) a.scale[r] = scale;
+#pragma unroll
+    for (int m = 1; m < (L < 64 ? L : 64); m *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    if constexpr (L > 64) {
+      if (threadIdx.x % 64 == 0) s_top[turn][threadIdx.x / 64] = top;
+      __syncthreads();
+      top = max(max(s_top[turn][0], s_top[turn][1]), max(s_top[turn][2], s_top[turn][3]));
+    }
+    const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : NAN;
+    const bool usual = scale >= 0x1p-100f && scale <= 0x1p100f;
+    const float rcp = 1.0f / scale;
+    int8_t* q = a.q + r * a.stride;
+#pragma unroll
+    for (int i = 0; i < (C ? C : 1); ++i) {
+      for (uint32_t c = i * L + lane; 8 * c < a.stride; c += L) {
+        if constexpr (C == 0) v[0] = eight_of<T>(x, c, a.d);
+        u32x2 out = {0, 0};
+        if (usual) out = codes<T>(v[i], scale, rcp);
+        else if (scale > 0.0f) out = codes_any<T>(v[i], scale);
+        *reinterpret_cast<u32x2*>(q + 8 * c) = out;
+        if constexpr (C > 0) break;
+      }
+    }
+    if (lane == 0) a.scale[r] = scale;
   }
 }
 
-hipError_t launch_quant(const QuantArgs& a, bool f32, hipStream_t s) {
+template <typename T, int L, int C>
+void launch_quant_rows(const QuantArgs& a, hipStream_t s) {
+  constexpr uint32_t kTeams = kThreads / L;
+  const uint32_t blocks = (a.rows + kTeams - 1) / kTeams;
+  hipLaunchKernelGGL((k_quant_rows<T, L, C>), dim3(std::min(blocks, kMaxGrid)), dim3(kThreads), 0, s, a);
+}
+
+template <typename T>
+hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  const dim3 grid(std::min(a.rows, kMaxGrid));
-  if (f32) hipLaunchKernelGGL(k_quant_rows<float>, grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL(k_quant_rows<__bf16>, grid, dim3(kThreads), 0, s, a);
+  if (a.d <= 128) launch_quant_rows<T, 16, 1>(a, s);
+  else if (a.d <= 512) launch_quant_rows<T, 64, 1>(a, s);
+  else if (a.d <= 1024) launch_quant_rows<T, 64, 2>(a, s);
+  else if (a.d <= 2048) launch_quant_rows<T, 256, 1>(a, s);
+  else if (a.d <= 4096) launch_quant_rows<T, 256, 2>(a, s);
+  else if (a.d <= 8192) launch_quant_rows<T, 256, 4>(a, s);
+  else launch_quant_rows<T, 256, 0>(a, s);
   return hipGetLastError();
+}
+
+hipError_t launch_quant(const QuantArgs& a, bool f32, hipStream_t s) {
+  return f32 ? launch_quant<float>(a, s) : launch_quant<__bf16>(a, s);
 }
 
 // ---- products ----------------------------------------------------------------
@@ -285,6 +408,7 @@ template <typename P, bool kLoad>
 __device__ __forceinline__ void schedule() {
   constexpr int M = P::MI * P::NI, R = P::MI + P::NI, L = kLoad ? P::LA + P::LB : 0;
   constexpr int kReads = kLoad && M > 2 ? (M - 1) / 2 : M;  // products among which the reads are spread
+  constexpr int kLoads = M > kReads ? M - kReads : 1;       // and the loads
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -294,7 +418,7 @@ __device__ __forceinline__ void schedule() {
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     } else {
 #pragma unroll
-      for (int l = L * (m - kReads) / (M - kReads); l < L * (m + 1 - kReads) / (M - kReads); ++l)
+      for (int l = L * (m - kReads) / kLoads; l < L * (m + 1 - kReads) / kLoads; ++l)
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   }
