@@ -277,11 +277,15 @@ struct RowOf {
   uint32_t in;
   int64_t out;
 };
+// (without branches: it stands between products and what is done with them)
+__device__ __forceinline__ RowOf row_from(const Q8Args& a, uint32_t i, int32_t g) {
+  const bool indexed = a.src_index != nullptr, none = indexed && (g < 0 || (uint32_t)g >= a.tuples);
+  const uint32_t in = indexed && a.gather ? (uint32_t)g / max(a.gather, 1u) : i;
+  const uint32_t out = indexed && a.scatter ? (uint32_t)g : i;
+  return {none ? 0u : in, none ? (int64_t)-1 : (int64_t)out};
+}
 __device__ __forceinline__ RowOf row_of(const Q8Args& a, uint32_t i) {
-  if (!a.src_index) return {i, (int64_t)i};
-  const int32_t g = a.src_index[i];
-  if (g < 0 || (uint32_t)g >= a.tuples) return {0, -1};
-  return {a.gather ? (uint32_t)g / a.gather : i, a.scatter ? (int64_t)g : (int64_t)i};
+  return row_from(a, i, a.src_index ? a.src_index[i] : 0);
 }
 
 // bf16 results take the GELU of gemm.h (5.1e-5 of its value off, a seventieth of
@@ -318,16 +322,25 @@ __device__ __forceinline__ void store_run(const i32x16& acc, float s, const floa
 }
 
 // Shape of a tile: BM x BN results by WM x WN waves, each MI x NI blocks of
-// v_mfma_i32_32x32x32_i8; operands pass through a ring of S stages of 64 bytes
-// of each row in LDS.
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+// v_mfma_i32_32x32x32_i8; operands pass through a ring of S stages of D bytes of
+// each row in LDS.
+template <int BM_, int BN_, int WM_, int WN_, int D_, int S_, int kWaves_ = 2>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, D = D_, S = S_;
   static constexpr int NT = 64 * WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
-  static constexpr int LA = BM * 4 / NT, LB = BN * 4 / NT;  // 16-byte loads of a lane and stage
-  static constexpr int kB = BM * 64, kStage = (BM + BN) * 64;
+  static constexpr int kChunks = D / 16, kRows = 64 / kChunks;  // 16-byte chunks of a row; rows of a wave-wide load
+  static constexpr int LA = BM * kChunks / NT, LB = BN * kChunks / NT;  // 16-byte loads of a lane and stage
+  static constexpr int kB = BM * D, kStage = (BM + BN) * D;
   static constexpr int kLds = S * kStage;
+  static constexpr int kWaves = kWaves_;  // of a SIMD at once: they share its registers
 };
+
+// Slot of a row of D bytes in LDS that holds chunk c: an LDS read serves 16 lanes
+// (256 bytes) at a time, here 16 rows at one chunk, which so lie in all the banks.
+template <typename P>
+__device__ __forceinline__ int slot_of(int c, int row) {
+  return c ^ (P::D == 64 ? row >> 2 & 3 : row >> 1 & 7);
+}
 
 // Column of a tile that row r of B's LDS block holds: inside 32 columns the
 // order that leaves a lane with 16 neighbouring columns of its row in the
@@ -348,15 +361,24 @@ __device__ __forceinline__ void load_direct(const int8_t* from, unsigned char* t
   __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 16, 0, 0);
 }
 
+// Loads stage ks. Rows of 64 bytes more than whole stages of 128 end in half a
+// stage: lanes whose chunk would lie behind the row repeat the one 64 bytes before
+// (the chunk's number has bit 2 set: of the lane's slots in even rows of eight, or odd).
 template <typename P>
-__device__ __forceinline__ void load_stage(const Feed<P>& f, uint32_t k, unsigned char* stage) {
+__device__ __forceinline__ void load_stage(const Feed<P>& f, uint32_t ks, uint32_t stride, unsigned char* stage) {
+  static_assert(P::D == 64 || (P::D == 128 && P::LA % 2 == 0 && P::LB % 2 == 0), "see slot_of");
   const int w = threadIdx.x >> 6;
+  const uint32_t k = ks * P::D;
+  int32_t even = (int32_t)k, odd = (int32_t)k;
+  if constexpr (P::D == 128) {
+    const int32_t back = k + P::D > stride ? 64 : 0, high = -(int32_t)(threadIdx.x >> 2 & 1);
+    even -= back & high;
+    odd -= back & ~high;
+  }
 #pragma unroll
-  for (int i = 0; i < P::LA; ++i)
-    load_direct(f.a[i] + k, stage + (w * P::LA + i) * 1024);
+  for (int i = 0; i < P::LA; ++i) load_direct(f.a[i] + (i % 2 ? odd : even), stage + (w * P::LA + i) * 1024);
 #pragma unroll
-  for (int i = 0; i < P::LB; ++i)
-    load_direct(f.b[i] + k, stage + P::kB + (w * P::LB + i) * 1024);
+  for (int i = 0; i < P::LB; ++i) load_direct(f.b[i] + (i % 2 ? odd : even), stage + P::kB + (w * P::LB + i) * 1024);
 }
 
 template <typename P>
@@ -364,32 +386,34 @@ struct Frags {
   i32x4 a[P::MI], b[P::NI];
 };
 
-// Byte offsets in a stage of the lane's operands in each half of its 64 columns
+// Byte offsets in a stage of the lane's operands in each 32 of its columns
 // (those of the wave's other blocks follow in steps of 32 rows).
+template <typename P>
 struct Places {
-  int a[2], b[2];
+  int a[P::D / 32], b[P::D / 32];
 };
 
 template <typename P>
-__device__ __forceinline__ Places places() {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+__device__ __forceinline__ Places<P> places() {
+  const uint32_t tid = mm::opaque_tid();
+  const int lane = tid & 63, w = tid >> 6;
   const int ra = w / P::WN * (P::BM / P::WM) + (lane & 31), rb = w % P::WN * (P::BN / P::WN) + (lane & 31);
-  Places p;
+  Places<P> p;
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
+  for (int kk = 0; kk < P::D / 32; ++kk) {
     const int c = 2 * kk + (lane >> 5);
-    p.a[kk] = ra * 64 + ((c ^ mm::swz(ra)) << 4);
-    p.b[kk] = P::kB + rb * 64 + ((c ^ mm::swz(rb)) << 4);
+    p.a[kk] = ra * P::D + (slot_of<P>(c, ra) << 4);
+    p.b[kk] = P::kB + rb * P::D + (slot_of<P>(c, rb) << 4);
   }
   return p;
 }
 
 template <typename P>
-__device__ __forceinline__ void read_frags(const unsigned char* stage, const Places& p, int kk, Frags<P>& f) {
+__device__ __forceinline__ void read_frags(const unsigned char* stage, const Places<P>& p, int kk, Frags<P>& f) {
 #pragma unroll
-  for (int i = 0; i < P::MI; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(stage + p.a[kk] + i * 2048);
+  for (int i = 0; i < P::MI; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(stage + p.a[kk] + i * 32 * P::D);
 #pragma unroll
-  for (int j = 0; j < P::NI; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(stage + p.b[kk] + j * 2048);
+  for (int j = 0; j < P::NI; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(stage + p.b[kk] + j * 32 * P::D);
 }
 
 template <typename P>
@@ -401,12 +425,12 @@ __device__ __forceinline__ void multiply(const Frags<P>& f, i32x16 (&acc)[P::MI]
       acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
 }
 
-// Instruction order of half a stage: the reads of the next half's operands
-// follow its first products, the loads of a stage the others (the compiler keeps
-// loads that write LDS behind earlier reads of it).
-template <typename P, bool kLoad>
+// Instruction order of 32 columns: the reads of the next ones' operands (kRead)
+// follow the first products, the loads of a stage (kLoad) the others (the
+// compiler keeps loads that write LDS behind earlier reads of it).
+template <typename P, bool kRead, bool kLoad>
 __device__ __forceinline__ void schedule() {
-  constexpr int M = P::MI * P::NI, R = P::MI + P::NI, L = kLoad ? P::LA + P::LB : 0;
+  constexpr int M = P::MI * P::NI, R = kRead ? P::MI + P::NI : 0, L = kLoad ? P::LA + P::LB : 0;
   constexpr int kReads = kLoad && M > 2 ? (M - 1) / 2 : M;  // products among which the reads are spread
   constexpr int kLoads = M > kReads ? M - kReads : 1;       // and the loads
 #pragma unroll
@@ -422,12 +446,12 @@ __device__ __forceinline__ void schedule() {
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   }
-  __builtin_amdgcn_sched_barrier(0);  // no product moves across: each has waited for its operands' reads
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-// The slots of the ring that a stage, the next one and the one that is loaded take.
+// The slots of the ring that a stage and the next one take.
 struct Ring {
-  uint32_t cur, next, load;
+  uint32_t cur, next;
 };
 
 template <typename P>
@@ -435,35 +459,80 @@ __device__ __forceinline__ uint32_t after(uint32_t slot) {
   return slot + P::kStage == P::S * P::kStage ? 0u : slot + P::kStage;
 }
 
-// Stage ks: its second half's operands are read while the first half
-// multiplies, the next stage's first half's while the second does. The barrier
-// between them publishes stage ks + 1 and frees the slot of stage ks - 1, which
-// stage ks + S - 1 (kLoad) takes. kWait: loads that may still be in flight
-// then, -1: there is no stage ks + 1.
+// Stage ks, 32 columns after 32: each one's operands are read while the ones
+// before multiply. Before the last ones multiply, a barrier publishes stage
+// ks + 1 and, every wave having read all of stage ks, frees its slot, which stage
+// ks + S (kLoad) takes. kWait: loads that may still be in flight then, -1: there
+// is no stage ks + 1. On entry and on exit f[0] holds the next 32 columns.
 template <typename P, bool kLoad, int kWait>
-__device__ __forceinline__ void stage_step(const Feed<P>& f, const Places& p, unsigned char* lds, uint32_t ks, Ring& slot,
-                                           Frags<P>& f0, Frags<P>& f1, i32x16 (&acc)[P::MI][P::NI]) {
-  read_frags<P>(lds + slot.cur, p, 1, f1);
-  multiply<P>(f0, acc);
-  schedule<P, false>();
+__device__ __forceinline__ void stage_step(const Feed<P>& f, const Places<P>& p, unsigned char* lds, uint32_t ks,
+                                           uint32_t stride, Ring& slot, Frags<P> (&g)[2], i32x16 (&acc)[P::MI][P::NI]) {
+  constexpr int N = P::D / 32;
+#pragma unroll
+  for (int kk = 0; kk + 1 < N; ++kk) {
+    read_frags<P>(lds + slot.cur, p, kk + 1, g[(kk + 1) % 2]);
+    if (P::D == 128 && kWait < 0 && kk >= 1) {  // half a stage: the rest of it multiplies with zeros
+      const int keep = stride % 128 ? 0 : ~0;
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i) g[(kk + 1) % 2].a[i] &= keep;
+    }
+    multiply<P>(g[kk % 2], acc);
+    schedule<P, true, false>();
+  }
   if constexpr (kWait >= 0) {
-    mm::wait_vmem<kWait>();
+    __builtin_amdgcn_s_waitcnt((kWait & 15) | ((kWait >> 4) << 14) | (7 << 4));  // vmcnt(kWait), lgkmcnt(0)
     mm::ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_frags<P>(lds + slot.next, p, 0, f0);
-    if constexpr (kLoad) load_stage<P>(f, (ks + P::S - 1) * 64, lds + slot.load);
+    read_frags<P>(lds + slot.next, p, 0, g[0]);
+    if constexpr (kLoad) load_stage<P>(f, ks + P::S, stride, lds + slot.cur);
   }
-  multiply<P>(f1, acc);
-  schedule<P, kLoad>();
-  slot = {slot.next, after<P>(slot.next), slot.cur};
+  multiply<P>(g[1], acc);
+  schedule<P, (kWait >= 0), kLoad>();
+  slot = {slot.next, after<P>(slot.next)};
 }
 
+// The products of a tile whose first S stages are in flight or in LDS, the first
+// one published (read by every wave after a barrier). On return every wave has
+// read all of the ring (barrier) and no load is in flight.
+template <typename P>
+__device__ __forceinline__ void multiply_tile(const Feed<P>& f, unsigned char* lds, uint32_t stride,
+                                              i32x16 (&acc)[P::MI][P::NI]) {
+  constexpr int LD = P::LA + P::LB;
+#pragma unroll
+  for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) acc[i][j] = i32x16{};
+  const Places<P> p = places<P>();
+  Ring slot = {0, after<P>(0)};
+  Frags<P> g[2];
+  read_frags<P>(lds, p, 0, g[0]);
+  const uint32_t nk = (stride + P::D - 1) / P::D;
+  uint32_t ks = 0;
+  for (; ks + P::S < nk; ++ks) stage_step<P, true, (P::S - 2) * LD>(f, p, lds, ks, stride, slot, g, acc);
+  for (; ks + 1 < nk; ++ks) stage_step<P, false, 0>(f, p, lds, ks, stride, slot, g, acc);
+  stage_step<P, false, -1>(f, p, lds, ks, stride, slot, g, acc);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  mm::ring_barrier();
+}
+
+// The lane's part of B's rows: of expert e, columns from col0 on.
+template <typename P>
+__device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>& f) {
+  const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = tid >> 6;
+#pragma unroll
+  for (int i = 0; i < P::LB; ++i) {
+    const uint32_t r = (w * P::LB + i) * P::kRows + lane / P::kChunks;
+    const uint32_t c = min(g.col0 + column_of((int)r), a.n - 1);
+    f.b[i] = a.w + ((uint64_t)g.e * a.n + c) * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
+  }
+}
+
+// One tile a workgroup, two workgroups a CU: one multiplies while the other starts or ends.
 template <typename P, typename T, bool kGelu>
-__global__ __launch_bounds__(P::NT, 2) void k_q8_tile(Q8Args a) {
+__global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_tile(Q8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ float s_scale[P::BM], s_ws[P::BN];
   __shared__ int64_t s_out[P::BM];
-  constexpr int LD = P::LA + P::LB;
   for (uint64_t b = blockIdx.x;; b += gridDim.x) {
     const Piece g = piece_of<P::BM, P::BN>(a, b);
     if (g.rows == 0) return;  // nor is there a later one
@@ -471,44 +540,27 @@ __global__ __launch_bounds__(P::NT, 2) void k_q8_tile(Q8Args a) {
     Feed<P> f;
 #pragma unroll
     for (int i = 0; i < P::LA; ++i) {
-      const uint32_t r = (w * P::LA + i) * 16 + (lane >> 2);
+      const uint32_t r = (w * P::LA + i) * P::kRows + lane / P::kChunks;
       const RowOf row = row_of(a, g.row0 + min(r, g.rows - 1));
-      f.a[i] = a.q + (uint64_t)row.in * a.stride + (((lane & 3) ^ mm::swz((int)r)) << 4);
-      if ((lane & 3) == 0) {
+      f.a[i] = a.q + (uint64_t)row.in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
+      if (lane % P::kChunks == 0) {
         s_scale[r] = a.q_scale[row.in];
         s_out[r] = r < g.rows ? row.out : -1;
       }
     }
-    const uint64_t wrow = (uint64_t)g.e * a.n;
-#pragma unroll
-    for (int i = 0; i < P::LB; ++i) {
-      const uint32_t r = (w * P::LB + i) * 16 + (lane >> 2);
-      const uint32_t c = min(g.col0 + column_of((int)r), a.n - 1);
-      f.b[i] = a.w + (wrow + c) * a.stride + (((lane & 3) ^ mm::swz((int)r)) << 4);
-    }
-    for (int c = tid; c < P::BN; c += P::NT) s_ws[c] = a.w_scale[wrow + min(g.col0 + c, a.n - 1)];
+    feed_b<P>(a, g, f);
+    for (int c = tid; c < P::BN; c += P::NT) s_ws[c] = a.w_scale[(uint64_t)g.e * a.n + min(g.col0 + c, a.n - 1)];
     mm::wait_vmem<0>();  // from here on the counter counts stages
-    const uint32_t nk = a.stride / 64;
+    const uint32_t nk = (a.stride + P::D - 1) / P::D;
 #pragma unroll
-    for (uint32_t s = 0; s < P::S - 1; ++s)
-      if (s < nk) load_stage<P>(f, s * 64, lds + s * P::kStage);
-    i32x16 acc[P::MI][P::NI];
-#pragma unroll
-    for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-      for (int j = 0; j < P::NI; ++j) acc[i][j] = i32x16{};
-    if (nk >= P::S - 1) mm::wait_vmem<(P::S - 2) * LD>();
+    for (uint32_t s = 0; s < P::S; ++s)
+      if (s < nk) load_stage<P>(f, s, a.stride, lds + s * P::kStage);
+    if (nk >= P::S) mm::wait_vmem<(P::S - 1) * (P::LA + P::LB)>();
     else mm::wait_vmem<0>();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // s_scale, s_out, s_ws are written
     mm::ring_barrier();
-    const Places p = places<P>();
-    Ring slot = {0, after<P>(0), (P::S - 1) * P::kStage};
-    Frags<P> f0, f1;
-    read_frags<P>(lds, p, 0, f0);
-    uint32_t ks = 0;
-    for (; ks + P::S - 1 < nk; ++ks) stage_step<P, true, (P::S - 3) * LD>(f, p, lds, ks, slot, f0, f1, acc);
-    for (; ks + 1 < nk; ++ks) stage_step<P, false, 0>(f, p, lds, ks, slot, f0, f1, acc);
-    stage_step<P, false, -1>(f, p, lds, ks, slot, f0, f1, acc);
+    i32x16 acc[P::MI][P::NI];
+    multiply_tile<P>(f, lds, a.stride, acc);
     // the lane holds 16 neighbouring columns of a row in each block
     T* out = static_cast<T*>(a.out);
 #pragma unroll
@@ -526,6 +578,163 @@ __global__ __launch_bounds__(P::NT, 2) void k_q8_tile(Q8Args a) {
   }
 }
 
+// ---- many tiles: workgroups that stay ------------------------------------------
+
+// 4 bytes a lane into 256 bytes of LDS, past the registers.
+__device__ __forceinline__ void load_words(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 4, 0, 0);
+}
+
+// Where the experts' rows begin and how many blocks of M rows there are up to each
+// one's end (s_upto, all ones behind the last); returns the blocks in all. By
+// one wave; every lane takes part.
+template <uint32_t M>
+__device__ __forceinline__ uint32_t list_blocks(const Q8Args& a, uint32_t* s_begin, uint32_t* s_upto) {
+  const uint32_t lane = threadIdx.x & 63;
+  const int64_t most = a.rows;
+  if (!a.offsets) {
+    const uint32_t blocks = (a.rows + M - 1) / M;
+    s_upto[lane] = lane ? ~0u : blocks;
+    if (lane < 2) s_begin[lane] = lane * a.rows;
+    return blocks;
+  }
+  uint32_t from = (uint32_t)min(max(a.offsets[0], (int64_t)0), most), done = 0;
+  if (lane == 0) s_begin[0] = from;
+  for (uint32_t e0 = 0; e0 < a.E; e0 += 64) {
+    const uint32_t e = e0 + lane;
+    uint32_t end = max((uint32_t)min(max(a.offsets[min(e + 1, a.E)], (int64_t)0), most), from);
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) end = max(end, (uint32_t)__shfl_up((int)end, m));  // a lane too low keeps its own
+    uint32_t begin = (uint32_t)__shfl_up((int)end, 1);
+    if (lane == 0) begin = from;
+    uint32_t upto = (end - begin + M - 1) / M;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const uint32_t o = (uint32_t)__shfl_up((int)upto, m);
+      if ((int)lane >= m) upto += o;
+    }
+    upto += done;
+    s_upto[e] = e < a.E ? upto : ~0u;
+    if (e < a.E) s_begin[e + 1] = end;
+    done = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    from = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+  }
+  return done;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// The tile of workgroup turn b (below the total), from the list.
+template <typename P>
+__device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint32_t total, const uint32_t* s_begin,
+                                              const uint32_t* s_upto) {
+  b = xcd_contiguous(b, total);
+  const uint32_t rb = b / a.col_tiles, lane = threadIdx.x & 63;
+  uint32_t e = 0;
+  for (uint32_t e0 = 0; e0 < a.E; e0 += 64) e += __popcll(__ballot(s_upto[e0 + lane] <= rb));
+  e = uniform(e);
+  const uint32_t lo = uniform(s_begin[e]), hi = uniform(s_begin[e + 1]), before = e ? uniform(s_upto[e - 1]) : 0u;
+  const uint32_t row0 = lo + (rb - before) * P::BM;
+  return {e, row0, min((uint32_t)P::BM, hi - row0), b % a.col_tiles * P::BN};
+}
+
+// As k_q8_tile, with one workgroup a CU that walks over tiles: the next tile's
+// rows are looked up while this one multiplies, and its first stages are on their
+// way while this one's results are scaled and stored. No branch stands between
+// the products and the stores (it would make the accumulators move): behind the
+// last tile it is started once more, in vain.
+template <typename P, typename T, bool kGelu>
+__global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
+  static_assert(P::NT == P::BM + P::BN && P::BM % 64 == 0, "a thread for each scale");
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float s_scale[2][P::NT];  // of the rows, then of the columns
+  __shared__ int32_t s_src[2][P::NT];  // of the rows; the rest is not looked at
+  __shared__ uint32_t s_begin[kMaxQ8Experts + 1], s_upto[kMaxQ8Experts], s_total;
+  if (threadIdx.x < 64) {
+    const uint32_t blocks = list_blocks<P::BM>(a, s_begin, s_upto);
+    if (threadIdx.x == 0) s_total = blocks * a.col_tiles;
+  }
+  __syncthreads();
+  const uint32_t total = uniform(s_total);
+  uint32_t b = blockIdx.x;
+  if (b >= total) return;
+
+  // ids of a tile's rows (without an index: any words)
+  auto load_ids = [&](const Piece& g, int32_t* to) {
+    const uint32_t tid = mm::opaque_tid(), i = g.row0 + min(tid & (P::BM - 1), g.rows - 1);
+    load_words(a.src_index ? (const void*)(a.src_index + i) : (const void*)a.w_scale, to + (tid & ~63u));
+  };
+  auto row_at = [&](const Piece& g, const int32_t* ids, uint32_t r) { return row_from(a, g.row0 + min(r, g.rows - 1), ids[r]); };
+  // a tile's scales, then its first stages
+  auto start = [&](const Piece& g, const int32_t* ids, float* scale, Feed<P>& f) {
+    const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = tid >> 6;
+    const float* of_row = a.q_scale + row_at(g, ids, tid & (P::BM - 1)).in;
+    const float* of_column = a.w_scale + (uint64_t)g.e * a.n + min(g.col0 + (tid & (P::BM - 1)), a.n - 1);
+    load_words(tid < P::BM ? of_row : of_column, scale + (tid & ~63u));
+#pragma unroll
+    for (int i = 0; i < P::LA; ++i) {
+      const uint32_t r = (w * P::LA + i) * P::kRows + lane / P::kChunks;
+      f.a[i] = a.q + (uint64_t)row_at(g, ids, r).in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
+    }
+    feed_b<P>(a, g, f);
+    const uint32_t last = (a.stride + P::D - 1) / P::D - 1;
+#pragma unroll
+    for (uint32_t s = 0; s < P::S; ++s) load_stage<P>(f, min(s, last), a.stride, lds + s * P::kStage);
+  };
+
+  Piece g = listed_piece<P>(a, b, total, s_begin, s_upto);
+  load_ids(g, s_src[0]);
+  mm::wait_vmem<0>();
+  mm::ring_barrier();
+  Feed<P> f;
+  start(g, s_src[0], s_scale[0], f);
+  mm::wait_vmem<0>();
+  uint32_t turn = 0;
+  while (true) {
+    mm::ring_barrier();  // the tile's first stages and its scales are there
+    const bool more = b + gridDim.x < total;
+    const Piece next = more ? listed_piece<P>(a, b + gridDim.x, total, s_begin, s_upto) : g;
+    load_ids(next, s_src[turn ^ 1]);
+    i32x16 acc[P::MI][P::NI];
+    multiply_tile<P>(f, lds, a.stride, acc);
+    start(next, s_src[turn ^ 1], s_scale[turn ^ 1], f);
+    const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = tid >> 6;
+    T* out = static_cast<T*>(a.out);
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i) {
+      const uint32_t r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
+      const RowOf row = row_at(g, s_src[turn], r);
+      const float s = s_scale[turn][r];
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) {
+        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
+        store_run<T, kGelu>(acc[i][j], s, &s_scale[turn][P::BM + c], out + (uint64_t)row.out * a.n, g.col0 + c,
+                            r < g.rows && row.out >= 0 ? a.n : 0u);
+      }
+    }
+    mm::wait_vmem<0>();
+    if (!more) return;
+    b += gridDim.x;
+    g = next;
+    turn ^= 1;
+  }
+}
+
+template <typename P, typename T, bool kGelu>
+hipError_t launch_stay(Q8Args a, hipStream_t s) {
+  a.col_tiles = (a.n + P::BN - 1) / P::BN;
+  const uint64_t tiles = ((uint64_t)a.rows / P::BM + (a.offsets ? a.E : 1)) * a.col_tiles;  // at most
+  int device = 0, cus = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+  if (e == hipSuccess)
+    e = hipFuncSetAttribute((const void*)k_q8_stay<P, T, kGelu>, hipFuncAttributeMaxDynamicSharedMemorySize, P::kLds);
+  if (e != hipSuccess) return e;
+  const uint32_t grid = (uint32_t)std::min<uint64_t>(tiles, std::max(8, cus / 8 * 8));
+  hipLaunchKernelGGL((k_q8_stay<P, T, kGelu>), dim3(grid), dim3(P::NT), P::kLds, s, a);
+  return hipGetLastError();
+}
+
 template <typename P, typename T, bool kGelu>
 hipError_t launch_tile(Q8Args a, hipStream_t s) {
   a.col_tiles = (a.n + P::BN - 1) / P::BN;
@@ -539,10 +748,12 @@ hipError_t launch_tile(Q8Args a, hipStream_t s) {
 
 template <typename T, bool kGelu>
 hipError_t launch_product(const Q8Args& a, hipStream_t s) {
-  typedef Shape<128, 256, 2, 2, 3> Large;
-  typedef Shape<64, 64, 2, 2, 4> Small;
-  const uint64_t large = (uint64_t)(a.rows / Large::BM) * ((a.n + Large::BN - 1) / Large::BN);
-  return large >= 256 ? launch_tile<Large, T, kGelu>(a, s) : launch_tile<Small, T, kGelu>(a, s);
+  typedef Shape<256, 256, 2, 4, 128, 2> Large;
+  typedef Shape<128, 256, 2, 2, 64, 3> Middle;
+  typedef Shape<64, 64, 2, 2, 64, 4> Small;
+  const uint64_t cols = (a.n + 255) / 256, large = a.rows / 256 * cols;
+  if (large >= 1024 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
+  return large >= 128 ? launch_tile<Middle, T, kGelu>(a, s) : launch_tile<Small, T, kGelu>(a, s);
 }
 
 // ---- host --------------------------------------------------------------------

@@ -162,6 +162,41 @@ def test_product(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
     assert f.forward(dev(x, DT[dtype]), **kw).shape == (rows, n)
 
 
+@pytest.mark.parametrize("T,k,E,d,n,kind,gather,scatter,act,dtype",
+                         [(5500, 2, 5, 192, 6500, "skewed", True, False, True, "bf16"), (6000, 2, 3, 64, 6144, "padded", False, True, False, "f32"),
+                          (20000, 1, 1, 512, 4096, "even", False, False, True, "bf16"), (4000, 8, 130, 320, 2500, "skewed", True, True, False, "bf16"),
+                          (70000, 1, 2, 100, 1030, "one", False, True, False, "bf16"), (17000, 2, 64, 1024, 2048, "padded", True, False, True, "f32")])
+def test_many_tiles(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
+    """As test_product at sizes where workgroups walk over tiles; the plain form in 64 bits by torch, on the GPU."""
+    print(f"product T={T} k={k} E={E} d={d} n={n} {kind} gather={gather} scatter={scatter} {dtype}", flush=True)
+    rng = np.random.default_rng([T, k, E, d, n])
+    rows = T * k
+    w, ws = weights(gpu, rng, E, n, d)
+    off, src = route(rng, T, k, E, kind) if E > 1 else (np.array([0, rows]), np.arange(rows, dtype=np.int32))
+    x = rows_of(rng, T if gather else rows, d, dtype)
+    q, s = (dev(t) for t in ox.quant(x))
+    W, WS, S = dev(w), dev(ws), dev(src).long()
+    f = gpu.Int8Product(W, WS, d, rows, gather=k if gather else 0, scatter=scatter, gelu=act, dtype=pwt(gpu, dtype))
+    out = torch.full((rows, n), 7.0, dtype=DT[dtype], device="cuda")
+    f.forward(q, x_scale=s, out=out, offsets=None if E == 1 else dev(off), src_index=dev(src) if gather or scatter else None)
+    again = torch.full_like(out, 7.0)
+    f.forward(dev(x, DT[dtype]), out=again, offsets=None if E == 1 else dev(off), src_index=dev(src) if gather or scatter else None)
+    assert torch.equal(out, again)
+    seen = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for e in range(E):
+        i = torch.arange(int(off[e]), int(off[e + 1]), device="cuda")
+        for i in i.split(8192):
+            a = S[i] // k if gather else i
+            o = S[i] if scatter else i
+            z = (q[a].double() @ W[e].double().t().contiguous()) * s[a].double().unsqueeze(1) * WS[e].double()
+            want = z * 0.5 * torch.special.erfc(-z * 0.5 ** 0.5) if act else z
+            err = 3 * U * (z * z + 2 if act else 1) + ((5.2e-5 if dtype == "bf16" else (8 + 3 * z * z) * U) if act else 0)
+            bad = (out[o].double() - want).abs() > want.abs() * (HALF[dtype] + 1.01 * err) + 1e-37
+            assert not bool(bad.any()), (e, bad.nonzero()[:5])
+            seen[o] = True
+    assert bool((out[~seen] == 7.0).all()) and int(seen.sum()) == int(off[E])
+
+
 @pytest.mark.parametrize("n", [64, 130, 256])
 @pytest.mark.parametrize("E", [3, 70])
 def test_offsets_and_indexes_that_are_none(gpu, n, E):
