@@ -103,6 +103,22 @@ __device__ __forceinline__ u32x2 codes_any(const typename Eight<T>::Vec& v, floa
   return out;
 }
 
+// A row's scale from its largest magnitude (as bits).
+struct CodeScale {
+  float scale, rcp;
+  bool usual;  // codes() holds
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t top) {
+  const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : NAN;
+  return {scale, 1.0f / scale, scale >= 0x1p-100f && scale <= 0x1p100f};
+}
+
+template <typename T>
+__device__ __forceinline__ u32x2 codes_of(const typename Eight<T>::Vec& v, const CodeScale& s) {
+  if (s.usual) return codes<T>(v, s.scale, s.rcp);
+  return s.scale > 0.0f ? codes_any<T>(v, s.scale) : u32x2{0, 0};
+}
+
 // Elements 8 c to 8 c + 7 of a row of d, zeros behind the row.
 template <typename T>
 __device__ __forceinline__ typename Eight<T>::Vec eight_of(const T* row, uint32_t c, uint32_t d) {
@@ -147,22 +163,17 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantArgs a) {
       __syncthreads();
       top = max(max(s_top[turn][0], s_top[turn][1]), max(s_top[turn][2], s_top[turn][3]));
     }
-    const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : NAN;
-    const bool usual = scale >= 0x1p-100f && scale <= 0x1p100f;
-    const float rcp = 1.0f / scale;
+    const CodeScale s = code_scale(top);
     int8_t* q = a.q + r * a.stride;
 #pragma unroll
     for (int i = 0; i < (C ? C : 1); ++i) {
       for (uint32_t c = i * L + lane; 8 * c < a.stride; c += L) {
         if constexpr (C == 0) v[0] = eight_of<T>(x, c, a.d);
-        u32x2 out = {0, 0};
-        if (usual) out = codes<T>(v[i], scale, rcp);
-        else if (scale > 0.0f) out = codes_any<T>(v[i], scale);
-        *reinterpret_cast<u32x2*>(q + 8 * c) = out;
+        *reinterpret_cast<u32x2*>(q + 8 * c) = codes_of<T>(v[i], s);
         if constexpr (C > 0) break;
       }
     }
-    if (lane == 0) a.scale[r] = scale;
+    if (lane == 0) a.scale[r] = s.scale;
   }
 }
 
@@ -193,6 +204,8 @@ hipError_t launch_quant(const QuantArgs& a, bool f32, hipStream_t s) {
 // ---- products ----------------------------------------------------------------
 
 struct Q8Args {
+  const void* x;             // rows to be coded in the call (k_q8_few)
+  uint32_t d;
   const int8_t* q;
   const float* q_scale;
   const int8_t* w;
@@ -298,42 +311,61 @@ __device__ __forceinline__ float finish(int sum, float s, float ws) {
   else return 0.5f * z * erfcf(z * -0.70710678f);
 }
 
-// Scale, activation, one rounding and the store of 16 neighbouring results from
-// column c on, of a row of n (0: not stored). Rows may begin anywhere.
-template <typename T, bool kGelu>
-__device__ __forceinline__ void store_run(const i32x16& acc, float s, const float* ws, T* row, uint32_t c, uint32_t n) {
-  constexpr int V = 16 / sizeof(T);
+// 16 neighbouring results of a row, rounded, in vectors of 16 bytes.
+template <typename T>
+struct Run {
+  static constexpr int V = 16 / sizeof(T);
   typedef T Vec __attribute__((ext_vector_type(V)));
-  typedef T At __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+  typedef T At __attribute__((ext_vector_type(V), aligned(sizeof(T))));  // rows may begin anywhere
+  Vec v[16 / V];
+};
+
+// Scale, activation and the one rounding.
+template <typename T, bool kGelu>
+__device__ __forceinline__ Run<T> finish_run(const i32x16& acc, float s, const float* ws) {
+  Run<T> r;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) r.v[e / Run<T>::V][e % Run<T>::V] = (T)finish<T, kGelu>(acc[e], s, ws[e]);
+  return r;
+}
+
+// Stores a run to columns c on of a row of n (0: it is not stored).
+template <typename T>
+__device__ __forceinline__ void store_run(const Run<T>& r, T* row, uint32_t c, uint32_t n) {
+  constexpr int V = Run<T>::V;
 #pragma unroll
   for (int p = 0; p < 16 / V; ++p) {
-    Vec v;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = (T)finish<T, kGelu>(acc[p * V + e], s, ws[p * V + e]);
     const uint32_t at = c + p * V;
     if (at + V <= n) {
-      *reinterpret_cast<At*>(row + at) = v;
+      *reinterpret_cast<typename Run<T>::At*>(row + at) = r.v[p];
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (at + e < n) row[at + e] = v[e];
+        if (at + e < n) row[at + e] = r.v[p][e];
     }
   }
 }
 
 // Shape of a tile: BM x BN results by WM x WN waves, each MI x NI blocks of
 // v_mfma_i32_32x32x32_i8; operands pass through a ring of S stages of D bytes of
-// each row in LDS.
-template <int BM_, int BN_, int WM_, int WN_, int D_, int S_, int kWaves_ = 2>
+// each row in LDS. KS such groups of waves share a tile, each with a ring and a
+// part of the rows' length of its own.
+template <int BM_, int BN_, int WM_, int WN_, int D_, int S_, int KS_ = 1, int kWaves_ = 2>
 struct Shape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, D = D_, S = S_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, D = D_, S = S_, KS = KS_;
   static constexpr int NT = 64 * WM * WN, MI = BM / WM / 32, NI = BN / WN / 32;
   static constexpr int kChunks = D / 16, kRows = 64 / kChunks;  // 16-byte chunks of a row; rows of a wave-wide load
   static constexpr int LA = BM * kChunks / NT, LB = BN * kChunks / NT;  // 16-byte loads of a lane and stage
   static constexpr int kB = BM * D, kStage = (BM + BN) * D;
-  static constexpr int kLds = S * kStage;
+  static constexpr int kRing = S * kStage, kLds = KS * kRing;
   static constexpr int kWaves = kWaves_;  // of a SIMD at once: they share its registers
 };
+
+// A thread's wave inside its group.
+template <typename P>
+__device__ __forceinline__ int wave_of(uint32_t tid) {
+  return (int)(tid % P::NT >> 6);
+}
 
 // Slot of a row of D bytes in LDS that holds chunk c: an LDS read serves 16 lanes
 // (256 bytes) at a time, here 16 rows at one chunk, which so lie in all the banks.
@@ -361,13 +393,18 @@ __device__ __forceinline__ void load_direct(const int8_t* from, unsigned char* t
   __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 16, 0, 0);
 }
 
+// 4 bytes a lane into 256 bytes of LDS, past the registers.
+__device__ __forceinline__ void load_words(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 4, 0, 0);
+}
+
 // Loads stage ks. Rows of 64 bytes more than whole stages of 128 end in half a
 // stage: lanes whose chunk would lie behind the row repeat the one 64 bytes before
 // (the chunk's number has bit 2 set: of the lane's slots in even rows of eight, or odd).
 template <typename P>
 __device__ __forceinline__ void load_stage(const Feed<P>& f, uint32_t ks, uint32_t stride, unsigned char* stage) {
   static_assert(P::D == 64 || (P::D == 128 && P::LA % 2 == 0 && P::LB % 2 == 0), "see slot_of");
-  const int w = threadIdx.x >> 6;
+  const int w = wave_of<P>(threadIdx.x);
   const uint32_t k = ks * P::D;
   int32_t even = (int32_t)k, odd = (int32_t)k;
   if constexpr (P::D == 128) {
@@ -396,7 +433,7 @@ struct Places {
 template <typename P>
 __device__ __forceinline__ Places<P> places() {
   const uint32_t tid = mm::opaque_tid();
-  const int lane = tid & 63, w = tid >> 6;
+  const int lane = tid & 63, w = wave_of<P>(tid);
   const int ra = w / P::WN * (P::BM / P::WM) + (lane & 31), rb = w % P::WN * (P::BN / P::WN) + (lane & 31);
   Places<P> p;
 #pragma unroll
@@ -462,12 +499,16 @@ __device__ __forceinline__ uint32_t after(uint32_t slot) {
 // Stage ks, 32 columns after 32: each one's operands are read while the ones
 // before multiply. Before the last ones multiply, a barrier publishes stage
 // ks + 1 and, every wave having read all of stage ks, frees its slot, which stage
-// ks + S (kLoad) takes. kWait: loads that may still be in flight then, -1: there
-// is no stage ks + 1. On entry and on exit f[0] holds the next 32 columns.
+// ks + S (kLoad) takes. kWait: loads that may still be in flight then (63:
+// any), -1: there is no stage ks + 1. On entry and on exit f[0] holds the next 32 columns.
 template <typename P, bool kLoad, int kWait>
 __device__ __forceinline__ void stage_step(const Feed<P>& f, const Places<P>& p, unsigned char* lds, uint32_t ks,
-                                           uint32_t stride, Ring& slot, Frags<P> (&g)[2], i32x16 (&acc)[P::MI][P::NI]) {
+                                           uint32_t own, uint32_t stride, Ring& slot, Frags<P> (&g)[2],
+                                           i32x16 (&acc)[P::MI][P::NI]) {
   constexpr int N = P::D / 32;
+  static_assert(P::KS == 1 || N == 2, "both halves of a stage are here before it multiplies");
+  // (a group whose part is shorter than the others' repeats its last stage, times zero)
+  const int mine = P::KS == 1 || ks < own ? ~0 : 0;
 #pragma unroll
   for (int kk = 0; kk + 1 < N; ++kk) {
     read_frags<P>(lds + slot.cur, p, kk + 1, g[(kk + 1) % 2]);
@@ -475,6 +516,10 @@ __device__ __forceinline__ void stage_step(const Feed<P>& f, const Places<P>& p,
       const int keep = stride % 128 ? 0 : ~0;
 #pragma unroll
       for (int i = 0; i < P::MI; ++i) g[(kk + 1) % 2].a[i] &= keep;
+    }
+    if (P::KS > 1) {
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i) g[0].a[i] &= mine, g[1].a[i] &= mine;
     }
     multiply<P>(g[kk % 2], acc);
     schedule<P, true, false>();
@@ -484,7 +529,7 @@ __device__ __forceinline__ void stage_step(const Feed<P>& f, const Places<P>& p,
     mm::ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_frags<P>(lds + slot.next, p, 0, g[0]);
-    if constexpr (kLoad) load_stage<P>(f, ks + P::S, stride, lds + slot.cur);
+    if constexpr (kLoad) load_stage<P>(f, P::KS == 1 ? ks + P::S : min(ks + P::S, max(own, 1u) - 1), stride, lds + slot.cur);
   }
   multiply<P>(g[1], acc);
   schedule<P, (kWait >= 0), kLoad>();
@@ -492,10 +537,12 @@ __device__ __forceinline__ void stage_step(const Feed<P>& f, const Places<P>& p,
 }
 
 // The products of a tile whose first S stages are in flight or in LDS, the first
-// one published (read by every wave after a barrier). On return every wave has
-// read all of the ring (barrier) and no load is in flight.
-template <typename P>
-__device__ __forceinline__ void multiply_tile(const Feed<P>& f, unsigned char* lds, uint32_t stride,
+// one published (read by every wave after a barrier); kHere: all of them, and the
+// end of the first stage waits for no load nor for stores before this call. On
+// return every wave has read all of the ring (barrier) and no load is in flight.
+// nk: stages; own: those of them that are the group's.
+template <typename P, bool kHere>
+__device__ __forceinline__ void multiply_tile(const Feed<P>& f, unsigned char* lds, uint32_t nk, uint32_t own, uint32_t stride,
                                               i32x16 (&acc)[P::MI][P::NI]) {
   constexpr int LD = P::LA + P::LB;
 #pragma unroll
@@ -506,19 +553,19 @@ __device__ __forceinline__ void multiply_tile(const Feed<P>& f, unsigned char* l
   Ring slot = {0, after<P>(0)};
   Frags<P> g[2];
   read_frags<P>(lds, p, 0, g[0]);
-  const uint32_t nk = (stride + P::D - 1) / P::D;
   uint32_t ks = 0;
-  for (; ks + P::S < nk; ++ks) stage_step<P, true, (P::S - 2) * LD>(f, p, lds, ks, stride, slot, g, acc);
-  for (; ks + 1 < nk; ++ks) stage_step<P, false, 0>(f, p, lds, ks, stride, slot, g, acc);
-  stage_step<P, false, -1>(f, p, lds, ks, stride, slot, g, acc);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  if (kHere && P::S < nk) stage_step<P, true, 63>(f, p, lds, ks++, own, stride, slot, g, acc);
+  for (; ks + P::S < nk; ++ks) stage_step<P, true, (P::S - 2) * LD>(f, p, lds, ks, own, stride, slot, g, acc);
+  for (; ks + 1 < nk; ++ks) stage_step<P, false, 0>(f, p, lds, ks, own, stride, slot, g, acc);
+  stage_step<P, false, -1>(f, p, lds, ks, own, stride, slot, g, acc);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   mm::ring_barrier();
 }
 
 // The lane's part of B's rows: of expert e, columns from col0 on.
 template <typename P>
 __device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>& f) {
-  const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = tid >> 6;
+  const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = wave_of<P>(tid);
 #pragma unroll
   for (int i = 0; i < P::LB; ++i) {
     const uint32_t r = (w * P::LB + i) * P::kRows + lane / P::kChunks;
@@ -527,51 +574,88 @@ __device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>&
   }
 }
 
-// One tile a workgroup, two workgroups a CU: one multiplies while the other starts or ends.
+// One tile a workgroup; while one multiplies, others of its CU start or end.
 template <typename P, typename T, bool kGelu>
-__global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_tile(Q8Args a) {
+__global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ float s_scale[P::BM], s_ws[P::BN];
   __shared__ int64_t s_out[P::BM];
+  constexpr int NT = P::NT * P::KS;
   for (uint64_t b = blockIdx.x;; b += gridDim.x) {
     const Piece g = piece_of<P::BM, P::BN>(a, b);
     if (g.rows == 0) return;  // nor is there a later one
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_of<P>(tid), group = tid / P::NT;
+    const uint32_t stages = (a.stride + P::D - 1) / P::D, nk = (stages + P::KS - 1) / P::KS;  // of the rows; of a group at most
+    const uint32_t first = min(group * nk, stages - 1), own = min(stages - min(group * nk, stages), nk);
+    unsigned char* ring = lds + group * P::kRing;
     Feed<P> f;
+    RowOf row[P::LA];
 #pragma unroll
     for (int i = 0; i < P::LA; ++i) {
       const uint32_t r = (w * P::LA + i) * P::kRows + lane / P::kChunks;
-      const RowOf row = row_of(a, g.row0 + min(r, g.rows - 1));
-      f.a[i] = a.q + (uint64_t)row.in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
-      if (lane % P::kChunks == 0) {
-        s_scale[r] = a.q_scale[row.in];
-        s_out[r] = r < g.rows ? row.out : -1;
-      }
+      row[i] = row_of(a, g.row0 + min(r, g.rows - 1));
+      f.a[i] = a.q + (uint64_t)row[i].in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4) + first * P::D;
     }
     feed_b<P>(a, g, f);
-    for (int c = tid; c < P::BN; c += P::NT) s_ws[c] = a.w_scale[(uint64_t)g.e * a.n + min(g.col0 + c, a.n - 1)];
-    mm::wait_vmem<0>();  // from here on the counter counts stages
-    const uint32_t nk = (a.stride + P::D - 1) / P::D;
+#pragma unroll
+    for (int i = 0; i < P::LB; ++i) f.b[i] += first * P::D;
+    // the scales before the stages: who waits for a stage has waited for them
+    const int wave = tid / 64;
+    for (int c = wave; c < P::BM / 64; c += NT / 64)
+      load_words(a.q_scale + row_of(a, g.row0 + min((uint32_t)(64 * c + lane), g.rows - 1)).in, s_scale + 64 * c);
+    for (int c = wave; c < P::BN / 64; c += NT / 64)
+      load_words(a.w_scale + (uint64_t)g.e * a.n + min(g.col0 + 64 * c + lane, a.n - 1), s_ws + 64 * c);
 #pragma unroll
     for (uint32_t s = 0; s < P::S; ++s)
-      if (s < nk) load_stage<P>(f, s, a.stride, lds + s * P::kStage);
+      if (s < nk) load_stage<P>(f, P::KS == 1 ? s : min(s, max(own, 1u) - 1), a.stride, ring + s * P::kStage);
+#pragma unroll
+    for (int i = 0; i < P::LA; ++i) {
+      const uint32_t r = (w * P::LA + i) * P::kRows + lane / P::kChunks;
+      if (lane % P::kChunks == 0 && group == 0) s_out[r] = r < g.rows ? row[i].out : -1;
+    }
     if (nk >= P::S) mm::wait_vmem<(P::S - 1) * (P::LA + P::LB)>();
     else mm::wait_vmem<0>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // s_scale, s_out, s_ws are written
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // s_out is written
     mm::ring_barrier();
     i32x16 acc[P::MI][P::NI];
-    multiply_tile<P>(f, lds, a.stride, acc);
+    multiply_tile<P, false>(f, ring, nk, own, a.stride, acc);
+    if constexpr (P::KS > 1) {  // the groups' sums meet in the first one, in the place of its stages
+      i32x4* part = reinterpret_cast<i32x4*>(lds);
+      constexpr int Q = P::MI * P::NI * 4;
+      static_assert((P::KS - 1) * Q * P::NT * 16 <= P::kLds, "the sums fit");
+      if (group > 0) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const i32x16& v = acc[q / 4 / P::NI][q / 4 % P::NI];
+          part[((group - 1) * Q + q) * P::NT + tid % P::NT] = i32x4{v[q % 4 * 4], v[q % 4 * 4 + 1], v[q % 4 * 4 + 2], v[q % 4 * 4 + 3]};
+        }
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int p = 0; p < P::KS - 1; ++p)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const i32x4 v = part[(p * Q + q) * P::NT + tid % P::NT];
+            i32x16& to = acc[q / 4 / P::NI][q / 4 % P::NI];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[q % 4 * 4 + e] += v[e];
+          }
+      }
+    }
     // the lane holds 16 neighbouring columns of a row in each block
     T* out = static_cast<T*>(a.out);
+    if (P::KS == 1 || group == 0) {
 #pragma unroll
-    for (int i = 0; i < P::MI; ++i) {
-      const int r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
-      const int64_t o = s_out[r];
-      const float s = s_scale[r];
+      for (int i = 0; i < P::MI; ++i) {
+        const int r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
+        const int64_t o = s_out[r];
+        const float s = s_scale[r];
 #pragma unroll
-      for (int j = 0; j < P::NI; ++j) {
-        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
-        store_run<T, kGelu>(acc[i][j], s, s_ws + c, out + (uint64_t)o * a.n, g.col0 + c, o < 0 ? 0u : a.n);
+        for (int j = 0; j < P::NI; ++j) {
+          const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
+          store_run<T>(finish_run<T, kGelu>(acc[i][j], s, s_ws + c), out + (uint64_t)o * a.n, g.col0 + c, o < 0 ? 0u : a.n);
+        }
       }
     }
     __syncthreads();  // before the next tile's scales and stages
@@ -579,11 +663,6 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_tile(Q8Args a) {
 }
 
 // ---- many tiles: workgroups that stay ------------------------------------------
-
-// 4 bytes a lane into 256 bytes of LDS, past the registers.
-__device__ __forceinline__ void load_words(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds(from, (mm::lds_ptr)to, 4, 0, 0);
-}
 
 // Where the experts' rows begin and how many blocks of M rows there are up to each
 // one's end (s_upto, all ones behind the last); returns the blocks in all. By
@@ -624,18 +703,26 @@ __device__ __forceinline__ uint32_t list_blocks(const Q8Args& a, uint32_t* s_beg
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
-// The tile of workgroup turn b (below the total), from the list.
+// The tile of workgroup turn b (below the total), from the list. An XCD's tiles are
+// contiguous, in patches of kPatch row blocks by 4 column tiles, as many as its 32
+// CUs work on at a time: they share what they load.
+constexpr uint32_t kPatch = 8;
+
 template <typename P>
 __device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint32_t total, const uint32_t* s_begin,
                                               const uint32_t* s_upto) {
   b = xcd_contiguous(b, total);
-  const uint32_t rb = b / a.col_tiles, lane = threadIdx.x & 63;
+  const uint32_t band = b / (kPatch * a.col_tiles), high = min(kPatch, total / a.col_tiles - band * kPatch);
+  uint32_t at = b % (kPatch * a.col_tiles);
+  const uint32_t col = at / (high * 4) * 4, wide = min(4u, a.col_tiles - col);
+  at -= col * high;
+  const uint32_t rb = band * kPatch + at / wide, lane = threadIdx.x & 63;
   uint32_t e = 0;
   for (uint32_t e0 = 0; e0 < a.E; e0 += 64) e += __popcll(__ballot(s_upto[e0 + lane] <= rb));
   e = uniform(e);
   const uint32_t lo = uniform(s_begin[e]), hi = uniform(s_begin[e + 1]), before = e ? uniform(s_upto[e - 1]) : 0u;
   const uint32_t row0 = lo + (rb - before) * P::BM;
-  return {e, row0, min((uint32_t)P::BM, hi - row0), b % a.col_tiles * P::BN};
+  return {e, row0, min((uint32_t)P::BM, hi - row0), (col + at % wide) * P::BN};
 }
 
 // As k_q8_tile, with one workgroup a CU that walks over tiles: the next tile's
@@ -655,7 +742,7 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
     if (threadIdx.x == 0) s_total = blocks * a.col_tiles;
   }
   __syncthreads();
-  const uint32_t total = uniform(s_total);
+  const uint32_t total = uniform(s_total), stages = (a.stride + P::D - 1) / P::D;
   uint32_t b = blockIdx.x;
   if (b >= total) return;
 
@@ -677,9 +764,8 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
       f.a[i] = a.q + (uint64_t)row_at(g, ids, r).in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
     }
     feed_b<P>(a, g, f);
-    const uint32_t last = (a.stride + P::D - 1) / P::D - 1;
 #pragma unroll
-    for (uint32_t s = 0; s < P::S; ++s) load_stage<P>(f, min(s, last), a.stride, lds + s * P::kStage);
+    for (uint32_t s = 0; s < P::S; ++s) load_stage<P>(f, min(s, stages - 1), a.stride, lds + s * P::kStage);
   };
 
   Piece g = listed_piece<P>(a, b, total, s_begin, s_upto);
@@ -696,23 +782,40 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
     const Piece next = more ? listed_piece<P>(a, b + gridDim.x, total, s_begin, s_upto) : g;
     load_ids(next, s_src[turn ^ 1]);
     i32x16 acc[P::MI][P::NI];
-    multiply_tile<P>(f, lds, a.stride, acc);
+    multiply_tile<P, true>(f, lds, stages, stages, a.stride, acc);
     start(next, s_src[turn ^ 1], s_scale[turn ^ 1], f);
     const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = tid >> 6;
     T* out = static_cast<T*>(a.out);
+    // half of the results are finished before the loads are waited for, and the
+    // first store follows that wait: the counter then holds stores alone
+    constexpr int H = (P::MI + 1) / 2;
+    Run<T> first[H][P::NI];
 #pragma unroll
     for (int i = 0; i < P::MI; ++i) {
       const uint32_t r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
-      const RowOf row = row_at(g, s_src[turn], r);
       const float s = s_scale[turn][r];
 #pragma unroll
       for (int j = 0; j < P::NI; ++j) {
         const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
-        store_run<T, kGelu>(acc[i][j], s, &s_scale[turn][P::BM + c], out + (uint64_t)row.out * a.n, g.col0 + c,
-                            r < g.rows && row.out >= 0 ? a.n : 0u);
+        const Run<T> run = finish_run<T, kGelu>(acc[i][j], s, &s_scale[turn][P::BM + c]);
+        if (i < H) {
+          first[i][j] = run;
+          if (i < H - 1 || j < P::NI - 1) continue;
+        }
+        if (i == H - 1) mm::wait_vmem<0>();
+#pragma unroll
+        for (int i0 = i == H - 1 ? 0 : i; i0 <= i; ++i0) {
+          const uint32_t r0 = w / P::WN * (P::BM / P::WM) + 32 * i0 + (lane & 31);
+          const RowOf row = row_at(g, s_src[turn], r0);
+          const uint32_t n = r0 < g.rows && row.out >= 0 ? a.n : 0u;
+#pragma unroll
+          for (int j0 = i == H - 1 ? 0 : j; j0 <= j; ++j0) {
+            const uint32_t c0 = w % P::WN * (P::BN / P::WN) + 32 * j0 + 16 * (lane >> 5);
+            store_run<T>(i0 < H ? first[i0 < H ? i0 : 0][j0] : run, out + (uint64_t)row.out * a.n, g.col0 + c0, n);
+          }
+        }
       }
     }
-    mm::wait_vmem<0>();
     if (!more) return;
     b += gridDim.x;
     g = next;
@@ -742,18 +845,176 @@ hipError_t launch_tile(Q8Args a, hipStream_t s) {
   const uint32_t grid = (uint32_t)std::min<uint64_t>(blocks * a.col_tiles, kMaxGrid);
   const hipError_t e = hipFuncSetAttribute((const void*)k_q8_tile<P, T, kGelu>, hipFuncAttributeMaxDynamicSharedMemorySize, P::kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_q8_tile<P, T, kGelu>), dim3(grid), dim3(P::NT), P::kLds, s, a);
+  hipLaunchKernelGGL((k_q8_tile<P, T, kGelu>), dim3(grid), dim3(P::NT * P::KS), P::kLds, s, a);
   return hipGetLastError();
 }
+
+// ---- few rows: the weights pass through registers ------------------------------
+
+// Each wave multiplies 16 columns of its expert's matrix, over one of KS parts of
+// their length, with up to 16 R rows: all 16 KiB of the matrix that it can hold
+// are on their way at once, and no other wave reads them. The parts' sums (whole
+// numbers: exact in any order) meet in LDS. kCode: x's rows themselves are given,
+// at most 16 of a workgroup; it makes their codes on the way.
+constexpr int kHeld = 16;              // 64-byte steps of 16 columns in registers
+constexpr uint32_t kCodeWidth = 4096;  // of the rows that a workgroup codes: 8 chunks a lane
+
+template <typename T, bool kGelu, int KS, int R, bool kCode>
+__global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
+  constexpr int kGroups = 4 / KS;  // of 16 columns
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ int32_t s_sum[KS > 1 ? KS : 1][16][20];  // [part][row][column]
+  __shared__ float s_scale[16];
+  const Piece g = piece_of<16 * R, 16 * kGroups>(a, blockIdx.x);
+  if (g.rows == 0) return;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int part = w % KS, group = w / KS;
+  const uint32_t nk = a.stride / 64, each = (nk + KS - 1) / KS, k0 = min(part * each, nk), k1 = min(k0 + each, nk);
+  const uint32_t chunk = lane / 16 * 16, pitch = a.stride + 16;  // (of the codes in LDS: rows in different banks)
+
+  // the rows to be coded come first: nothing waits for the matrix before it has to
+  constexpr int kRowsEach = 4, kEach = kCodeWidth / 512;
+  typename Eight<T>::Vec v[kCode ? kEach : 1];
+  RowOf coded{};
+  if constexpr (kCode) {
+    coded = row_of(a, g.row0 + min((uint32_t)w, g.rows - 1));
+#pragma unroll
+    for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
+  }
+  const uint32_t col0 = g.col0 + group * 16;
+  const int8_t* pw = a.w + ((uint64_t)g.e * a.n + min(col0 + lane % 16, a.n - 1)) * a.stride + chunk;
+  i32x4 b[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k0 + i, nk - 1) * 64);
+  RowOf row[R];
+#pragma unroll
+  for (int m = 0; m < R; ++m) row[m] = row_of(a, g.row0 + min((uint32_t)(16 * m + lane % 16), g.rows - 1));
+
+  if constexpr (kCode) {
+#pragma unroll 1
+    for (int i = 0; i < kRowsEach; ++i) {  // rows w, w + 4, ...
+      const uint32_t r = w + 4 * i;
+      if (r >= g.rows) break;
+      if (i > 0) {
+        coded = row_of(a, g.row0 + r);
+#pragma unroll
+        for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < kEach; ++c) top = max(top, Eight<T>::top(v[c]));
+#pragma unroll
+      for (int m = 1; m < 64; m *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+      const CodeScale s = code_scale(top);
+#pragma unroll
+      for (int c = 0; c < kEach; ++c)
+        if (512 * c + 8 * lane < a.stride) *reinterpret_cast<u32x2*>(lds + r * pitch + 512 * c + 8 * lane) = codes_of<T>(v[c], s);
+      if (lane == 0) s_scale[r] = s.scale;
+    }
+    __syncthreads();
+  }
+
+  i32x4 acc[R] = {};
+  for (uint32_t k = k0; k < k1; k += kHeld) {
+    if (k > k0) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k + i, nk - 1) * 64);
+    }
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+      if (16 * (uint32_t)m >= g.rows) break;
+      const unsigned char* from = kCode ? lds + min((uint32_t)lane % 16, g.rows - 1) * pitch
+                                        : reinterpret_cast<const unsigned char*>(a.q + (uint64_t)row[m].in * a.stride);
+      i32x4 x[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) x[i] = *reinterpret_cast<const i32x4*>(from + min(k + i, nk - 1) * 64 + chunk);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int keep = k + i < k1 ? ~0 : 0;  // the steps behind the part's last are zeros
+        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], x[i] & keep, acc[m], 0, 0, 0);
+      }
+    }
+  }
+
+  // the lane holds 4 columns from 4 (lane / 16) on of row 16 m + lane % 16
+  const float* ws = a.w_scale + (uint64_t)g.e * a.n;
+#pragma unroll
+  for (int m = 0; m < R; ++m) {
+    if (16 * (uint32_t)m >= g.rows) break;
+    if constexpr (KS == 1) {
+      const uint32_t r = 16 * m + lane % 16;
+      if (r < g.rows && row[m].out >= 0) {
+        const float s = kCode ? s_scale[r] : a.q_scale[row[m].in];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t c = col0 + lane / 16 * 4 + e;
+          if (c < a.n) static_cast<T*>(a.out)[(uint64_t)row[m].out * a.n + c] = (T)finish<T, kGelu>(acc[m][e], s, ws[c]);
+        }
+      }
+    } else {
+      // one group of columns after the other: its parts' sums, then a thread for each result
+      for (int t = 0; t < kGroups; ++t) {
+        __syncthreads();
+        if (group == t) *reinterpret_cast<i32x4*>(&s_sum[part][lane % 16][lane / 16 * 4]) = acc[m];
+        __syncthreads();
+        const uint32_t r = 16 * m + threadIdx.x / 16, c = g.col0 + 16 * t + threadIdx.x % 16;
+        if (r < g.rows && c < a.n) {
+          const RowOf to = row_of(a, g.row0 + r);
+          int sum = 0;
+#pragma unroll
+          for (int p = 0; p < KS; ++p) sum += s_sum[p][threadIdx.x / 16][threadIdx.x % 16];
+          const float s = kCode ? s_scale[r] : a.q_scale[to.in];
+          if (to.out >= 0) static_cast<T*>(a.out)[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(sum, s, ws[c]);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, bool kGelu, int KS, int R, bool kCode>
+hipError_t launch_few(Q8Args a, hipStream_t s) {
+  constexpr uint32_t N = 16 * (4 / KS);
+  a.col_tiles = (a.n + N - 1) / N;
+  const uint64_t blocks = a.offsets ? std::min<uint64_t>(a.rows, a.rows / (16 * R) + a.E) : (a.rows + 16 * R - 1) / (16 * R);
+  const uint32_t lds = kCode ? 16 * (a.stride + 16) : 0;
+  if (kCode) {
+    const hipError_t e = hipFuncSetAttribute((const void*)k_q8_few<T, kGelu, KS, R, kCode>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             16 * (kCodeWidth + 16));
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((k_q8_few<T, kGelu, KS, R, kCode>), dim3((uint32_t)(blocks * a.col_tiles)), dim3(kThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kGelu, int R, bool kCode>
+hipError_t launch_few_rows(const Q8Args& a, hipStream_t s) {
+  if (a.stride > 32 * 64) return launch_few<T, kGelu, 4, R, kCode>(a, s);
+  if (a.stride > 16 * 64) return launch_few<T, kGelu, 2, R, kCode>(a, s);
+  return launch_few<T, kGelu, 1, R, kCode>(a, s);
+}
+
+// Whether a product makes the codes of x itself, in one launch.
+bool codes_inside(uint32_t rows, uint32_t stride) { return rows <= 8 && stride <= kCodeWidth; }
 
 template <typename T, bool kGelu>
 hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<256, 256, 2, 4, 128, 2> Large;
   typedef Shape<128, 256, 2, 2, 64, 3> Middle;
+  typedef Shape<128, 128, 2, 2, 64, 4> Square;
   typedef Shape<64, 64, 2, 2, 64, 4> Small;
-  const uint64_t cols = (a.n + 255) / 256, large = a.rows / 256 * cols;
-  if (large >= 1024 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
-  return large >= 128 ? launch_tile<Middle, T, kGelu>(a, s) : launch_tile<Small, T, kGelu>(a, s);
+  typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
+  if (a.x) return launch_few_rows<T, kGelu, 1, true>(a, s);
+  // tiles of a height and width that there will be about, half of each expert's last one empty
+  auto tiles = [&](uint32_t m, uint32_t n) {
+    const uint64_t blocks = a.E > 1 ? std::min<uint64_t>(a.rows, a.rows / m + a.E / 2) : ((uint64_t)a.rows + m - 1) / m;
+    return blocks * ((a.n + n - 1) / n);
+  };
+  const uint64_t each = a.rows / a.E, large = tiles(256, 256);
+  if (each >= 512 && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
+  if (each >= 32 && tiles(128, 256) >= 384) return launch_tile<Middle, T, kGelu>(a, s);
+  if (each >= 32 && tiles(128, 128) >= 256) return launch_tile<Square, T, kGelu>(a, s);
+  if (tiles(64, 64) <= 256 && a.stride >= 2048) return launch_tile<Parted, T, kGelu>(a, s);
+  return launch_tile<Small, T, kGelu>(a, s);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -854,7 +1115,10 @@ extern "C" int pw_q8_product(const pw_q8_desc* d, const pw_q8_io* io, void* ws, 
   a.gather = d->gather;
   a.scatter = d->scatter;
   hipError_t e;
-  if (io->x) {
+  if (io->x && codes_inside(a.rows, a.stride)) {
+    a.x = io->x;
+    a.d = d->d;
+  } else if (io->x) {
     int8_t* q = static_cast<int8_t*>(ws);
     float* scale = reinterpret_cast<float*>(q + up256(d->x_rows * a.stride));
     // rows behind the last segment are not looked at
