@@ -565,7 +565,8 @@ int pw_block_norm_grad(const pw_norm_desc* d, const pw_norm_io* io, void* ws, si
 /* ---- routing ---------------------------------------------------------------
  * Of a token's logits l over E experts, with a bias b that balances the choice:
  *   s_e = softmax(l)_e  or  1 / (1 + exp(-l_e))
- *   c_e = s_e + b_e, compared in 64 bits
+ *   c_e = s_e + b_e, compared in 64 bits; without a bias and marks, scores are
+ *   compared by their logits, whose order is theirs before any rounding
  *   mark of a group of E / groups neighbouring experts: the sum of its group_best
  *   highest c; the experts of the top_groups groups of highest mark may be chosen
  *   experts[j]: the k highest c among them, best first

@@ -56,7 +56,9 @@ def route(logits, bias, valid, k, sigmoid, groups=1, top_groups=1, group_best=2,
         if valid is not None and not valid[t]:
             continue
         free = [e for e in range(E) if _usable(logits[t:t + 1, e:e + 1])[0, 0] > -np.inf and b[e] > -np.inf]
-        c = {e: s[t, e] + b[e] for e in free}
+        # scores grow with their logits: alone, their order is that of the logits, also where they round to one value
+        plain = bias is None and top_groups == groups
+        c = {e: _usable(logits[t:t + 1, e:e + 1])[0, 0] if plain else s[t, e] + b[e] for e in free}
         if top_groups < groups:
             marks = []
             for g in range(groups):

@@ -865,9 +865,12 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int32_t s_sum[KS > 1 ? KS : 1][16][20];  // [part][row][column]
   __shared__ float s_scale[16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  // every row's id at once with the segments: nothing else stands before the rows
+  const int32_t ids = kCode && a.src_index ? a.src_index[min((uint32_t)lane, a.rows - 1)] : 0;
+  auto row_at = [&](uint32_t i) { return kCode ? row_from(a, i, __shfl(ids, (int)i)) : row_of(a, i); };
   const Piece g = piece_of<16 * R, 16 * kGroups>(a, blockIdx.x);
   if (g.rows == 0) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int part = w % KS, group = w / KS;
   const uint32_t nk = a.stride / 64, each = (nk + KS - 1) / KS, k0 = min(part * each, nk), k1 = min(k0 + each, nk);
   const uint32_t chunk = lane / 16 * 16, pitch = a.stride + 16;  // (of the codes in LDS: rows in different banks)
@@ -877,7 +880,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
   typename Eight<T>::Vec v[kCode ? kEach : 1];
   RowOf coded{};
   if constexpr (kCode) {
-    coded = row_of(a, g.row0 + min((uint32_t)w, g.rows - 1));
+    coded = row_at(g.row0 + min((uint32_t)w, g.rows - 1));
 #pragma unroll
     for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
   }
@@ -888,7 +891,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
   for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k0 + i, nk - 1) * 64);
   RowOf row[R];
 #pragma unroll
-  for (int m = 0; m < R; ++m) row[m] = row_of(a, g.row0 + min((uint32_t)(16 * m + lane % 16), g.rows - 1));
+  for (int m = 0; m < R; ++m) row[m] = row_at(g.row0 + min((uint32_t)(16 * m + lane % 16), g.rows - 1));
 
   if constexpr (kCode) {
 #pragma unroll 1
@@ -896,7 +899,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
       const uint32_t r = w + 4 * i;
       if (r >= g.rows) break;
       if (i > 0) {
-        coded = row_of(a, g.row0 + r);
+        coded = row_at(g.row0 + r);
 #pragma unroll
         for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
       }
@@ -959,7 +962,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
         __syncthreads();
         const uint32_t r = 16 * m + threadIdx.x / 16, c = g.col0 + 16 * t + threadIdx.x % 16;
         if (r < g.rows && c < a.n) {
-          const RowOf to = row_of(a, g.row0 + r);
+          const RowOf to = row_at(g.row0 + r);
           int sum = 0;
 #pragma unroll
           for (int p = 0; p < KS; ++p) sum += s_sum[p][threadIdx.x / 16][threadIdx.x % 16];
