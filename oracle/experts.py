@@ -50,25 +50,21 @@ def route(logits, bias, valid, k, sigmoid, groups=1, top_groups=1, group_best=2,
     T, E = logits.shape
     s, _ = scores(logits, sigmoid)
     b = np.zeros(E) if bias is None else np.where(np.isnan(bias), -np.inf, bias).astype(np.float64)
-    experts = np.full((T, k), E, np.int64)
-    size = E // groups
-    for t in range(T):
-        if valid is not None and not valid[t]:
-            continue
-        free = [e for e in range(E) if _usable(logits[t:t + 1, e:e + 1])[0, 0] > -np.inf and b[e] > -np.inf]
-        # scores grow with their logits: alone, their order is that of the logits, also where they round to one value
-        plain = bias is None and top_groups == groups
-        c = {e: _usable(logits[t:t + 1, e:e + 1])[0, 0] if plain else s[t, e] + b[e] for e in free}
-        if top_groups < groups:
-            marks = []
-            for g in range(groups):
-                best = sorted((c[e] for e in free if e // size == g), reverse=True)[:group_best]
-                if best:
-                    marks.append((-math.fsum(best) if len(best) < 2 else -(best[0] + best[1]), g))
-            kept = {g for _, g in sorted(marks)[:top_groups]}
-            free = [e for e in free if e // size in kept]
-        chosen = sorted(free, key=lambda e: (-c[e], e))[:k]
-        experts[t, :len(chosen)] = chosen
+    l = _usable(logits)
+    # scores grow with their logits: alone, their order is that of the logits, also where they round to one value
+    c = l.copy() if bias is None and top_groups == groups else s + b
+    c[(l == -np.inf) | (b == -np.inf)] = -np.inf
+    if valid is not None:
+        c[~np.asarray(valid, bool)] = -np.inf
+    if top_groups < groups:
+        best = -np.sort(-c.reshape(T, groups, E // groups), axis=2)[:, :, :group_best]
+        mark = np.where(best[:, :, 0] == -np.inf, -np.inf, np.where(best == -np.inf, 0, best).sum(axis=2))
+        order = np.argsort(-mark, axis=1, kind="stable")[:, :top_groups]
+        kept = np.zeros((T, groups), bool)
+        np.put_along_axis(kept, order, True, axis=1)
+        c[~np.repeat(kept, E // groups, axis=1)] = -np.inf
+    experts = np.argsort(-c, axis=1, kind="stable")[:, :k]
+    experts = np.where(np.take_along_axis(c, experts, 1) == -np.inf, E, experts)
     return experts, scale * _weights(logits, experts, sigmoid, renorm)
 
 

@@ -16,7 +16,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kMaxRouteExperts = 256, kMaxK = 8, kMaxGroups = 16;
-constexpr uint32_t kManyTokens = 16384;  // fewer lanes a token from here on
+// Fewer lanes a token, and a second launch, from so many logits on (of more than 16
+// experts; 64 experts, k = 6: 16384 tokens 11.3 us so and 10.0 us in one launch, 131072 27
+// and 54; 256 experts in groups, k = 8: 4096 tokens 16.6 and 13.2 us, 8192 17.8 and 21.9;
+// 131072 tokens of 8 experts 8.9 and 7.0).
+constexpr uint64_t kManyLogits = 1ull << 21;
 
 struct RouteArgs {
   const float* logits;
@@ -37,8 +41,12 @@ struct RouteArgs {
   uint32_t per_group;  // 2^16 / experts of a group, rounded up
 };
 
-// A logit as it is used: +infinity is the largest finite value, NaN is none.
-__device__ __forceinline__ float usable(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
+// A logit as it is used: +infinity is the largest finite value, NaN is none (the
+// larger of a NaN and a number is the number).
+__device__ __forceinline__ float usable(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
+
+// e^x for x up to 0: off by (1.5 |x| + 2) 2^-24 of itself.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // Weights of the chosen logits: lane j of each aligned group of 8 lanes holds
 // the j-th (-infinity: no expert). u_j = s_j e^-m with m = min(0, the largest
@@ -61,19 +69,21 @@ __device__ __forceinline__ float chosen_score(float l, bool renorm) {
 // (logits where nothing is added to their scores and no group is marked, else
 // c in fp32) are cut to the bits that leave room for the expert's number, so
 // that one 32-bit integer orders and names an expert, and the k + 2 best are
-// found with integer maxima. Where two of them are so close that the cut or
-// the fp32 evaluation might have changed their order, the k + 1 best are
-// compared in 64 bits (`settle`), and where even the (k + 2)-th might belong to
-// the k best, or two groups' marks are that close, all of the token's scores are
-// computed in 64 bits (`choose_slowly`).
+// found with integer maxima. Tokens of whose order this leaves a doubt are listed
+// and seen to at the end: where two of the k + 1 best are so close that the cut or
+// the fp32 evaluation might have exchanged them, these are compared in 64 bits (16
+// lanes a token); where even the (k + 2)-th might belong to the k best, or two
+// groups' marks are that close, or the scores are a softmax, whose 64-bit value
+// needs all logits, a wave takes the token anew in 64 bits. Logits of fewer bits
+// than are cut (bf16 ones; equal ones) leave no doubt.
 
-// Order-preserving integers of floats.
+// Order-preserving integers of floats other than negative zero.
 __device__ __forceinline__ int32_t ordered(float f) {
-  const int32_t b = __builtin_bit_cast(int32_t, f + 0.0f);  // no negative zero
+  const int32_t b = __builtin_bit_cast(int32_t, f);
   return b ^ (b >> 31 & 0x7fffffff);
 }
 __device__ __forceinline__ float unordered(int32_t i) { return __builtin_bit_cast(float, i ^ (i >> 31 & 0x7fffffff)); }
-constexpr int32_t kNone = INT32_MIN;  // below every value's
+constexpr int32_t kLowest = (int32_t)0x80800000;  // of the finite values; those below are no experts
 
 template <int M>
 __device__ __forceinline__ int32_t across_int(int32_t v) {
@@ -89,62 +99,54 @@ __device__ __forceinline__ uint32_t lanes_or(uint32_t v) {
   if constexpr (M < L) return lanes_or<L, 2 * M>(v | (uint32_t)across_int<M>((int32_t)v));
   return v;
 }
+__device__ __forceinline__ int32_t middle(int32_t a, int32_t b, int32_t c) { return max(min(a, b), min(max(a, b), c)); }
 
-// Score of a logit in 64 bits: l - top's exponential over `total`, or the sigmoid.
-template <bool kSigmoid>
-__device__ __forceinline__ double score64(float l, float top, double total) {
-  if constexpr (kSigmoid) return 1.0 / (1.0 + exp(-(double)l));
-  return exp((double)l - (double)top) / total;
-}
-
-// What a token's lanes know of it. at(i): the first of the four experts of the
-// lane's i-th chunk; elements before 4 chunk(i) are the chunk's before.
+// A token's logits in its lanes: element v of the lane's chunk i is expert
+// first(i) + v. The last chunk is moved back to end with the row; what the chunk
+// before has of it counts as no expert, as does what lies behind the row.
 template <int L, int C>
 struct Token {
   const float* in;
   float l[4 * C];
   uint32_t E, sub;
-  __device__ __forceinline__ uint32_t expert(int i, int v) const {
+  __device__ __forceinline__ uint32_t first(int i) const { return min(4 * (i * L + sub), max(E, 4u) - 4); }
+  __device__ __forceinline__ uint32_t expert(int i) const { return first(i / 4) + i % 4; }  // of l[i]
+  __device__ __forceinline__ uint32_t skipped(int i, bool live) const {  // of chunk i's elements
     const uint32_t c = 4 * (i * L + sub);
-    return min(c, max(E, 4u) - 4) + v;
+    return live && c < E ? c - first(i) : 4u;
   }
-  // E >= 4: rows of any count in 16-byte loads, the last chunk moved back
-  __device__ __forceinline__ void load(bool live) {
+  __device__ __forceinline__ void load(const RouteArgs& a, uint64_t at, bool live) {
     typedef float At __attribute__((ext_vector_type(4), aligned(4)));
     typedef float Vec __attribute__((ext_vector_type(4)));
+    in = a.logits + at * a.E;
+    E = a.E;
     Vec x[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       if (E >= 4) {
-        x[i] = *reinterpret_cast<const At*>(in + expert(i, 0));
+        x[i] = *reinterpret_cast<const At*>(in + first(i));
       } else {
 #pragma unroll
         for (uint32_t v = 0; v < 4; ++v) x[i][v] = in[min(v, E - 1)];
       }
     }
 #pragma unroll
-    for (int i = 0; i < C; ++i)
+    for (int i = 0; i < C; ++i) {
+      const uint32_t skip = skipped(i, live);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t e = expert(i, v);
-        l[4 * i + v] = live && e < E && e >= 4 * (i * L + sub) ? usable(x[i][v]) : -INFINITY;
-      }
+      for (uint32_t v = 0; v < 4; ++v) l[4 * i + v] = v >= skip && v < E ? usable(x[i][v]) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ float top() const {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < 4 * C; ++i) m = fmaxf(m, l[i]);
+    return lanes_max<L>(m);
   }
 };
 
-// Softmax statistics in 64 bits.
-template <int L, int C>
-__device__ __forceinline__ double total64(const Token<L, C>& t, float top) {
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < 4 * C; ++i) sum += t.l[i] == -INFINITY ? 0.0 : exp((double)t.l[i] - (double)top);
-#pragma unroll
-  for (int m = 1; m < L; m *= 2) sum += __shfl_xor(sum, m);
-  return sum;
-}
-
-// The kept groups as bits from the marks in s_c, the row's c (missing: -infinity);
-// *close: a kept and a left one differ by `margin` of the larger or less.
+// The kept groups as bits, from the row's c in LDS (no expert: -infinity); *close:
+// a kept and a left one differ by `margin` (relatively, or of one) or less.
 template <int L, typename F>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, uint32_t sub, F margin, bool* close) {
   constexpr int kEach = L >= (int)kMaxGroups ? 1 : (int)kMaxGroups / L;  // groups of a lane
@@ -156,8 +158,10 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, 
     const uint32_t g = h * L + sub;
     F m1 = low, m2 = low;
     if (g < a.groups) {
+      uint32_t at = g % size;  // lanes begin in different banks
       for (uint32_t i = 0; i < size; ++i) {
-        const F x = c[g * size + i];
+        const F x = c[g * size + at];
+        at = at + 1 == size ? 0 : at + 1;
         m2 = max(m2, min(m1, x));
         m1 = max(m1, x);
       }
@@ -194,6 +198,24 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, 
   return kept;
 }
 
+// c in LDS, then the experts of left groups out of it.
+template <int L, int C, typename F>
+__device__ __forceinline__ void leave_groups(const RouteArgs& a, const Token<L, C>& t, F* s_c, F (&c)[4 * C], F margin, bool* close) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const uint32_t skip = t.skipped(i, true);
+#pragma unroll
+    for (uint32_t v = 0; v < 4; ++v)
+      if (v >= skip && v < t.E) s_c[t.first(i) + v] = c[4 * i + v];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const uint32_t kept = keep_groups<L, F>(a, s_c, t.sub, margin, close);
+#pragma unroll
+  for (int i = 0; i < 4 * C; ++i)
+    if (!(kept >> (min(t.expert(i), a.E - 1) * a.per_group >> 16) & 1)) c[i] = -(F)INFINITY;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // Lane q of the first eight of a token's (or of its four) has the q-th expert, with
 // four lanes a token also the (q + 4)-th.
 template <int L>
@@ -202,271 +224,324 @@ struct Places {
   int32_t id[kEach];  // E: none
 };
 
-// The k best by 64-bit values, everything computed anew.
-template <int L, int C, bool kSigmoid>
-__device__ __forceinline__ void choose_slowly(const RouteArgs& a, const Token<L, C>& t, bool scored, double* s_c, Places<L>& to) {
-  typedef Places<L> P;
-  double c[4 * C];
-  float top = t.l[0];
+// Experts and weights of token `at`; top and total: of its softmax (without renorm).
+template <int L, bool kSigmoid>
+__device__ __forceinline__ void store_token(const RouteArgs& a, const float* in, uint64_t at, uint32_t sub, bool live,
+                                            const Places<L>& p, float top, float total) {
+  constexpr int kLanes = Places<L>::kLanes, kEach = Places<L>::kEach;
+  float l[kEach], u[kEach], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-  for (int i = 1; i < 4 * C; ++i) top = fmaxf(top, t.l[i]);
-  top = lanes_max<L>(top);
-  const double total = kSigmoid || !scored ? 1.0 : total64<L, C>(t, top);
+  for (int h = 0; h < kEach; ++h) l[h] = in[min((uint32_t)p.id[h], a.E - 1)];
 #pragma unroll
-  for (int i = 0; i < 4 * C; ++i) {
-    c[i] = -(double)INFINITY;
-    if (t.l[i] != -INFINITY) {
-      c[i] = scored ? score64<kSigmoid>(t.l[i], top, total) : (double)t.l[i];
-      if (a.bias) c[i] += (double)a.bias[t.expert(i / 4, i % 4)];
-      if (!(c[i] > -(double)INFINITY)) c[i] = -(double)INFINITY;
+  for (int h = 0; h < kEach; ++h) {
+    l[h] = p.id[h] < (int32_t)a.E ? usable(l[h]) : -INFINITY;
+    m = fmaxf(m, l[h]);
+  }
+  m = lanes_max<kLanes>(m);
+  if constexpr (kSigmoid) m = a.renorm ? fminf(m, 0.0f) : 0.0f;
+  else m = a.renorm ? m : top;
+#pragma unroll
+  for (int h = 0; h < kEach; ++h) {
+    u[h] = 0.0f;
+    if (l[h] != -INFINITY) {
+      // s e^-m with m = min(0, the largest logit) keeps the ratios of scores that underflow
+      if constexpr (kSigmoid) u[h] = exp_of(fminf(l[h], 0.0f) - m) * __builtin_amdgcn_rcpf(1.0f + exp_of(-fabsf(l[h])));
+      else u[h] = exp_of(l[h] - m);
     }
+    sum += u[h];
+  }
+  sum = lanes_sum<kLanes>(sum);
+  const float by = a.scale * __builtin_amdgcn_rcpf(a.renorm ? sum : total);
+#pragma unroll
+  for (int h = 0; h < kEach; ++h) {
+    const uint32_t j = h * kLanes + sub;
+    if (live && sub < (uint32_t)kLanes && j < a.k) {
+      a.experts[at * a.k + j] = p.id[h];
+      a.weights[at * a.k + j] = p.id[h] < (int32_t)a.E ? u[h] * by : 0.0f;
+    }
+  }
+}
+
+// A token in 64 bits, by a wave.
+template <bool kSigmoid>
+__device__ __forceinline__ void route_exactly(const RouteArgs& a, uint64_t at, double* s_c) {
+  typedef Places<64> P;
+  Token<64, 1> t;
+  t.sub = threadIdx.x & 63;
+  t.load(a, at, true);
+  const float top = t.top();
+  double c[4], total = 1.0;
+  if constexpr (!kSigmoid) {
+    total = 0.0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      c[v] = t.l[v] == -INFINITY ? 0.0 : exp((double)t.l[v] - (double)top);
+      total += c[v];
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) total += __shfl_xor(total, m);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if constexpr (kSigmoid) c[v] = 1.0 / (1.0 + exp(-(double)t.l[v]));
+    else c[v] /= total;
+    if (!a.bias && !a.by_group) c[v] = (double)t.l[v];
+    if (a.bias) c[v] += (double)a.bias[min(t.expert(v), a.E - 1)];
+    if (t.l[v] == -INFINITY || !(c[v] > -(double)INFINITY)) c[v] = -(double)INFINITY;
   }
   if (a.by_group) {
-#pragma unroll
-    for (int i = 0; i < 4 * C; ++i) {
-      const uint32_t e = t.expert(i / 4, i % 4);
-      if (e < a.E && e >= 4 * (i / 4 * L + t.sub)) s_c[e] = c[i];
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     bool close;
-    const uint32_t kept = keep_groups<L, double>(a, s_c, t.sub, 0.0, &close), size = a.E / a.groups;
-#pragma unroll
-    for (int i = 0; i < 4 * C; ++i)
-      if (!(kept >> min(t.expert(i / 4, i % 4) / size, 31u) & 1)) c[i] = -(double)INFINITY;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    leave_groups<64, 1, double>(a, t, s_c, c, 0.0, &close);
   }
+  P place;
+  place.id[0] = (int32_t)a.E;
 #pragma unroll 1
   for (int j = 0; j < (int)a.k; ++j) {
     double best = -(double)INFINITY;
-    int32_t at = (int32_t)a.E;
+    int32_t e = (int32_t)a.E;
 #pragma unroll
-    for (int i = 0; i < 4 * C; ++i)
-      if (c[i] > best) best = c[i], at = (int32_t)t.expert(i / 4, i % 4);
+    for (int v = 0; v < 4; ++v)
+      if (c[v] > best) best = c[v], e = (int32_t)t.expert(v);
 #pragma unroll
-    for (int m = 1; m < L; m *= 2) {
+    for (int m = 1; m < 64; m *= 2) {
       const double o = __shfl_xor(best, m);
-      const int32_t n = __shfl_xor(at, m);
-      if (o > best || (o == best && n < at)) best = o, at = n;
+      const int32_t n = __shfl_xor(e, m);
+      if (o > best || (o == best && n < e)) best = o, e = n;
     }
+    if ((int)t.sub % P::kLanes == j) place.id[0] = e;
 #pragma unroll
-    for (int h = 0; h < P::kEach; ++h)
-      if (h * P::kLanes + (int)t.sub % P::kLanes == j) to.id[h] = at;
-#pragma unroll
-    for (int i = 0; i < 4 * C; ++i)
-      if ((int32_t)t.expert(i / 4, i % 4) == at) c[i] = -(double)INFINITY;
+    for (int v = 0; v < 4; ++v)
+      if ((int32_t)t.expert(v) == e) c[v] = -(double)INFINITY;
   }
+  store_token<64, kSigmoid>(a, t.in, at, t.sub, true, place, top, (float)total);
 }
 
-// Puts the N candidates of keys[] (of a sigmoid, or plain logits) in the order of
-// their 64-bit values.
-template <int L, int C, bool kSigmoid, int N>
-__device__ __forceinline__ void settle(const RouteArgs& a, const Token<L, C>& t, bool scored, uint32_t names, int32_t (&keys)[N]) {
-  constexpr int kEach = (N + L - 1) / L;
-  double c[kEach];
-  int32_t key[kEach];
-  uint32_t before[kEach] = {};
-#pragma unroll
-  for (int h = 0; h < kEach; ++h) {
-    key[h] = kNone;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (h * L + (int)t.sub == j) key[h] = keys[j];
-    c[h] = -(double)INFINITY;
-    if (key[h] != kNone) {
-      const uint32_t e = names - ((uint32_t)key[h] & names);
-      const float l = usable(t.in[e]);
-      c[h] = scored ? score64<kSigmoid>(l, 0.0f, 1.0) : (double)l;
-      if (a.bias) c[h] += (double)a.bias[e];
-    }
+// The k best of k + 1 candidates, by 64-bit scores of a sigmoid, or by logits; 16
+// lanes a token, lane q has the q-th candidate's key.
+template <bool kSigmoid>
+__device__ __forceinline__ void settle(const RouteArgs& a, uint64_t at, int32_t key) {
+  typedef Places<16> P;
+  const int q = threadIdx.x & 15, base = (int)(threadIdx.x & 48);
+  const float* in = a.logits + at * a.E;
+  const bool some = (uint32_t)q <= a.k && key >= kLowest;
+  const uint32_t e = min(a.names - ((uint32_t)key & a.names), a.E - 1);
+  double c = (double)usable(in[e]);
+  if (a.bias || a.by_group) c = 1.0 / (1.0 + exp(-c));
+  if (a.bias) c += (double)a.bias[e];
+  if (!some) c = -(double)INFINITY;
+  uint32_t before = 0;
+  for (uint32_t j = 0; j <= a.k; ++j) {
+    const double o = __shfl(c, base + (int)j);
+    const uint32_t n = (uint32_t)__shfl((int)e, base + (int)j);
+    before += o > c || (o == c && n < e);
   }
-  const int base = (int)(threadIdx.x & 63) / L * L;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const double o = __shfl(c[j / L], base + j % L);
-    const int32_t other = __shfl(key[j / L], base + j % L);
-    if (other == kNone) continue;
-#pragma unroll
-    for (int h = 0; h < kEach; ++h)  // equal values: the larger name bits are the lower index
-      before[h] += o > c[h] || (o == c[h] && (other & names) > (key[h] & names));
+  const uint32_t mine = some ? before << 16 | e : ~0u;
+  P place;
+  place.id[0] = (int32_t)a.E;
+  for (uint32_t j = 0; j <= a.k; ++j) {
+    const uint32_t o = (uint32_t)__shfl((int)mine, base + (int)j);
+    if (o >> 16 == (uint32_t)(q & 7) && o >> 16 < a.k) place.id[0] = (int32_t)(o & 0xffff);
   }
-  int32_t to[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    int32_t mine = 0;
-#pragma unroll
-    for (int h = 0; h < kEach; ++h)
-      if (key[h] != kNone && before[h] == (uint32_t)j) mine = key[h];
-    to[j] = (int32_t)lanes_or<L>((uint32_t)mine);
-    if (keys[j] == kNone) to[j] = kNone;
+  float top = 0.0f, total = 1.0f;
+  if (!kSigmoid && !a.renorm) {
+    top = -INFINITY, total = 0.0f;
+    for (uint32_t i = q; i < a.E; i += 16) top = fmaxf(top, usable(in[i]));
+    top = lanes_max<16>(top);
+    for (uint32_t i = q; i < a.E; i += 16) total += usable(in[i]) == -INFINITY ? 0.0f : expf(usable(in[i]) - top);
+    total = lanes_sum<16>(total);
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) keys[j] = to[j];
+  store_token<16, kSigmoid>(a, in, at, q, true, place, top, total);
 }
 
-// K: the largest top_k of this instance.
-template <int L, int C, int K, bool kSigmoid>
-__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
+// What k_route leaves in the first place of a token that k_route_rest sees to: one
+// to be settled, whose other places and weights hold the k + 1 keys, or one to be
+// taken anew.
+constexpr int32_t kSettle = INT32_MIN, kAnew = INT32_MIN + 1;
+
+// K: the largest top_k of this instance. kScored: c orders the experts, not their logits.
+// kWhole: tokens in doubt are seen to here, else left for k_route_rest. The latter takes
+// fewer registers (131072 x 64, k = 6, sigmoid with bias: 3 waves a SIMD instead of 2,
+// 23 us instead of 41), for a launch more.
+template <int L, int C, int K, bool kSigmoid, bool kScored, bool kWhole>
+__global__ __launch_bounds__(kThreads, kWhole ? 2 : 3) void k_route(RouteArgs a) {
   constexpr int kRows = kThreads / L, N = K + 2, kList = N < 4 * C ? N : 4 * C;
-  // Two fp32 values of c are off by less than this, and their roundings by less than
-  // a.cut of themselves. Sigmoid: the exponent is off by 1.5 x 2^-24 of itself, e^x by 2^-23, the
-  // sum and the reciprocal by 2^-23 each, and s (1 - s) |l| is at most 0.224: 4.3 x 2^-23 of c
-  // each. Softmax: (D + 4) 2^-24 of e^-D, 30 x 2^-24 of the sum and the quotient: 31 x 2^-24 each.
-  constexpr float kOff = kSigmoid ? 0x1p-19f : 0x1p-17f;
-  extern __shared__ __attribute__((aligned(16))) double s_row[];  // [rows][E] by group: c, in 32 or 64 bits
-  Token<L, C> t;
-  t.E = a.E;
-  t.sub = threadIdx.x % L;
-  const uint32_t row = threadIdx.x / L, names = a.names;
-  const bool scored = a.bias || a.by_group;
-  double* s_c = s_row + row * a.E;
+  extern __shared__ __attribute__((aligned(16))) float s_rows[];  // by group: [rows][E], c
+  constexpr bool kSettled = kSigmoid || !kScored;  // (a softmax needs all of its logits)
+  __shared__ double s_c[kWhole && kScored ? kThreads / 64 : 1][kWhole && kScored ? kMaxRouteExperts : 1];
+  __shared__ uint32_t s_listed[2];  // to be settled, to be taken anew
+  __shared__ uint8_t s_list[2][kRows];
+  __shared__ int32_t s_key[kWhole && kSettled ? kRows : 1][N];
+  const uint32_t row = threadIdx.x / L, names = a.names, k = a.k;
+  if constexpr (kWhole) {
+    if (threadIdx.x < 2) s_listed[threadIdx.x] = 0;
+    __syncthreads();
+  }
   for (uint64_t t0 = (uint64_t)blockIdx.x * kRows; t0 < a.tokens; t0 += (uint64_t)gridDim.x * kRows) {
     const uint64_t at = min(t0 + row, (uint64_t)a.tokens - 1);
-    const bool live = !a.valid || a.valid[at];
-    t.in = a.logits + at * a.E;
-    t.load(live);
-    // what orders the experts
-    float c[4 * C];
-    float top = -INFINITY, total = 1.0f;
-    if constexpr (!kSigmoid) {
-      if (scored || !a.renorm) {
+    const bool mine = t0 + row < a.tokens, live = !a.valid || a.valid[at];
+    Token<L, C> t;
+    t.sub = threadIdx.x % L;
+    t.load(a, at, live);
+    float c[4 * C], top = 0.0f, total = 1.0f;
 #pragma unroll
-        for (int i = 0; i < 4 * C; ++i) top = fmaxf(top, t.l[i]);
-        top = lanes_max<L>(top);
+    for (int i = 0; i < 4 * C; ++i) c[i] = t.l[i];
+    if constexpr (!kSigmoid) {
+      if (kScored || !a.renorm) {
+        top = t.top();
         total = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * C; ++i) {
-          c[i] = t.l[i] == -INFINITY ? 0.0f : expf(t.l[i] - top);
-          total += c[i];
+          const float z = t.l[i] == -INFINITY ? 0.0f : expf(t.l[i] - top);
+          total += z;
+          if (kScored) c[i] = z;
         }
         total = lanes_sum<L>(total);
       }
     }
-    if (scored) {
+    bool doubt = false, anew = false;
+    // What two fp32 values of c are off by together, beside their last bits. Sigmoid:
+    // the exponent is off by 1.5 x 2^-24 of itself, e^x, the sum and the reciprocal by 2^-23
+    // each, and s (1 - s) |l| is at most 0.224: 4.3 x 2^-23 each. Softmax, with p the largest:
+    // (D + 4) 2^-24 of e^-D p (D e^-D is at most 0.37) and 30 x 2^-24 of the sum and the
+    // quotient: 35 p 2^-24 each.
+    float off = 0x1p-19f;
+    if constexpr (kScored) {
       const float inv = 1.0f / total;
+      if constexpr (!kSigmoid) off = (1.0f + 70.0f * inv) * 0x1p-24f;
 #pragma unroll
       for (int i = 0; i < 4 * C; ++i) {
         if constexpr (kSigmoid) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t.l[i] * -1.44269504f));
         else c[i] *= inv;
-        if (a.bias) c[i] += a.bias[min(t.expert(i / 4, i % 4), a.E - 1)];
-        if (t.l[i] == -INFINITY || !(c[i] > -INFINITY)) c[i] = -INFINITY;
+        if (a.bias) c[i] += fmaxf(a.bias[min(t.expert(i), a.E - 1)], -INFINITY);  // (of a NaN: -infinity)
+        if (t.l[i] == -INFINITY) c[i] = -INFINITY;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4 * C; ++i) c[i] = t.l[i];
+      if (a.by_group) leave_groups<L, C, float>(a, t, s_rows + row * a.E, c, 4 * off, &anew);
     }
-    bool slow = false;
-    if (a.by_group) {
-      float* s = reinterpret_cast<float*>(s_c);
-#pragma unroll
-      for (int i = 0; i < 4 * C; ++i) {
-        const uint32_t e = t.expert(i / 4, i % 4);
-        if (e < a.E && e >= 4 * (i / 4 * L + t.sub)) s[e] = c[i];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const uint32_t kept = keep_groups<L, float>(a, s, t.sub, 2 * kOff, &slow);
-#pragma unroll
-      for (int i = 0; i < 4 * C; ++i) {
-        const uint32_t e = min(t.expert(i / 4, i % 4), a.E - 1);
-        if (!(kept >> (e * a.per_group >> 16) & 1)) c[i] = -INFINITY;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    // the lane's best, in order: each new one moves the lesser ones down
+    // the lane's best in order: each new one moves the lesser ones down
     int32_t list[kList];
+    uint32_t cut = 0;  // bits that are cut off
 #pragma unroll
-    for (int n = 0; n < kList; ++n) list[n] = kNone;
+    for (int n = 0; n < kList; ++n) list[n] = INT32_MIN;
 #pragma unroll
     for (int i = 0; i < 4 * C; ++i) {
-      const uint32_t e = t.expert(i / 4, i % 4);
-      const int32_t x = c[i] == -INFINITY ? kNone : (int32_t)(((uint32_t)ordered(c[i]) & ~names) | (names - e));
+      const uint32_t bits = (uint32_t)ordered(kScored ? c[i] : c[i] + 0.0f);  // (s + b is no negative zero)
+      if (!kScored) cut |= c[i] == -INFINITY ? 0u : bits;
+      const int32_t x = (int32_t)((bits & ~names) | ((names - t.expert(i)) & names));
 #pragma unroll
-      for (int n = kList - 1; n > 0; --n) list[n] = max(min(list[n - 1], x), list[n]);
+      for (int n = (i < kList - 1 ? i : kList - 1); n > 0; --n) list[n] = middle(list[n - 1], x, list[n]);
       list[0] = max(list[0], x);
     }
-    // the token's best
-    int32_t keys[N];
+    // the token's best, and whether they are in order
+    if (!kScored) cut = lanes_or<L>(cut) & names;
+    typedef Places<L> P;
+    P place;
+#pragma unroll
+    for (int h = 0; h < P::kEach; ++h) place.id[h] = INT32_MIN;
+    int32_t one = 0, two = 0, keys[N];  // one, two: the keys before
+    float u1 = 0.0f, u2 = 0.0f;         // and their values
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int32_t best = lanes_max_int<L>(list[0]);
+      if (j < K && (int)t.sub % P::kLanes == j % P::kLanes) place.id[j / P::kLanes] = best;
+      const float v = unordered(best & (int32_t)~names);
+      // (j - 1, j) up to the (k + 1)-th, and the (k + 2)-th against the k-th
+      if (j > 0 && (uint32_t)j <= k + 1) {
+        bool near;
+        if constexpr (kScored) {
+          // the lesser one may be a whole cut higher
+          const float u = (uint32_t)j <= k ? u1 : u2;
+          near = !(u - v > fmaf(fmaxf(fabsf(u), fabsf(v)), a.cut + 0x1p-22f, off));
+        } else {
+          near = cut && ((uint32_t)(((uint32_t)j <= k ? one : two) ^ best) & ~names) == 0;
+        }
+        near &= best >= kLowest;
+        if ((uint32_t)j <= k && kSettled) doubt |= near;
+        else anew |= near;
+      }
       keys[j] = best;
+      two = one;
+      one = best;
+      u2 = u1;
+      u1 = v;
       const bool pop = list[0] == best;
 #pragma unroll
-      for (int n = 0; n + 1 < kList; ++n) list[n] = pop ? list[n + 1] : list[n];
-      if (pop) list[kList - 1] = kNone;
-    }
-    // are they in order?
-    const uint32_t k = a.k;
-    bool close = false;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      // (j, j + 1) inside the k + 1 best; the (k + 2)-th against the k-th
-      const int i = j + 1 < N ? j + 1 : j;
-      const int32_t x = keys[j] & (int32_t)~names, y = keys[i] & (int32_t)~names;
-      const float u = unordered(x), v = unordered(y);
-      const float margin = (fabsf(u) + fabsf(v)) * a.cut + kOff;
-      const bool near = scored ? !(u - v > margin) : x == y;
-      if ((uint32_t)j < k && i > j && keys[i] != kNone) close |= near;
+      for (int n = 0; n + 1 < kList; ++n)
+        if (n + j + 1 < N) list[n] = pop ? list[n + 1] : list[n];
+      if (pop) list[kList - 1] = INT32_MIN;
     }
 #pragma unroll
-    for (int j = 0; j + 2 < N; ++j) {
-      const int32_t x = keys[j] & (int32_t)~names, y = keys[j + 2] & (int32_t)~names;
-      const float u = unordered(x), v = unordered(y);
-      const float margin = (fabsf(u) + fabsf(v)) * a.cut + kOff;
-      const bool near = scored ? !(u - v > margin) : x == y;
-      if ((uint32_t)j + 1 == k && keys[j + 2] != kNone) slow |= near;
+    for (int h = 0; h < P::kEach; ++h) {
+      const bool some = (uint32_t)h * P::kLanes + t.sub % P::kLanes < k && place.id[h] >= kLowest;
+      place.id[h] = some ? (int32_t)(names - ((uint32_t)place.id[h] & names)) : (int32_t)a.E;
     }
-    slow |= close && scored && !kSigmoid;  // a softmax needs all of its logits
-    if (close && !slow) {
-      // the (k + 2)-th stays where it is
+    store_token<L, kSigmoid>(a, t.in, at, t.sub, mine && !doubt && !anew, place, top, total);
+    if constexpr (!kWhole) {
+      if (doubt || anew) {
+        if (k == 1) anew = true;  // no room for two keys
+        if (mine && t.sub == 0) {
+          a.experts[at * k] = anew ? kAnew : kSettle;
+          if (kSettled && !anew) {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if ((uint32_t)j > k) keys[j] = kNone;
-      settle<L, C, kSigmoid, N>(a, t, scored, names, keys);
-    }
-    typedef Places<L> P;
-    constexpr int kLanes = P::kLanes, kEach = P::kEach;
-    P place;
-    int32_t(&id)[kEach] = place.id;
-#pragma unroll
-    for (int h = 0; h < kEach; ++h) {
-      id[h] = (int32_t)a.E;
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (h * kLanes + (int)t.sub % kLanes == j && (uint32_t)j < k && keys[j] != kNone)
-          id[h] = (int32_t)(names - ((uint32_t)keys[j] & names));
-    }
-    if (slow) choose_slowly<L, C, kSigmoid>(a, t, scored, s_c, place);
-    // the weights
-    float l[kEach], u[kEach], m = -INFINITY, sum = 0.0f;
-#pragma unroll
-    for (int h = 0; h < kEach; ++h) l[h] = t.in[min((uint32_t)id[h], a.E - 1)];
-#pragma unroll
-    for (int h = 0; h < kEach; ++h) {
-      l[h] = id[h] < (int32_t)a.E ? usable(l[h]) : -INFINITY;
-      m = fmaxf(m, l[h]);
-    }
-    m = lanes_max<kLanes>(m);
-    if constexpr (kSigmoid) m = a.renorm ? fminf(m, 0.0f) : 0.0f;
-    else m = a.renorm ? m : top;
-#pragma unroll
-    for (int h = 0; h < kEach; ++h) {
-      u[h] = 0.0f;
-      if (l[h] != -INFINITY) {
-        // s e^-m with m = min(0, the largest logit) keeps the ratios of scores that underflow
-        if constexpr (kSigmoid) u[h] = expf(fminf(l[h], 0.0f) - m) / (1.0f + expf(-fabsf(l[h])));
-        else u[h] = expf(l[h] - m);
+            for (int j = 0; j < N - 1; ++j)
+              if ((uint32_t)j <= k) {
+                int32_t* to = (uint32_t)j + 1 < k ? a.experts + at * k + j + 1 : reinterpret_cast<int32_t*>(a.weights) + at * k + j + 1 - k;
+                *to = keys[j];
+              }
+          }
+        }
       }
-      sum += u[h];
-    }
-    sum = lanes_sum<kLanes>(sum);
-    const float by = a.renorm ? sum : total;
+    } else {
+      if ((doubt || anew) && mine && t.sub == 0) {
+        s_list[anew][atomicAdd(&s_listed[anew], 1u)] = (uint8_t)row;
+        if constexpr (kSettled) {
 #pragma unroll
-    for (int h = 0; h < kEach; ++h) {
-      const uint32_t j = h * kLanes + t.sub;
-      if (t0 + row < a.tokens && t.sub < (uint32_t)kLanes && j < k) {
-        a.experts[at * k + j] = id[h];
-        a.weights[at * k + j] = id[h] < (int32_t)a.E ? a.scale * (u[h] / by) : 0.0f;
+          for (int j = 0; j < N; ++j) s_key[row][j] = keys[j];
+        }
       }
+      __syncthreads();
+      const uint32_t settled = s_listed[0], again = s_listed[1];
+      __syncthreads();  // before the next tokens are listed
+      if (settled | again) {
+        if constexpr (kSettled) {
+          for (uint32_t i = threadIdx.x / 16; i < settled; i += kThreads / 16)
+            settle<kSigmoid>(a, t0 + s_list[0][i], s_key[s_list[0][i]][min(threadIdx.x & 15, k)]);
+        }
+        for (uint32_t i = threadIdx.x / 64; i < again; i += kThreads / 64)
+          route_exactly<kSigmoid>(a, t0 + s_list[1][i], s_c[kScored ? threadIdx.x / 64 : 0]);
+        __syncthreads();
+        if (threadIdx.x < 2) s_listed[threadIdx.x] = 0;
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// The tokens that k_route left, out of 64 a wave.
+template <bool kSigmoid>
+__global__ __launch_bounds__(kThreads) void k_route_rest(RouteArgs a) {
+  __shared__ double s_c[kThreads / 64][kMaxRouteExperts];
+  const uint32_t lane = threadIdx.x & 63, w = threadIdx.x / 64;
+  for (uint64_t t0 = ((uint64_t)blockIdx.x * (kThreads / 64) + w) * 64; t0 < a.tokens; t0 += (uint64_t)gridDim.x * kThreads) {
+    const int32_t place = t0 + lane < a.tokens ? a.experts[(t0 + lane) * a.k] : 0;
+    uint64_t settled = __ballot(place == kSettle), again = __ballot(place == kAnew);
+    while (settled) {  // four at a time, 16 lanes each
+      int mine = -1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if ((int)lane / 16 == g && settled) mine = __builtin_ctzll(settled);
+        settled &= settled - 1;
+      }
+      if (mine >= 0) {
+        const uint64_t at = t0 + mine;
+        const uint32_t j = min(lane & 15, a.k);
+        const int32_t* from = j + 1 < a.k ? a.experts + at * a.k + j + 1 : reinterpret_cast<const int32_t*>(a.weights) + at * a.k + j + 1 - a.k;
+        settle<kSigmoid>(a, at, *from);
+      }
+    }
+    while (again) {
+      const int mine = __builtin_ctzll(again);
+      again &= again - 1;
+      route_exactly<kSigmoid>(a, t0 + mine, s_c[w]);
     }
   }
 }
@@ -474,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
 template <int L, bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
   constexpr int kRows = kThreads / L;
-  const int sub = threadIdx.x % L, row = threadIdx.x / L;
+  const uint32_t sub = threadIdx.x % L, row = threadIdx.x / L;
   const int base = (threadIdx.x & 63) / L * L;
   for (uint64_t t0 = (uint64_t)blockIdx.x * kRows; t0 < a.tokens; t0 += (uint64_t)gridDim.x * kRows) {
     const uint64_t t = t0 + row;
@@ -482,7 +557,7 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
     const float* in = a.logits + (t < a.tokens ? t : 0) * a.E;
     int id = -1;
     float g = 0.0f, l = -INFINITY;
-    if (live && (uint32_t)sub < a.k) {
+    if (live && sub < a.k) {
       id = a.experts[t * a.k + sub];
       if ((uint32_t)id < a.E) {
         l = usable(in[id]);
@@ -523,15 +598,24 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
       const int e = __shfl(id, base + (int)j);
       const float x = __shfl(u, base + (int)j);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) d[v] += e == 4 * sub + v ? x : 0.0f;
+      for (int v = 0; v < 4; ++v) d[v] += e == (int)(4 * sub + v) ? x : 0.0f;
     }
-    if (t < a.tokens) {
+    if (t >= a.tokens) continue;
+    float* out = a.dlogits + t * a.E + 4 * sub;
+    if (a.E % 4 == 0) {
+      typedef float At __attribute__((ext_vector_type(4), aligned(4)));
+      typedef float Vec __attribute__((ext_vector_type(4)));
+      Vec r = {d[0], d[1], d[2], d[3]};
+      if (4 * sub < a.E) {
+        if (a.add) r += *reinterpret_cast<const At*>(a.add + t * a.E + 4 * sub);
+        __builtin_nontemporal_store(live ? r : Vec{}, reinterpret_cast<At*>(out));
+      }
+    } else {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t e = 4 * sub + v;
-        if (e >= a.E) continue;
-        if (a.add && live) d[v] += a.add[t * a.E + e];
-        a.dlogits[t * a.E + e] = live ? d[v] : 0.0f;
+      for (uint32_t v = 0; v < 4; ++v) {
+        if (4 * sub + v >= a.E) continue;
+        if (a.add) d[v] += a.add[t * a.E + 4 * sub + v];
+        out[v] = live ? d[v] : 0.0f;
       }
     }
   }
@@ -581,27 +665,39 @@ RouteArgs args(const pw_route_desc& d, const pw_route_io& io) {
   return a;
 }
 
-template <int L, int C, int K, bool kSigmoid>
+template <int L, int C, int K, bool kSigmoid, bool kWhole>
 void launch_route_k(const RouteArgs& a, hipStream_t s) {
   constexpr uint32_t R = kThreads / L;
-  const uint32_t lds = a.by_group ? R * a.E * sizeof(double) : 0;
-  hipLaunchKernelGGL((k_route<L, C, K, kSigmoid>), dim3(std::min((a.tokens + R - 1) / R, kMaxGrid)), dim3(kThreads), lds, s, a);
+  const dim3 grid(std::min((a.tokens + R - 1) / R, kMaxGrid));
+  if (a.bias || a.by_group)
+    hipLaunchKernelGGL((k_route<L, C, K, kSigmoid, true, kWhole>), grid, dim3(kThreads), a.by_group ? R * a.E * sizeof(float) : 0, s, a);
+  else
+    hipLaunchKernelGGL((k_route<L, C, K, kSigmoid, false, kWhole>), grid, dim3(kThreads), 0, s, a);
 }
 
-template <int L, int C, bool kSigmoid>
+template <int L, int C, bool kSigmoid, bool kWhole>
 void launch_route_lanes(const RouteArgs& a, hipStream_t s) {
-  if (a.k <= 2) launch_route_k<L, C, 2, kSigmoid>(a, s);
-  else if (a.k <= 4) launch_route_k<L, C, 4, kSigmoid>(a, s);
-  else if (a.k <= 6) launch_route_k<L, C, 6, kSigmoid>(a, s);
-  else launch_route_k<L, C, 8, kSigmoid>(a, s);
+  if (a.k <= 2) launch_route_k<L, C, 2, kSigmoid, kWhole>(a, s);
+  else if (a.k <= 4) launch_route_k<L, C, 4, kSigmoid, kWhole>(a, s);
+  else if (a.k <= 6) launch_route_k<L, C, 6, kSigmoid, kWhole>(a, s);
+  else launch_route_k<L, C, 8, kSigmoid, kWhole>(a, s);
 }
 
 template <bool kSigmoid>
-void launch_route(const RouteArgs& a, hipStream_t s) {
-  const bool many = a.tokens >= kManyTokens;
-  if (a.E <= 16) launch_route_lanes<4, 1, kSigmoid>(a, s);
-  else if (a.E <= 64) many ? launch_route_lanes<4, 4, kSigmoid>(a, s) : launch_route_lanes<16, 1, kSigmoid>(a, s);
-  else many ? launch_route_lanes<16, 4, kSigmoid>(a, s) : launch_route_lanes<64, 1, kSigmoid>(a, s);
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  if (a.E <= 16 || (uint64_t)a.tokens * a.E < kManyLogits) {
+    if (a.E <= 16) launch_route_lanes<4, 1, kSigmoid, true>(a, s);
+    else if (a.E <= 64) launch_route_lanes<16, 1, kSigmoid, true>(a, s);
+    else launch_route_lanes<64, 1, kSigmoid, true>(a, s);
+    return hipGetLastError();
+  }
+  if (a.E <= 64) launch_route_lanes<4, 4, kSigmoid, false>(a, s);
+  else launch_route_lanes<16, 4, kSigmoid, false>(a, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const uint32_t blocks = (a.tokens + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL(k_route_rest<kSigmoid>, dim3(std::min(blocks, kMaxGrid)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int L, bool kSigmoid>
@@ -636,8 +732,7 @@ extern "C" int pw_route(const pw_route_desc* d, const pw_route_io* io, void* str
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if ((st = check_stream(s))) return st;
   const RouteArgs a = args(*d, *io);
-  d->score == PW_SCORE_SIGMOID ? launch_route<true>(a, s) : launch_route<false>(a, s);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = d->score == PW_SCORE_SIGMOID ? launch_route<true>(a, s) : launch_route<false>(a, s);
   return e == hipSuccess ? PW_OK : hip_fail(e, "launch route");
 }
 

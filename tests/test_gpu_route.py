@@ -27,7 +27,10 @@ CASES = [(1, 2, 1, False, False, 1, 1, 2, True, False), (1, 256, 8, True, True, 
          (255, 130, 1, True, True, 2, 1, 2, False, False), (300, 16, 4, False, False, 16, 5, 2, True, True),
          (999, 5, 2, False, False, 1, 1, 2, False, True), (1000, 128, 6, True, True, 4, 2, 2, True, True),
          (1500, 33, 7, True, False, 3, 2, 2, True, False), (2000, 64, 2, False, False, 1, 1, 2, True, True),
-         (4099, 12, 5, True, True, 6, 4, 1, True, False), (5000, 3, 3, True, True, 1, 1, 2, True, True)]
+         (4099, 12, 5, True, True, 6, 4, 1, True, False), (5000, 3, 3, True, True, 1, 1, 2, True, True),
+         (16384, 64, 6, True, True, 1, 1, 2, True, True), (17001, 30, 3, False, False, 5, 2, 2, False, False),
+         (16500, 9, 1, True, True, 1, 1, 2, True, False), (20001, 200, 8, True, True, 8, 3, 2, True, True),
+         (16999, 256, 4, False, True, 1, 1, 2, True, False), (16400, 13, 7, True, False, 1, 1, 2, False, True)]
 
 
 def make(T, E, k, bias, masked, seed=0):
@@ -85,7 +88,7 @@ def test_choice_weights_and_gradient(gpu, T, E, k, sigmoid, bias, groups, top_gr
 
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("E,groups,top_groups", [(8, 1, 1), (64, 8, 3), (256, 16, 5), (100, 4, 2)])
-@pytest.mark.parametrize("T", [40, 3000])
+@pytest.mark.parametrize("T", [40, 3000, 16500])
 def test_equal_scores_take_the_lowest_index(gpu, sigmoid, E, groups, top_groups, T):
     rng = np.random.default_rng(E)
     k = min(8, E // groups * top_groups)
@@ -98,7 +101,7 @@ def test_equal_scores_take_the_lowest_index(gpu, sigmoid, E, groups, top_groups,
 
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("E", [6, 64, 200])
-@pytest.mark.parametrize("T", [50, 2500])
+@pytest.mark.parametrize("T", [50, 2500, 16400])
 def test_scores_that_differ_in_their_last_bits(gpu, sigmoid, E, T):
     """Neighbouring fp32 logits and biases: sums that fp32 cannot tell apart."""
     rng = np.random.default_rng([E, sigmoid])
@@ -142,7 +145,7 @@ def other_group(experts, l, b, k, sigmoid):
 
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
-@pytest.mark.parametrize("E,pad", [(8, 0), (8, 2500), (96, 0), (96, 2500)])
+@pytest.mark.parametrize("E,pad", [(8, 0), (8, 2500), (96, 0), (96, 2500), (8, 16384), (40, 16384), (96, 16384)])
 def test_masked_and_infinite_logits(gpu, sigmoid, renorm, E, pad):
     """Rows whose mask leaves nothing, or fewer than k; the lowest value; NaN and infinities; padding that holds anything."""
     k, inf, low = 3, np.inf, np.finfo(np.float32).min
