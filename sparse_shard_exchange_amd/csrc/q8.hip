@@ -578,7 +578,7 @@ __device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>&
 template <typename P, typename T, bool kGelu>
 __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ float s_scale[P::BM], s_ws[P::BN];
+  __shared__ float s_scale[(P::BM + 63) / 64 * 64], s_ws[P::BN];
   __shared__ int64_t s_out[P::BM];
   constexpr int NT = P::NT * P::KS;
   for (uint64_t b = blockIdx.x;; b += gridDim.x) {
@@ -601,7 +601,7 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
     for (int i = 0; i < P::LB; ++i) f.b[i] += first * P::D;
     // the scales before the stages: who waits for a stage has waited for them
     const int wave = tid / 64;
-    for (int c = wave; c < P::BM / 64; c += NT / 64)
+    for (int c = wave; c < (P::BM + 63) / 64; c += NT / 64)
       load_words(a.q_scale + row_of(a, g.row0 + min((uint32_t)(64 * c + lane), g.rows - 1)).in, s_scale + 64 * c);
     for (int c = wave; c < P::BN / 64; c += NT / 64)
       load_words(a.w_scale + (uint64_t)g.e * a.n + min(g.col0 + 64 * c + lane, a.n - 1), s_ws + 64 * c);
@@ -1006,6 +1006,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<128, 128, 2, 2, 64, 4> Square;
   typedef Shape<64, 64, 2, 2, 64, 4> Small;
   typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
+  typedef Shape<32, 64, 1, 2, 128, 5> Flat;
   if (a.x) return launch_few_rows<T, kGelu, 1, true>(a, s);
   // tiles of a height and width that there will be about, half of each expert's last one empty
   auto tiles = [&](uint32_t m, uint32_t n) {
@@ -1016,6 +1017,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   if (each >= 512 && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 256) >= 384) return launch_tile<Middle, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 128) >= 256) return launch_tile<Square, T, kGelu>(a, s);
+  if (a.E > 1 && a.stride >= 2048 && each < 32 && tiles(32, 64) >= 512) return launch_tile<Flat, T, kGelu>(a, s);
   if (tiles(64, 64) <= 256 && a.stride >= 2048) return launch_tile<Parted, T, kGelu>(a, s);
   return launch_tile<Small, T, kGelu>(a, s);
 }

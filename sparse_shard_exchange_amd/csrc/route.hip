@@ -91,8 +91,15 @@ __device__ __forceinline__ int32_t across_int(int32_t v) {
 }
 template <int L, int M = 1>
 __device__ __forceinline__ int32_t lanes_max_int(int32_t v) {
-  if constexpr (M < L) return lanes_max_int<L, 2 * M>(max(v, across_int<M>(v)));
-  return v;
+  if constexpr (M >= L) return v;
+  else if constexpr (M < 16) return lanes_max_int<L, 2 * M>(max(v, across_int<M>(v)));
+  else if constexpr (M == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // rows 0 0 2 2 and 1 1 3 3
+    return lanes_max_int<L, 32>(max((int32_t)r[0], (int32_t)r[1]));
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max((int32_t)r[0], (int32_t)r[1]);
+  }
 }
 template <int L, int M = 1>
 __device__ __forceinline__ uint32_t lanes_or(uint32_t v) {
@@ -150,21 +157,28 @@ struct Token {
 template <int L, typename F>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, uint32_t sub, F margin, bool* close) {
   constexpr int kEach = L >= (int)kMaxGroups ? 1 : (int)kMaxGroups / L;  // groups of a lane
+  constexpr int kShare = L > (int)kMaxGroups ? L / (int)kMaxGroups : 1;   // neighbouring lanes of a group
   const uint32_t size = a.E / a.groups;
   const F low = -(F)INFINITY;
   F mark[kEach];
 #pragma unroll
   for (int h = 0; h < kEach; ++h) {
-    const uint32_t g = h * L + sub;
+    const uint32_t g = (h * L + sub) / kShare;
     F m1 = low, m2 = low;
     if (g < a.groups) {
-      uint32_t at = g % size;  // lanes begin in different banks
-      for (uint32_t i = 0; i < size; ++i) {
+      uint32_t at = (g + sub % kShare) % size;  // lanes begin in different banks
+      for (uint32_t i = sub % kShare; i < size; i += kShare) {
         const F x = c[g * size + at];
-        at = at + 1 == size ? 0 : at + 1;
+        at = at + kShare < size ? at + kShare : at + kShare - size;
         m2 = max(m2, min(m1, x));
         m1 = max(m1, x);
       }
+    }
+#pragma unroll
+    for (int m = 1; m < kShare; m *= 2) {
+      const F o1 = __shfl_xor(m1, m), o2 = __shfl_xor(m2, m);
+      m2 = max(max(m2, o2), min(m1, o1));
+      m1 = max(m1, o1);
     }
     mark[h] = a.group_best == 2 && m2 > low ? m1 + m2 : m1;
   }
@@ -175,14 +189,14 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, 
 #pragma unroll
     for (int h = 1; h < kEach; ++h)
       if (g / L == (uint32_t)h) m = mark[h];
-    m = __shfl(m, base + (int)(g % L));
+    m = __shfl(m, base + (int)(g * kShare % L));
 #pragma unroll
-    for (int h = 0; h < kEach; ++h) better[h] += m > mark[h] || (m == mark[h] && g < h * L + sub);
+    for (int h = 0; h < kEach; ++h) better[h] += m > mark[h] || (m == mark[h] && g < (h * L + sub) / kShare);
   }
   F least = (F)INFINITY, most = low;  // of the kept, of the left
 #pragma unroll
   for (int h = 0; h < kEach; ++h) {
-    const uint32_t g = h * L + sub;
+    const uint32_t g = (h * L + sub) / kShare;
     const bool keep = g < a.groups && better[h] < a.top_groups;
     kept |= keep ? 1u << g : 0u;
     if (keep) least = min(least, mark[h]);

@@ -133,7 +133,11 @@ CASES = [(1, 1, 1, 1, 1, "even", True, False, False, "f32"), (1, 8, 16, 64, 64, 
          (700, 4, 2, 128, 128, "one", True, False, False, "bf16"), (1025, 1, 1, 640, 512, "even", False, False, True, "bf16"),
          (1500, 2, 4, 320, 513, "skewed", True, False, False, "bf16"), (1111, 2, 6, 130, 520, "padded", False, True, False, "f32"),
          (2048, 2, 3, 256, 768, "padded", True, True, True, "bf16"), (4000, 1, 1, 448, 250, "even", False, False, False, "bf16"),
-         (3000, 2, 8, 512, 512, "skewed", True, False, True, "bf16")]
+         (3000, 2, 8, 512, 512, "skewed", True, False, True, "bf16"),
+         (40, 8, 64, 2100, 600, "skewed", True, False, True, "bf16"), (60, 4, 40, 4096, 777, "padded", False, True, False, "f32"),
+         (30, 1, 1, 4000, 700, "even", False, False, False, "bf16"), (90, 2, 3, 2048, 128, "padded", True, False, True, "bf16"),
+         (8, 1, 1, 4096, 300, "even", False, False, True, "f32"), (2, 4, 8, 1500, 100, "even", True, False, False, "bf16"),
+         (4, 2, 6, 2500, 96, "one", False, True, True, "bf16"), (600, 1, 1, 1000, 2000, "even", False, False, True, "bf16")]
 
 
 @pytest.mark.parametrize("T,k,E,d,n,kind,gather,scatter,act,dtype", CASES)
