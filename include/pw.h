@@ -664,7 +664,8 @@ typedef struct {
   const int8_t* w;           /* [E][n][PW_Q8_ROW(d)], zeros behind the d-th     */
   const float* w_scale;      /* [E][n]                                          */
   const int64_t* offsets;    /* [E + 1] ascending (one below an earlier one counts as
-                                that); nullable if num_experts == 1             */
+                                that, one above the last as the last); nullable if
+                                num_experts == 1                                */
   const int32_t* src_index;  /* [rows] (with gather or scatter)                 */
   void* out;                 /* [rows][n]                                       */
 } pw_q8_io;

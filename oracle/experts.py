@@ -133,7 +133,7 @@ def product(q, q_scale, w, w_scale, offsets, src_index, rows, gather=0, scatter=
     E, n, _ = w.shape
     out = np.zeros((rows, n)) if out is None else out.astype(np.float64).copy()
     pre = np.zeros((rows, n))
-    bounds = [0, rows] if offsets is None else np.maximum.accumulate(np.clip(offsets, 0, rows))
+    bounds = [0, rows] if offsets is None else np.maximum.accumulate(np.clip(offsets, 0, min(rows, max(0, offsets[E]))))
     most = min(rows, 1 << 31) if not gather else q.shape[0] * gather if not scatter else min(rows, q.shape[0] * gather)
     for e in range(E):
         i = np.arange(bounds[e], bounds[e + 1])

@@ -240,7 +240,7 @@ __device__ __forceinline__ Piece piece_of(const Q8Args& a, uint64_t b) {
   }
   constexpr uint32_t kChunks = kMaxQ8Experts / 64;
   const uint32_t lane = threadIdx.x & 63;
-  const int64_t most = a.rows;
+  const int64_t most = min(max(a.offsets[a.E], (int64_t)0), (int64_t)a.rows);  // no row lies behind offsets[E]
   // the rows where the lane's experts (64 c + lane) begin and end, and the blocks up to theirs
   uint32_t begin[kChunks], end[kChunks], upto[kChunks];
   uint32_t from = (uint32_t)min(max(a.offsets[0], (int64_t)0), most), done = 0;
@@ -311,7 +311,8 @@ __device__ __forceinline__ float finish(int sum, float s, float ws) {
   else return 0.5f * z * erfcf(z * -0.70710678f);
 }
 
-// 16 neighbouring results of a row, rounded, in vectors of 16 bytes.
+// A lane's 16 results of 32 columns of a row, rounded, in runs of 16 bytes: every
+// other one, the rest is the other half wave's.
 template <typename T>
 struct Run {
   static constexpr int V = 16 / sizeof(T);
@@ -320,22 +321,23 @@ struct Run {
   Vec v[16 / V];
 };
 
-// Scale, activation and the one rounding.
+// Scale, activation and the one rounding; ws: of the lane's first column.
 template <typename T, bool kGelu>
 __device__ __forceinline__ Run<T> finish_run(const i32x16& acc, float s, const float* ws) {
+  constexpr int V = Run<T>::V;
   Run<T> r;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) r.v[e / Run<T>::V][e % Run<T>::V] = (T)finish<T, kGelu>(acc[e], s, ws[e]);
+  for (int e = 0; e < 16; ++e) r.v[e / V][e % V] = (T)finish<T, kGelu>(acc[e], s, ws[e / V * 2 * V + e % V]);
   return r;
 }
 
-// Stores a run to columns c on of a row of n (0: it is not stored).
+// Stores a lane's results of 32 columns, its first one c, of a row of n (0: it is not stored).
 template <typename T>
 __device__ __forceinline__ void store_run(const Run<T>& r, T* row, uint32_t c, uint32_t n) {
   constexpr int V = Run<T>::V;
 #pragma unroll
   for (int p = 0; p < 16 / V; ++p) {
-    const uint32_t at = c + p * V;
+    const uint32_t at = c + p * 2 * V;
     if (at + V <= n) {
       *reinterpret_cast<typename Run<T>::At*>(row + at) = r.v[p];
     } else {
@@ -374,11 +376,14 @@ __device__ __forceinline__ int slot_of(int c, int row) {
   return c ^ (P::D == 64 ? row >> 2 & 3 : row >> 1 & 7);
 }
 
-// Column of a tile that row r of B's LDS block holds: inside 32 columns the
-// order that leaves a lane with 16 neighbouring columns of its row in the
-// accumulators (register 4 q + e of lane l is MFMA row 8 q + 4 (l / 32) + e).
+// Column of a tile that row r of B's LDS block holds. Register 4 q + e of lane l is
+// MFMA row 8 q + 4 (l / 32) + e; of each 32 columns a lane gets the runs of V (16
+// bytes of results) that begin at V (l / 32), so that one store instruction writes
+// 32 neighbouring bytes of every row.
+template <int V>
 __device__ __forceinline__ int column_of(int r) {
-  return (r & ~31) | (r >> 2 & 1) << 4 | (r >> 3 & 3) << 2 | (r & 3);
+  if constexpr (V == 4) return r;
+  return (r & ~15) | (r >> 2 & 1) << 3 | (r >> 3 & 1) << 2 | (r & 3);
 }
 
 // What one lane loads: the chunk of its rows that its slot of each stage holds.
@@ -563,13 +568,13 @@ __device__ __forceinline__ void multiply_tile(const Feed<P>& f, unsigned char* l
 }
 
 // The lane's part of B's rows: of expert e, columns from col0 on.
-template <typename P>
+template <typename P, int V>
 __device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>& f) {
   const uint32_t tid = mm::opaque_tid(), lane = tid & 63, w = wave_of<P>(tid);
 #pragma unroll
   for (int i = 0; i < P::LB; ++i) {
     const uint32_t r = (w * P::LB + i) * P::kRows + lane / P::kChunks;
-    const uint32_t c = min(g.col0 + column_of((int)r), a.n - 1);
+    const uint32_t c = min(g.col0 + column_of<V>((int)r), a.n - 1);
     f.b[i] = a.w + ((uint64_t)g.e * a.n + c) * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
   }
 }
@@ -596,7 +601,7 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
       row[i] = row_of(a, g.row0 + min(r, g.rows - 1));
       f.a[i] = a.q + (uint64_t)row[i].in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4) + first * P::D;
     }
-    feed_b<P>(a, g, f);
+    feed_b<P, Run<T>::V>(a, g, f);
 #pragma unroll
     for (int i = 0; i < P::LB; ++i) f.b[i] += first * P::D;
     // the scales before the stages: who waits for a stage has waited for them
@@ -643,7 +648,6 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
           }
       }
     }
-    // the lane holds 16 neighbouring columns of a row in each block
     T* out = static_cast<T*>(a.out);
     if (P::KS == 1 || group == 0) {
 #pragma unroll
@@ -653,7 +657,7 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
         const float s = s_scale[r];
 #pragma unroll
         for (int j = 0; j < P::NI; ++j) {
-          const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
+          const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + Run<T>::V * (lane >> 5);
           store_run<T>(finish_run<T, kGelu>(acc[i][j], s, s_ws + c), out + (uint64_t)o * a.n, g.col0 + c, o < 0 ? 0u : a.n);
         }
       }
@@ -670,13 +674,13 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
 template <uint32_t M>
 __device__ __forceinline__ uint32_t list_blocks(const Q8Args& a, uint32_t* s_begin, uint32_t* s_upto) {
   const uint32_t lane = threadIdx.x & 63;
-  const int64_t most = a.rows;
   if (!a.offsets) {
     const uint32_t blocks = (a.rows + M - 1) / M;
     s_upto[lane] = lane ? ~0u : blocks;
     if (lane < 2) s_begin[lane] = lane * a.rows;
     return blocks;
   }
+  const int64_t most = min(max(a.offsets[a.E], (int64_t)0), (int64_t)a.rows);
   uint32_t from = (uint32_t)min(max(a.offsets[0], (int64_t)0), most), done = 0;
   if (lane == 0) s_begin[0] = from;
   for (uint32_t e0 = 0; e0 < a.E; e0 += 64) {
@@ -763,7 +767,7 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
       const uint32_t r = (w * P::LA + i) * P::kRows + lane / P::kChunks;
       f.a[i] = a.q + (uint64_t)row_at(g, ids, r).in * a.stride + (slot_of<P>(lane % P::kChunks, (int)r) << 4);
     }
-    feed_b<P>(a, g, f);
+    feed_b<P, Run<T>::V>(a, g, f);
 #pragma unroll
     for (uint32_t s = 0; s < P::S; ++s) load_stage<P>(f, min(s, stages - 1), a.stride, lds + s * P::kStage);
   };
@@ -796,7 +800,7 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
       const float s = s_scale[turn][r];
 #pragma unroll
       for (int j = 0; j < P::NI; ++j) {
-        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + 16 * (lane >> 5);
+        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + Run<T>::V * (lane >> 5);
         const Run<T> run = finish_run<T, kGelu>(acc[i][j], s, &s_scale[turn][P::BM + c]);
         if (i < H) {
           first[i][j] = run;
@@ -810,7 +814,7 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
           const uint32_t n = r0 < g.rows && row.out >= 0 ? a.n : 0u;
 #pragma unroll
           for (int j0 = i == H - 1 ? 0 : j; j0 <= j; ++j0) {
-            const uint32_t c0 = w % P::WN * (P::BN / P::WN) + 32 * j0 + 16 * (lane >> 5);
+            const uint32_t c0 = w % P::WN * (P::BN / P::WN) + 32 * j0 + Run<T>::V * (lane >> 5);
             store_run<T>(i0 < H ? first[i0 < H ? i0 : 0][j0] : run, out + (uint64_t)row.out * a.n, g.col0 + c0, n);
           }
         }
@@ -823,6 +827,11 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
   }
 }
 
+// More LDS than 64 KiB has to be asked for.
+hipError_t allow_lds(const void* kernel, uint32_t bytes) {
+  return bytes > 60 * 1024 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : hipSuccess;
+}
+
 template <typename P, typename T, bool kGelu>
 hipError_t launch_stay(Q8Args a, hipStream_t s) {
   a.col_tiles = (a.n + P::BN - 1) / P::BN;
@@ -830,8 +839,7 @@ hipError_t launch_stay(Q8Args a, hipStream_t s) {
   int device = 0, cus = 0;
   hipError_t e = hipGetDevice(&device);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
-  if (e == hipSuccess)
-    e = hipFuncSetAttribute((const void*)k_q8_stay<P, T, kGelu>, hipFuncAttributeMaxDynamicSharedMemorySize, P::kLds);
+  if (e == hipSuccess) e = allow_lds((const void*)k_q8_stay<P, T, kGelu>, P::kLds);
   if (e != hipSuccess) return e;
   const uint32_t grid = (uint32_t)std::min<uint64_t>(tiles, std::max(8, cus / 8 * 8));
   hipLaunchKernelGGL((k_q8_stay<P, T, kGelu>), dim3(grid), dim3(P::NT), P::kLds, s, a);
@@ -843,161 +851,127 @@ hipError_t launch_tile(Q8Args a, hipStream_t s) {
   a.col_tiles = (a.n + P::BN - 1) / P::BN;
   const uint64_t blocks = a.offsets ? std::min<uint64_t>(a.rows, a.rows / P::BM + a.E) : ((uint64_t)a.rows + P::BM - 1) / P::BM;
   const uint32_t grid = (uint32_t)std::min<uint64_t>(blocks * a.col_tiles, kMaxGrid);
-  const hipError_t e = hipFuncSetAttribute((const void*)k_q8_tile<P, T, kGelu>, hipFuncAttributeMaxDynamicSharedMemorySize, P::kLds);
+  const hipError_t e = allow_lds((const void*)k_q8_tile<P, T, kGelu>, P::kLds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_q8_tile<P, T, kGelu>), dim3(grid), dim3(P::NT * P::KS), P::kLds, s, a);
   return hipGetLastError();
 }
 
-// ---- few rows: the weights pass through registers ------------------------------
+// ---- a few rows: the weights pass through registers ----------------------------
 
 // Each wave multiplies 16 columns of its expert's matrix, over one of KS parts of
-// their length, with up to 16 R rows: all 16 KiB of the matrix that it can hold
+// their length, with up to 16 rows: all 16 KiB of the matrix that it can hold
 // are on their way at once, and no other wave reads them. The parts' sums (whole
-// numbers: exact in any order) meet in LDS. kCode: x's rows themselves are given,
-// at most 16 of a workgroup; it makes their codes on the way.
+// numbers: exact in any order) meet in LDS. Every workgroup makes the codes of its
+// rows itself, while the matrix is on its way.
 constexpr int kHeld = 16;              // 64-byte steps of 16 columns in registers
 constexpr uint32_t kCodeWidth = 4096;  // of the rows that a workgroup codes: 8 chunks a lane
+constexpr uint32_t kFewRows = 8;       // of a call
 
-template <typename T, bool kGelu, int KS, int R, bool kCode>
+template <typename T, bool kGelu, int KS>
 __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
   constexpr int kGroups = 4 / KS;  // of 16 columns
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int32_t s_sum[KS > 1 ? KS : 1][16][20];  // [part][row][column]
-  __shared__ float s_scale[16];
+  __shared__ float s_scale[kFewRows];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   // every row's id at once with the segments: nothing else stands before the rows
-  const int32_t ids = kCode && a.src_index ? a.src_index[min((uint32_t)lane, a.rows - 1)] : 0;
-  auto row_at = [&](uint32_t i) { return kCode ? row_from(a, i, __shfl(ids, (int)i)) : row_of(a, i); };
-  const Piece g = piece_of<16 * R, 16 * kGroups>(a, blockIdx.x);
+  const int32_t ids = a.src_index ? a.src_index[min((uint32_t)lane, a.rows - 1)] : 0;
+  auto row_at = [&](uint32_t i) { return row_from(a, i, __shfl(ids, (int)i)); };  // by whole waves
+  const Piece g = piece_of<16, 16 * kGroups>(a, blockIdx.x);
   if (g.rows == 0) return;
   const int part = w % KS, group = w / KS;
   const uint32_t nk = a.stride / 64, each = (nk + KS - 1) / KS, k0 = min(part * each, nk), k1 = min(k0 + each, nk);
   const uint32_t chunk = lane / 16 * 16, pitch = a.stride + 16;  // (of the codes in LDS: rows in different banks)
 
   // the rows to be coded come first: nothing waits for the matrix before it has to
-  constexpr int kRowsEach = 4, kEach = kCodeWidth / 512;
-  typename Eight<T>::Vec v[kCode ? kEach : 1];
-  RowOf coded{};
-  if constexpr (kCode) {
-    coded = row_at(g.row0 + min((uint32_t)w, g.rows - 1));
+  constexpr int kEach = kCodeWidth / 512;
+  typename Eight<T>::Vec v[kEach];
+  auto load_row = [&](uint32_t r) {
+    const T* x = static_cast<const T*>(a.x) + (uint64_t)row_at(g.row0 + r).in * a.d;
 #pragma unroll
-    for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
-  }
+    for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(x, c * 64 + lane, a.d);
+  };
+  load_row(min((uint32_t)w, g.rows - 1));
   const uint32_t col0 = g.col0 + group * 16;
   const int8_t* pw = a.w + ((uint64_t)g.e * a.n + min(col0 + lane % 16, a.n - 1)) * a.stride + chunk;
   i32x4 b[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k0 + i, nk - 1) * 64);
-  RowOf row[R];
-#pragma unroll
-  for (int m = 0; m < R; ++m) row[m] = row_at(g.row0 + min((uint32_t)(16 * m + lane % 16), g.rows - 1));
-
-  if constexpr (kCode) {
 #pragma unroll 1
-    for (int i = 0; i < kRowsEach; ++i) {  // rows w, w + 4, ...
-      const uint32_t r = w + 4 * i;
-      if (r >= g.rows) break;
-      if (i > 0) {
-        coded = row_at(g.row0 + r);
+  for (uint32_t r = w; r < g.rows; r += 4) {
+    if (r >= 4) load_row(r);
+    uint32_t top = 0;
 #pragma unroll
-        for (int c = 0; c < kEach; ++c) v[c] = eight_of<T>(static_cast<const T*>(a.x) + (uint64_t)coded.in * a.d, c * 64 + lane, a.d);
-      }
-      uint32_t top = 0;
+    for (int c = 0; c < kEach; ++c) top = max(top, Eight<T>::top(v[c]));
 #pragma unroll
-      for (int c = 0; c < kEach; ++c) top = max(top, Eight<T>::top(v[c]));
+    for (int m = 1; m < 64; m *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    const CodeScale s = code_scale(top);
 #pragma unroll
-      for (int m = 1; m < 64; m *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-      const CodeScale s = code_scale(top);
-#pragma unroll
-      for (int c = 0; c < kEach; ++c)
-        if (512 * c + 8 * lane < a.stride) *reinterpret_cast<u32x2*>(lds + r * pitch + 512 * c + 8 * lane) = codes_of<T>(v[c], s);
-      if (lane == 0) s_scale[r] = s.scale;
-    }
-    __syncthreads();
+    for (int c = 0; c < kEach; ++c)
+      if (512 * c + 8 * lane < a.stride) *reinterpret_cast<u32x2*>(lds + r * pitch + 512 * c + 8 * lane) = codes_of<T>(v[c], s);
+    if (lane == 0) s_scale[r] = s.scale;
   }
+  __syncthreads();
 
-  i32x4 acc[R] = {};
+  i32x4 acc = {};
+  const unsigned char* from = lds + min((uint32_t)lane % 16, g.rows - 1) * pitch + chunk;
   for (uint32_t k = k0; k < k1; k += kHeld) {
     if (k > k0) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k + i, nk - 1) * 64);
     }
 #pragma unroll
-    for (int m = 0; m < R; ++m) {
-      if (16 * (uint32_t)m >= g.rows) break;
-      const unsigned char* from = kCode ? lds + min((uint32_t)lane % 16, g.rows - 1) * pitch
-                                        : reinterpret_cast<const unsigned char*>(a.q + (uint64_t)row[m].in * a.stride);
-      i32x4 x[kHeld];
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) x[i] = *reinterpret_cast<const i32x4*>(from + min(k + i, nk - 1) * 64 + chunk);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int keep = k + i < k1 ? ~0 : 0;  // the steps behind the part's last are zeros
-        acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], x[i] & keep, acc[m], 0, 0, 0);
-      }
+    for (int i = 0; i < kHeld; ++i) {
+      const int keep = k + i < k1 ? ~0 : 0;  // the steps behind the part's last are zeros
+      const i32x4 x = *reinterpret_cast<const i32x4*>(from + min(k + i, nk - 1) * 64) & keep;
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], x, acc, 0, 0, 0);
     }
   }
 
-  // the lane holds 4 columns from 4 (lane / 16) on of row 16 m + lane % 16
+  // the lane holds 4 columns from 4 (lane / 16) on of row lane % 16
   const float* ws = a.w_scale + (uint64_t)g.e * a.n;
+  T* out = static_cast<T*>(a.out);
+  if constexpr (KS == 1) {
+    const uint32_t r = lane % 16;
+    const RowOf to = row_at(g.row0 + min(r, g.rows - 1));
+    if (r < g.rows && to.out >= 0) {
 #pragma unroll
-  for (int m = 0; m < R; ++m) {
-    if (16 * (uint32_t)m >= g.rows) break;
-    if constexpr (KS == 1) {
-      const uint32_t r = 16 * m + lane % 16;
-      if (r < g.rows && row[m].out >= 0) {
-        const float s = kCode ? s_scale[r] : a.q_scale[row[m].in];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t c = col0 + lane / 16 * 4 + e;
-          if (c < a.n) static_cast<T*>(a.out)[(uint64_t)row[m].out * a.n + c] = (T)finish<T, kGelu>(acc[m][e], s, ws[c]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t c = col0 + lane / 16 * 4 + e;
+        if (c < a.n) out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(acc[e], s_scale[r], ws[c]);
       }
-    } else {
-      // one group of columns after the other: its parts' sums, then a thread for each result
-      for (int t = 0; t < kGroups; ++t) {
-        __syncthreads();
-        if (group == t) *reinterpret_cast<i32x4*>(&s_sum[part][lane % 16][lane / 16 * 4]) = acc[m];
-        __syncthreads();
-        const uint32_t r = 16 * m + threadIdx.x / 16, c = g.col0 + 16 * t + threadIdx.x % 16;
-        if (r < g.rows && c < a.n) {
-          const RowOf to = row_at(g.row0 + r);
-          int sum = 0;
+    }
+  } else {
+    // one group of columns after the other: its parts' sums, then a thread for each result
+    const uint32_t r = threadIdx.x / 16;
+    const RowOf to = row_at(g.row0 + min(r, g.rows - 1));
+    for (int t = 0; t < kGroups; ++t) {
+      __syncthreads();
+      if (group == t) *reinterpret_cast<i32x4*>(&s_sum[part][lane % 16][lane / 16 * 4]) = acc;
+      __syncthreads();
+      const uint32_t c = g.col0 + 16 * t + threadIdx.x % 16;
+      if (r < g.rows && c < a.n && to.out >= 0) {
+        int sum = 0;
 #pragma unroll
-          for (int p = 0; p < KS; ++p) sum += s_sum[p][threadIdx.x / 16][threadIdx.x % 16];
-          const float s = kCode ? s_scale[r] : a.q_scale[to.in];
-          if (to.out >= 0) static_cast<T*>(a.out)[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(sum, s, ws[c]);
-        }
+        for (int p = 0; p < KS; ++p) sum += s_sum[p][r][threadIdx.x % 16];
+        out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(sum, s_scale[r], ws[c]);
       }
     }
   }
 }
 
-template <typename T, bool kGelu, int KS, int R, bool kCode>
+template <typename T, bool kGelu, int KS>
 hipError_t launch_few(Q8Args a, hipStream_t s) {
   constexpr uint32_t N = 16 * (4 / KS);
   a.col_tiles = (a.n + N - 1) / N;
-  const uint64_t blocks = a.offsets ? std::min<uint64_t>(a.rows, a.rows / (16 * R) + a.E) : (a.rows + 16 * R - 1) / (16 * R);
-  const uint32_t lds = kCode ? 16 * (a.stride + 16) : 0;
-  if (kCode) {
-    const hipError_t e = hipFuncSetAttribute((const void*)k_q8_few<T, kGelu, KS, R, kCode>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             16 * (kCodeWidth + 16));
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((k_q8_few<T, kGelu, KS, R, kCode>), dim3((uint32_t)(blocks * a.col_tiles)), dim3(kThreads), lds, s, a);
+  const uint32_t blocks = a.offsets ? a.rows : 1, lds = kFewRows * (a.stride + 16);
+  hipLaunchKernelGGL((k_q8_few<T, kGelu, KS>), dim3(blocks * a.col_tiles), dim3(kThreads), lds, s, a);
   return hipGetLastError();
 }
 
-template <typename T, bool kGelu, int R, bool kCode>
-hipError_t launch_few_rows(const Q8Args& a, hipStream_t s) {
-  if (a.stride > 32 * 64) return launch_few<T, kGelu, 4, R, kCode>(a, s);
-  if (a.stride > 16 * 64) return launch_few<T, kGelu, 2, R, kCode>(a, s);
-  return launch_few<T, kGelu, 1, R, kCode>(a, s);
-}
-
 // Whether a product makes the codes of x itself, in one launch.
-bool codes_inside(uint32_t rows, uint32_t stride) { return rows <= 8 && stride <= kCodeWidth; }
+bool codes_inside(uint32_t rows, uint32_t stride) { return rows <= kFewRows && stride <= kCodeWidth; }
 
 template <typename T, bool kGelu>
 hipError_t launch_product(const Q8Args& a, hipStream_t s) {
@@ -1007,7 +981,10 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<64, 64, 2, 2, 64, 4> Small;
   typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
   typedef Shape<32, 64, 1, 2, 128, 5> Flat;
-  if (a.x) return launch_few_rows<T, kGelu, 1, true>(a, s);
+  if (a.x) {
+    if (a.stride > 32 * 64) return launch_few<T, kGelu, 4>(a, s);
+    return a.stride > 16 * 64 ? launch_few<T, kGelu, 2>(a, s) : launch_few<T, kGelu, 1>(a, s);
+  }
   // tiles of a height and width that there will be about, half of each expert's last one empty
   auto tiles = [&](uint32_t m, uint32_t n) {
     const uint64_t blocks = a.E > 1 ? std::min<uint64_t>(a.rows, a.rows / m + a.E / 2) : ((uint64_t)a.rows + m - 1) / m;

@@ -137,7 +137,8 @@ CASES = [(1, 1, 1, 1, 1, "even", True, False, False, "f32"), (1, 8, 16, 64, 64, 
          (40, 8, 64, 2100, 600, "skewed", True, False, True, "bf16"), (60, 4, 40, 4096, 777, "padded", False, True, False, "f32"),
          (30, 1, 1, 4000, 700, "even", False, False, False, "bf16"), (90, 2, 3, 2048, 128, "padded", True, False, True, "bf16"),
          (8, 1, 1, 4096, 300, "even", False, False, True, "f32"), (2, 4, 8, 1500, 100, "even", True, False, False, "bf16"),
-         (4, 2, 6, 2500, 96, "one", False, True, True, "bf16"), (600, 1, 1, 1000, 2000, "even", False, False, True, "bf16")]
+         (4, 2, 6, 2500, 96, "one", False, True, True, "bf16"), (2, 4, 8, 700, 9, "even", True, True, False, "bf16"),
+         (1, 7, 64, 1100, 37, "padded", True, False, True, "f32"), (8, 1, 3, 3000, 21, "skewed", False, True, False, "bf16"), (600, 1, 1, 1000, 2000, "even", False, False, True, "bf16")]
 
 
 @pytest.mark.parametrize("T,k,E,d,n,kind,gather,scatter,act,dtype", CASES)
@@ -201,12 +202,12 @@ def test_many_tiles(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
     assert bool((out[~seen] == 7.0).all()) and int(seen.sum()) == int(off[E])
 
 
-@pytest.mark.parametrize("n", [64, 130, 256])
+@pytest.mark.parametrize("n,T", [(64, 60), (130, 60), (256, 60), (21, 4), (4096, 4500)])
 @pytest.mark.parametrize("E", [3, 70])
-def test_offsets_and_indexes_that_are_none(gpu, n, E):
+def test_offsets_and_indexes_that_are_none(gpu, n, E, T):
     """Descending, negative and far offsets, ids outside the tuples: nothing out of range is read or written, no row twice."""
     rng = np.random.default_rng(n)
-    T, k, d = 60, 2, 96
+    k, d = 2, 96
     rows = T * k
     w, ws = weights(gpu, rng, E, n, d)
     x = rows_of(rng, T, d, "bf16")
@@ -215,7 +216,7 @@ def test_offsets_and_indexes_that_are_none(gpu, n, E):
     src[::7] = -1
     src[3::11] = 1 << 30
     src[4::13] = rows
-    for off in ([0, 50, 40, 200], [-5, 10, 100, 1 << 40], [60, 60, 60, 60]):
+    for off in ([0, 50, 40, 200], [-5, 10, 100, 1 << 40], [60, 60, 60, 60], [3, 100, 1 << 33, 7], [0, 5, rows + 9, -1]):
         off = np.array(off + [off[-1]] * (E - 3), np.int64)
         for gather, scatter in ((k, False), (k, True), (0, True)):
             xs = x if gather else np.concatenate([x, x])
@@ -378,10 +379,10 @@ def test_route_order_products_and_combine(gpu, T, E, k, d, hidden, masked):
     assert np.all(np.abs(out - want) <= (k + 2) * U * size + HALF["bf16"] * np.abs(want) * 1.01)
 
 
-def test_captured_with_the_exchange_and_replayed(gpu):
+@pytest.mark.parametrize("T,E,k,d,hidden", [(2, 16, 4, 128, 192), (24, 16, 4, 128, 192), (500, 4, 2, 128, 192), (9000, 3, 2, 128, 4096)])
+def test_captured_with_the_exchange_and_replayed(gpu, T, E, k, d, hidden):
     """The whole way in a graph, with the exchange's form that can be captured; and two objects in one graph."""
     rng = np.random.default_rng(9)
-    T, E, k, d, hidden = 24, 16, 4, 128, 192
     rows = T * k
     w1, s1 = (dev(t) for t in weights(gpu, rng, E, hidden, d))
     w2, s2 = (dev(t) for t in weights(gpu, rng, E, d, hidden))
