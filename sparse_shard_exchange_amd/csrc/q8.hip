@@ -978,6 +978,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<256, 256, 2, 4, 128, 2> Large;
   typedef Shape<128, 256, 2, 2, 64, 3> Middle;
   typedef Shape<128, 128, 2, 2, 64, 4> Square;
+  typedef Shape<64, 128, 2, 2, 128, 3> Long;
   typedef Shape<64, 64, 2, 2, 64, 4> Small;
   typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
   typedef Shape<32, 64, 1, 2, 128, 5> Flat;
@@ -993,6 +994,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   const uint64_t each = a.rows / a.E, large = tiles(256, 256);
   if (each >= 512 && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 256) >= 384) return launch_tile<Middle, T, kGelu>(a, s);
+  if (each >= 32 && a.stride >= 2048 && tiles(64, 128) >= 256) return launch_tile<Long, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 128) >= 256) return launch_tile<Square, T, kGelu>(a, s);
   if (a.E > 1 && a.stride >= 2048 && each < 32 && tiles(32, 64) >= 512) return launch_tile<Flat, T, kGelu>(a, s);
   if (tiles(64, 64) <= 256 && a.stride >= 2048) return launch_tile<Parted, T, kGelu>(a, s);

@@ -138,6 +138,7 @@ CASES = [(1, 1, 1, 1, 1, "even", True, False, False, "f32"), (1, 8, 16, 64, 64, 
          (30, 1, 1, 4000, 700, "even", False, False, False, "bf16"), (90, 2, 3, 2048, 128, "padded", True, False, True, "bf16"),
          (8, 1, 1, 4096, 300, "even", False, False, True, "f32"), (2, 4, 8, 1500, 100, "even", True, False, False, "bf16"),
          (4, 2, 6, 2500, 96, "one", False, True, True, "bf16"), (2, 4, 8, 700, 9, "even", True, True, False, "bf16"),
+         (2100, 1, 1, 2112, 1000, "even", False, False, True, "bf16"), (1000, 4, 20, 2304, 700, "skewed", False, True, False, "f32"),
          (1, 7, 64, 1100, 37, "padded", True, False, True, "f32"), (8, 1, 3, 3000, 21, "skewed", False, True, False, "bf16"), (600, 1, 1, 1000, 2000, "even", False, False, True, "bf16")]
 
 
