@@ -114,7 +114,7 @@ def quant(x):
     rows, d = x.shape
     x = x.astype(np.float32)
     with np.errstate(all="ignore"):
-        scale = np.abs(x).max(axis=1) / np.float32(127)
+        scale = np.abs(x).max(axis=1) * (np.float32(1) / np.float32(127))
         scale = np.where(np.isfinite(x).all(axis=1), scale, np.float32(np.nan)).astype(np.float32)
         some = scale > 0
         z = np.rint(x / np.where(some, scale, np.float32(1))[:, None]).clip(-127, 127)

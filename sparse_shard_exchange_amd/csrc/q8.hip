@@ -109,7 +109,7 @@ struct CodeScale {
   bool usual;  // codes() holds
 };
 __device__ __forceinline__ CodeScale code_scale(uint32_t top) {
-  const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) / 127.0f : NAN;
+  const float scale = top < 0x7f800000u ? __builtin_bit_cast(float, top) * (1.0f / 127.0f) : NAN;
   return {scale, 1.0f / scale, scale >= 0x1p-100f && scale <= 0x1p100f};
 }
 
