@@ -48,20 +48,6 @@ __device__ __forceinline__ float usable(float l) { return fminf(fmaxf(l, -INFINI
 // e^x for x up to 0: off by (1.5 |x| + 2) 2^-24 of itself.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-// Weights of the chosen logits: lane j of each aligned group of 8 lanes holds
-// the j-th (-infinity: no expert). u_j = s_j e^-m with m = min(0, the largest
-// logit) keeps the ratios of scores that underflow.
-template <bool kSigmoid>
-__device__ __forceinline__ float chosen_score(float l, bool renorm) {
-  float m = lanes_max<8>(l);
-  if (m == -INFINITY) return 0.0f;
-  if constexpr (kSigmoid) {
-    m = renorm ? fminf(m, 0.0f) : 0.0f;
-    return expf(fminf(l, 0.0f) - m) / (1.0f + expf(-fabsf(l)));
-  }
-  return expf(l - m);
-}
-
 // ---- the choice -------------------------------------------------------------------
 //
 // L lanes a token, C times four neighbouring experts a lane. The choice is that
@@ -560,33 +546,72 @@ __global__ __launch_bounds__(kThreads) void k_route_rest(RouteArgs a) {
   }
 }
 
+// ---- the gradient -----------------------------------------------------------------
+//
+// With v_j = s_ej / sum s over the chosen and g_j = scale dw_j:
+//   renorm:     dl_ej = v_j (g_j - sum_i g_i v_i), times 1 - s_ej for a sigmoid (the sum
+//               over the chosen drops out, so ratios that underflow keep their gradient)
+//   otherwise:  dl_ej = g_j s_ej (1 - s_ej) for a sigmoid,
+//               dl_e = s_e (sum of the g_j with e_j = e - sum_j g_j s_ej) for a softmax
+// L lanes a token, four neighbouring experts a lane.
 template <int L, bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
-  constexpr int kRows = kThreads / L;
+  typedef float At __attribute__((ext_vector_type(4), aligned(4)));
+  typedef float Vec __attribute__((ext_vector_type(4)));
+  constexpr int kRows = kThreads / L, kLanes = Places<L>::kLanes, kEach = Places<L>::kEach;
   const uint32_t sub = threadIdx.x % L, row = threadIdx.x / L;
   const int base = (threadIdx.x & 63) / L * L;
+  const bool whole = 4 * sub + 4 <= a.E;
   for (uint64_t t0 = (uint64_t)blockIdx.x * kRows; t0 < a.tokens; t0 += (uint64_t)gridDim.x * kRows) {
     const uint64_t t = t0 + row;
     const bool live = t < a.tokens && (!a.valid || a.valid[t]);
     const float* in = a.logits + (t < a.tokens ? t : 0) * a.E;
-    int id = -1;
-    float g = 0.0f, l = -INFINITY;
-    if (live && sub < a.k) {
-      id = a.experts[t * a.k + sub];
-      if ((uint32_t)id < a.E) {
-        l = usable(in[id]);
-        g = a.dweights[t * a.k + sub] * a.scale;
+    int id[kEach];
+    float g[kEach], l[kEach], u[kEach], m = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) {
+      const uint32_t j = h * kLanes + sub;
+      id[h] = -1;
+      g[h] = 0.0f, l[h] = -INFINITY;
+      if (live && sub < (uint32_t)kLanes && j < a.k) {
+        id[h] = a.experts[t * a.k + j];
+        if ((uint32_t)id[h] < a.E) {
+          l[h] = usable(in[id[h]]);
+          g[h] = a.dweights[t * a.k + j] * a.scale;
+        }
       }
+      if (l[h] == -INFINITY) g[h] = 0.0f;  // no expert
+      m = fmaxf(m, l[h]);
     }
-    float u = chosen_score<kSigmoid>(l, a.renorm), d[4] = {0, 0, 0, 0};
+    // s, or s e^-m with m = min(0, the largest logit): the ratios of scores that underflow
+    m = lanes_max<kLanes>(m);
+    if constexpr (kSigmoid) m = a.renorm ? fminf(m, 0.0f) : 0.0f;
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) {
+      u[h] = 0.0f;
+      if (l[h] == -INFINITY) continue;
+      if constexpr (kSigmoid) u[h] = expf(fminf(l[h], 0.0f) - m) / (1.0f + expf(-fabsf(l[h])));
+      else u[h] = expf(l[h] - m);
+    }
+    auto sum_of = [&](auto f) {
+      float s = 0.0f;
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) s += f(h);
+      return lanes_sum<kLanes>(s);
+    };
+    float d[4] = {0, 0, 0, 0};
     if (!kSigmoid && !a.renorm) {  // the softmax over all experts
       float x[4], top = -INFINITY, sum = 0.0f;
+      if (whole) {
+        const Vec q = *reinterpret_cast<const At*>(in + 4 * sub);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const uint32_t e = 4 * sub + v;
-        x[v] = live && e < a.E ? usable(in[e]) : -INFINITY;
-        top = fmaxf(top, x[v]);
+        for (int v = 0; v < 4; ++v) x[v] = live ? usable(q[v]) : -INFINITY;
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = live && 4 * sub + v < a.E ? usable(in[4 * sub + v]) : -INFINITY;
       }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) top = fmaxf(top, x[v]);
       top = lanes_max<L>(top);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -595,35 +620,44 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
       }
       sum = lanes_sum<L>(sum);
       const float inv = sum > 0 ? 1.0f / sum : 0.0f;
-      u = l == -INFINITY ? 0.0f : expf(l - top) * inv;
-      const float dot = __shfl(lanes_sum<8>(u * g), base);  // lanes from 8 on hold no expert
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) u[h] = l[h] == -INFINITY ? 0.0f : expf(l[h] - top) * inv * g[h];
+      const float dot = __shfl(sum_of([&](int h) { return u[h]; }), base);  // lanes from 8 on hold no expert
 #pragma unroll
       for (int v = 0; v < 4; ++v) d[v] = -x[v] * inv * dot;
-      u *= g;
     } else if (a.renorm) {
-      const float sum = lanes_sum<8>(u);
-      u = sum > 0 ? u / sum : 0.0f;
-      u *= g - lanes_sum<8>(u * g);
-      if constexpr (kSigmoid) u /= 1.0f + expf(l);
+      const float sum = sum_of([&](int h) { return u[h]; });
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) u[h] = sum > 0 ? u[h] / sum : 0.0f;
+      const float dot = sum_of([&](int h) { return u[h] * g[h]; });
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) {
+        u[h] *= g[h] - dot;
+        if constexpr (kSigmoid) u[h] /= 1.0f + expf(l[h]);
+      }
     } else {
-      u *= g / (1.0f + expf(l));
+#pragma unroll
+      for (int h = 0; h < kEach; ++h) u[h] *= g[h] / (1.0f + expf(l[h]));
     }
     for (uint32_t j = 0; j < a.k; ++j) {
-      const int e = __shfl(id, base + (int)j);
-      const float x = __shfl(u, base + (int)j);
+      const int at = base + (int)j % kLanes;
+      int e = __shfl(id[0], at);
+      float x = __shfl(u[0], at);
+#pragma unroll
+      for (int h = 1; h < kEach; ++h) {
+        const int eh = __shfl(id[h], at);
+        const float xh = __shfl(u[h], at);
+        if ((int)j / kLanes == h) e = eh, x = xh;
+      }
 #pragma unroll
       for (int v = 0; v < 4; ++v) d[v] += e == (int)(4 * sub + v) ? x : 0.0f;
     }
     if (t >= a.tokens) continue;
     float* out = a.dlogits + t * a.E + 4 * sub;
-    if (a.E % 4 == 0) {
-      typedef float At __attribute__((ext_vector_type(4), aligned(4)));
-      typedef float Vec __attribute__((ext_vector_type(4)));
+    if (whole) {
       Vec r = {d[0], d[1], d[2], d[3]};
-      if (4 * sub < a.E) {
-        if (a.add) r += *reinterpret_cast<const At*>(a.add + t * a.E + 4 * sub);
-        __builtin_nontemporal_store(live ? r : Vec{}, reinterpret_cast<At*>(out));
-      }
+      if (a.add) r += *reinterpret_cast<const At*>(a.add + t * a.E + 4 * sub);
+      __builtin_nontemporal_store(live ? r : Vec{}, reinterpret_cast<At*>(out));
     } else {
 #pragma unroll
       for (uint32_t v = 0; v < 4; ++v) {
@@ -723,7 +757,8 @@ void launch_grad(const RouteArgs& a, hipStream_t s) {
 
 #define PW_BY_SCORE(fn, score, a, s)                                                                 \
   do {                                                                                               \
-    if ((a).E <= 64) (score) == PW_SCORE_SIGMOID ? fn<16, true>(a, s) : fn<16, false>(a, s);         \
+    if ((a).E <= 16) (score) == PW_SCORE_SIGMOID ? fn<4, true>(a, s) : fn<4, false>(a, s);          \
+    else if ((a).E <= 64) (score) == PW_SCORE_SIGMOID ? fn<16, true>(a, s) : fn<16, false>(a, s);         \
     else (score) == PW_SCORE_SIGMOID ? fn<64, true>(a, s) : fn<64, false>(a, s);                     \
   } while (0)
 

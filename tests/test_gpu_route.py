@@ -31,7 +31,7 @@ CASES = [(1, 2, 1, False, False, 1, 1, 2, True, False), (1, 256, 8, True, True, 
          (70, 2, 1, True, True, 2, 1, 2, False, False), (90, 3, 2, False, False, 3, 2, 1, True, True),
          (16384, 64, 6, True, True, 1, 1, 2, True, True), (34000, 64, 4, False, False, 1, 1, 2, False, True),
          (40000, 60, 1, True, True, 4, 2, 2, True, False), (33000, 64, 8, False, True, 8, 2, 2, False, False), (17001, 30, 3, False, False, 5, 2, 2, False, False),
-         (16500, 9, 1, True, True, 1, 1, 2, True, False), (20001, 200, 8, True, True, 8, 3, 2, True, True),
+         (16500, 9, 1, True, True, 1, 1, 2, True, False), (3000, 7, 7, True, False, 1, 1, 2, True, True), (777, 16, 8, False, True, 1, 1, 2, False, True), (20001, 200, 8, True, True, 8, 3, 2, True, True),
          (16999, 256, 4, False, True, 1, 1, 2, True, False), (16400, 13, 7, True, False, 1, 1, 2, False, True)]
 
 
