@@ -1,7 +1,7 @@
 // Products of an expert's rows in 8-bit integers: rows as codes with a scale
 // each, and the matrix product of codes by expert segments.
 //
-//   s_t = max |x_t| / 127,  q = rint(x / s)
+//   s_t = max |x_t| fp32(1 / 127),  q = rint(fp32(x / s))
 //   out = act(s_t ws_en sum_k q_tk w_enk)
 #include "ops.h"
 
@@ -134,7 +134,12 @@ __device__ __forceinline__ typename Eight<T>::Vec eight_of(const T* row, uint32_
 
 // A team of L lanes takes a row into registers, C times eight elements a lane
 // (C == 0: a wider row, read twice), finds its largest magnitude and writes its
-// codes.
+// codes. Bound by memory: 6.7 TB/s at 262144 rows of 4096 in bf16 (480 us), 6.3 at
+// 65536 of 1024 (31 us). One vector a lane leaves too few bytes in flight and too
+// many workgroups to start: of bf16 (two or four vectors / one) 32768 x 2048 takes
+// 31 / 71 us, 65536 x 512 17.3 / 35, 262144 x 64 10.5 / 18.6. From 2049 elements on
+// a workgroup takes a row: eight vectors a lane of a wave take 146 us for 65536 x
+// 4096, two a lane of four waves 136. With few rows it is all one launch.
 template <typename T, int L, int C>
 __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantArgs a) {
   constexpr int kTeams = kThreads / L, kHold = C ? C : 1;
@@ -187,10 +192,12 @@ void launch_quant_rows(const QuantArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  if (a.d <= 128) launch_quant_rows<T, 16, 1>(a, s);
-  else if (a.d <= 512) launch_quant_rows<T, 64, 1>(a, s);
-  else if (a.d <= 1024) launch_quant_rows<T, 64, 2>(a, s);
-  else if (a.d <= 2048) launch_quant_rows<T, 256, 1>(a, s);
+  if (a.d <= 64) launch_quant_rows<T, 4, 2>(a, s);
+  else if (a.d <= 128) launch_quant_rows<T, 8, 2>(a, s);
+  else if (a.d <= 256) launch_quant_rows<T, 8, 4>(a, s);
+  else if (a.d <= 512) launch_quant_rows<T, 16, 4>(a, s);
+  else if (a.d <= 1024) launch_quant_rows<T, 32, 4>(a, s);
+  else if (a.d <= 2048) launch_quant_rows<T, 64, 4>(a, s);
   else if (a.d <= 4096) launch_quant_rows<T, 256, 2>(a, s);
   else if (a.d <= 8192) launch_quant_rows<T, 256, 4>(a, s);
   else launch_quant_rows<T, 256, 0>(a, s);
@@ -992,7 +999,8 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
     return blocks * ((a.n + n - 1) / n);
   };
   const uint64_t each = a.rows / a.E, large = tiles(256, 256);
-  if (each >= 512 && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
+  const bool finishing = a.E == 1 && a.stride <= 512 && (sizeof(T) == 2 || kGelu);
+  if (each >= 512 && !finishing && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 256) >= 384) return launch_tile<Middle, T, kGelu>(a, s);
   if (each >= 32 && a.stride >= 2048 && tiles(64, 128) >= 256) return launch_tile<Long, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 128) >= 256) return launch_tile<Square, T, kGelu>(a, s);

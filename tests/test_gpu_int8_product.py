@@ -40,7 +40,7 @@ def rows_of(rng, rows, d, dtype, scale=1.0):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,d", [(1, 1), (3, 7), (5, 64), (70, 65), (300, 128), (33, 200), (64, 1000), (257, 1024),
-                                    (9, 2048), (20, 2049), (5, 4096), (7, 8191), (3, 8192), (2, 12345), (2, 65536)])
+                                    (9, 2048), (20, 2049), (1001, 120), (401, 250), (130, 500), (70, 1500), (5, 4096), (7, 8191), (3, 8192), (2, 12345), (2, 65536)])
 def test_codes_are_equal(gpu, rows, d, dtype):
     print(f"quant {rows} x {d} {dtype}", flush=True)
     rng = np.random.default_rng([rows, d])
@@ -171,7 +171,8 @@ def test_product(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
 @pytest.mark.parametrize("T,k,E,d,n,kind,gather,scatter,act,dtype",
                          [(5500, 2, 5, 192, 6500, "skewed", True, False, True, "bf16"), (6000, 2, 3, 64, 6144, "padded", False, True, False, "f32"),
                           (20000, 1, 1, 512, 4096, "even", False, False, True, "bf16"), (4000, 8, 130, 320, 2500, "skewed", True, True, False, "bf16"),
-                          (70000, 1, 2, 100, 1030, "one", False, True, False, "bf16"), (17000, 2, 64, 1024, 2048, "padded", True, False, True, "f32")])
+                          (70000, 1, 2, 100, 1030, "one", False, True, False, "bf16"), (17000, 2, 64, 1024, 2048, "padded", True, False, True, "f32"),
+                          (9000, 2, 5, 700, 1030, "skewed", True, False, True, "bf16"), (16000, 1, 1, 1152, 2049, "even", False, False, False, "bf16")])
 def test_many_tiles(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
     """As test_product at sizes where workgroups walk over tiles; the plain form in 64 bits by torch, on the GPU."""
     print(f"product T={T} k={k} E={E} d={d} n={n} {kind} gather={gather} scatter={scatter} {dtype}", flush=True)
