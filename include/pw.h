@@ -612,12 +612,11 @@ int pw_route_grad(const pw_route_desc* d, const pw_route_io* io, void* stream);
 
 /* ---- rows as 8-bit codes ----------------------------------------------------
  *   scale = max |x| times the fp32 number nearest to 1 / 127,  q = the whole number
- * nearest to x / scale (product and quotient rounded to fp32, ties to even), x ~ scale
- * q. A row of zeros, or whose scale
- * underflows to zero, has zeros; one that holds an infinity or a NaN has zeros and the
- * scale NaN, so that what is computed from it is NaN. A row of codes takes
- * PW_Q8_ROW(d) bytes, zeros behind the d-th. Weights are rows too: one for each
- * output channel. */
+ * nearest to x / scale (product and quotient rounded to fp32, ties to even), so that
+ * x ~ scale q. A row of zeros, or whose scale underflows to zero, has zeros; one that
+ * holds an infinity or a NaN has zeros and the scale NaN, so that what is computed
+ * from it is NaN. A row of codes takes PW_Q8_ROW(d) bytes, zeros behind the d-th.
+ * Weights are rows too: one for each output channel. */
 #define PW_Q8_ROW(d) (((uint64_t)(d) + 63) / 64 * 64)
 
 typedef struct {

@@ -3,6 +3,12 @@
 //
 //   s_t = max |x_t| fp32(1 / 127),  q = rint(fp32(x / s))
 //   out = act(s_t ws_en sum_k q_tk w_enk)
+//
+// The sum is of whole numbers and exact in 32 bits (127^2 65536 < 2^31), in any
+// order, so every shape below gives the same bits. Many rows an expert: bound by the
+// matrix instructions (v_mfma_i32_32x32x32_i8; a library product of 8192^3 reaches
+// 2.08 P operations/s here); few: by reading the weights once, from memory
+// (4.4 to 5.1 TB/s).
 #include "ops.h"
 
 #include <float.h>
@@ -586,7 +592,10 @@ __device__ __forceinline__ void feed_b(const Q8Args& a, const Piece& g, Feed<P>&
   }
 }
 
-// One tile a workgroup; while one multiplies, others of its CU start or end.
+// One tile a workgroup; while one multiplies, others of its CU start or end. Results
+// go out as they are finished, 32 bytes of a row from each lane pair, past no cache:
+// nontemporal stores of such parts of lines reach memory one by one (131072 x 2
+// 1024 -> 4096 with 64 experts: 2194 us instead of 1804).
 template <typename P, typename T, bool kGelu>
 __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -716,7 +725,8 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__bui
 
 // The tile of workgroup turn b (below the total), from the list. An XCD's tiles are
 // contiguous, in patches of kPatch row blocks by 4 column tiles, as many as its 32
-// CUs work on at a time: they share what they load.
+// CUs work on at a time: they share what they load (262144 x 1024 -> 4096 with kPatch
+// 2, 4, 8, 16: 1424, 1406, 1340, 1352 us).
 constexpr uint32_t kPatch = 8;
 
 template <typename P>
@@ -740,7 +750,15 @@ __device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint3
 // rows are looked up while this one multiplies, and its first stages are on their
 // way while this one's results are scaled and stored. No branch stands between
 // the products and the stores (it would make the accumulators move): behind the
-// last tile it is started once more, in vain.
+// last tile it is started once more, in vain. 131072 x 2 rows of 64 experts, codes given:
+// 4096 -> 1024 in 1.0 to 1.1 ms (2.0 P operations/s, as the library's one large product),
+// 1024 -> 4096 with GELU in 1.78 ms: a product per 8 KiB tile row is short there, and
+// what a CU's one workgroup does between products (GELU, stores: 0.23 ms) nothing
+// covers; the first use of an expert's weights costs 12 %, and the clock 15 % (so much less
+// time do weights of zeros take). Two workgroups a CU with tiles of
+// 128 x 256 cover it but load twice as much from the caches: 1.9 ms and more; waves of
+// 4 x 2 or of raised priority change nothing. 64-byte stages instead of 128: 8192^3 in 595 us
+// instead of 571 (a CU's loads are then twice as many, of half a line each).
 template <typename P, typename T, bool kGelu>
 __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
   static_assert(P::NT == P::BM + P::BN && P::BM % 64 == 0, "a thread for each scale");
@@ -870,7 +888,12 @@ hipError_t launch_tile(Q8Args a, hipStream_t s) {
 // their length, with up to 16 rows: all 16 KiB of the matrix that it can hold
 // are on their way at once, and no other wave reads them. The parts' sums (whole
 // numbers: exact in any order) meet in LDS. Every workgroup makes the codes of its
-// rows itself, while the matrix is on its way.
+// rows itself, while the matrix is on its way. Against codes in a launch of their
+// own and tiles: one row 4096 -> 1024 in 7.1 us instead of 15.3, one token's 8 experts 4096 ->
+// 1024 in 10.1 instead of 18.1 (33.8 MB: 6.6 us at a large copy's rate; what is left is
+// the launch and the ramp of the loads), 1024 -> 4096 in 11.3 instead of 12.2. From
+// 4 tokens of 8 on it loses (31 us instead of 25.6; 48 of 8 77 instead of 47, weights in the
+// caches): codes are made over and over, and no tile shares what it loads.
 constexpr int kHeld = 16;              // 64-byte steps of 16 columns in registers
 constexpr uint32_t kCodeWidth = 4096;  // of the rows that a workgroup codes: 8 chunks a lane
 constexpr uint32_t kFewRows = 8;       // of a call
@@ -990,6 +1013,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
   typedef Shape<32, 64, 1, 2, 128, 5> Flat;
   if (a.x) {
+    // as many parts of a row as a wave's registers hold in one or, from 4 on, two turns
     if (a.stride > 32 * 64) return launch_few<T, kGelu, 4>(a, s);
     return a.stride > 16 * 64 ? launch_few<T, kGelu, 2>(a, s) : launch_few<T, kGelu, 1>(a, s);
   }
@@ -998,6 +1022,26 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
     const uint64_t blocks = a.E > 1 ? std::min<uint64_t>(a.rows, a.rows / m + a.E / 2) : ((uint64_t)a.rows + m - 1) / m;
     return blocks * ((a.n + n - 1) / n);
   };
+  // Times in us with the codes given, where no other case is named for 64 experts and two of
+  // them a token ("dense": one expert); rows are counted on the host as a call's most, so an
+  // expert's are a guess.
+  //  Large, stays: tiles enough for every CU. Dense 1024 -> 4096, 65536 rows: Large 458,
+  //    Middle 503, Small 775; 4096 rows 31.6, 33.2, 46.2; 16384 tokens (512 rows an
+  //    expert) 285, 285, 463, but 8192 tokens 191, 160, 265. Few codes a row and one expert leave
+  //    mostly the finishing of results, which two workgroups a CU share (65536 rows
+  //    64 -> 1792: 64 and 51, 512 -> 1792: 113 and 99; fp32 results without GELU 118 and 132
+  //    at 128 -> 1792; with 19 experts 155 and 168 at 150396 rows 46 -> 1792).
+  //  Middle: three tiles for two CUs at least. 2048 tokens 1024 -> 4096: Middle 84, Small 98,
+  //    Square 91; 256 tokens (8 rows an expert) 62, 48, 69.
+  //  Long: 128-byte stages are whole lines and half as many waits. Dense 4096 -> 1024, 2048 rows
+  //    17.3 (Square 23.3, Small 21.3), 4096 rows 26.8 (Square 27.7, Small 39.9).
+  //  Square: dense 1024 -> 4096, 2048 rows 20.9 (Middle 21.9, Small 26.3); dense 4096 -> 1024,
+  //    8192 rows 46.6 (Middle 43.5, Small 75).
+  //  Flat: few rows an expert, so the weights come from memory: tiles of whole lines and a
+  //    deep ring. 48 tokens of 8, 4096 -> 1024: 61.5 (Small 68.4), 128 tokens of 8: 70.8 and
+  //    78.7 (weights not in the caches).
+  //  Parted: fewer tiles than CUs and long rows: four groups of waves share a tile's length.
+  //    Dense 4096 -> 1024, 16 to 256 rows: 13.2 to 14.2 (Small 16.4).
   const uint64_t each = a.rows / a.E, large = tiles(256, 256);
   const bool finishing = a.E == 1 && a.stride <= 512 && (sizeof(T) == 2 || kGelu);
   if (each >= 512 && !finishing && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);

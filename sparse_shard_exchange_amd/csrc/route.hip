@@ -62,6 +62,11 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // groups' marks are that close, or the scores are a softmax, whose 64-bit value
 // needs all logits, a wave takes the token anew in 64 bits. Logits of fewer bits
 // than are cut (bf16 ones; equal ones) leave no doubt.
+//
+// What bounds it: 32 x 256 in groups takes 6.8 us, a launch and one chain of dependent
+// steps (the row, its scores, the groups' marks, eight maxima, the weights); 131072 x 64,
+// k = 6, sigmoid with bias 22.8 us, of vector instructions (its 40 MB would take 7.8), and
+// 4.8 of the second launch. All in 64 bits, as a simple kernel does it, takes 51.6.
 
 // Order-preserving integers of floats other than negative zero.
 __device__ __forceinline__ int32_t ordered(float f) {
@@ -516,7 +521,8 @@ __global__ __launch_bounds__(kThreads, kWhole ? 2 : 3) void k_route(RouteArgs a)
   }
 }
 
-// The tokens that k_route left, out of 64 a wave.
+// The tokens that k_route left, out of 64 a wave: their marks are found in one load and
+// a vote, so tokens without doubt cost this launch four bytes each.
 template <bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void k_route_rest(RouteArgs a) {
   __shared__ double s_c[kThreads / 64][kMaxRouteExperts];
@@ -553,7 +559,10 @@ __global__ __launch_bounds__(kThreads) void k_route_rest(RouteArgs a) {
 //               over the chosen drops out, so ratios that underflow keep their gradient)
 //   otherwise:  dl_ej = g_j s_ej (1 - s_ej) for a sigmoid,
 //               dl_e = s_e (sum of the g_j with e_j = e - sum_j g_j s_ej) for a softmax
-// L lanes a token, four neighbouring experts a lane.
+// L lanes a token, four neighbouring experts a lane; the chosen ones' logits are gathered,
+// each by its own lane, all at once. Bound by memory: 131072 x 64, k = 6, with add, in 18.4 us
+// (77 MB needed; the gathered logits bring whole lines, 110 MB: 6 TB/s). Four lanes a token up
+// to 16 experts, not 16: 131072 x 16 7.4 us instead of 14.1.
 template <int L, bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
   typedef float At __attribute__((ext_vector_type(4), aligned(4)));

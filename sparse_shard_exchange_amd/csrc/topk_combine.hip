@@ -1,5 +1,6 @@
 // out[t] = add[t] + sum_j w[t][j] y[t][j]: the expert rows of each token, in
-// tuple order, joined by their routing weights.
+// tuple order, joined by their routing weights. Bound by memory: every row of y is
+// read once and past the caches (nothing reads it again), every row of out written so.
 #include "ops.h"
 
 #include <algorithm>
@@ -29,6 +30,9 @@ struct Chunk {
 // back to end with it and stores its own elements alone (out may be add). A row of
 // weight 0 is not read: its lanes read the buffer's first row instead, a line
 // that is in the caches, since loads under a branch would wait one for another.
+// bf16 with add, d = 1024: 131072 tokens of 6 in 343 us, a tenth of the tokens masked (2.0 GB
+// moved, 5.8 TB/s; a large copy reaches 5.1). Nontemporal neither way / stores only / both,
+// without add: 131072 x 6 x 1024 381 / 362 / 304 us, 131072 x 2 x 1024 136 / 133 / 121, 16384 x 2 x 4096 70 / 57 / 63.
 template <typename T, int V, int L, int K>
 __global__ __launch_bounds__(kThreads) void k_topk_combine(CombineArgs a) {
   typedef Chunk<T, V> C;
@@ -76,6 +80,8 @@ void launch(const CombineArgs& a, hipStream_t s) {
                      0, s, a);
 }
 
+// Lanes a token: a row in one turn of 16-byte chunks, up to a workgroup. K is a
+// constant so that a lane's rows are all in registers, on their way at once.
 template <typename T, int K>
 void launch_width(const CombineArgs& a, hipStream_t s) {
   constexpr uint32_t V = 16 / sizeof(T);
