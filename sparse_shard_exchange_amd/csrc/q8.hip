@@ -140,8 +140,8 @@ __device__ __forceinline__ typename Eight<T>::Vec eight_of(const T* row, uint32_
 
 // A team of L lanes takes a row into registers, C times eight elements a lane
 // (C == 0: a wider row, read twice), finds its largest magnitude and writes its
-// codes. Bound by memory: 6.7 TB/s at 262144 rows of 4096 in bf16 (480 us), 6.3 at
-// 65536 of 1024 (31 us). One vector a lane leaves too few bytes in flight and too
+// codes. Bound by memory: 236000 rows of 4096 in bf16 take 480 us (6.0 TB/s), 65536 of
+// 1024 31 us. One vector a lane leaves too few bytes in flight and too
 // many workgroups to start: of bf16 (two or four vectors / one) 32768 x 2048 takes
 // 31 / 71 us, 65536 x 512 17.3 / 35, 262144 x 64 10.5 / 18.6. From 2049 elements on
 // a workgroup takes a row: eight vectors a lane of a wave take 146 us for 65536 x
