@@ -344,21 +344,59 @@ __device__ __forceinline__ Run<T> finish_run(const i32x16& acc, float s, const f
   return r;
 }
 
+// Four chunks of each of four rows, a row's in the lanes that differ from one of them in
+// bits 4 and 2 alone, change places: element k = 2 j + i of lane (bit 4: m, bit 2: n)
+// becomes element 2 n + m of lane (bit 4: i, bit 2: j). A store of one element then
+// writes whole lines. By whole waves.
+template <typename Vec>
+__device__ __forceinline__ void turn_rows(Vec* x) {
+  i32x4 v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __builtin_bit_cast(i32x4, x[k]);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const auto both = __builtin_amdgcn_permlane16_swap((uint32_t)v[k][d], (uint32_t)v[k + 1][d], false, false);
+      v[k][d] = (int)both[0];
+      v[k + 1][d] = (int)both[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lo = v[k][d], hi = v[k + 2][d];
+      v[k][d] = __builtin_amdgcn_update_dpp(lo, hi, 0x114, 15, 10, false);      // lanes of bit 2: from 4 lanes below
+      v[k + 2][d] = __builtin_amdgcn_update_dpp(hi, lo, 0x104, 15, 5, false);   // the others: from 4 above
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = __builtin_bit_cast(Vec, v[k]);
+}
+
+// Rows of results: of any length, of whole 16-byte chunks (k_q8_stay turns those into
+// whole lines), of whole lines that go past the caches.
+enum { kAnyRow, kWholeChunks, kPastCaches };
+
+// Stores 16 bytes of results from column c on, of a row of n (0: it is not stored).
+template <typename T, int kRow>
+__device__ __forceinline__ void store_chunk(const typename Run<T>::Vec& v, T* row, uint32_t c, uint32_t n) {
+  constexpr int V = Run<T>::V;
+  if (c + V <= n) {
+    typename Run<T>::At* to = reinterpret_cast<typename Run<T>::At*>(row + c);
+    if constexpr (kRow == kPastCaches) __builtin_nontemporal_store(v, to);
+    else *to = v;
+  } else if constexpr (kRow == kAnyRow) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (c + e < n) row[c + e] = v[e];
+  }
+}
+
 // Stores a lane's results of 32 columns, its first one c, of a row of n (0: it is not stored).
 template <typename T>
 __device__ __forceinline__ void store_run(const Run<T>& r, T* row, uint32_t c, uint32_t n) {
   constexpr int V = Run<T>::V;
 #pragma unroll
-  for (int p = 0; p < 16 / V; ++p) {
-    const uint32_t at = c + p * 2 * V;
-    if (at + V <= n) {
-      *reinterpret_cast<typename Run<T>::At*>(row + at) = r.v[p];
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (at + e < n) row[at + e] = r.v[p][e];
-    }
-  }
+  for (int p = 0; p < 16 / V; ++p) store_chunk<T, kAnyRow>(r.v[p], row, c + p * 2 * V, n);
 }
 
 // Shape of a tile: BM x BN results by WM x WN waves, each MI x NI blocks of
@@ -752,14 +790,17 @@ __device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint3
 // the products and the stores (it would make the accumulators move): behind the
 // last tile it is started once more, in vain. 131072 x 2 rows of 64 experts, codes given:
 // 4096 -> 1024 in 1.0 to 1.1 ms (2.0 P operations/s, as the library's one large product),
-// 1024 -> 4096 with GELU in 1.78 ms: a product per 8 KiB tile row is short there, and
-// what a CU's one workgroup does between products (GELU, stores: 0.23 ms) nothing
-// covers; the first use of an expert's weights costs 12 %, and the clock 15 % (so much less
+// 1024 -> 4096 with GELU in 1.75 ms: a tile multiplies for 8 stages only there, and what a CU's
+// one workgroup does then (GELU 0.37 ms, stores 0.25) nothing covers. Results are turned
+// among lanes so that a store writes whole lines, past the caches where they are many (whole
+// lines / 32 bytes of each of 32 rows a store: 1.80 and 1.88 ms with GELU, 1.44 and 1.56
+// without; 65536 x 2 of 8 experts in fp32 without GELU 0.82 and 1.20 ms; 32768 x 2 bf16 with GELU
+// 219 and 215 us; rows that end inside a chunk, 2001 long, 238 and 223, so those stay as they are); the first use of an expert's weights costs 12 %, and the clock 15 % (so much less
 // time do weights of zeros take). Two workgroups a CU with tiles of
 // 128 x 256 cover it but load twice as much from the caches: 1.9 ms and more; waves of
 // 4 x 2 or of raised priority change nothing. 64-byte stages instead of 128: 8192^3 in 595 us
 // instead of 571 (a CU's loads are then twice as many, of half a line each).
-template <typename P, typename T, bool kGelu>
+template <typename P, typename T, bool kGelu, int kRow>
 __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
   static_assert(P::NT == P::BM + P::BN && P::BM % 64 == 0, "a thread for each scale");
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -817,30 +858,44 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
     T* out = static_cast<T*>(a.out);
     // half of the results are finished before the loads are waited for, and the
     // first store follows that wait: the counter then holds stores alone
-    constexpr int H = (P::MI + 1) / 2;
-    Run<T> first[H][P::NI];
+    constexpr int H = (P::MI + 1) / 2, V = Run<T>::V, G = P::NI * 4 / V;  // groups of 4 chunks of a row
+    constexpr bool kTurn = kRow != kAnyRow;
+    static_assert(P::NI * 16 == G * 4 * V, "whole groups");
+    typename Run<T>::Vec first[H][4 * G];
 #pragma unroll
     for (int i = 0; i < P::MI; ++i) {
       const uint32_t r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
       const float s = s_scale[turn][r];
+      typename Run<T>::Vec chunk[4 * G];
 #pragma unroll
       for (int j = 0; j < P::NI; ++j) {
-        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + Run<T>::V * (lane >> 5);
+        const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + V * (lane >> 5);
         const Run<T> run = finish_run<T, kGelu>(acc[i][j], s, &s_scale[turn][P::BM + c]);
-        if (i < H) {
-          first[i][j] = run;
-          if (i < H - 1 || j < P::NI - 1) continue;
-        }
-        if (i == H - 1) mm::wait_vmem<0>();
 #pragma unroll
-        for (int i0 = i == H - 1 ? 0 : i; i0 <= i; ++i0) {
-          const uint32_t r0 = w / P::WN * (P::BM / P::WM) + 32 * i0 + (lane & 31);
+        for (int p = 0; p < 16 / V; ++p) chunk[16 / V * j + p] = run.v[p];
+      }
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+        if constexpr (kTurn) turn_rows(&chunk[4 * q]);
+      if (i < H) {
+#pragma unroll
+        for (int q = 0; q < 4 * G; ++q) first[i][q] = chunk[q];
+        if (i < H - 1) continue;
+      }
+      if (i == H - 1) mm::wait_vmem<0>();
+#pragma unroll
+      for (int i0 = i == H - 1 ? 0 : i; i0 <= i; ++i0) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t r0 = w / P::WN * (P::BM / P::WM) + 32 * i0 + (kTurn ? (lane & 11) | m / 2 << 2 | m % 2 << 4 : lane & 31);
           const RowOf row = row_at(g, s_src[turn], r0);
           const uint32_t n = r0 < g.rows && row.out >= 0 ? a.n : 0u;
+          T* to = out + (uint64_t)row.out * a.n;
 #pragma unroll
-          for (int j0 = i == H - 1 ? 0 : j; j0 <= j; ++j0) {
-            const uint32_t c0 = w % P::WN * (P::BN / P::WN) + 32 * j0 + Run<T>::V * (lane >> 5);
-            store_run<T>(i0 < H ? first[i0 < H ? i0 : 0][j0] : run, out + (uint64_t)row.out * a.n, g.col0 + c0, n);
+          for (int q = 0; q < G; ++q) {
+            const uint32_t k = kTurn ? (lane >> 4 & 1) | (lane >> 2 & 1) << 1 : m;
+            const uint32_t c0 = g.col0 + w % P::WN * (P::BN / P::WN) + 8 * V * q + 2 * V * k + V * (lane >> 5);
+            store_chunk<T, kRow>(i0 < H ? first[i0 < H ? i0 : 0][4 * q + m] : chunk[4 * q + m], to, c0, n);
           }
         }
       }
@@ -857,6 +912,11 @@ hipError_t allow_lds(const void* kernel, uint32_t bytes) {
   return bytes > 60 * 1024 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : hipSuccess;
 }
 
+// Results of so many bytes are not in the last-level cache (256 MiB) when they are read
+// (past the caches / through them: 262144 x 1024 -> 4096 1.24 / 1.32 ms, 131072 x 1024 -> 4096 of
+// 8 experts in fp32 0.79 / 0.96 ms).
+constexpr uint64_t kManyBytes = 512ull << 20;
+
 template <typename P, typename T, bool kGelu>
 hipError_t launch_stay(Q8Args a, hipStream_t s) {
   a.col_tiles = (a.n + P::BN - 1) / P::BN;
@@ -864,10 +924,17 @@ hipError_t launch_stay(Q8Args a, hipStream_t s) {
   int device = 0, cus = 0;
   hipError_t e = hipGetDevice(&device);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
-  if (e == hipSuccess) e = allow_lds((const void*)k_q8_stay<P, T, kGelu>, P::kLds);
   if (e != hipSuccess) return e;
-  const uint32_t grid = (uint32_t)std::min<uint64_t>(tiles, std::max(8, cus / 8 * 8));
-  hipLaunchKernelGGL((k_q8_stay<P, T, kGelu>), dim3(grid), dim3(P::NT), P::kLds, s, a);
+  auto launch = [&](void (*kernel)(Q8Args)) {
+    if ((e = allow_lds((const void*)kernel, P::kLds)) != hipSuccess) return;
+    const uint32_t grid = (uint32_t)std::min<uint64_t>(tiles, std::max(8, cus / 8 * 8));
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(P::NT), P::kLds, s, a);
+  };
+  const uint64_t row = a.n * sizeof(T);
+  if (a.rows * row >= kManyBytes && row % 128 == 0 && (uintptr_t)a.out % 128 == 0) launch(k_q8_stay<P, T, kGelu, kPastCaches>);
+  else if (row % 16 == 0) launch(k_q8_stay<P, T, kGelu, kWholeChunks>);
+  else launch(k_q8_stay<P, T, kGelu, kAnyRow>);
+  if (e != hipSuccess) return e;
   return hipGetLastError();
 }
 

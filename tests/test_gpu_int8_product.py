@@ -172,7 +172,9 @@ def test_product(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
                          [(5500, 2, 5, 192, 6500, "skewed", True, False, True, "bf16"), (6000, 2, 3, 64, 6144, "padded", False, True, False, "f32"),
                           (20000, 1, 1, 512, 4096, "even", False, False, True, "bf16"), (4000, 8, 130, 320, 2500, "skewed", True, True, False, "bf16"),
                           (70000, 1, 2, 100, 1030, "one", False, True, False, "bf16"), (17000, 2, 64, 1024, 2048, "padded", True, False, True, "f32"),
-                          (9000, 2, 5, 700, 1030, "skewed", True, False, True, "bf16"), (16000, 1, 1, 1152, 2049, "even", False, False, False, "bf16")])
+                          (9000, 2, 5, 700, 1030, "skewed", True, False, True, "bf16"), (16000, 1, 1, 1152, 2049, "even", False, False, False, "bf16"),
+                          (33000, 2, 5, 640, 4096, "padded", True, True, False, "bf16"), (33000, 2, 3, 576, 2080, "skewed", False, True, True, "f32"),
+                          (8000, 2, 2, 640, 2060, "padded", True, False, False, "f32"), (9000, 1, 1, 600, 3000, "even", False, False, True, "bf16")])
 def test_many_tiles(gpu, T, k, E, d, n, kind, gather, scatter, act, dtype):
     """As test_product at sizes where workgroups walk over tiles; the plain form in 64 bits by torch, on the GPU."""
     print(f"product T={T} k={k} E={E} d={d} n={n} {kind} gather={gather} scatter={scatter} {dtype}", flush=True)
