@@ -793,8 +793,8 @@ __device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint3
 // 1024 -> 4096 with GELU in 1.75 ms: a tile multiplies for 8 stages only there, and what a CU's
 // one workgroup does then (GELU 0.37 ms, stores 0.25) nothing covers. Results are turned
 // among lanes so that a store writes whole lines, past the caches where they are many (whole
-// lines / 32 bytes of each of 32 rows a store: 1.80 and 1.88 ms with GELU, 1.44 and 1.56
-// without; 65536 x 2 of 8 experts in fp32 without GELU 0.82 and 1.20 ms; 32768 x 2 bf16 with GELU
+// lines / 32 bytes of each of 32 rows a store: 1.82 and 1.89 ms with GELU, 1.45 and 1.57
+// without; 65536 x 2 of 8 experts in fp32 without GELU 0.82 to 0.92 and 1.2 ms; 32768 x 2 bf16 with GELU
 // 219 and 215 us; rows that end inside a chunk, 2001 long, 238 and 223, so those stay as they are); the first use of an expert's weights costs 12 %, and the clock 15 % (so much less
 // time do weights of zeros take). Two workgroups a CU with tiles of
 // 128 x 256 cover it but load twice as much from the caches: 1.9 ms and more; waves of
