@@ -1,4 +1,5 @@
-"""Derive the constants of the GEMM epilogue's GELU (csrc/gemm.h, gelu()).
+"""Derive the constants of the GEMM epilogue's GELU (csrc/gemm.h, gelu(): degree
+4) and of the 8-bit products' (csrc/q8.hip, gelu_bf16(): degree 7).
 
 GELU(z) = z Phi(z). With h(a) = erfc(a / sqrt 2) / 2 for a = |z| >= 0, this is
 z (1 - h) for z >= 0 and z h for z < 0, i.e. max(z, 0) - |z| h(|z|).
@@ -12,21 +13,23 @@ the whole tail (the Chebyshev-style form t exp(-x^2 + poly(t)) of Numerical
 Recipes' erfcc; the degree, p and coefficients here are fitted afresh).
 
 The fit is minimax on a dense grid of a in [0, 16] (a linear program), for
-degree 4 and the p that minimises the error. It prints the constants and the
+the degree given (4 without one) and the p that minimises the error. It prints the constants and the
 maximum relative error of h and of GELU when the formula is evaluated in fp32
 the way the kernel does (fused multiply-adds, fp32 reciprocal and exp2),
 emulated here with fp32 rounding after every operation.
 
-    python sparse_shard_exchange_amd/csrc/gelu_fit.py
+    python sparse_shard_exchange_amd/csrc/gelu_fit.py [degree]
 """
 from __future__ import annotations
+
+import sys
 
 import numpy as np
 from scipy.optimize import linprog
 from scipy.special import erfc
 
 C = np.log2(np.e) / 2.0
-DEG = 4
+DEG = int(sys.argv[1]) if len(sys.argv) > 1 else 4
 
 
 def _grid(amax: float = 16.0, n: int = 6000) -> np.ndarray:

@@ -422,3 +422,31 @@ def test_captured_with_the_exchange_and_replayed(gpu, T, E, k, d, hidden):
         got = out.clone()
         assert torch.equal(got, way())
         torch.cuda.synchronize()
+
+
+# ---- rounding and range of the results ------------------------------------------
+
+def dense(gpu, rows, d, n, dtype, act, x_scale, w_scale, seed=0):
+    """A product of one matrix from given scales: (got, z in 64 bits, from the codes)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randint(-127, 128, (rows, ox.q8_row(d)), dtype=torch.int8, device="cuda", generator=gen)
+    w = torch.randint(-127, 128, (1, n, ox.q8_row(d)), dtype=torch.int8, device="cuda", generator=gen)
+    q[:, d:], w[:, :, d:] = 0, 0
+    s = torch.full((rows,), x_scale, device="cuda") if np.isscalar(x_scale) else x_scale
+    ws = torch.full((1, n), w_scale, device="cuda") if np.isscalar(w_scale) else w_scale
+    got = gpu.Int8Product(w, ws, d, rows, gelu=act, dtype=pwt(gpu, dtype)).forward(q, x_scale=s)
+    z = (q.double() @ w[0].double().t().contiguous()) * s.double().unsqueeze(1) * ws.double()
+    return got, z
+
+
+@pytest.mark.parametrize("rows,d,n", [(8, 700, 4000), (40, 2100, 1000), (300, 1000, 515), (2500, 512, 520), (20000, 640, 4096)])
+def test_gelu_is_rounded_to_the_nearest_but_for_its_own_last_bits(gpu, rows, d, n):
+    """bf16 results are those of a number that is at most e off z Phi(z): z is rounded three times and carries z^2 + 2
+    times that, and GELU adds (2 z^2 + 26) u and 2.9e-7 of itself (below 5 u)."""
+    got, z = dense(gpu, rows, d, n, "bf16", True, 1.8 / 73.3, 1 / (73.3 * d ** 0.5))
+    for g, y in zip(got.split(2048), z.split(2048)):
+        e = (3 * (y * y + 2) + 2 * y * y + 31) * U * 1.01
+        want = y * 0.5 * torch.special.erfc(-y * 0.5 ** 0.5)
+        ends = torch.stack([want * (1 - e), want * (1 + e)]).float().bfloat16()
+        ok = (g >= ends.min(0).values) & (g <= ends.max(0).values) | (y.abs() > 12)
+        assert bool(ok.all()), (int((~ok).sum()), ok.numel())
