@@ -639,7 +639,7 @@ int pw_quant_rows(const pw_quant_desc* d, const pw_quant_io* io, void* stream);
  * For each dispatched row i of expert e (offsets[e] <= i < offsets[e + 1]):
  *   out[o][j] = act(q_scale[a] w_scale[e][j] sum_k q[a][k] w[e][j][k])
  * with q and q_scale the codes of x as pw_quant_rows makes them, the sum exact,
- * act GELU (z Phi(z)) or nothing, the result rounded once. Row a of x is i, or
+ * act GELU (z Phi(z), 0 of -infinity) or nothing, the result rounded once. Row a of x is i, or
  * src_index[i] / gather where gather > 0 (x holds tokens, of gather tuples each);
  * row o of out is i, or src_index[i] where scatter is set (out is in tuple
  * order). Rows of out that no i names are left as they are: those behind

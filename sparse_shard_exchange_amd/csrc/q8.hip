@@ -330,16 +330,18 @@ __device__ __forceinline__ float gelu_bf16(float z) {
   q = fmaf(q, t, 1.4347367f);
   q = fmaf(q, t, -2.8902936f);
   const float e = __builtin_amdgcn_exp2f(fmaf(z * z, -0.72134752f, q));  // -log2(e) / 2
-  return fmaf(-a, t * e, fmaxf(z, 0.0f));
+  // (behind 20 the tail is zero; an infinite factor would make it NaN. NaN stays, by t)
+  return fmaf(-fminf(a, 20.0f), t * e, fmaxf(z, 0.0f));
 }
 
-// bf16 results take the GELU above, fp32 ones the library's error function.
+// bf16 results take the GELU above, fp32 ones the library's error function (-infinity
+// gives zero, by a finite factor).
 template <typename T, bool kGelu>
 __device__ __forceinline__ float finish(int sum, float s, float ws) {
   const float z = (float)sum * s * ws;
   if constexpr (!kGelu) return z;
   else if constexpr (sizeof(T) == 2) return gelu_bf16(z);
-  else return 0.5f * z * erfcf(z * -0.70710678f);
+  else return 0.5f * fmaxf(z, -FLT_MAX) * erfcf(z * -0.70710678f);
 }
 
 // A lane's 16 results of 32 columns of a row, rounded, in runs of 16 bytes: every

@@ -450,3 +450,25 @@ def test_gelu_is_rounded_to_the_nearest_but_for_its_own_last_bits(gpu, rows, d, 
         ends = torch.stack([want * (1 - e), want * (1 + e)]).float().bfloat16()
         ok = (g >= ends.min(0).values) & (g <= ends.max(0).values) | (y.abs() > 12)
         assert bool(ok.all()), (int((~ok).sum()), ok.numel())
+
+
+VARIANTS = [(7, 700, 400), (40, 2100, 1000), (300, 1000, 515), (2500, 512, 520), (20000, 640, 1024)]  # every kernel
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d,n", VARIANTS)
+def test_infinite_and_huge_results(gpu, rows, d, n, dtype):
+    """z Phi(z) of +infinity is +infinity, of -infinity 0; 0 x infinity and NaN are NaN; the same without GELU but for -infinity."""
+    s = torch.full((rows,), 1e-3, device="cuda")
+    ws = torch.full((1, n), 1e-3, device="cuda")
+    s[1], s[2], s[rows - 1] = float("inf"), float("nan"), 1e30
+    ws[0, 3], ws[0, 5], ws[0, 7], ws[0, n - 1] = float("inf"), float("nan"), 1e34, -float("inf")
+    for act in (False, True):
+        got, z = dense(gpu, rows, d, n, dtype, act, s, ws)
+        z = torch.where(z.abs() > torch.finfo(torch.float32).max, torch.sign(z) * float("inf"), z)
+        want = torch.where(z < -40, torch.zeros_like(z), z * 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)) if act else z
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.isinf(got), torch.isinf(want)) and bool((got[torch.isinf(got)].sign() == z[torch.isinf(got)].sign()).all())
+        ok = torch.isfinite(want)
+        err = (5 * torch.where(ok & (z.abs() < 13), z, torch.zeros_like(z)) ** 2 + 32) * U + HALF[dtype] * 1.01
+        assert bool(((got.double() - want).abs() <= want.abs() * err + 1e-30)[ok].all())
