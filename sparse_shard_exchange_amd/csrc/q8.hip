@@ -336,9 +336,21 @@ __device__ __forceinline__ float gelu_bf16(float z) {
 
 // bf16 results take the GELU above, fp32 ones the library's error function (-infinity
 // gives zero, by a finite factor).
+// A row's scale in two factors. A sum reaches 2^30, so that sum x scale of a scale from
+// 2^97 on may pass the range of fp32 where the result, times the column's scale, does not;
+// such a scale is divided by 2^32 and the product multiplied by that in the end. (No result
+// loses bits on the way down: the sum times the least scales is a multiple of the least number.)
+struct RowScale {
+  float s, up;
+};
+__device__ __forceinline__ RowScale row_scale(float s) {
+  const bool large = fabsf(s) >= 0x1p97f;
+  return {large ? s * 0x1p-32f : s, large ? 0x1p32f : 1.0f};
+}
+
 template <typename T, bool kGelu>
-__device__ __forceinline__ float finish(int sum, float s, float ws) {
-  const float z = (float)sum * s * ws;
+__device__ __forceinline__ float finish(int sum, const RowScale& s, float ws) {
+  const float z = (float)sum * s.s * ws * s.up;
   if constexpr (!kGelu) return z;
   else if constexpr (sizeof(T) == 2) return gelu_bf16(z);
   else return 0.5f * fmaxf(z, -FLT_MAX) * erfcf(z * -0.70710678f);
@@ -356,7 +368,7 @@ struct Run {
 
 // Scale, activation and the one rounding; ws: of the lane's first column.
 template <typename T, bool kGelu>
-__device__ __forceinline__ Run<T> finish_run(const i32x16& acc, float s, const float* ws) {
+__device__ __forceinline__ Run<T> finish_run(const i32x16& acc, const RowScale& s, const float* ws) {
   constexpr int V = Run<T>::V;
   Run<T> r;
 #pragma unroll
@@ -728,7 +740,7 @@ __global__ __launch_bounds__(P::NT * P::KS, P::kWaves) void k_q8_tile(Q8Args a) 
       for (int i = 0; i < P::MI; ++i) {
         const int r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
         const int64_t o = s_out[r];
-        const float s = s_scale[r];
+        const RowScale s = row_scale(s_scale[r]);
 #pragma unroll
         for (int j = 0; j < P::NI; ++j) {
           const uint32_t c = w % P::WN * (P::BN / P::WN) + 32 * j + Run<T>::V * (lane >> 5);
@@ -885,7 +897,7 @@ __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
 #pragma unroll
     for (int i = 0; i < P::MI; ++i) {
       const uint32_t r = w / P::WN * (P::BM / P::WM) + 32 * i + (lane & 31);
-      const float s = s_scale[turn][r];
+      const RowScale s = row_scale(s_scale[turn][r]);
       typename Run<T>::Vec chunk[4 * G];
 #pragma unroll
       for (int j = 0; j < P::NI; ++j) {
@@ -1056,7 +1068,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t c = col0 + lane / 16 * 4 + e;
-        if (c < a.n) out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(acc[e], s_scale[r], ws[c]);
+        if (c < a.n) out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(acc[e], row_scale(s_scale[r]), ws[c]);
       }
     }
   } else {
@@ -1072,7 +1084,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
         int sum = 0;
 #pragma unroll
         for (int p = 0; p < KS; ++p) sum += s_sum[p][r][threadIdx.x % 16];
-        out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(sum, s_scale[r], ws[c]);
+        out[(uint64_t)to.out * a.n + c] = (T)finish<T, kGelu>(sum, row_scale(s_scale[r]), ws[c]);
       }
     }
   }

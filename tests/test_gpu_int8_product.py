@@ -472,3 +472,26 @@ def test_infinite_and_huge_results(gpu, rows, d, n, dtype):
         ok = torch.isfinite(want)
         err = (5 * torch.where(ok & (z.abs() < 13), z, torch.zeros_like(z)) ** 2 + 32) * U + HALF[dtype] * 1.01
         assert bool(((got.double() - want).abs() <= want.abs() * err + 1e-30)[ok].all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d,n", VARIANTS)
+def test_rows_of_the_largest_numbers(gpu, rows, d, n, dtype):
+    """Sums that pass fp32 before the column's scale brings them back, and scales below the normal numbers: a result
+    is off by three roundings and its own (z^2 + 2 times them with GELU, and (2 z^2 + 31) u), whatever the scales."""
+    top = torch.finfo(torch.float32).max / 127
+    s = torch.full((rows,), 1.0, device="cuda")
+    s[::5], s[1::5], s[2::5], s[3::5] = top, 2.0 ** 97, 1.5 * 2.0 ** 96, 2.0 ** -149
+    for scale in (1.0, 1e-3, 1e-36, 1e-38, 1e30):
+        for act in (False, True):
+            got, z = dense(gpu, rows, d, n, dtype, act, s, scale, seed=rows)
+            want = z * 0.5 * torch.special.erfc(-z * 0.5 ** 0.5) if act else z
+            # (where the result passes the type it is infinite; next to its end either will do)
+            most = float(torch.finfo(DT[dtype]).max)
+            fits = want.abs() < most * (1 - 2.0 ** -7)
+            assert bool(torch.isinf(got[want.abs() > most * (1 + 2.0 ** -7)]).all())
+            a = z.abs().clamp(max=13.0)
+            err = (3 * (a * a + 2) + 2 * a * a + 31 if act else torch.full_like(z, 3)) * U * 1.01 + HALF[dtype] * 1.01
+            if act:
+                fits &= z > -13
+            assert bool(((got.double() - want).abs() <= want.abs() * err + 2.0 ** -126)[fits].all())
