@@ -144,14 +144,18 @@ struct Token {
 };
 
 // The kept groups as bits, from the row's c in LDS (no expert: -infinity); *close:
-// a kept and a left one differ by `margin` (relatively, or of one) or less.
+// the marks of a kept and a left one differ by `margin` (relatively, or of one) and
+// the rounding of their members or less. A member is off by 2^-24 of itself, which may be far
+// more than of their sum, the mark: four of them, two a mark, by 2^-22 of the largest. A mark
+// of two lowest values that passes the range of fp32 tells nothing.
 template <int L, typename F>
 __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, uint32_t sub, F margin, bool* close) {
   constexpr int kEach = L >= (int)kMaxGroups ? 1 : (int)kMaxGroups / L;  // groups of a lane
   constexpr int kShare = L > (int)kMaxGroups ? L / (int)kMaxGroups : 1;   // neighbouring lanes of a group
   const uint32_t size = a.E / a.groups;
   const F low = -(F)INFINITY;
-  F mark[kEach];
+  F mark[kEach], largest = 0;
+  uint32_t lost = 0;
 #pragma unroll
   for (int h = 0; h < kEach; ++h) {
     const uint32_t g = (h * L + sub) / kShare;
@@ -171,7 +175,10 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, 
       m2 = max(max(m2, o2), min(m1, o1));
       m1 = max(m1, o1);
     }
-    mark[h] = a.group_best == 2 && m2 > low ? m1 + m2 : m1;
+    const bool two = a.group_best == 2 && m2 > low;
+    mark[h] = two ? m1 + m2 : m1;
+    if (m1 > low) largest = max(largest, max((F)fabs(m1), two ? (F)fabs(m2) : (F)0));
+    lost |= m1 > low && !(mark[h] > low);
   }
   uint32_t better[kEach] = {}, kept = 0;
   const int base = (int)(threadIdx.x & 63) / L * L;
@@ -198,8 +205,9 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteArgs& a, const F* c, 
   for (int m = 1; m < L; m *= 2) {
     least = min(least, (F)__shfl_xor(least, m));
     most = max(most, (F)__shfl_xor(most, m));
+    largest = max(largest, (F)__shfl_xor(largest, m));
   }
-  *close = most > low && !(least - most > margin * (1 + max(fabs(least), fabs(most))));
+  *close = lanes_or<L>(lost) || (most > low && !(least - most > margin * (1 + max(fabs(least), fabs(most))) + (F)0x1p-22 * largest));
   return kept;
 }
 

@@ -311,3 +311,35 @@ def test_on_another_stream_and_captured(gpu, T, E, k):
         torch.cuda.synchronize()
         i = check_route((ids, w), l2, b, None, k, True)
         check_grad(d, l2, i, dw2, None, None, True, True)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("T,E,groups", [(3000, 16, 8), (20000, 16, 8), (4000, 32, 16), (40000, 64, 16), (1000, 128, 16), (20000, 128, 16)])
+def test_groups_whose_best_cancel(gpu, sigmoid, T, E, groups):
+    """Marks of a large bias and its negative: what fp32 loses of the two is far more than what tells the marks apart."""
+    rng = np.random.default_rng([T, E, sigmoid])
+    l = (rng.standard_normal((T, E)) * 1e-2).astype(np.float32)
+    for size in (100.0, 1000.0, 30000.0):
+        b = np.full((groups, E // groups), -4 * size, np.float32)
+        b[:, 0], b[:, 1] = size, -size
+        for top in (1, 3):
+            f = router(gpu, T, E, 2, sigmoid, groups, top)
+            got = f.forward(dev(l), bias=dev(b.reshape(-1)))
+            check_route(got, l, b.reshape(-1), None, 2, sigmoid, groups, top)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("T,E,groups", [(50, 16, 8), (20000, 16, 8), (40000, 64, 16), (300, 128, 16), (20000, 128, 16)])
+def test_marks_below_the_least_number(gpu, sigmoid, T, E, groups):
+    """Two biases near the type's lowest value, whose sum fp32 cannot hold: the groups' order is that of the sums."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    b = np.full((groups, E // groups), -3.4e38, np.float32)
+    b[:, 0] = b[:, 1] = -(3.3e38 - 1e37 * np.arange(groups))   # the last group is the best
+    b = b.reshape(-1)
+    for best in (1, 2):
+        f = router(gpu, T, E, 4, sigmoid, groups, 3, best)
+        check_route(f.forward(dev(l), bias=dev(b)), l, b, None, 4, sigmoid, groups, 3, best)
+    b[2 * (E // groups)] = 0.0                                  # one group of an ordinary and a lowest value
+    f = router(gpu, T, E, 4, sigmoid, groups, 2)
+    check_route(f.forward(dev(l), bias=dev(b)), l, b, None, 4, sigmoid, groups, 2)
