@@ -45,9 +45,6 @@ struct RouteArgs {
 // larger of a NaN and a number is the number).
 __device__ __forceinline__ float usable(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
-// e^x for x up to 0: off by (1.5 |x| + 2) 2^-24 of itself.
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
-
 // ---- the choice -------------------------------------------------------------------
 //
 // L lanes a token, C times four neighbouring experts a lane. The choice is that
@@ -237,7 +234,10 @@ struct Places {
   int32_t id[kEach];  // E: none
 };
 
-// Experts and weights of token `at`; top and total: of its softmax (without renorm).
+// Experts and weights of token `at`; top and total: of its softmax (without renorm). Unlike
+// the scores that order the experts, the weights take expf and divisions: a sigmoid's is a few
+// 2^-24 off whatever its logit, a softmax's as many as logits are apart more, by
+// the rounding of their difference.
 template <int L, bool kSigmoid>
 __device__ __forceinline__ void store_token(const RouteArgs& a, const float* in, uint64_t at, uint32_t sub, bool live,
                                             const Places<L>& p, float top, float total) {
@@ -258,19 +258,19 @@ __device__ __forceinline__ void store_token(const RouteArgs& a, const float* in,
     u[h] = 0.0f;
     if (l[h] != -INFINITY) {
       // s e^-m with m = min(0, the largest logit) keeps the ratios of scores that underflow
-      if constexpr (kSigmoid) u[h] = exp_of(fminf(l[h], 0.0f) - m) * __builtin_amdgcn_rcpf(1.0f + exp_of(-fabsf(l[h])));
-      else u[h] = exp_of(l[h] - m);
+      if constexpr (kSigmoid) u[h] = expf(fminf(l[h], 0.0f) - m) / (1.0f + expf(-fabsf(l[h])));
+      else u[h] = expf(l[h] - m);
     }
     sum += u[h];
   }
   sum = lanes_sum<kLanes>(sum);
-  const float by = a.scale * __builtin_amdgcn_rcpf(a.renorm ? sum : total);
+  const float by = a.renorm ? sum : total;
 #pragma unroll
   for (int h = 0; h < kEach; ++h) {
     const uint32_t j = h * kLanes + sub;
     if (live && sub < (uint32_t)kLanes && j < a.k) {
       a.experts[at * a.k + j] = p.id[h];
-      a.weights[at * a.k + j] = p.id[h] < (int32_t)a.E ? u[h] * by : 0.0f;
+      a.weights[at * a.k + j] = p.id[h] < (int32_t)a.E ? u[h] / by * a.scale : 0.0f;
     }
   }
 }

@@ -343,3 +343,27 @@ def test_marks_below_the_least_number(gpu, sigmoid, T, E, groups):
     b[2 * (E // groups)] = 0.0                                  # one group of an ordinary and a lowest value
     f = router(gpu, T, E, 4, sigmoid, groups, 2)
     check_route(f.forward(dev(l), bias=dev(b)), l, b, None, 4, sigmoid, groups, 2)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(200, 8, 4), (20000, 16, 8), (300, 64, 6), (40000, 64, 8), (500, 256, 8), (20000, 200, 7)])
+def test_weights_of_far_logits(gpu, sigmoid, renorm, T, E, k):
+    """Weights keep their bits far from zero. An exponential (of one ulp at most) is off by 2 u, and by D u for the
+    rounding of a difference of logits that are D apart; 1 + e by 3 u at most and its quotient by u: a sigmoid's score by 6 u,
+    and D u with renorm. A sum's terms e^-D carry D u of themselves, at most 0.37 u of the largest each, and as much besides as
+    one score; adding k of them rounds 3 times, all E up to 21 times (16 in a lane, 6 levels), the quotient and the scale once each."""
+    rng = np.random.default_rng([T, E, k])
+    l = rng.uniform(-80, -10, (T, E)).astype(np.float32)
+    f = router(gpu, T, E, k, sigmoid, renorm=renorm)
+    ids, w = f.forward(dev(l))
+    want_ids, want = ox.route(l, None, None, k, sigmoid, renorm=renorm, scale=SCALE)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    chosen = np.take_along_axis(l, want_ids, 1).astype(np.float64)
+    apart = chosen.max(1, keepdims=True) - chosen  # (without a bias the best has the highest logit of all)
+    if sigmoid:
+        bar = apart + 6 + (0.37 * k + 6) + 3 + 2 if renorm else np.full(want.shape, 6.0 + 2)
+    else:
+        bar = apart + 2 + (0.37 * (k if renorm else E) + 2) + (3 if renorm else 21) + 2
+    ok = np.abs(w.cpu().numpy().astype(np.float64) - want) <= bar * U * want + 1e-44 * SCALE
+    assert ok.all(), (int((~ok).sum()), ok.size)
