@@ -10,6 +10,8 @@
 
 #include <algorithm>
 
+#include "route_key.h"
+
 namespace pw {
 
 namespace {
@@ -57,20 +59,15 @@ __device__ __forceinline__ float usable(float l) { return fminf(fmaxf(l, -INFINI
 // the fp32 evaluation might have exchanged them, these are compared in 64 bits (16
 // lanes a token); where even the (k + 2)-th might belong to the k best, or two
 // groups' marks are that close, or the scores are a softmax, whose 64-bit value
-// needs all logits, a wave takes the token anew in 64 bits. Logits of fewer bits
-// than are cut (bf16 ones; equal ones) leave no doubt.
+// needs all logits, a wave takes the token anew in 64 bits. Where logits alone order
+// the experts, those of fewer bits than are cut (bf16 ones) leave no doubt. Equal scores do,
+// and so do scores that fp32 cannot tell apart.
 //
 // What bounds it: 32 x 256 in groups takes 6.8 us, a launch and one chain of dependent
 // steps (the row, its scores, the groups' marks, eight maxima, the weights); 131072 x 64,
 // k = 6, sigmoid with bias 22.8 us, of vector instructions (its 40 MB would take 7.8), and
 // 4.8 of the second launch. All in 64 bits, as a simple kernel does it, takes 51.6.
 
-// Order-preserving integers of floats other than negative zero.
-__device__ __forceinline__ int32_t ordered(float f) {
-  const int32_t b = __builtin_bit_cast(int32_t, f);
-  return b ^ (b >> 31 & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int32_t i) { return __builtin_bit_cast(float, i ^ (i >> 31 & 0x7fffffff)); }
 constexpr int32_t kLowest = (int32_t)0x80800000;  // of the finite values; those below are no experts
 
 template <int M>
@@ -432,20 +429,20 @@ __global__ __launch_bounds__(kThreads, kWhole ? 2 : 3) void k_route(RouteArgs a)
     }
     // the lane's best in order: each new one moves the lesser ones down
     int32_t list[kList];
-    uint32_t cut = 0;  // bits that are cut off
+    uint32_t cut = 0;  // bits that the keys lack
 #pragma unroll
     for (int n = 0; n < kList; ++n) list[n] = INT32_MIN;
 #pragma unroll
     for (int i = 0; i < 4 * C; ++i) {
-      const uint32_t bits = (uint32_t)ordered(kScored ? c[i] : c[i] + 0.0f);  // (s + b is no negative zero)
-      if (!kScored) cut |= c[i] == -INFINITY ? 0u : bits;
-      const int32_t x = (int32_t)((bits & ~names) | ((names - t.expert(i)) & names));
+      const float v = kScored ? c[i] : c[i] + 0.0f;  // (s + b is no negative zero)
+      if (!kScored) cut |= v == -INFINITY ? 0u : key_lacks(v, names);
+      const int32_t x = route_key(v, t.expert(i), names);
 #pragma unroll
       for (int n = (i < kList - 1 ? i : kList - 1); n > 0; --n) list[n] = middle(list[n - 1], x, list[n]);
       list[0] = max(list[0], x);
     }
     // the token's best, and whether they are in order
-    if (!kScored) cut = lanes_or<L>(cut) & names;
+    if (!kScored) cut = lanes_or<L>(cut);
     typedef Places<L> P;
     P place;
 #pragma unroll
