@@ -670,6 +670,7 @@ typedef struct {
   void* out;                 /* [rows][n]                                       */
 } pw_q8_io;
 
+/* Room for the codes of x; a call that is given q needs none (ws may be NULL). */
 int pw_q8_product_workspace(const pw_q8_desc* d, size_t* bytes);
 int pw_q8_product(const pw_q8_desc* d, const pw_q8_io* io, void* ws, size_t ws_bytes, void* stream);
 

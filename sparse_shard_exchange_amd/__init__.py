@@ -627,10 +627,11 @@ class _Operator:
                                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _run(self, fn, d, io, stream, ws=False):
+        """ws: whether fn takes the workspace (None: it does, but this call has no use for one)."""
         if ws and self._ws_args is None:
             b = self._buf("workspace", (self._ws_bytes,), torch.uint8, stream)
             self._ws_args = (b.data_ptr(), self._ws_bytes)
-        args = self._ws_args if ws else ()
+        args = self._ws_args if ws else (None, 0) if ws is None else ()
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
         if torch.cuda.current_device() == self._index:
             check(fn(C.byref(d), C.byref(io), *args, s))
@@ -920,7 +921,7 @@ class Int8Product(_Operator):
 
     def forward(self, x, x_scale=None, offsets=None, src_index=None, out=None, stream=None):
         """out [rows][n]. x [x_rows][d], or its codes [x_rows][q8_row(d)] with
-        x_scale [x_rows]. Rows of out that no dispatched row gives are left as they
+        x_scale [x_rows] (no workspace is made for those). Rows of out that no dispatched row gives are left as they
         are; out=None: a kept buffer."""
         if out is None:
             out = self._buf("out", (self.rows, self.n), self.dtype, stream)
@@ -934,7 +935,7 @@ class Int8Product(_Operator):
         io.offsets = self._arg("offsets", offsets, (self.E + 1,), torch.int64)
         io.src_index = self._arg("src_index", src_index, (self.rows,), torch.int32)
         io.out = self._arg("out", out, (self.rows, self.n), self.dtype)
-        self._run(lib.pw_q8_product, self.desc, io, stream, ws=True)
+        self._run(lib.pw_q8_product, self.desc, io, stream, ws=True if x_scale is None else None)
         return out
 
 

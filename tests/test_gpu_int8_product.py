@@ -495,3 +495,28 @@ def test_rows_of_the_largest_numbers(gpu, rows, d, n, dtype):
             if act:
                 fits &= z > -13
             assert bool(((got.double() - want).abs() <= want.abs() * err + 2.0 ** -126)[fits].all())
+
+
+@pytest.mark.parametrize("rows,d,n", [(8, 512, 64), (3000, 4096, 64)])
+def test_codes_need_no_workspace(gpu, rows, d, n):
+    """A call that is given codes makes no room for any: nothing is allocated, also under capture, where nothing may be."""
+    w, ws = torch.ones(1, n, d, dtype=torch.int8, device="cuda"), torch.ones(1, n, device="cuda")
+    q, s = torch.ones(rows, d, dtype=torch.int8, device="cuda"), torch.ones(rows, device="cuda")
+    x, out = torch.ones(rows, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    f = gpu.Int8Product(w, ws, d, rows)
+    before = torch.cuda.memory_allocated()
+    f.forward(q, x_scale=s, out=out)
+    assert torch.cuda.memory_allocated() == before and bool((out == d).all())
+    out.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gpu.Int8Product(w, ws, d, rows).forward(q, x_scale=s, out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert bool((out == d).all())
+    with pytest.raises(gpu.PwError):          # this one needs it
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            f.forward(x, out=out)
+    f.forward(x, out=out)
+    assert torch.cuda.memory_allocated() > before and bool((out == d).all())
