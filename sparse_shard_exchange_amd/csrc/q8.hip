@@ -1045,17 +1045,11 @@ __global__ __launch_bounds__(kThreads) void k_q8_few(Q8Args a) {
 
   i32x4 acc = {};
   const unsigned char* from = lds + min((uint32_t)lane % 16, g.rows - 1) * pitch + chunk;
-  for (uint32_t k = k0; k < k1; k += kHeld) {
-    if (k > k0) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) b[i] = *reinterpret_cast<const i32x4*>(pw + min(k + i, nk - 1) * 64);
-    }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int keep = k + i < k1 ? ~0 : 0;  // the steps behind the part's last are zeros
-      const i32x4 x = *reinterpret_cast<const i32x4*>(from + min(k + i, nk - 1) * 64) & keep;
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], x, acc, 0, 0, 0);
-    }
+  for (int i = 0; i < kHeld; ++i) {
+    const int keep = k0 + i < k1 ? ~0 : 0;  // the steps behind the part's last are zeros
+    const i32x4 x = *reinterpret_cast<const i32x4*>(from + min(k0 + i, nk - 1) * 64) & keep;
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[i], x, acc, 0, 0, 0);
   }
 
   // the lane holds 4 columns from 4 (lane / 16) on of row lane % 16
@@ -1112,9 +1106,11 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   typedef Shape<64, 64, 2, 2, 64, 4, 4, 4> Parted;
   typedef Shape<32, 64, 1, 2, 128, 5> Flat;
   if (a.x) {
-    // as many parts of a row as a wave's registers hold in one or, from 4 on, two turns
-    if (a.stride > 32 * 64) return launch_few<T, kGelu, 4>(a, s);
-    return a.stride > 16 * 64 ? launch_few<T, kGelu, 2>(a, s) : launch_few<T, kGelu, 1>(a, s);
+    // as many parts of a row as waves need to hold it in their registers
+    constexpr uint32_t kPart = kHeld * 64;
+    static_assert(kCodeWidth <= 4 * kPart, "four parts hold the longest row");
+    if (a.stride > 2 * kPart) return launch_few<T, kGelu, 4>(a, s);
+    return a.stride > kPart ? launch_few<T, kGelu, 2>(a, s) : launch_few<T, kGelu, 1>(a, s);
   }
   // tiles of a height and width that there will be about, half of each expert's last one empty
   auto tiles = [&](uint32_t m, uint32_t n) {

@@ -520,3 +520,17 @@ def test_codes_need_no_workspace(gpu, rows, d, n):
             f.forward(x, out=out)
     f.forward(x, out=out)
     assert torch.cuda.memory_allocated() > before and bool((out == d).all())
+
+
+@pytest.mark.parametrize("d", [64, 960, 1024, 1025, 1088, 2048, 2049, 2112, 3000, 4032, 4096])
+@pytest.mark.parametrize("rows", [1, 5, 8])
+def test_few_rows_at_the_ends_of_what_a_wave_holds(gpu, rows, d):
+    rng = np.random.default_rng([rows, d])
+    n, E = 70, 3
+    w, ws = weights(gpu, rng, E, n, d)
+    x = rows_of(rng, rows, d, "bf16")
+    q, s = ox.quant(x)
+    off = np.array([0, rows // 2, rows // 2, rows])
+    out = gpu.Int8Product(dev(w), dev(ws), d, rows).forward(dev(x, torch.bfloat16), offsets=dev(off))
+    want, pre = ox.product(q, s, w, ws, off, None, rows)
+    check_product(out, want, pre, "bf16", False)
