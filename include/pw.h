@@ -606,8 +606,8 @@ typedef struct {
 } pw_route_io;
 
 int pw_route(const pw_route_desc* d, const pw_route_io* io, void* stream);
-/* The gradient of the weights with the choice as a constant (groups, top_groups and
- * group_best are not looked at). */
+/* The gradient of the weights with the choice as a constant: groups, top_groups and
+ * group_best change nothing, but the descriptor is one that pw_route takes. */
 int pw_route_grad(const pw_route_desc* d, const pw_route_io* io, void* stream);
 
 /* ---- rows as 8-bit codes ----------------------------------------------------

@@ -1,6 +1,7 @@
 """The oracle of the routing, its gradient, the 8-bit codes and products against
 independent forms, and the refusals of the operators' entry points (host only)."""
 import ctypes as C
+import os
 
 import numpy as np
 import pytest
@@ -171,3 +172,13 @@ def test_quant_and_combine_are_refused():
     for kw in (dict(y=None), dict(weights=None), dict(out=None), dict(y=P + 1), dict(weights=P + 2), dict(add=P + 1)):
         assert c((4, 8, 2, 1), **kw) == pw.PW_ERR_INVALID
     assert c((0, 8, 2, 1), y=None) == pw.PW_OK
+
+
+def test_the_gradient_takes_the_descriptors_that_the_routing_takes():
+    """What the header says of pw_route_grad: group fields that pw_route refuses are refused, here with every buffer there."""
+    full = pw.pw_route_io(logits=P, experts=P, weights=P, dweights=P, dlogits=P)
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "pw.h")).read()
+    assert "not looked at). */\nint pw_route_grad" not in text
+    for bad in (dict(groups=0), dict(top_groups=0), dict(group_best=0), dict(groups=0, top_groups=0, group_best=0)):
+        d = route_desc(tokens=0, **bad)
+        assert code(pw.lib.pw_route, d, full, None) == code(pw.lib.pw_route_grad, d, full, None) == pw.PW_ERR_INVALID
