@@ -1132,9 +1132,11 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   //    17.3 (Square 23.3, Small 21.3), 4096 rows 26.8 (Square 27.7, Small 39.9).
   //  Square: dense 1024 -> 4096, 2048 rows 20.9 (Middle 21.9, Small 26.3); dense 4096 -> 1024,
   //    8192 rows 46.6 (Middle 43.5, Small 75).
-  //  Flat: few rows an expert, so the weights come from memory: tiles of whole lines and a
-  //    deep ring. 48 tokens of 8, 4096 -> 1024: 61.5 (Small 68.4), 128 tokens of 8: 70.8 and
-  //    78.7 (weights not in the caches).
+  //  Flat: few rows an expert and long rows, so the weights come from memory: tiles of whole lines
+  //    and a deep ring. Weights not in the caches, 16, 48, 128, 200 tokens of 8 (Flat / Small),
+  //    codes made in the call: 4096 -> 1024 60 / 62, 65 / 67, 77 / 78, 80 / 83; 4096 -> 2048 99 / 98,
+  //    112 / 116, 121 / 133, 137 / 147; 2560 -> 1024 38 / 39, 41 / 44, 51 / 52, 55 / 57; but 2048 -> 1024
+  //    33 / 31, 36 / 34, 44 / 40, 47 / 45 and 1024 -> 4096 (codes given) 69 / 56, 78 / 63, 88 / 71.
   //  Parted: fewer tiles than CUs and long rows: four groups of waves share a tile's length.
   //    Dense 4096 -> 1024, 16 to 256 rows: 13.2 to 14.2 (Small 16.4).
   const uint64_t each = a.rows / a.E, large = tiles(256, 256);
@@ -1143,7 +1145,7 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   if (each >= 32 && tiles(128, 256) >= 384) return launch_tile<Middle, T, kGelu>(a, s);
   if (each >= 32 && a.stride >= 2048 && tiles(64, 128) >= 256) return launch_tile<Long, T, kGelu>(a, s);
   if (each >= 32 && tiles(128, 128) >= 256) return launch_tile<Square, T, kGelu>(a, s);
-  if (a.E > 1 && a.stride >= 2048 && each < 32 && tiles(32, 64) >= 512) return launch_tile<Flat, T, kGelu>(a, s);
+  if (a.E > 1 && a.stride > 2048 && each < 32 && tiles(32, 64) >= 512) return launch_tile<Flat, T, kGelu>(a, s);
   if (tiles(64, 64) <= 256 && a.stride >= 2048) return launch_tile<Parted, T, kGelu>(a, s);
   return launch_tile<Small, T, kGelu>(a, s);
 }
