@@ -852,7 +852,9 @@ class Router(_Operator):
 
     def grad(self, logits, experts, dweights, valid=None, add=None, stream=None):
         """dlogits [tokens][E] of dweights, with the choice as a constant; add: a
-        gradient of the logits that is added (RouterBalance.grad's)."""
+        gradient of the logits that is added (RouterBalance.grad's). dweights[t][j]
+        is the caller's: dout[t] . y[t][j] of a combine (MoEGrad.combine gives it
+        for two bf16 rows a token, as dgates; there is no operator for more)."""
         io = self._io(logits, valid)
         io.experts = self._arg("experts", experts, (self.T, self.k), torch.int32)
         io.dweights = self._arg("dweights", dweights, (self.T, self.k), torch.float32)

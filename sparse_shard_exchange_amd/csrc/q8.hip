@@ -822,16 +822,18 @@ __device__ __forceinline__ Piece listed_piece(const Q8Args& a, uint32_t b, uint3
 // the products and the stores (it would make the accumulators move): behind the
 // last tile it is started once more, in vain. 131072 x 2 rows of 64 experts, codes given:
 // 4096 -> 1024 in 1.0 to 1.1 ms (2.0 P operations/s, as the library's one large product),
-// 1024 -> 4096 with GELU in 1.75 ms: a tile multiplies for 8 stages only there, and what a CU's
-// one workgroup does then (GELU 0.37 ms, stores 0.25) nothing covers. Results are turned
+// 1024 -> 4096 with GELU in 1.84 ms, without in 1.47: a tile multiplies for 8 stages only there, and
+// what a CU's one workgroup does then (GELU 0.37 ms, stores 0.25) nothing covers. Results are turned
 // among lanes so that a store writes whole lines, past the caches where they are many (whole
-// lines / 32 bytes of each of 32 rows a store: 1.82 and 1.89 ms with GELU, 1.45 and 1.57
-// without; 65536 x 2 of 8 experts in fp32 without GELU 0.82 to 0.92 and 1.2 ms; 32768 x 2 bf16 with GELU
-// 219 and 215 us; rows that end inside a chunk, 2001 long, 238 and 223, so those stay as they are); the first use of an expert's weights costs 12 %, and the clock 15 % (so much less
-// time do weights of zeros take). Two workgroups a CU with tiles of
-// 128 x 256 cover it but load twice as much from the caches: 1.9 ms and more; waves of
-// 4 x 2 or of raised priority change nothing. 64-byte stages instead of 128: 8192^3 in 595 us
-// instead of 571 (a CU's loads are then twice as many, of half a line each).
+// lines / 32 bytes of each of 32 rows a store, in turn on one card: 1.95 and 2.01 ms with GELU, 1.49 and
+// 1.57 without; 65536 x 2 of 8 experts in fp32 without GELU 0.94 and 1.36 ms; 32768 x 2 -> 2048 fp32
+// 212 and 299 us, with GELU 385 and 412, bf16 with GELU 248 and 242; rows that end inside a chunk,
+// 2001 long, 238 and 223 with a shorter GELU, so those stay as they are); the first use of an expert's
+// weights costs 12 %, and the clock 15 % (so much less time do weights of zeros take). Two workgroups a
+// CU with tiles of 128 x 256 cover it but load 768 rows of operands for the 512 of one 256 x 256 tile, 1.5
+// times as much from the caches: 1.98 ms with GELU, 1.78 without; waves of 4 x 2 or of raised
+// priority change nothing. 64-byte stages instead of 128: 8192^3 in 595 us instead of 571 (a CU's loads are then
+// twice as many, of half a line each).
 template <typename P, typename T, bool kGelu, int kRow>
 __global__ __launch_bounds__(P::NT, P::kWaves) void k_q8_stay(Q8Args a) {
   static_assert(P::NT == P::BM + P::BN && P::BM % 64 == 0, "a thread for each scale");
@@ -989,10 +991,11 @@ hipError_t launch_tile(Q8Args a, hipStream_t s) {
 // numbers: exact in any order) meet in LDS. Every workgroup makes the codes of its
 // rows itself, while the matrix is on its way. Against codes in a launch of their
 // own and tiles: one row 4096 -> 1024 in 7.1 us instead of 15.3, one token's 8 experts 4096 ->
-// 1024 in 10.1 instead of 18.1 (33.8 MB: 6.6 us at a large copy's rate; what is left is
-// the launch and the ramp of the loads), 1024 -> 4096 in 11.3 instead of 12.2. From
-// 4 tokens of 8 on it loses (31 us instead of 25.6; 48 of 8 77 instead of 47, weights in the
-// caches): codes are made over and over, and no tile shares what it loads.
+// 1024 in 10.1 instead of 18.1, 1024 -> 4096 in 11.4 instead of 12.2 (33.8 MB: 4.8 us at the rate of a
+// large read; what is left is the launch, the codes and the ramp of the loads). With more rows codes are
+// made over and over, and no tile shares what it loads (tiles / so, weights not in the caches): 2
+// tokens of 8 1024 -> 4096 19.1 and 19.9, 4096 -> 1024 18.1 and 19.2, 3 25.8 and 26.2, 26.0 and 24.8; of one
+// expert 9 rows 9.4 and 9.7, 12.8 and 11.3, 16 rows 9.5 and 11.4, 13.0 and 14.2.
 constexpr int kHeld = 16;              // 64-byte steps of 16 columns in registers
 constexpr uint32_t kCodeWidth = 4096;  // of the rows that a workgroup codes: 8 chunks a lane
 constexpr uint32_t kFewRows = 8;       // of a call
@@ -1120,25 +1123,32 @@ hipError_t launch_product(const Q8Args& a, hipStream_t s) {
   // Times in us with the codes given, where no other case is named for 64 experts and two of
   // them a token ("dense": one expert); rows are counted on the host as a call's most, so an
   // expert's are a guess.
-  //  Large, stays: tiles enough for every CU. Dense 1024 -> 4096, 65536 rows: Large 458,
-  //    Middle 503, Small 775; 4096 rows 31.6, 33.2, 46.2; 16384 tokens (512 rows an
-  //    expert) 285, 285, 463, but 8192 tokens 191, 160, 265. Few codes a row and one expert leave
-  //    mostly the finishing of results, which two workgroups a CU share (65536 rows
-  //    64 -> 1792: 64 and 51, 512 -> 1792: 113 and 99; fp32 results without GELU 118 and 132
-  //    at 128 -> 1792; with 19 experts 155 and 168 at 150396 rows 46 -> 1792).
-  //  Middle: three tiles for two CUs at least. 2048 tokens 1024 -> 4096: Middle 84, Small 98,
-  //    Square 91; 256 tokens (8 rows an expert) 62, 48, 69.
-  //  Long: 128-byte stages are whole lines and half as many waits. Dense 4096 -> 1024, 2048 rows
-  //    17.3 (Square 23.3, Small 21.3), 4096 rows 26.8 (Square 27.7, Small 39.9).
-  //  Square: dense 1024 -> 4096, 2048 rows 20.9 (Middle 21.9, Small 26.3); dense 4096 -> 1024,
-  //    8192 rows 46.6 (Middle 43.5, Small 75).
+  //  Large, stays: tiles enough for every CU. Dense 1024 -> 4096, 65536 rows: Large 396,
+  //    Middle 448, Square 546, Small 732; 4096 rows 31, 32, 34, 46; 16384 tokens (512 rows an
+  //    expert) 287, 291, 347, 478, but 8192 tokens 194, 166, 200, 273. Few codes a row and one expert leave
+  //    mostly the finishing of results, which two workgroups a CU share (65536 rows with GELU
+  //    64 -> 1792: 109 and 86, 512 -> 1792: 138 and 131, in fp32 242 and 232; 128 -> 1792 without 61 and 56, but 512
+  //    97 and 100, and fp32 103 and 129). 19 experts, 150396 rows -> 1792, without GELU 143 and 182 at 46 codes,
+  //    228 and 291 at 512, fp32 215 and 278, 305 and 444; with GELU 263 and 233, 323 and 344, fp32 516 and 415,
+  //    559 and 555: there the shortest rows would gain by Middle too.
+  //  Middle: three tiles for two CUs at least. 2048 tokens 1024 -> 4096: Middle 88, Square 93,
+  //    Small 102; 256 tokens (8 rows an expert) 69, 76, 63. Dense, 2048 rows: 20.2, 18.8, 24.5.
+  //  Long: 128-byte stages are whole lines and half as many waits, where rows are long. Dense 4096 -> 1024,
+  //    2048 rows 15.6 (Square 20.6, Small 18.4), 4096 rows 23.8 (22.7, 35.3); 2048 -> 1024, 2048 rows 10.9 (Square
+  //    11.8), 3000 rows 14.8 (16.9). Shorter rows: 1984 codes 11.4 (Small 12.8) and 16.0 (17.3) but 18.1 (16.5)
+  //    for 4096 rows; 1024 codes 8.2 (8.3), 10.9 (10.9), 11.3 (11.6); 512 codes 6.8 (6.7), 9.0 (7.9), 8.9 (9.5); with
+  //    fewer than 256 tiles it loses (1000 rows 2048 -> 1024 10.7 and 9.1, 1024 -> 1024 8.1 and 6.8).
+  //  Square: dense 1024 -> 4096, 2048 rows 18.8 (Middle 20.2, Small 24.5); dense 4096 -> 1024,
+  //    8192 rows 43.3 (Middle 39.7, Small 69.5).
   //  Flat: few rows an expert and long rows, so the weights come from memory: tiles of whole lines
   //    and a deep ring. Weights not in the caches, 16, 48, 128, 200 tokens of 8 (Flat / Small),
   //    codes made in the call: 4096 -> 1024 60 / 62, 65 / 67, 77 / 78, 80 / 83; 4096 -> 2048 99 / 98,
   //    112 / 116, 121 / 133, 137 / 147; 2560 -> 1024 38 / 39, 41 / 44, 51 / 52, 55 / 57; but 2048 -> 1024
   //    33 / 31, 36 / 34, 44 / 40, 47 / 45 and 1024 -> 4096 (codes given) 69 / 56, 78 / 63, 88 / 71.
   //  Parted: fewer tiles than CUs and long rows: four groups of waves share a tile's length.
-  //    Dense 4096 -> 1024, 16 to 256 rows: 13.2 to 14.2 (Small 16.4).
+  //    Dense 4096 -> 1024, 16 to 256 rows: 13.2 to 14.2 (Small 16.4); 2048 -> 1024 7.8 to 8.4 (8.9 to 9.1), 512 rows
+  //    8.9 (9.2); 1984 codes 7.9 to 8.9 (8.9 to 9.1), 1024 codes 5.5 to 6.6 (5.8 to 6.5), 512 codes 5.0 to 5.5 (4.5
+  //    to 5.2); 512 tiles 11.6 (8.3, 1024 codes).
   const uint64_t each = a.rows / a.E, large = tiles(256, 256);
   const bool finishing = a.E == 1 && a.stride <= 512 && (sizeof(T) == 2 || kGelu);
   if (each >= 512 && !finishing && large >= 256 && large <= 0x3fffffff) return launch_stay<Large, T, kGelu>(a, s);

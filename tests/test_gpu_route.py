@@ -367,3 +367,17 @@ def test_weights_of_far_logits(gpu, sigmoid, renorm, T, E, k):
         bar = apart + 2 + (0.37 * (k if renorm else E) + 2) + (3 if renorm else 21) + 2
     ok = np.abs(w.cpu().numpy().astype(np.float64) - want) <= bar * U * want + 1e-44 * SCALE
     assert ok.all(), (int((~ok).sum()), ok.size)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("T,E,groups", [(60, 8, 4), (20000, 8, 4), (60, 64, 8), (34000, 64, 8), (50, 200, 10), (12000, 200, 10)])
+def test_infinite_biases(gpu, sigmoid, T, E, groups):
+    """An infinite bias is above every score, of several the lowest index comes first; a group that holds one is kept."""
+    rng = np.random.default_rng([T, E])
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    b[[1, E // 2, E - 1]] = np.inf
+    b[[0, E // 2 + 1]] = -np.inf
+    for g, top in ((1, 1), (groups, 2), (groups, 3)):
+        f = router(gpu, T, E, 4, sigmoid, g, top)
+        check_route(f.forward(dev(l), bias=dev(b)), l, b, None, 4, sigmoid, g, top)
