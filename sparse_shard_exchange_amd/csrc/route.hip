@@ -70,10 +70,10 @@ __device__ __forceinline__ float usable(float l) { return fminf(fmaxf(l, -INFINI
 // 1570. bf16 logits and a zero bias: 137 / 47, in groups 156 / 54; with a bias of random bits as
 // fp32 ones. 4096 x 64: 5.5, 9.3 / 6.3, 11 without, 28 / 27, 31 with every token in doubt.
 //
-// What bounds it: 32 x 256 in groups takes 6.8 us, a launch and one chain of dependent
+// What bounds it: 32 x 256 in groups takes 7.7 us, a launch and one chain of dependent
 // steps (the row, its scores, the groups' marks, eight maxima, the weights); 131072 x 64,
-// k = 6, sigmoid with bias 22.8 us, of vector instructions (its 40 MB would take 7.8), and
-// 4.8 of the second launch. All in 64 bits, as a simple kernel does it, takes 51.6.
+// k = 6, sigmoid with bias 23.7 us, of vector instructions (three of four cycles of a SIMD issue one, with
+// 2.7 waves; its 40 MB would take 6.1), and 4.4 to 5 of the second launch. All in 64 bits, as a simple kernel does it, takes 51.6.
 
 constexpr int32_t kLowest = (int32_t)0x80800000;  // of the finite values; those below are no experts
 
@@ -572,9 +572,9 @@ __global__ __launch_bounds__(kThreads) void k_route_rest(RouteArgs a) {
 //   otherwise:  dl_ej = g_j s_ej (1 - s_ej) for a sigmoid,
 //               dl_e = s_e (sum of the g_j with e_j = e - sum_j g_j s_ej) for a softmax
 // L lanes a token, four neighbouring experts a lane; the chosen ones' logits are gathered,
-// each by its own lane, all at once. Bound by memory: 131072 x 64, k = 6, with add, in 18.4 us
-// (77 MB needed; the gathered logits bring whole lines, 110 MB: 6 TB/s). Four lanes a token up
-// to 16 experts, not 16: 131072 x 16 7.4 us instead of 14.1.
+// each by its own lane, all at once. Bound by vector instructions (one in nearly every cycle) and
+// memory alike: 131072 x 64, k = 6, with add, in 18.4 us (77 MB needed; the gathered logits bring
+// whole lines, 110 MB: 6 TB/s); a softmax without renorm or add 17.8. Four lanes a token up to 16 experts, not 16: 131072 x 16 7.4 us instead of 14.1.
 template <int L, bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void k_route_grad(RouteArgs a) {
   typedef float At __attribute__((ext_vector_type(4), aligned(4)));
