@@ -124,8 +124,9 @@ def quant(x):
 
 
 def gelu(z):
+    """z Phi(z), 0 of -infinity."""
     erfc = np.frompyfunc(math.erfc, 1, 1)
-    return z * 0.5 * erfc(-z / math.sqrt(2.0)).astype(np.float64)
+    return np.maximum(z, -np.finfo(np.float64).max) * 0.5 * erfc(-z / math.sqrt(2.0)).astype(np.float64)
 
 
 def product(q, q_scale, w, w_scale, offsets, src_index, rows, gather=0, scatter=False, act=False, out=None):

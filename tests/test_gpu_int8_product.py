@@ -534,3 +534,111 @@ def test_few_rows_at_the_ends_of_what_a_wave_holds(gpu, rows, d):
     out = gpu.Int8Product(dev(w), dev(ws), d, rows).forward(dev(x, torch.bfloat16), offsets=dev(off))
     want, pre = ox.product(q, s, w, ws, off, None, rows)
     check_product(out, want, pre, "bf16", False)
+
+
+# ---- calls that the documentation allows ------------------------------------------
+
+@pytest.mark.parametrize("E,each,d,n,kind", [(256, 600, 64, 520, "even"), (200, 640, 192, 512, "holes"), (64, 2100, 320, 300, "holes")])
+def test_many_experts_where_workgroups_walk(gpu, E, each, d, n, kind):
+    """Up to 256 experts, many of them without a row, in the kernel whose workgroups walk over tiles; misaligned outputs too."""
+    rng = np.random.default_rng([E, n])
+    rows = E * each
+    p = np.ones(E) if kind == "even" else (rng.random(E) < 0.4) + 1e-9
+    dest = rng.choice(E, rows, p=p / p.sum())
+    off = np.concatenate([[0], np.cumsum(np.bincount(dest, minlength=E))])
+    src = np.argsort(dest, kind="stable").astype(np.int32)
+    w, ws = weights(gpu, rng, E, n, d)
+    q = rng.integers(-127, 128, (rows, ox.q8_row(d))).astype(np.int8)
+    q[:, d:] = 0
+    s = (rng.random(rows) * 0.02).astype(np.float32)
+    f = gpu.Int8Product(dev(w), dev(ws), d, rows, scatter=True)
+    flat = torch.full((rows * n + 1,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[1:].view(rows, n)
+    f.forward(dev(q), x_scale=dev(s), offsets=dev(off), src_index=dev(src), out=out)
+    pick = np.sort(rng.choice(rows, 3000, replace=False))           # dispatched rows that are looked at
+    e = np.searchsorted(off, pick, side="right") - 1
+    W, P, X = dev(w), torch.from_numpy(pick), dev(q)
+    for i in range(0, len(pick), 500):
+        rr, ee = P[i:i + 500].cuda(), torch.from_numpy(e[i:i + 500]).cuda()
+        z = (X[rr].double().unsqueeze(1) * W[ee].double()).sum(2) if n * d < 40000 else torch.stack(
+            [W[int(b)].double() @ X[int(a)].double() for a, b in zip(rr, ee)])
+        want = z * dev(s)[rr].double().unsqueeze(1) * dev(ws)[ee].double()
+        got = out[dev(src)[rr].long()].double()
+        assert bool(((got - want).abs() <= want.abs() * (HALF["bf16"] + 3.03 * U) + 1e-37).all())
+    assert float(flat[0]) == 7.0
+
+
+@pytest.mark.parametrize("rows,d,n,E", [(8, 700, 64, 5), (40, 2100, 1000, 5), (300, 1000, 515, 5), (6000, 512, 520, 5), (20000, 640, 1024, 5), (20000, 640, 1024, 1)])
+def test_no_row_at_all(gpu, rows, d, n, E):
+    """Segments that are all empty: nothing is read, nothing written."""
+    rng = np.random.default_rng(rows)
+    w, ws = weights(gpu, rng, E, n, d)
+    x = torch.full((rows, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for at in (0, -3, 1 << 40):
+        off = torch.full((E + 1,), at, dtype=torch.int64, device="cuda")
+        out = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        gpu.Int8Product(dev(w), dev(ws), d, rows).forward(x, offsets=off, out=out)
+        assert bool((out == 7.0).all())
+
+
+def test_two_streams_at_once(gpu):
+    """Objects of their own on two streams, products of every kernel among them, give what they give one after the other."""
+    rng = np.random.default_rng(11)
+    calls = []
+    for i, (rows, d, n) in enumerate(VARIANTS * 2):
+        w, ws = weights(gpu, rng, 1, n, d)
+        x = dev(rows_of(rng, rows, d, "bf16"), torch.bfloat16)
+        f = gpu.Int8Product(dev(w), dev(ws), d, rows, gelu=bool(i % 2))
+        calls.append((f, x, f.forward(x).clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(3):
+        for i, (f, x, want) in enumerate(calls):
+            outs.append((f.forward(x, stream=streams[i % 2]), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
+@pytest.mark.parametrize("rows,d,n", [(7, 701, 65), (40, 2101, 130), (300, 999, 131)])
+def test_rows_that_begin_anywhere(gpu, rows, d, n):
+    """x, out and the scales aligned to their elements alone."""
+    rng = np.random.default_rng(rows)
+    w, ws = weights(gpu, rng, 1, n, d)
+    for dtype in ("bf16", "f32"):
+        x = rows_of(rng, rows, d, dtype)
+        q, s = ox.quant(x)
+
+        def off(a, t):
+            flat = torch.zeros(a.size + 1, dtype=t, device="cuda")
+            v = flat[1:].view(a.shape)
+            v.copy_(dev(a))
+            return v
+
+        for act in (False, True):
+            f = gpu.Int8Product(dev(w), off(ws, torch.float32), d, rows, gelu=act, dtype=pwt(gpu, dtype))
+            out = off(np.zeros((rows, n), np.float32), DT[dtype])
+            f.forward(off(x, DT[dtype]), out=out)
+            want, pre = ox.product(q, s, w, ws, None, None, rows, act=act)
+            check_product(out, want, pre, dtype, act)
+
+
+def test_codes_captured_with_a_limit_that_changes(gpu):
+    rng = np.random.default_rng(13)
+    x = rows_of(rng, 900, 300, "bf16")
+    wq, ws = ox.quant(x)
+    X, limit = dev(x, torch.bfloat16), torch.zeros(1, dtype=torch.int64, device="cuda")
+    f = gpu.RowQuant(900, 300)
+    q, s = f.forward(X, limit=limit)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f.forward(X, limit=limit)
+    for n in (5, 900, 0, 77, 1 << 35):
+        q.fill_(99)
+        s.fill_(-1.0)
+        limit.fill_(n)
+        g.replay()
+        n = min(n, 900)
+        assert np.array_equal(q.cpu().numpy()[:n], wq[:n]) and np.array_equal(s.cpu().numpy()[:n], ws[:n])
+        assert bool((q[n:] == 99).all()) and bool((s[n:] == -1).all())

@@ -182,3 +182,9 @@ def test_the_gradient_takes_the_descriptors_that_the_routing_takes():
     for bad in (dict(groups=0), dict(top_groups=0), dict(group_best=0), dict(groups=0, top_groups=0, group_best=0)):
         d = route_desc(tokens=0, **bad)
         assert code(pw.lib.pw_route, d, full, None) == code(pw.lib.pw_route_grad, d, full, None) == pw.PW_ERR_INVALID
+
+
+def test_gelu_of_infinities():
+    got = ox.gelu(np.array([-np.inf, np.inf, np.nan, -1e300, 0.0, 1.0]))
+    assert got[0] == 0 and got[1] == np.inf and np.isnan(got[2]) and got[3] == 0 and got[4] == 0
+    assert abs(got[5] - 0.8413447460685429) < 1e-15
